@@ -220,6 +220,145 @@ int gtms_attention_softmax_backward(const void* p, const void* dout, const void*
                                     int64_t B, int64_t M, int64_t S, int64_t head_dim, float scale, int dtype,
                                     int32_t* status, void* stream);
 
+/*
+ * A [B, H, S, head_dim] tensor of `dtype` whose element (b, h, s, j) stands at
+ * data + b * stride_b + h * stride_h + s * stride_s + j (strides in elements):
+ * the rows of a head are contiguous vectors, and the three outer dimensions may
+ * be laid out in any order (a [B, S, H, head_dim] projection, or the q, k and v
+ * parts of one fused projection, need no copy). Strides are not negative; the
+ * stride of a dimension of extent 1 is ignored. An input may repeat itself
+ * (stride 0 over an extent above 1: one head or batch broadcast); an output's
+ * elements must be distinct.
+ */
+typedef struct {
+    void* data;
+    int64_t stride_b, stride_h, stride_s;
+} gtms_heads;
+
+/*
+ * Sizes and options of the attention calls. Hq is a multiple of Hkv: query head
+ * h reads key/value head h / (Hq / Hkv). The mask families are those of
+ * gtms_forward_masked with row i of batch b at position
+ * r = q_offsets[b] + i (r = i without q_offsets) and L = clamp(seq_lens[b], 0, Skv):
+ * nothing is kept of rows with r < 0 or r >= L, otherwise
+ *   GTMS_MASK_GROUPED_TRIL   c <= r,
+ *   GTMS_MASK_LENGTH         c < L,
+ *   GTMS_MASK_SLIDING_WINDOW r - window < c <= r.
+ * Whole sequences take Sq == Skv and no offsets. New tokens over a cache take
+ * the cache's capacity as Skv, the live length (new tokens included) as
+ * seq_lens[b] and seq_lens[b] - Sq as q_offsets[b]; one new token is Sq == 1.
+ */
+typedef struct {
+    int64_t B, Hq, Hkv, Sq, Skv, head_dim;
+    int64_t window;
+    int32_t mask_kind, dtype;
+    float scale;
+} gtms_attention_shape;
+
+#define GTMS_ATTENTION_MAX_S (1 << 24)
+
+/*
+ * Attention: with s_ic = scale * q_i . k_c over the kept entries c of row i,
+ *   o_i = sum_c softmax(s_i)_c v_c,   lse_i = log sum_c exp(s_ic)
+ * in one pass, the scores and probabilities staying on the chip. Rows that keep
+ * nothing get o = +0.0 and lse = -inf.
+ *   q        [B, Hq, Sq, head_dim], k, v [B, Hkv, Skv, head_dim], read-only.
+ *   o        [B, Hq, Sq, head_dim], every element written.
+ *   lse      fp32 [B, Hq, Sq], contiguous, or NULL.
+ *   seq_lens device int32[B]; q_offsets device int32[B] or NULL.
+ *   status   as in gtms_attention_softmax_backward.
+ * k and v at c >= L and q at r >= L are never used: anything may stand there,
+ * NaN too. Inside the live length a NaN or infinity in k stays in the rows that
+ * keep it; one in v can reach other rows of the same tile of up to 256 rows.
+ * Sums, maxima and accumulators are fp32; probabilities are rounded once to
+ * `dtype` for the product with v, and o once on its way out.
+ * dtype GTMS_BF16 or GTMS_F16, head_dim 64 or 128. Data 16-byte aligned,
+ * strides multiples of 8 elements. o must not overlap the inputs.
+ * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, Hq not a
+ * multiple of Hkv, a non-finite scale, a window below 1 with the sliding window,
+ * overlaps, an output that repeats itself, misaligned lse, seq_lens, q_offsets
+ * (4 bytes). GTMS_ERR_UNSUPPORTED: other dtypes and head dims, Sq or Skv above
+ * GTMS_ATTENTION_MAX_S, an unknown mask kind, data or strides not aligned as
+ * above, more work than a grid holds. Nothing to do (no rows of o) is GTMS_OK.
+ */
+int gtms_attention_forward(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,
+                           const gtms_heads* v, const gtms_heads* o, float* lse, const int32_t* seq_lens,
+                           const int32_t* q_offsets, int32_t* status, void* stream);
+
+/*
+ * The gradients of gtms_attention_forward, from its inputs and results; the
+ * probabilities are recomputed as p_ic = exp(s_ic - lse_i):
+ *   D_i  = do_i . o_i            ds_ic = p_ic (do_i . v_c - D_i)
+ *   dq_i = scale sum_c ds_ic k_c dk_c = scale sum_i ds_ic q_i   dv_c = sum_i p_ic do_i
+ * with dk and dv summed over the query heads that share the key/value head.
+ *   o, lse, dout      the forward's results and the gradient of o.
+ *   dq, dk, dv        every element written; +0.0 where nothing is kept.
+ *   workspace         device memory of at least the bytes that
+ *                     gtms_attention_backward_workspace gives, 16-byte aligned;
+ *                     its contents need not be set, and calls that may run at
+ *                     the same time need one each.
+ * The sums run in a fixed order (no atomics on the gradients): the same inputs
+ * give the same bits. p and ds are rounded once to `dtype` for their products.
+ * q, o, lse and dout of rows that keep nothing, and k and v at c >= L, are never
+ * used. The three gradients must not overlap each other or any input. Otherwise
+ * as gtms_attention_forward.
+ */
+int gtms_attention_backward(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,
+                            const gtms_heads* v, const gtms_heads* o, const float* lse, const gtms_heads* dout,
+                            const gtms_heads* dq, const gtms_heads* dk, const gtms_heads* dv,
+                            const int32_t* seq_lens, const int32_t* q_offsets, void* workspace,
+                            uint64_t workspace_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace that gtms_attention_backward needs for this shape. Host-only, enqueues nothing. */
+int gtms_attention_backward_workspace(const gtms_attention_shape* shape, uint64_t* bytes);
+
+/*
+ * Rotary positions: pair j of the first rot_dim elements of each head is turned
+ * by the angle a = positions[b][s] * inv_freq[j],
+ *   y1 = amplitude (x1 cos a - x2 sin a),  y2 = amplitude (x2 cos a + x1 sin a),
+ * and the elements from rot_dim on are copied. The pair is (j, j + rot_dim / 2),
+ * or (2j, 2j + 1) when `interleaved` is not 0. With `inverse` not 0 the angle is
+ * -a: the gradient of the forward call.
+ *   x, y      [B, H, S, head_dim]; y may be x itself (same data and strides).
+ *   x2, y2    a second tensor of H2 heads turned by the same call (q and k), or
+ *             both NULL.
+ *   positions device int32 [position_batches, S], position_batches 1 or B.
+ *   inv_freq  device fp32 [rot_dim / 2].
+ * The angle is formed and reduced in extended precision, so positions far from
+ * zero keep full fp32 accuracy. Arithmetic is fp32 for every dtype (GTMS_F32,
+ * GTMS_BF16, GTMS_F16); outputs are rounded once.
+ * head_dim up to 1024, rot_dim even, 0 <= rot_dim <= head_dim. Data and strides
+ * need only be element-aligned; 16-byte aligned ones take the wide kernel.
+ * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, an odd or too
+ * large rot_dim, a non-finite amplitude, misaligned pointers, an output that
+ * repeats itself or overlaps an input other than as its exact alias.
+ * GTMS_ERR_UNSUPPORTED: an unknown dtype, head_dim above 1024, S above
+ * GTMS_ATTENTION_MAX_S.
+ */
+int gtms_rotary(const gtms_heads* x, const gtms_heads* y, const gtms_heads* x2, const gtms_heads* y2, int64_t B,
+                int64_t H, int64_t H2, int64_t S, int64_t head_dim, int64_t rot_dim, const int32_t* positions,
+                int64_t position_batches, const float* inv_freq, int interleaved, float amplitude, int inverse,
+                int dtype, void* stream);
+
+/*
+ * Inverse frequencies of gtms_rotary, into `inv_freq` (host memory, rot_dim / 2
+ * floats): f_j = base^(-2j / rot_dim), then for long contexts
+ *   GTMS_ROTARY_PLAIN    f_j
+ *   GTMS_ROTARY_LINEAR   f_j / factor
+ *   GTMS_ROTARY_BY_PARTS (1 - m) f_j / factor + m f_j with
+ *                        m = clamp((turns_j - low_turns) / (high_turns - low_turns), 0, 1),
+ *                        turns_j = original_length f_j / (2 pi): pairs that turn more than
+ *                        high_turns times over the original length keep their frequency,
+ *                        those below low_turns are stretched.
+ * Computed in double and rounded once. GTMS_ERR_INVALID_ARG: a null pointer, an
+ * odd or negative rot_dim, base or factor not above 0 or not finite, and by parts
+ * high_turns <= low_turns or original_length < 1; GTMS_ERR_UNSUPPORTED: an
+ * unknown kind. Host-only, enqueues nothing.
+ */
+typedef enum { GTMS_ROTARY_PLAIN = 0, GTMS_ROTARY_LINEAR = 1, GTMS_ROTARY_BY_PARTS = 2 } gtms_rotary_scaling;
+int gtms_rotary_frequencies(int64_t rot_dim, double base, int scaling, double factor, double low_turns,
+                            double high_turns, int64_t original_length, float* inv_freq);
+
 /* Static, NUL-terminated name of a status code ("GTMS_OK", ...). */
 const char* gtms_status_string(int status);
 

@@ -1,4 +1,4 @@
-"""Grouped-tril masked softmax for GB300 (sm_103a): thin Python binding of libgtms.
+"""Grouped-tril masked softmax and attention for GB300 (sm_103a): thin Python binding of libgtms.
 
 The compute runs in hand-written CUDA kernels behind the C ABI of
 ``include/gtms.h``. This module only marshals arguments: it passes device
@@ -25,16 +25,35 @@ GTMS_F32, GTMS_BF16, GTMS_F16 = 0, 1, 2
 GTMS_OK, GTMS_ERR_INVALID_ARG, GTMS_ERR_UNSUPPORTED, GTMS_ERR_CUDA, GTMS_ERR_TIMEOUT = 0, 1, 2, 3, 4
 GTMS_MAX_S = 65536
 GTMS_MASK_GROUPED_TRIL, GTMS_MASK_LENGTH, GTMS_MASK_SLIDING_WINDOW = 0, 1, 2
+GTMS_ATTENTION_MAX_S = 1 << 24
+GTMS_ROTARY_PLAIN, GTMS_ROTARY_LINEAR, GTMS_ROTARY_BY_PARTS = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("gtms_forward", "gtms_backward", "gtms_status_string", "gtms_version",
                     "gtms_kernel_name", "gtms_kernel_name_masked", "gtms_kernel_name_explicit",
                     "gtms_device_pointer_of_host",
                     "gtms_forward_masked",
                     "gtms_backward_masked", "gtms_forward_explicit", "gtms_backward_explicit",
-                    "gtms_attention_softmax_backward", "gtms_forward_staged")
+                    "gtms_attention_softmax_backward", "gtms_forward_staged",
+                    "gtms_attention_forward", "gtms_attention_backward", "gtms_attention_backward_workspace",
+                    "gtms_rotary", "gtms_rotary_frequencies")
 
 _lib = None
 _lock = threading.Lock()
+
+
+class Heads(ctypes.Structure):
+    """``gtms_heads``: a strided [B, H, S, head_dim] tensor."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_s", ctypes.c_int64)]
+
+
+class AttentionShape(ctypes.Structure):
+    """``gtms_attention_shape``: sizes and options of the attention calls."""
+
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("Sq", ctypes.c_int64),
+                ("Skv", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("mask_kind", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class GtmsError(RuntimeError):
@@ -77,6 +96,20 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.gtms_attention_softmax_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.c_float,
                                                         ctypes.c_int, vp, vp]
         lib.gtms_attention_softmax_backward.restype = ctypes.c_int
+        heads, shape = ctypes.POINTER(Heads), ctypes.POINTER(AttentionShape)
+        lib.gtms_attention_forward.argtypes = [shape, heads, heads, heads, heads, vp, vp, vp, vp, vp]
+        lib.gtms_attention_forward.restype = ctypes.c_int
+        lib.gtms_attention_backward.argtypes = [shape, heads, heads, heads, heads, vp, heads, heads, heads, heads, vp,
+                                                vp, vp, ctypes.c_uint64, vp, vp]
+        lib.gtms_attention_backward.restype = ctypes.c_int
+        lib.gtms_attention_backward_workspace.argtypes = [shape, ctypes.POINTER(ctypes.c_uint64)]
+        lib.gtms_attention_backward_workspace.restype = ctypes.c_int
+        lib.gtms_rotary.argtypes = [heads, heads, heads, heads, i64, i64, i64, i64, i64, i64, vp, i64, vp, ctypes.c_int,
+                                    ctypes.c_float, ctypes.c_int, ctypes.c_int, vp]
+        lib.gtms_rotary.restype = ctypes.c_int
+        lib.gtms_rotary_frequencies.argtypes = [i64, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                                                ctypes.c_double, i64, vp]
+        lib.gtms_rotary_frequencies.restype = ctypes.c_int
         lib.gtms_status_string.argtypes = [ctypes.c_int]
         lib.gtms_status_string.restype = ctypes.c_char_p
         lib.gtms_version.argtypes = []
@@ -130,6 +163,31 @@ def gtms_attention_softmax_backward(p, dout, v, ds, seq_lens, B, M, S, head_dim,
                                     stream) -> int:
     return load_library().gtms_attention_softmax_backward(p, dout, v, ds, seq_lens, B, M, S, head_dim, scale, dtype,
                                                           status, stream)
+
+
+def gtms_attention_forward(shape, q, k, v, o, lse, seq_lens, q_offsets, status, stream) -> int:
+    return load_library().gtms_attention_forward(shape, q, k, v, o, lse, seq_lens, q_offsets, status, stream)
+
+
+def gtms_attention_backward(shape, q, k, v, o, lse, dout, dq, dk, dv, seq_lens, q_offsets, workspace, workspace_bytes,
+                            status, stream) -> int:
+    return load_library().gtms_attention_backward(shape, q, k, v, o, lse, dout, dq, dk, dv, seq_lens, q_offsets,
+                                                  workspace, workspace_bytes, status, stream)
+
+
+def gtms_attention_backward_workspace(shape, num_bytes) -> int:
+    return load_library().gtms_attention_backward_workspace(shape, num_bytes)
+
+
+def gtms_rotary(x, y, x2, y2, B, H, H2, S, head_dim, rot_dim, positions, position_batches, inv_freq, interleaved,
+                amplitude, inverse, dtype, stream) -> int:
+    return load_library().gtms_rotary(x, y, x2, y2, B, H, H2, S, head_dim, rot_dim, positions, position_batches,
+                                      inv_freq, interleaved, amplitude, inverse, dtype, stream)
+
+
+def gtms_rotary_frequencies(rot_dim, base, scaling, factor, low_turns, high_turns, original_length, inv_freq) -> int:
+    return load_library().gtms_rotary_frequencies(rot_dim, base, scaling, factor, low_turns, high_turns,
+                                                  original_length, inv_freq)
 
 
 def status_string(status: int) -> str:
@@ -434,3 +492,261 @@ def grouped_tril_mask_softmax(x, seq_lens, scale: float = 1.0):
     if _fn is None:
         _fn = _autograd_function()
     return _fn.apply(x, seq_lens, float(scale))
+
+
+# ---------------------------------------------------------------------------
+# Attention and rotary positions: strided [B, H, S, head_dim] tensors.
+# ---------------------------------------------------------------------------
+
+def _check_heads(name, t, like=None):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, H, S, head_dim], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match the first tensor in dtype and device")
+
+
+def _heads(t):
+    s = t.stride()
+    return Heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+class _On:
+    """The tensors' device as the current one, where it is not already."""
+
+    def __init__(self, device):
+        import torch
+
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status):
+    import torch
+
+    _check_heads("q", q)
+    _check_heads("k", k, q)
+    _check_heads("v", v, q)
+    B, Hq, Sq, d = q.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"k and v must be [B, Hkv, Skv, head_dim] matching q, got {tuple(k.shape)} and {tuple(v.shape)}")
+    Hkv, Skv = k.shape[1], k.shape[2]
+    _check_lens(seq_lens, B, q.device)
+    if q_offsets is not None and (q_offsets.dtype != torch.int32 or q_offsets.shape != (B,)
+                                  or q_offsets.device != q.device or not q_offsets.is_contiguous()):
+        raise ValueError("q_offsets must be a contiguous int32 CUDA tensor of shape [B] on q's device")
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != q.device):
+        raise ValueError("status must be an int32 CUDA tensor of one element on q's device")
+    return AttentionShape(B, Hq, Hkv, Sq, Skv, d, int(window), int(mask_kind), _dtype_code(q), float(scale))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def attention_forward(q, k, v, seq_lens, scale: float = 1.0, out=None, mask_kind: int = GTMS_MASK_GROUPED_TRIL,
+                      window: int = 0, q_offsets=None, status=None):
+    """(o, lse) of attention under a mask family, the scores staying on the chip (gtms_attention_forward).
+
+    ``q`` [B, Hq, Sq, d], ``k`` / ``v`` [B, Hkv, Skv, d] (bf16 or fp16, d 64 or 128, Hq a multiple of Hkv), any
+    strides with a contiguous last dimension; ``o`` is laid out like ``q``, ``lse`` is fp32 [B, Hq, Sq]. Row i of
+    batch b stands at position i, or ``q_offsets[b] + i``: for new tokens over a cache pass the cache as ``k`` and
+    ``v``, the lengths with the new tokens as ``seq_lens`` and ``seq_lens - Sq`` as ``q_offsets``. Rows that keep
+    nothing give o = 0 and lse = -inf. ``status`` as in ``attention_softmax_backward``."""
+    import torch
+
+    shape = _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status)
+    o = torch.empty_like(q) if out is None else out
+    _check_heads("out", o, q)
+    if o.shape != q.shape:
+        raise ValueError("out must match q in shape")
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    with _On(q.device):
+        rc = gtms_attention_forward(shape, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
+                                    seq_lens.data_ptr(), _ptr(q_offsets), _ptr(status),
+                                    torch.cuda.current_stream(q.device).cuda_stream)
+    if rc != GTMS_OK:
+        raise GtmsError("gtms_attention_forward", rc)
+    return o, lse
+
+
+def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=None,
+                       mask_kind: int = GTMS_MASK_GROUPED_TRIL, window: int = 0, q_offsets=None, status=None):
+    """(dq, dk, dv) of ``attention_forward``, the probabilities recomputed from ``lse`` (gtms_attention_backward);
+    dk and dv are summed over the query heads that share them. The same inputs give the same bits. ``out`` is an
+    optional triple of tensors to write to."""
+    import torch
+
+    shape = _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status)
+    for name, t in (("o", o), ("dout", dout)):
+        _check_heads(name, t, q)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must match q in shape")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq] on q's device")
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v)) if out is None else out
+    for name, t, of in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_heads(name, t, q)
+        if t.shape != of.shape:
+            raise ValueError(f"{name} must match {name[1:]} in shape")
+    need = ctypes.c_uint64()
+    rc = gtms_attention_backward_workspace(shape, ctypes.byref(need))
+    if rc != GTMS_OK:
+        raise GtmsError("gtms_attention_backward_workspace", rc)
+    with _On(q.device):
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        rc = gtms_attention_backward(shape, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(), _heads(dout),
+                                     _heads(dq), _heads(dk), _heads(dv), seq_lens.data_ptr(), _ptr(q_offsets),
+                                     workspace.data_ptr(), need.value, _ptr(status),
+                                     torch.cuda.current_stream(q.device).cuda_stream)
+    if rc != GTMS_OK:
+        raise GtmsError("gtms_attention_backward", rc)
+    return dq, dk, dv
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = GTMS_ROTARY_PLAIN, factor: float = 1.0,
+                       low_turns: float = 1.0, high_turns: float = 4.0, original_length: int = 8192, device=None):
+    """Inverse frequencies [rot_dim / 2] (fp32) for ``rotary``, plain or scaled for long contexts
+    (gtms_rotary_frequencies)."""
+    import torch
+
+    f = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float32)
+    rc = gtms_rotary_frequencies(int(rot_dim), float(base), int(scaling), float(factor), float(low_turns),
+                                 float(high_turns), int(original_length), f.data_ptr())
+    if rc != GTMS_OK:
+        raise GtmsError("gtms_rotary_frequencies", rc)
+    return f if device is None else f.to(device)
+
+
+def _rotary(x, positions, inv_freq, other, interleaved, amplitude, out, out_other, inverse):
+    import torch
+
+    _check_heads("x", x)
+    B, H, S, d = x.shape
+    dtype = _dtype_code(x)
+    if positions.dtype != torch.int32 or positions.device != x.device or not positions.is_contiguous() \
+            or positions.shape not in ((S,), (1, S), (B, S)):
+        raise ValueError("positions must be a contiguous int32 CUDA tensor [S] or [B, S] on x's device")
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != x.device \
+            or not inv_freq.is_contiguous() or 2 * inv_freq.numel() > d:
+        raise ValueError("inv_freq must be a contiguous fp32 CUDA tensor of at most head_dim / 2 elements on x's device")
+    y = torch.empty_like(x) if out is None else out
+    _check_heads("out", y, x)
+    if y.shape != x.shape:
+        raise ValueError("out must match x in shape")
+    y2, H2, x2_ref, y2_ref = None, 0, None, None
+    if other is not None:
+        _check_heads("other", other, x)
+        if other.shape[0] != B or other.shape[2:] != x.shape[2:]:
+            raise ValueError("other must match x in every dimension but the heads")
+        y2 = torch.empty_like(other) if out_other is None else out_other
+        _check_heads("out_other", y2, x)
+        if y2.shape != other.shape:
+            raise ValueError("out_other must match other in shape")
+        H2, x2_ref, y2_ref = other.shape[1], _heads(other), _heads(y2)
+    with _On(x.device):
+        rc = gtms_rotary(_heads(x), _heads(y), x2_ref, y2_ref, B, H, H2, S, d, 2 * inv_freq.numel(),
+                         positions.data_ptr(), B if positions.dim() == 2 and positions.shape[0] == B else 1,
+                         inv_freq.data_ptr(), int(interleaved), float(amplitude), int(inverse), dtype,
+                         torch.cuda.current_stream(x.device).cuda_stream)
+    if rc != GTMS_OK:
+        raise GtmsError("gtms_rotary", rc)
+    return y if other is None else (y, y2)
+
+
+def rotary_forward(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                   out_other=None):
+    """Rotary positions on ``x`` [B, H, S, d] and, in the same launch, on ``other`` [B, H2, S, d] (q and k): the first
+    ``2 * len(inv_freq)`` elements of each head turned by ``positions * inv_freq``, the rest copied (gtms_rotary).
+    Returns y, or (y, y_other). ``out`` may be ``x`` itself, ``out_other`` may be ``other``."""
+    return _rotary(x, positions, inv_freq, other, interleaved, amplitude, out, out_other, False)
+
+
+def rotary_backward(dy, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                    out_other=None):
+    """Gradient of ``rotary_forward``: the inverse rotation of ``dy`` (and of ``other``'s gradient)."""
+    return _rotary(dy, positions, inv_freq, other, interleaved, amplitude, out, out_other, True)
+
+
+def _usable(t):
+    """A gradient as the kernels take it: one that autograd expanded or sliced is copied."""
+    aligned = 16 // t.element_size()
+    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(n <= 1 or s % aligned == 0
+                                                            for n, s in zip(t.shape[:3], t.stride()[:3]))
+    return t if ok else t.contiguous()
+
+
+def _attention_functions():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Attention(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, seq_lens, q_offsets, scale, mask_kind, window):
+            o, lse = attention_forward(q, k, v, seq_lens, scale, mask_kind=mask_kind, window=window,
+                                       q_offsets=q_offsets)
+            ctx.save_for_backward(q, k, v, o, lse, seq_lens, q_offsets)
+            ctx.options = scale, mask_kind, window
+            return o
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dout):
+            q, k, v, o, lse, seq_lens, q_offsets = ctx.saved_tensors
+            scale, mask_kind, window = ctx.options
+            dq, dk, dv = attention_backward(q, k, v, o, lse, _usable(dout), seq_lens, scale, mask_kind=mask_kind,
+                                            window=window, q_offsets=q_offsets)
+            return dq, dk, dv, None, None, None, None, None
+
+    class Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, positions, inv_freq, interleaved, amplitude, x, *other):
+            ctx.save_for_backward(positions, inv_freq)
+            ctx.options = interleaved, amplitude
+            return rotary_forward(x, positions, inv_freq, *other, interleaved=interleaved, amplitude=amplitude)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, *dy):
+            positions, inv_freq = ctx.saved_tensors
+            interleaved, amplitude = ctx.options
+            dy = [_usable(t) for t in dy]
+            dx = rotary_backward(dy[0], positions, inv_freq, *dy[1:], interleaved=interleaved, amplitude=amplitude)
+            return (None, None, None, None) + (dx if isinstance(dx, tuple) else (dx,))
+
+    return Attention, Rotary
+
+
+_attention_fns = None
+
+
+def _attention_fn(i):
+    global _attention_fns
+    if _attention_fns is None:
+        _attention_fns = _attention_functions()
+    return _attention_fns[i]
+
+
+def attention(q, k, v, seq_lens, scale: float = 1.0, mask_kind: int = GTMS_MASK_GROUPED_TRIL, window: int = 0,
+              q_offsets=None):
+    """Differentiable ``attention_forward`` (o alone); the backward is ``attention_backward``.
+
+    To capture a training step into a CUDA graph, capture ``attention_forward`` and ``attention_backward``
+    themselves, which make no autograd nodes."""
+    return _attention_fn(0).apply(q, k, v, seq_lens, q_offsets, float(scale), int(mask_kind), int(window))
+
+
+def rotary(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0):
+    """Differentiable ``rotary_forward``: y, or (y, y_other)."""
+    rest = () if other is None else (other,)
+    return _attention_fn(1).apply(positions, inv_freq, bool(interleaved), float(amplitude), x, *rest)
