@@ -1,4 +1,5 @@
 // gtms_attention.cu -- the attention forward and backward launches.
+#include "gtms_attention_fwd.cuh"
 #include "gtms_attention_rows.cuh"
 
 namespace gtms {
@@ -6,8 +7,7 @@ namespace gtms {
 template <typename T, int D>
 cudaError_t launch_attention_forward(const AttentionArgs& a, cudaStream_t st)
 {
-    return launch_kernel(gtms_attention_rows_kernel<T, D>, rows_grid(static_cast<int64_t>(a.B) * a.Hq * a.Sq), kRowsThreads,
-                         0, st, a);
+    return launch_attention_fwd_tc<T, D>(a, st);
 }
 
 template <typename T, int D>

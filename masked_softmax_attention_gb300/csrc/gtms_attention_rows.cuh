@@ -1,9 +1,8 @@
-// gtms_attention_rows.cuh -- attention and its backward pass, a warp per row.
+// gtms_attention_rows.cuh -- attention's backward pass, a warp per row.
 //
 // A warp owns one query row (or, for dk and dv, one key row), each lane D / 32
 // of its elements, and walks over the row's kept entries: a dot product across
-// the lanes, then the running maximum and sum (or the saved lse), everything in
-// fp32. Nothing is shared between rows, so every masked entry is simply not
+// the lanes, then the probability from the saved lse, everything in fp32. Nothing is shared between rows, so every masked entry is simply not
 // visited. Bound by the shuffles of the dot products.
 #pragma once
 
@@ -57,37 +56,6 @@ struct RowVec {
         return v;
     }
 };
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowsThreads)
-gtms_attention_rows_kernel(const AttentionArgs a)
-{
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int64_t bh = w / a.Sq;
-    const int32_t i = static_cast<int32_t>(w - bh * a.Sq), b = static_cast<int32_t>(bh / a.Hq), h = static_cast<int32_t>(bh % a.Hq);
-    if (b >= a.B)
-        return;
-    int32_t c0, c1;
-    a.kept(a.offset(b) + i, a.length(b), c0, c1);
-    RowVec<T, D> q, o, x;
-    o.zero();
-    float m = -INFINITY, l = 0.0f;
-    if (c0 < c1)
-        q.load(a.q.row<T>(b, h, i), lane);
-    for (int32_t c = c0; c < c1; ++c) {
-        x.load(a.k.row<T>(b, h / a.group, c), lane);
-        const float s = q.dot(x) * a.scale, top = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.0f : expf(m - top), p = expf(s - top);
-        x.load(a.v.row<T>(b, h / a.group, c), lane);
-        o.scale_add(f, p, x);
-        l = l * f + p;
-        m = top;
-    }
-    o.store(a.o.row<T>(b, h, i), lane, c0 < c1 ? 1.0f / l : 0.0f);
-    if (a.lse && lane == 0)
-        a.lse[w] = c0 < c1 ? m + logf(l) : -INFINITY;
-}
 
 // dq, and D_i for the key rows.
 template <typename T, int D>
