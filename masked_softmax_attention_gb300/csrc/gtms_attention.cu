@@ -1,6 +1,6 @@
 // gtms_attention.cu -- the attention forward and backward launches.
+#include "gtms_attention_bwd.cuh"
 #include "gtms_attention_fwd.cuh"
-#include "gtms_attention_rows.cuh"
 
 namespace gtms {
 
@@ -13,14 +13,7 @@ cudaError_t launch_attention_forward(const AttentionArgs& a, cudaStream_t st)
 template <typename T, int D>
 cudaError_t launch_attention_backward(const AttentionArgs& a, cudaStream_t st)
 {
-    cudaError_t e = cudaSuccess;
-    if (a.Sq > 0)
-        e = launch_kernel(gtms_attention_rows_dq_kernel<T, D>, rows_grid(static_cast<int64_t>(a.B) * a.Hq * a.Sq),
-                          kRowsThreads, 0, st, a);
-    if (e == cudaSuccess && a.Skv > 0)
-        e = launch_kernel(gtms_attention_rows_dkv_kernel<T, D>, rows_grid(static_cast<int64_t>(a.B) * a.Hkv * a.Skv),
-                          kRowsThreads, 0, st, a);
-    return e;
+    return launch_attention_bwd_tc<T, D>(a, st);
 }
 
 #define GTMS_ATTENTION(T, D)                                                             \

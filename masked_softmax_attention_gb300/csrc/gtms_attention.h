@@ -30,7 +30,8 @@ static_assert(kMaxOffset > GTMS_ATTENTION_MAX_S, "a clamped offset must leave no
 struct AttentionArgs {
     HeadsRef q, k, v, o, dout, dq, dk, dv;
     float* lse;
-    float* delta;                 // backward: D_i, [B, Hq, Sq]
+    float *lse2, *delta, *norms;  // backward's workspace (see attention_workspace)
+    int32_t Sq_pad, norm_blocks;
     const int32_t* seq_lens;
     const int32_t* q_offsets;
     int32_t* status;
@@ -62,6 +63,24 @@ struct AttentionArgs {
     }
 #endif
 };
+
+// The backward's workspace: per query row, padded to whole tiles of 128, lse in
+// base 2 and D; then the partial maxima of the norms of dout and v.
+constexpr int64_t kWorkspaceNorms = 2 * 1024;
+
+inline int64_t attention_padded_rows(int64_t B, int64_t Hq, int64_t Sq) { return B * Hq * ((Sq + 127) / 128 * 128); }
+inline uint64_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Sq)
+{
+    return static_cast<uint64_t>(2 * attention_padded_rows(B, Hq, Sq) + kWorkspaceNorms) * 4;
+}
+inline void attention_workspace(AttentionArgs& a, void* workspace)
+{
+    a.Sq_pad = (a.Sq + 127) / 128 * 128;
+    const int64_t rows = attention_padded_rows(a.B, a.Hq, a.Sq);
+    a.lse2 = static_cast<float*>(workspace);
+    a.delta = a.lse2 + rows;
+    a.norms = a.delta + rows;
+}
 
 struct RotaryArgs {
     HeadsRef x[2], y[2];

@@ -126,12 +126,6 @@ struct Backward {
     static cudaError_t run(const gtms::AttentionArgs& a, cudaStream_t st) { return gtms::launch_attention_backward<T, D>(a, st); }
 };
 
-uint64_t backward_bytes(const gtms_attention_shape& p, int64_t rows)
-{
-    (void)p;
-    return (static_cast<uint64_t>(rows) * 4 + 15) / 16 * 16;
-}
-
 }  // namespace
 
 GTMS_EXPORT int gtms_attention_forward(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,
@@ -189,7 +183,7 @@ GTMS_EXPORT int gtms_attention_backward_workspace(const gtms_attention_shape* sh
         return rc;
     if (!bytes)
         return GTMS_ERR_INVALID_ARG;
-    *bytes = backward_bytes(*shape, rows);
+    *bytes = gtms::attention_workspace_bytes(shape->B, shape->Hq, shape->Sq);
     return GTMS_OK;
 }
 
@@ -219,9 +213,9 @@ GTMS_EXPORT int gtms_attention_backward(const gtms_attention_shape* shape, const
         if (rc != GTMS_OK)
             return rc;
     }
-    const uint64_t need = backward_bytes(p, rows);
+    const uint64_t need = gtms::attention_workspace_bytes(p.B, p.Hq, p.Sq);
     if (!seq_lens || !aligned_to(seq_lens, 4) || !aligned_to(q_offsets, 4) || !aligned_to(status, 4) ||
-        (rows > 0 && (!lse || !aligned_to(lse, 4))) || (need > 0 && (!workspace || workspace_bytes < need)) ||
+        (rows > 0 && (!lse || !aligned_to(lse, 4))) || !workspace || workspace_bytes < need ||
         !aligned_to(workspace, 16))
         return GTMS_ERR_INVALID_ARG;
     const uint64_t lens = static_cast<uint64_t>(p.B) * 4, lse_bytes = static_cast<uint64_t>(rows) * 4;
@@ -240,13 +234,11 @@ GTMS_EXPORT int gtms_attention_backward(const gtms_attention_shape* shape, const
             if (j != i && span[j].bytes != 0 && gtms::heads_may_overlap(span[i], span[j]))
                 return GTMS_ERR_INVALID_ARG;
     }
-    if (need > 0) {
-        HeadsSpan w;
-        w.base = reinterpret_cast<uint64_t>(workspace);
-        w.bytes = need;
-        if (hits(w, seq_lens, lens) || hits(w, q_offsets, lens) || hits(w, status, 4) || hits(w, lse, lse_bytes))
-            return GTMS_ERR_INVALID_ARG;
-    }
+    HeadsSpan w;
+    w.base = reinterpret_cast<uint64_t>(workspace);
+    w.bytes = need;
+    if (hits(w, seq_lens, lens) || hits(w, q_offsets, lens) || hits(w, status, 4) || hits(w, lse, lse_bytes))
+        return GTMS_ERR_INVALID_ARG;
     gtms::AttentionArgs a{};
     fill_args(a, p);
     gtms::HeadsRef* const ref[8] = {&a.q, &a.o, &a.dout, &a.dq, &a.k, &a.v, &a.dk, &a.dv};
@@ -254,7 +246,7 @@ GTMS_EXPORT int gtms_attention_backward(const gtms_attention_shape* shape, const
         if (span[i].bytes != 0)
             *ref[i] = device_ref(*ptr[i], span[i], 2);
     a.lse = const_cast<float*>(lse);
-    a.delta = static_cast<float*>(workspace);
+    gtms::attention_workspace(a, workspace);
     a.seq_lens = seq_lens;
     a.q_offsets = q_offsets;
     a.status = status;

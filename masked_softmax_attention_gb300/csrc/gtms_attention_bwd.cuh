@@ -1,0 +1,956 @@
+// gtms_attention_bwd.cuh -- attention's backward pass on the tensor cores.
+//
+//   p_ic = exp(s_ic - lse_i),  ds_ic = p_ic (do_i . v_c - D_i),  D_i = do_i . o_i
+//   dv_c = sum_i p_ic do_i,  dk_c = scale sum_i ds_ic q_i,  dq_i = scale sum_c ds_ic k_c
+//
+// Three launches. The first forms, per query row, D and lse in base 2, so that
+// the others never read o (bound by memory: one read of o and do). The second
+// owns 128 keys at a time and sums dk and dv over the query tiles, and the heads,
+// that keep them; the third owns 128 queries and sums dq over key tiles. Scores
+// and dP are formed in both: 7 products of 128 x 128 x d per tile pair instead of
+// the 5 that one pass with dq summed by atomics would take. In exchange nothing
+// but the results goes through memory, no order of sums depends on timing, and
+// each accumulator stays in tensor memory.
+#pragma once
+
+#include "gtms_attention_tc.cuh"
+
+namespace gtms {
+
+constexpr int kBwdGroups = 2;                            // warpgroups that share a tile's columns
+constexpr int kBwdWarps = 4 * kBwdGroups;                // element-wise warps
+constexpr int kBwdCols = kTile / kBwdGroups;             // columns of a tile per thread
+constexpr int kBwdMmaWarp = kBwdWarps, kBwdLoadWarp = kBwdWarps + 1;
+constexpr int kBwdThreads = 32 * (kBwdWarps + 4);
+constexpr int kBwdRegs = 168, kBwdElemRegs = 208, kBwdOtherRegs = 88;
+static_assert(kBwdGroups * kBwdElemRegs + kBwdOtherRegs <= (kBwdGroups + 1) * kBwdRegs, "register shares of one block");
+
+constexpr int kPrepThreads = 256, kPrepMaxBlocks = 1024;
+
+// fp16 holds p and ds scaled by powers of two, so that neither the p of long rows
+// nor the ds of small gradients falls out of its range: p <= 1 by 2^14, ds by the
+// power of two that takes the bound 2 max|do_i| max|v_c| of its size to at most
+// 2^14. bf16 has fp32's range and takes them as they are.
+template <typename T>
+constexpr int kPShift = std::is_same<T, __half>::value ? 14 : 0;
+
+__device__ __forceinline__ float gradient_factor(float do_norm, float v_norm)
+{
+    const float bound = 2.0f * do_norm * v_norm;
+    if (!(bound > 0.0f) || bound > 3e38f)
+        return 1.0f;
+    int e = 14 - (ilogbf(bound) + 1);
+    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+    return exp2f(static_cast<float>(e));
+}
+
+// Per padded query row: lse log2(e) - kPShift (+inf where nothing is kept, which
+// makes every p of the row zero) and D. For fp16 also the largest norms of the
+// live rows of do and of the live keys of v, one partial maximum per block.
+// D / 8 lanes hold a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPrepThreads)
+gtms_attention_bwd_prep_kernel(const AttentionArgs a, int64_t rows, int64_t keys)
+{
+    constexpr int LANES = D / 8, PER = kPrepThreads / LANES;
+    constexpr bool norms = std::is_same<T, __half>::value;
+    const int sub = threadIdx.x % LANES;
+    float do_norm = 0.0f, v_norm = 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * PER;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * PER; base < rows; base += step) {
+        const int64_t w = base + threadIdx.x / LANES;
+        float dot = 0.0f, sq = 0.0f;
+        bool live = false;
+        int64_t bh = 0;
+        int32_t i = 0;
+        if (w < rows) {
+            bh = w / a.Sq_pad;
+            i = static_cast<int32_t>(w - bh * a.Sq_pad);
+            const int32_t b = static_cast<int32_t>(bh / a.Hq), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.Hq);
+            int32_t c0 = 0, c1 = 0;
+            if (i < a.Sq)
+                a.kept(a.offset(b) + i, a.length(b), c0, c1);
+            live = c0 < c1;
+            if (live) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.dout.row<T>(b, h, i)) + sub);
+                const uint4 y = __ldg(reinterpret_cast<const uint4*>(a.o.row<T>(b, h, i)) + sub);
+                const T* xe = reinterpret_cast<const T*>(&x);
+                const T* ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float f = static_cast<float>(xe[k]);
+                    dot += f * static_cast<float>(ye[k]);
+                    sq += f * f;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (norms)
+                sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        }
+        do_norm = fmaxf(do_norm, sq);
+        if (sub == 0 && w < rows) {
+            a.delta[w] = dot;
+            a.lse2[w] = live ? a.lse[bh * a.Sq + i] * kLog2e - kPShift<T> : INFINITY;
+        }
+    }
+    if constexpr (norms) {
+        for (int64_t base = static_cast<int64_t>(blockIdx.x) * PER; base < keys; base += step) {
+            const int64_t w = base + threadIdx.x / LANES;
+            float sq = 0.0f;
+            if (w < keys) {
+                const int64_t bg = w / a.Skv;
+                const int32_t c = static_cast<int32_t>(w - bg * a.Skv), b = static_cast<int32_t>(bg / a.Hkv);
+                if (c < a.length(b)) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.v.row<T>(b, bg - static_cast<int64_t>(b) * a.Hkv, c)) + sub);
+                    const T* xe = reinterpret_cast<const T*>(&x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        sq += static_cast<float>(xe[k]) * static_cast<float>(xe[k]);
+                }
+            }
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1)
+                sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            v_norm = fmaxf(v_norm, sq);
+        }
+        __shared__ float part[2][kPrepThreads / 32];
+        do_norm = team_max<32>(do_norm, nullptr);
+        v_norm = team_max<32>(v_norm, nullptr);
+        if ((threadIdx.x & 31) == 0) {
+            part[0][threadIdx.x >> 5] = do_norm;
+            part[1][threadIdx.x >> 5] = v_norm;
+        }
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            float m = 0.0f;
+            for (int k = 0; k < kPrepThreads / 32; ++k)
+                m = fmaxf(m, part[threadIdx.x][k]);
+            a.norms[threadIdx.x * kPrepMaxBlocks + blockIdx.x] = sqrtf(m);
+        }
+    }
+}
+
+// The factor of ds, from the partial maxima (every thread of the block calls).
+template <typename T>
+__device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, float* shared2)
+{
+    if constexpr (!std::is_same<T, __half>::value)
+        return 1.0f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 2) {
+        float m = 0.0f;
+        for (int k = lane; k < a.norm_blocks; k += 32)
+            m = fmaxf(m, __ldg(a.norms + warp * kPrepMaxBlocks + k));
+        m = team_max<32>(m, nullptr);
+        if (lane == 0)
+            shared2[warp] = m;
+    }
+    __syncthreads();
+    return gradient_factor(shared2[0], shared2[1]);
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv. Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T
+// and dS^T are in tensor memory as the A operands of dV += P^T dO and
+// dK += dS^T Q. Tensor memory: S^T, dP^T (128 columns each; P^T and dS^T, 16 bits,
+// over them, each warpgroup's part over its own scores), dV, dK (head_dim each).
+// While the element-wise warps form dS of one query tile the tensor cores run
+// dV of that tile and S of the next, and while they form P of the next, dK and dP.
+// ---------------------------------------------------------------------------
+template <int D>
+struct DkvTile {
+    static constexpr int stages = 2;
+    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
+    static constexpr uint32_t off_k = 0, off_v = bytes, off_q = 2 * bytes, off_do = (2 + stages) * bytes;
+    static constexpr uint32_t off_rows = (2 + 2 * stages) * bytes;           // per stage: 128 lse2, 128 D
+    static constexpr uint32_t smem = off_rows + stages * 2 * kTile * 4 + 1024;
+};
+
+struct DkvShared {
+    uint64_t kfull, kempty, vfull, vempty;
+    uint64_t qfull[2], qempty[2], dofull[2], doempty[2], raw;
+    uint64_t sfull, pready, dpfull, dsready, accfull, accempty, mma_done;
+    uint32_t tmem_slot;
+    int flag;
+    float norm[2];
+};
+
+struct DkvItem {
+    int32_t b, g, j, off, L, lo, hi;   // key tile j of head g; query tiles [lo, hi)
+
+    __device__ __forceinline__ DkvItem(const AttentionArgs& a, int64_t item, int64_t heads)
+    {
+        // Under a causal mask the first key tiles are kept by the most rows.
+        j = static_cast<int32_t>(item / heads);
+        const int32_t bg = static_cast<int32_t>(item % heads);
+        b = bg / a.Hkv;
+        g = bg - b * a.Hkv;
+        off = a.offset(b);
+        L = a.length(b);
+        lo = hi = 0;
+        const int32_t ca = j * kTile, cb = (ca + kTile < L ? ca + kTile : L) - 1;   // live keys
+        if (ca > cb)
+            return;
+        int32_t ra = a.mask_kind == GTMS_MASK_LENGTH ? 0 : ca, rb = L - 1;
+        if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && cb + a.window - 1 < rb)
+            rb = cb + a.window - 1;
+        int32_t ia = ra - off, ib = rb - off;
+        ia = ia > 0 ? ia : 0;
+        ib = ib < a.Sq - 1 ? ib : a.Sq - 1;
+        if (ia <= ib) {
+            lo = ia / kTile;
+            hi = ib / kTile + 1;
+        }
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
+                          const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
+                          const __grid_constant__ AttentionArgs a, int64_t heads, int64_t items, uint64_t wait_ns)
+{
+    using TL = DkvTile<D>;
+    constexpr int ST = TL::stages;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ DkvShared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const GiveUp up{&sh.flag, a.status, wait_ns};
+
+    if (threadIdx.x == 0) {
+        uint64_t* const one[] = {&sh.kfull, &sh.kempty, &sh.vfull, &sh.vempty, &sh.raw, &sh.sfull, &sh.dpfull, &sh.accfull,
+                                 &sh.mma_done, &sh.qfull[0], &sh.qfull[1], &sh.qempty[0], &sh.qempty[1], &sh.dofull[0],
+                                 &sh.dofull[1], &sh.doempty[0], &sh.doempty[1]};
+        for (uint64_t* m : one)
+            tc::mbar_init(m, 1);
+        tc::mbar_init(&sh.pready, kBwdWarps);
+        tc::mbar_init(&sh.dsready, kBwdWarps);
+        tc::mbar_init(&sh.accempty, kBwdWarps);
+        sh.flag = 0;
+    }
+    if (warp == kBwdMmaWarp) {
+        __syncwarp();
+        tc::tmem_alloc<512>(&sh.tmem_slot);
+    }
+    const float factor = block_gradient_factor<T>(a, sh.norm);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + D;
+
+    if (warp >= kBwdMmaWarp) {
+        tc::regs_lower<kBwdOtherRegs>();
+        if (warp == kBwdLoadWarp) {
+            uint32_t gq = 0, nk = 0, nraw = 0;
+            uint32_t issued_q = 0, issued_do = 0, issued_k = 0, issued_v = 0;
+            bool ok = true;
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+                const DkvItem it(a, item, heads);
+                if (it.lo == it.hi)
+                    continue;
+                // A 128-row tile of queries or output gradients; rows that keep nothing may hold
+                // anything, and 0 x NaN is NaN: they are zeroed before the tensor cores see them.
+                auto rows = [&](const HeadsMap& m, uint32_t dst, int32_t i, int32_t h, uint64_t* full, uint32_t extra,
+                                uint32_t rows_dst, int64_t at) {
+                    const int32_t i0 = i * kTile;
+                    const int32_t n = a.Sq - i0 < kTile ? a.Sq - i0 : kTile;
+                    const int32_t za = -it.off - i0 > 0 ? -it.off - i0 : 0;
+                    const int32_t zb = it.L - it.off - i0 < n ? it.L - it.off - i0 : n;
+                    const bool patch = za > 0 || zb < n;
+                    uint64_t* bar = patch ? &sh.raw : full;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(bar, TL::bytes + extra);
+                        load_tile<D, kTile>(base + dst, m, i0, h, it.b, bar);
+                        if (extra) {
+                            tc::bulk_load_1d(base + rows_dst, a.lse2 + at, kTile * 4, bar);
+                            tc::bulk_load_1d(base + rows_dst + kTile * 4, a.delta + at, kTile * 4, bar);
+                        }
+                    }
+                    if (patch) {
+                        ok = up.warp_wait(&sh.raw, nraw & 1u);
+                        ++nraw;
+                        if (!ok)
+                            return;
+                        zero_tile_rows<D>(smem + dst, 0, za, lane);
+                        zero_tile_rows<D>(smem + dst, zb, n, lane);
+                        tc::fence_smem_for_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(full);
+                    }
+                };
+                bool first = true;
+                for (int32_t h = it.g * a.group; h < (it.g + 1) * a.group && ok; ++h)
+                    for (int32_t i = it.lo; i < it.hi && ok; ++i) {
+                        const uint32_t s = gq % ST, ph = ((gq / ST) & 1u) ^ 1u;
+                        const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + h) * a.Sq_pad + i * kTile;
+                        if (first) {
+                            ok = up.warp_wait(&sh.kempty, (nk & 1u) ^ 1u);
+                            if (!ok)
+                                break;
+                            if (lane == 0) {
+                                tc::mbar_arrive_expect_tx(&sh.kfull, TL::bytes);
+                                load_tile<D, kTile>(base + TL::off_k, mk, it.j * kTile, it.g, it.b, &sh.kfull);
+                            }
+                            issued_k = nk + 1;
+                        }
+                        ok = up.warp_wait(&sh.qempty[s], ph);
+                        if (!ok)
+                            break;
+                        rows(mq, TL::off_q + s * TL::bytes, i, h, &sh.qfull[s], 2 * kTile * 4, TL::off_rows + s * 2 * kTile * 4, at);
+                        if (!ok)
+                            break;
+                        issued_q = gq + 1;
+                        if (first) {
+                            ok = up.warp_wait(&sh.vempty, (nk & 1u) ^ 1u);
+                            if (!ok)
+                                break;
+                            if (lane == 0) {
+                                tc::mbar_arrive_expect_tx(&sh.vfull, TL::bytes);
+                                load_tile<D, kTile>(base + TL::off_v, mv, it.j * kTile, it.g, it.b, &sh.vfull);
+                            }
+                            issued_v = nk + 1;
+                            first = false;
+                        }
+                        ok = up.warp_wait(&sh.doempty[s], ph);
+                        if (!ok)
+                            break;
+                        rows(mdo, TL::off_do + s * TL::bytes, i, h, &sh.dofull[s], 0, 0, 0);
+                        if (!ok)
+                            break;
+                        issued_do = gq + 1;
+                        ++gq;
+                    }
+                ++nk;
+            }
+            if (!ok) {   // let the copies already issued land before the CTA can exit
+                for (uint32_t k = 0; k < static_cast<uint32_t>(ST); ++k) {
+                    if (k < issued_q)
+                        tc::mbar_wait(&sh.qfull[(issued_q - 1 - k) % ST], ((issued_q - 1 - k) / ST) & 1u, kAttnDrainWaitNs);
+                    if (k < issued_do)
+                        tc::mbar_wait(&sh.dofull[(issued_do - 1 - k) % ST], ((issued_do - 1 - k) / ST) & 1u, kAttnDrainWaitNs);
+                }
+                if (issued_k)
+                    tc::mbar_wait(&sh.kfull, (issued_k - 1) & 1u, kAttnDrainWaitNs);
+                if (issued_v)
+                    tc::mbar_wait(&sh.vfull, (issued_v - 1) & 1u, kAttnDrainWaitNs);
+                if (nraw)
+                    tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
+            }
+        } else if (warp == kBwdMmaWarp && lane == 0) {
+            constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
+            uint32_t gq = 0, gt = 0, nk = 0;   // query tiles, element-wise hand-offs, items
+            bool ok = true;
+            // acc += A B, A (16 bits, in tensor memory, a part of it per warpgroup) and B a tile of rows.
+            auto accumulate = [&](uint32_t acc, uint32_t t_a, uint32_t rows, bool more) {
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks) {
+                    const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
+                    tc::mma_f16_ts(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
+                }
+            };
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+                const DkvItem it(a, item, heads);
+                const int32_t n = (it.hi - it.lo) * a.group;
+                if (n == 0)
+                    continue;
+                auto scores = [&](uint32_t q) {
+                    ok = up.wait(&sh.qfull[q % ST], (q / ST) & 1u);
+                    if (!ok)
+                        return;
+                    tc::fence_after_sync();
+                    mma_abt<T, D>(t_s, base + TL::off_k, base + TL::off_q + (q % ST) * TL::bytes);
+                    tc::commit(&sh.sfull);
+                };
+                auto products = [&](uint32_t q) {
+                    ok = up.wait(&sh.dofull[q % ST], (q / ST) & 1u);
+                    if (!ok)
+                        return;
+                    tc::fence_after_sync();
+                    mma_abt<T, D>(t_dp, base + TL::off_v, base + TL::off_do + (q % ST) * TL::bytes);
+                    tc::commit(&sh.dpfull);
+                };
+                ok = up.wait(&sh.kfull, nk & 1u);
+                if (ok)
+                    scores(gq);
+                if (ok && n == 1)
+                    tc::commit(&sh.kempty);
+                if (ok)
+                    ok = up.wait(&sh.vfull, nk & 1u);
+                if (ok)
+                    products(gq);
+                if (ok && n == 1)
+                    tc::commit(&sh.vempty);
+                for (int32_t k = 0; k < n && ok; ++k, ++gq, ++gt) {
+                    ok = up.wait(&sh.pready, gt & 1u);
+                    if (ok && k == 0)
+                        ok = up.wait(&sh.accempty, (nk & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    accumulate(t_dv, t_s, base + TL::off_do + (gq % ST) * TL::bytes, k > 0);
+                    tc::commit(&sh.doempty[gq % ST]);
+                    if (k + 1 < n) {
+                        scores(gq + 1);
+                        if (ok && k + 2 == n)
+                            tc::commit(&sh.kempty);
+                    }
+                    if (ok)
+                        ok = up.wait(&sh.dsready, gt & 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    accumulate(t_dk, t_dp, base + TL::off_q + (gq % ST) * TL::bytes, k > 0);
+                    tc::commit(&sh.qempty[gq % ST]);
+                    if (k + 1 < n) {
+                        products(gq + 1);
+                        if (ok && k + 2 == n)
+                            tc::commit(&sh.vempty);
+                    }
+                }
+                if (ok)
+                    tc::commit(&sh.accfull);
+                ++nk;
+            }
+            tc::commit(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
+            tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
+        }
+    } else {
+        tc::regs_raise<kBwdElemRegs>();
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t my_s = t_s + lanes + part * kBwdCols, my_dp = t_dp + lanes + part * kBwdCols;
+        const float c = a.scale * kLog2e;
+        const float2 c2 = make_float2(c, c);
+        const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
+        uint32_t gt = 0, nk = 0;
+        bool ok = true;
+        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+            const DkvItem it(a, item, heads);
+            const int32_t key = it.j * kTile + row;
+            const bool any = it.lo != it.hi;
+            for (int32_t h = 0; h < (any ? a.group : 0) && ok; ++h)
+                for (int32_t i = it.lo; i < it.hi; ++i, ++gt) {
+                    const uint32_t s = gt % ST;
+                    ok = up.warp_wait(&sh.qfull[s], (gt / ST) & 1u) && up.warp_wait(&sh.sfull, gt & 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    const float* lse2 = reinterpret_cast<const float*>(smem + TL::off_rows + s * 2 * kTile * 4) + part * kBwdCols;
+                    const float* delta = lse2 + kTile;
+                    float p[kBwdCols];
+                    tc::tmem_ld64(my_s, p);
+#pragma unroll
+                    for (int j = 0; j < kBwdCols; j += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(lse2 + j);
+                        const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, make_float2(-e.x, -e.y));
+                        const float2 y = __ffma2_rn(make_float2(p[j + 2], p[j + 3]), c2, make_float2(-e.z, -e.w));
+                        p[j] = exp2_approx(x.x);
+                        p[j + 1] = exp2_approx(x.y);
+                        p[j + 2] = exp2_approx(y.x);
+                        p[j + 3] = exp2_approx(y.y);
+                    }
+                    const int32_t r0 = it.off + i * kTile;   // the tile's first position
+                    if (a.mask_kind != GTMS_MASK_LENGTH &&
+                        (r0 < it.j * kTile + kTile - 1 ||
+                         (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && r0 + kTile - 1 >= it.j * kTile + a.window))) {
+                        const int32_t k0 = key - r0 - part * kBwdCols;
+                        const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : kTile;
+#pragma unroll
+                        for (int j = 0; j < kBwdCols; ++j)
+                            p[j] = j >= k0 && j < k1 ? p[j] : 0.0f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBwdCols; k += 32) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            r[j] = pack2<T>(p[k + 2 * j], p[k + 2 * j + 1]);
+                        tc::tmem_st16(my_s + k / 2, r);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.pready);
+                    ok = up.warp_wait(&sh.dpfull, gt & 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    float ds[kBwdCols];
+                    tc::tmem_ld64(my_dp, ds);
+#pragma unroll
+                    for (int k = 0; k < kBwdCols; k += 32) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const int at = k + 2 * j;
+                            const float4 e = *reinterpret_cast<const float4*>(delta + at);
+                            float2 x = __fadd2_rn(make_float2(ds[at], ds[at + 1]), make_float2(-e.x, -e.y));
+                            float2 y = __fadd2_rn(make_float2(ds[at + 2], ds[at + 3]), make_float2(-e.z, -e.w));
+                            if (kPShift<T> != 0) {
+                                x = __fmul2_rn(x, make_float2(fk, fk));
+                                y = __fmul2_rn(y, make_float2(fk, fk));
+                            }
+                            x = __fmul2_rn(x, make_float2(p[at], p[at + 1]));
+                            y = __fmul2_rn(y, make_float2(p[at + 2], p[at + 3]));
+                            r[j] = pack2<T>(x.x, x.y);
+                            r[j + 1] = pack2<T>(y.x, y.y);
+                        }
+                        tc::tmem_st16(my_dp + k / 2, r);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.dsready);
+                }
+            if (!ok)
+                break;
+            // Half of the warpgroups write dV, the others dK: a row each, its share of the columns.
+            const bool is_dk = part >= kBwdGroups / 2;
+            constexpr int cols = D / (kBwdGroups / 2);
+            const int col0 = (part % (kBwdGroups / 2)) * cols;
+            T* out = (is_dk ? a.dk : a.dv).row<T>(it.b, it.g, key) + col0;
+            if (any) {
+                ok = up.warp_wait(&sh.accfull, nk & 1u);
+                ++nk;
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+                const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
+#pragma unroll 1
+                for (int k = 0; k < cols; k += 32) {
+                    float o[32];
+                    tc::tmem_ld32((is_dk ? t_dk : t_dv) + lanes + col0 + k, o);
+                    if (key < a.Skv) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (key < it.L)
+                                v = make_uint4(pack2<T>(o[j] * f + 0.0f, o[j + 1] * f + 0.0f),
+                                               pack2<T>(o[j + 2] * f + 0.0f, o[j + 3] * f + 0.0f),
+                                               pack2<T>(o[j + 4] * f + 0.0f, o[j + 5] * f + 0.0f),
+                                               pack2<T>(o[j + 6] * f + 0.0f, o[j + 7] * f + 0.0f));
+                            *reinterpret_cast<uint4*>(out + k + j) = v;
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.accempty);
+            } else if (key < a.Skv) {
+                for (int k = 0; k < cols; k += 8)
+                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kBwdMmaWarp) {
+        __syncwarp();
+        tc::tmem_free<512>(tmem);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dq. S = Q K^T twice buffered, dP = dO V^T (dS, 16 bits, over it, each
+// warpgroup's part over its own columns) and dQ in tensor memory. While the
+// element-wise warps form P of one key tile the tensor cores run dQ of the last,
+// dP of this one and S of the next.
+// ---------------------------------------------------------------------------
+template <int D>
+struct DqTile {
+    static constexpr int k_stages = 3, v_stages = 2;
+    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
+    static constexpr uint32_t off_q = 0, off_do = bytes, off_k = 2 * bytes, off_v = (2 + k_stages) * bytes;
+    static constexpr uint32_t smem = (2 + k_stages + v_stages) * bytes + 1024;
+};
+
+struct DqShared {
+    uint64_t qfull, qempty, dofull, doempty;
+    uint64_t kfull[3], kempty[3], vfull[2], vempty[2], raw;
+    uint64_t sfull[2], sempty[2], dpfull, dsready, accfull, accempty, mma_done;
+    uint32_t tmem_slot;
+    int flag;
+    float norm[2];
+};
+
+struct DqItem {
+    int32_t b, h, i0, off, L, lo, hi, full0, full1;
+
+    __device__ __forceinline__ DqItem(const AttentionArgs& a, int64_t item, int64_t heads, int32_t blocks)
+    {
+        const int32_t bh = static_cast<int32_t>(item % heads);
+        i0 = (blocks - 1 - static_cast<int32_t>(item / heads)) * kTile;
+        b = bh / a.Hq;
+        h = bh - b * a.Hq;
+        off = a.offset(b);
+        L = a.length(b);
+        const int32_t last = i0 + kTile < a.Sq ? i0 + kTile : a.Sq;
+        const int32_t ra = off + i0 > 0 ? off + i0 : 0, rb = (off + last < L ? off + last : L) - 1;
+        lo = hi = full0 = full1 = 0;
+        if (ra <= rb) {
+            int32_t a0, a1, b0, b1;
+            a.kept(ra, L, a0, a1);
+            a.kept(rb, L, b0, b1);
+            lo = a0 / kTile;
+            hi = (b1 + kTile - 1) / kTile;
+            full0 = b0;
+            full1 = a1;
+        }
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
+                         const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
+                         const __grid_constant__ AttentionArgs a, int64_t heads, int32_t blocks, uint64_t wait_ns)
+{
+    using TL = DqTile<D>;
+    constexpr int KS = TL::k_stages, VS = TL::v_stages;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ DqShared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const GiveUp up{&sh.flag, a.status, wait_ns};
+    const int64_t items = heads * blocks;
+
+    if (threadIdx.x == 0) {
+        uint64_t* const one[] = {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull[0], &sh.sfull[1],
+                                 &sh.dpfull, &sh.accfull, &sh.mma_done, &sh.kfull[0], &sh.kfull[1], &sh.kfull[2],
+                                 &sh.kempty[0], &sh.kempty[1], &sh.kempty[2], &sh.vfull[0], &sh.vfull[1], &sh.vempty[0],
+                                 &sh.vempty[1]};
+        for (uint64_t* m : one)
+            tc::mbar_init(m, 1);
+        tc::mbar_init(&sh.sempty[0], kBwdWarps);
+        tc::mbar_init(&sh.sempty[1], kBwdWarps);
+        tc::mbar_init(&sh.dsready, kBwdWarps);
+        tc::mbar_init(&sh.accempty, kBwdWarps);
+        sh.flag = 0;
+    }
+    if (warp == kBwdMmaWarp) {
+        __syncwarp();
+        tc::tmem_alloc<512>(&sh.tmem_slot);
+    }
+    const float factor = block_gradient_factor<T>(a, sh.norm);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem_slot, t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
+
+    if (warp >= kBwdMmaWarp) {
+        tc::regs_lower<kBwdOtherRegs>();
+        if (warp == kBwdLoadWarp) {
+            uint32_t gk = 0, gv = 0, nq = 0, ndo = 0, nraw = 0;
+            bool ok = true;
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+                const DqItem it(a, item, heads, blocks);
+                if (it.lo == it.hi)
+                    continue;
+                const int32_t hk = it.h / a.group;
+                auto queries = [&](const HeadsMap& m, uint32_t dst, uint64_t* full, uint64_t* empty, uint32_t& count) {
+                    ok = up.warp_wait(empty, (count & 1u) ^ 1u);
+                    if (!ok)
+                        return;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(full, TL::bytes);
+                        load_tile<D, kTile>(base + dst, m, it.i0, it.h, it.b, full);
+                    }
+                    ++count;
+                };
+                auto keys = [&](const HeadsMap& m, uint32_t dst, int32_t t, uint64_t* full, uint64_t* empty, uint32_t phase,
+                                bool tail) {
+                    ok = up.warp_wait(empty, phase ^ 1u);
+                    if (!ok)
+                        return;
+                    uint64_t* bar = tail ? &sh.raw : full;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(bar, TL::bytes);
+                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, it.b, bar);
+                    }
+                    if (tail) {   // keys behind the length meet a zero ds in dQ: they must be numbers
+                        ok = up.warp_wait(&sh.raw, nraw & 1u);
+                        ++nraw;
+                        if (!ok)
+                            return;
+                        zero_tile_rows<D>(smem + dst, it.L - t * kTile, kTile, lane);
+                        tc::fence_smem_for_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(full);
+                    }
+                };
+                for (int32_t t = it.lo; t < it.hi && ok; ++t) {
+                    if (t == it.lo)
+                        queries(mq, TL::off_q, &sh.qfull, &sh.qempty, nq);
+                    if (ok) {
+                        keys(mk, TL::off_k + (gk % KS) * TL::bytes, t, &sh.kfull[gk % KS], &sh.kempty[gk % KS], (gk / KS) & 1u,
+                             (t + 1) * kTile > it.L && it.L < a.Skv);
+                        gk += ok;
+                    }
+                    if (ok && t == it.lo)
+                        queries(mdo, TL::off_do, &sh.dofull, &sh.doempty, ndo);
+                    if (ok) {
+                        keys(mv, TL::off_v + (gv % VS) * TL::bytes, t, &sh.vfull[gv % VS], &sh.vempty[gv % VS], (gv / VS) & 1u, false);
+                        gv += ok;
+                    }
+                }
+            }
+            if (!ok) {   // let the copies already issued land before the CTA can exit
+                for (uint32_t k = 0; k < static_cast<uint32_t>(KS) && k < gk; ++k)
+                    tc::mbar_wait(&sh.kfull[(gk - 1 - k) % KS], ((gk - 1 - k) / KS) & 1u, kAttnDrainWaitNs);
+                for (uint32_t k = 0; k < static_cast<uint32_t>(VS) && k < gv; ++k)
+                    tc::mbar_wait(&sh.vfull[(gv - 1 - k) % VS], ((gv - 1 - k) / VS) & 1u, kAttnDrainWaitNs);
+                if (nq)
+                    tc::mbar_wait(&sh.qfull, (nq - 1) & 1u, kAttnDrainWaitNs);
+                if (ndo)
+                    tc::mbar_wait(&sh.dofull, (ndo - 1) & 1u, kAttnDrainWaitNs);
+                if (nraw)
+                    tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
+            }
+        } else if (warp == kBwdMmaWarp && lane == 0) {
+            constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
+            uint32_t g = 0, ni = 0;   // key tiles, items
+            bool ok = true;
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+                const DqItem it(a, item, heads, blocks);
+                const int32_t n = it.hi - it.lo;
+                if (n == 0)
+                    continue;
+                auto scores = [&](uint32_t k, bool last) {
+                    ok = up.wait(&sh.kfull[k % KS], (k / KS) & 1u) && up.wait(&sh.sempty[k & 1u], ((k >> 1) & 1u) ^ 1u);
+                    if (!ok)
+                        return;
+                    tc::fence_after_sync();
+                    mma_abt<T, D>(tmem + (k & 1u) * kTile, base + TL::off_q, base + TL::off_k + (k % KS) * TL::bytes);
+                    tc::commit(&sh.sfull[k & 1u]);
+                    if (last)
+                        tc::commit(&sh.qempty);
+                };
+                auto products = [&](uint32_t k, bool last) {
+                    ok = up.wait(&sh.vfull[k % VS], (k / VS) & 1u);
+                    if (!ok)
+                        return;
+                    tc::fence_after_sync();
+                    mma_abt<T, D>(t_dp, base + TL::off_do, base + TL::off_v + (k % VS) * TL::bytes);
+                    tc::commit(&sh.dpfull);
+                    tc::commit(&sh.vempty[k % VS]);
+                    if (last)
+                        tc::commit(&sh.doempty);
+                };
+                ok = up.wait(&sh.qfull, ni & 1u);
+                if (ok)
+                    scores(g, n == 1);
+                if (ok)
+                    ok = up.wait(&sh.dofull, ni & 1u);
+                if (ok)
+                    products(g, n == 1);
+                if (ok && n > 1)
+                    scores(g + 1, n == 2);
+                for (int32_t k = 0; k < n && ok; ++k, ++g) {
+                    ok = up.wait(&sh.dsready, g & 1u);
+                    if (ok && k == 0)
+                        ok = up.wait(&sh.accempty, (ni & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t k0 = base + TL::off_k + (g % KS) * TL::bytes;
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks) {
+                        const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
+                        tc::mma_f16_ts(t_dq, t_dp + at, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc, k > 0 || ks > 0);
+                    }
+                    tc::commit(&sh.kempty[g % KS]);
+                    if (k + 1 < n)
+                        products(g + 1, k + 2 == n);
+                    if (ok && k + 2 < n)
+                        scores(g + 2, k + 3 == n);
+                }
+                if (ok)
+                    tc::commit(&sh.accfull);
+                ++ni;
+            }
+            tc::commit(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
+            tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
+        }
+    } else {
+        tc::regs_raise<kBwdElemRegs>();
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t my_dp = t_dp + lanes + part * kBwdCols;
+        const float c = a.scale * kLog2e;
+        const float2 c2 = make_float2(c, c);
+        const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
+        uint32_t g = 0, ni = 0;
+        bool ok = true;
+        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+            const DqItem it(a, item, heads, blocks);
+            const int32_t i = it.i0 + row;
+            int32_t c0, c1;
+            a.kept(it.off + i, it.L, c0, c1);
+            const bool live = c0 < c1 && i < a.Sq;
+            const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq_pad + i;
+            const float neg_lse = -__ldg(a.lse2 + at), neg_delta = -__ldg(a.delta + at);
+            const float2 lse2 = make_float2(neg_lse, neg_lse), delta2 = make_float2(neg_delta, neg_delta);
+            for (int32_t t = it.lo; t < it.hi; ++t, ++g) {
+                ok = up.warp_wait(&sh.sfull[g & 1u], (g >> 1) & 1u);
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+                float p[kBwdCols];
+                tc::tmem_ld64(tmem + (g & 1u) * kTile + lanes + part * kBwdCols, p);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.sempty[g & 1u]);
+#pragma unroll
+                for (int j = 0; j < kBwdCols; j += 2) {
+                    const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, lse2);
+                    p[j] = exp2_approx(x.x);
+                    p[j + 1] = exp2_approx(x.y);
+                }
+                ok = up.warp_wait(&sh.dpfull, g & 1u);
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+                float ds[kBwdCols];
+                tc::tmem_ld64(my_dp, ds);
+#pragma unroll
+                for (int j = 0; j < kBwdCols; j += 2) {
+                    float2 x = __fadd2_rn(make_float2(ds[j], ds[j + 1]), delta2);
+                    if (kPShift<T> != 0)
+                        x = __fmul2_rn(x, make_float2(fk, fk));
+                    x = __fmul2_rn(x, make_float2(p[j], p[j + 1]));
+                    ds[j] = x.x;
+                    ds[j + 1] = x.y;
+                }
+                if (t * kTile < it.full0 || (t + 1) * kTile > it.full1) {
+                    const int32_t k0 = c0 - t * kTile - part * kBwdCols, k1 = c1 - t * kTile - part * kBwdCols;
+#pragma unroll
+                    for (int j = 0; j < kBwdCols; ++j)
+                        ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBwdCols; k += 32) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        r[j] = pack2<T>(ds[k + 2 * j], ds[k + 2 * j + 1]);
+                    tc::tmem_st16(my_dp + k / 2, r);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.dsready);
+            }
+            if (!ok)
+                break;
+            constexpr int cols = D / kBwdGroups;
+            T* out = a.dq.row<T>(it.b, it.h, i) + part * cols;
+            if (it.lo != it.hi) {
+                ok = up.warp_wait(&sh.accfull, ni & 1u);
+                ++ni;
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+                const float f = a.scale / factor;
+#pragma unroll 1
+                for (int k = 0; k < cols; k += 32) {
+                    float o[32];
+                    tc::tmem_ld32(t_dq + lanes + part * cols + k, o);
+                    if (i < a.Sq) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (live)
+                                v = make_uint4(pack2<T>(o[j] * f + 0.0f, o[j + 1] * f + 0.0f),
+                                               pack2<T>(o[j + 2] * f + 0.0f, o[j + 3] * f + 0.0f),
+                                               pack2<T>(o[j + 4] * f + 0.0f, o[j + 5] * f + 0.0f),
+                                               pack2<T>(o[j + 6] * f + 0.0f, o[j + 7] * f + 0.0f));
+                            *reinterpret_cast<uint4*>(out + k + j) = v;
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.accempty);
+            } else if (i < a.Sq) {
+                for (int k = 0; k < cols; k += 8)
+                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kBwdMmaWarp) {
+        __syncwarp();
+        tc::tmem_free<512>(tmem);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
+{
+    AttentionArgs a = args;
+    if (!bind_context())
+        return cudaErrorUnknown;
+    const int nsm = sm_count();
+    if (nsm <= 0)
+        return cudaErrorUnknown;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, kv_heads = static_cast<int64_t>(a.B) * a.Hkv;
+    // Where one side has no rows its tensors may be null: nothing of them is loaded, and the other side's
+    // stand in for them in the maps.
+    const bool rows = a.Sq > 0, keys = a.Skv > 0;
+    HeadsMap mq, mk, mv, mdo;
+    if (!encode_heads<T>(mq, rows ? a.q : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, kTile) ||
+        !encode_heads<T>(mdo, rows ? a.dout : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, kTile) ||
+        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
+        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    {
+        constexpr int per = kPrepThreads / (D / 8);
+        const int64_t n = heads * a.Sq_pad, m = std::is_same<T, __half>::value ? kv_heads * a.Skv : 0;
+        int64_t blocks = ((n > m ? n : m) + per - 1) / per;
+        blocks = blocks < 1 ? 1 : (blocks > kPrepMaxBlocks ? kPrepMaxBlocks : blocks);
+        a.norm_blocks = static_cast<int32_t>(blocks);
+        e = launch_kernel(gtms_attention_bwd_prep_kernel<T, D>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, a, n, m);
+    }
+    if (e == cudaSuccess && keys) {
+        auto* kern = gtms_attention_dkv_kernel<T, D>;
+        constexpr int smem = static_cast<int>(DkvTile<D>::smem);
+        const int64_t items = kv_heads * ((a.Skv + kTile - 1) / kTile);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
+                              kv_heads, items, wait_ns);
+    }
+    if (e == cudaSuccess && rows) {
+        auto* kern = gtms_attention_dq_kernel<T, D>;
+        constexpr int smem = static_cast<int>(DqTile<D>::smem);
+        const int32_t blocks = a.Sq_pad / kTile;
+        const int64_t items = heads * blocks;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
+                              heads, blocks, wait_ns);
+    }
+    return e;
+}
+
+}  // namespace gtms

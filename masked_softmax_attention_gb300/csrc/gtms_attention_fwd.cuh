@@ -146,7 +146,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         if (warp == kFwdLoadWarp) {
             uint32_t g = 0, nq[2] = {0, 0}, nraw = 0;
             bool ok = true;
-            for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
                 const FwdItem it(a, item, heads, blocks);
                 const int32_t hk = it.h / a.group;
                 auto tile = [&](const HeadsMap& m, int32_t t, bool tail) {
@@ -166,7 +166,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D>(smem + dst, it.L - t * kTile, lane);
+                        zero_tile_rows<D>(smem + dst, it.L - t * kTile, kTile, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -206,11 +206,10 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             }
         } else if (warp == kFwdMmaWarp) {
             if (lane == 0) {
-                constexpr uint32_t idesc_s = tc::idesc_f16<T>(kTile, kTile);
-                constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
+                    constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
                 uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
                 bool ok = true;
-                for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+                for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
                     const FwdItem it(a, item, heads, blocks);
                     const int32_t top = it.top(), bottom = it.bottom();
                     if (top == 0)
@@ -225,12 +224,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             tc::fence_after_sync();
                         }
                         const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
-    #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t at = (ks >> 2) * TL::box + (ks & 3) * 32;
-                            tc::mma_f16(tmem + w * kTile, tc::smem_desc_sw128(q0 + at, 1024), tc::smem_desc_sw128(k0 + at, 1024),
-                                        idesc_s, ks > 0);
-                        }
+                        mma_abt<T, D>(tmem + w * kTile, q0, k0);
                         tc::commit(&sh.sfull[w]);
                         if (t == it.lo[w])
                             tc::commit(&sh.qempty[w]);
@@ -300,7 +294,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         const float pre = a.scale > 0.0f ? 1.0f : (a.scale < 0.0f ? -1.0f : 0.0f);
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
             const FwdItem it(a, item, heads, blocks);
             const int32_t i = it.i0 + w * kTile + (warp & 3) * 32 + lane;
             int32_t c0, c1;
@@ -426,6 +420,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 template <typename T, int D>
 cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
 {
+    if (!bind_context())
+        return cudaErrorUnknown;
     // Without keys no tile is loaded, and q stands in for k and v in the maps.
     const bool keys = a.Skv > 0;
     HeadsMap mq, mk, mv;

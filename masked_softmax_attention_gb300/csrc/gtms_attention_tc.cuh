@@ -23,6 +23,14 @@ struct HeadsMap {
     int32_t mh, mb;
 };
 
+// Makes the current device's context this thread's: the tensor-map encoder is a
+// driver call, and a thread whose first CUDA call it is (autograd's, say) has none yet.
+inline bool bind_context()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 template <typename T>
 inline bool encode_heads(HeadsMap& m, const HeadsRef& t, int64_t B, int64_t H, int64_t S, int64_t D, uint32_t rows)
 {
@@ -90,14 +98,34 @@ struct GiveUp {
     }
 };
 
-// Zeroes rows [from, 128) of a swizzled tile of D / 64 boxes (a whole warp works).
+// Zeroes rows [from, to) of a swizzled 128-row tile of D / 64 boxes (a whole warp works).
 template <int D>
-__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int lane)
+__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int32_t to, int lane)
 {
-    const int32_t per_box = (kTile - from) * 8;   // 16-byte chunks
     for (int32_t x = 0; x < D / 64; ++x)
-        for (int32_t i = lane; i < per_box; i += 32)
-            *reinterpret_cast<uint4*>(tile + x * kTile * 128 + from * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int32_t i = from * 8 + lane; i < to * 8; i += 32)   // 16-byte chunks, 8 to a row
+            *reinterpret_cast<uint4*>(tile + x * kTile * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// Work item of this CTA's round n: the items come costliest first, and every
+// other round takes them the other way round, so that a CTA with a costly item
+// in one round gets a cheap one in the next.
+__device__ __forceinline__ int64_t snake_item(int64_t n)
+{
+    const int64_t g = gridDim.x, i = n & 1 ? g - 1 - blockIdx.x : blockIdx.x;
+    return n * g + i;
+}
+
+// S (or dP) = A B^T: two K-major operands of 128 rows x D.
+template <typename T, int D>
+__device__ __forceinline__ void mma_abt(uint32_t d, uint32_t a, uint32_t b)
+{
+    constexpr uint32_t idesc = tc::idesc_f16<T>(kTile, kTile);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t at = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;   // 16 columns of a swizzled 64-column box
+        tc::mma_f16(d, tc::smem_desc_sw128(a + at, 1024), tc::smem_desc_sw128(b + at, 1024), idesc, ks > 0);
+    }
 }
 
 template <typename T>

@@ -347,6 +347,13 @@ __device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(mbar)), "l"(pol) : "memory");
 }
 
+// bulk_load_1d without a cache policy.
+__device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint32_t bytes, uint64_t* mbar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(mbar)) : "memory");
+}
+
 // TMA: prefetch the box of a 3-D tensor map at (x, y, z) into L2 (no shared
 // memory, no completion signal), under an L2 cache policy.
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int32_t x, int32_t y, int32_t z, uint64_t pol)

@@ -9,6 +9,9 @@ dtype, every addition inside the tensor cores and every fp32 sum taken to lose a
 * a probability is then off by that, relatively, and by 2^-21 for the exponential; rounded to 16 bits
   it is off by u more, or by 2^-25 where fp16 runs out of exponents (probabilities are at most 1 before
   they are normalised, and the sum they are divided by is at least 1);
+* the exponential is zero where it would be below 2^-126, fp32's smallest normal number: p is off by up
+  to 2^-126 there, and ds by 2^-126 |dp - D| (seen as a gradient of 2e-37 that came out as zero: one
+  p of 2^-127 times dp - D and q of about 10 each);
 * o divides by a sum with the same relative errors, sums n products (n 2^-23 of their absolute sum) and
   is rounded once: u |o|;
 * D = do . o takes o rounded: u sum |do||o|, and d 2^-23 of that sum for the additions;
@@ -24,6 +27,7 @@ import torch
 UNIT = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}   # half a step, relative to the value
 TINY = {torch.bfloat16: 2.0 ** -126, torch.float16: 2.0 ** -25}  # half the smallest step
 F = 2.0 ** -23
+FLUSH = 2.0 ** -126
 
 
 def kept(seq_lens, Sq, Skv, mask_kind=0, window=0, q_offsets=None):
@@ -81,6 +85,7 @@ def forward(q, k, v, keep, scale):
     smax = torch.where(keep, s.abs(), 0.0).amax(-1)
     e = d * F * mag.amax(-1) + 2 * 2.0 ** -22 * smax + 2.0 ** -21
     tol = u * o.abs() + (u + 2 * e + 2 * n * F)[..., None] * A + tiny
+    tol = tol + FLUSH * torch.einsum("bhic,bhcd->bhid", keep.double().expand_as(p), vd.abs())
     if dtype == torch.float16:
         tol = tol + tiny * torch.einsum("bhic,bhcd->bhid", keep.double().expand_as(p), vd.abs())
     tol_lse = e + n * F + 2.0 ** -22 * safe.abs()
@@ -107,7 +112,8 @@ def backward(q, k, v, dout, keep, scale):
     ds = p * (dp - D)
     ep = d * F * mag + 2.0 ** -22 * (torch.where(keep, s.abs(), 0.0) + 2 * safe.abs()) + 2.0 ** -20
     e_ds = p * (d * F * adp + (u + d * F) * aD) + ds.abs() * (ep + u + 2.0 ** -21)
-    e_p = p * (u + ep)
+    e_p = p * (u + ep) + keep * FLUSH
+    e_ds = e_ds + keep * FLUSH * (dp - D).abs()
     if dtype == torch.float16:
         top = dout.norm(dim=-1).amax() * v.norm(dim=-1).amax()
         e_ds = e_ds + keep * (4 * top * 2.0 ** -38)
