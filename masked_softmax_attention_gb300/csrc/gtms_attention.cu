@@ -1,12 +1,15 @@
 // gtms_attention.cu -- the attention forward and backward launches.
 #include "gtms_attention_bwd.cuh"
 #include "gtms_attention_fwd.cuh"
+#include "gtms_attention_split.cuh"
 
 namespace gtms {
 
 template <typename T, int D>
 cudaError_t launch_attention_forward(const AttentionArgs& a, cudaStream_t st)
 {
+    if (a.group * static_cast<int64_t>(a.Sq) <= kSplitRows)
+        return launch_attention_split<T, D>(a, st);
     return launch_attention_fwd_tc<T, D>(a, st);
 }
 

@@ -1,0 +1,325 @@
+// gtms_attention_split.cuh -- attention forward for few query rows over many keys
+// (new tokens over a cache), the keys split over the CTAs of a cluster.
+//
+// What bounds it is one read of the live keys and values. The rows of the query
+// heads that share a key/value head are packed into tiles of 16, so that every
+// key is read once for all of them. A warp takes 16 keys at a time straight from
+// memory into the registers that the tensor-core instruction reads them from, the
+// next 16 in flight while it works, with a running maximum and sum per row; no
+// shared memory and no barrier until the end, where the warps' (m, l, O) are
+// joined in shared memory and the CTAs' through the cluster's. One launch, no
+// workspace.
+//
+// Operand layouts. A dot product does not care in which order its terms come, so
+// the k indices of S = Q K^T are dealt out such that a thread's share of a key is
+// 16 contiguous bytes (lane 4 g + t: key g, elements 32 x + 8 t .. + 7), and q is
+// dealt out likewise. For O += P V a thread reads 16 contiguous bytes (elements
+// 64 y + 8 g .. + 7) of the keys 2t, 2t + 1, 2t + 8, 2t + 9 and pairs up the keys
+// with byte permutations: column n of product j is element 64 y + 8 n + j.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "gtms_attention_tc.cuh"
+
+namespace gtms {
+
+constexpr int kSplitWarps = 4, kSplitThreads = 32 * kSplitWarps;
+constexpr int kSplitRows = 16, kSplitKeys = 16;   // rows of a tile; keys a warp takes at a time
+constexpr int kSplitMaxCluster = 8;               // the largest portable cluster
+
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes that are read once, zero where !use (nothing is read then).
+template <typename T>
+__device__ __forceinline__ uint4 load_once(const T* p, bool use)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (use)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int D>
+struct SplitShared {
+    uint4 q[kSplitRows][D / 8 + 1];                  // + 1: rows start in different banks
+    float m[kSplitWarps][kSplitRows], l[kSplitWarps][kSplitRows];
+    float o[kSplitWarps][kSplitRows][D + 4];
+    float cta_m[kSplitRows], cta_l[kSplitRows];      // joined over the warps; o[0] then holds the CTA's O
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSplitThreads, 3)
+gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
+{
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int32_t ranks = static_cast<int32_t>(cluster.num_blocks()), rank = static_cast<int32_t>(cluster.block_rank());
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SplitShared<D>& sh = *reinterpret_cast<SplitShared<D>*>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    const int64_t unit = blockIdx.x / ranks;
+    const int32_t tile = static_cast<int32_t>(unit % tiles);
+    const int64_t bg = unit / tiles;
+    const int32_t b = static_cast<int32_t>(bg / a.Hkv), hk = static_cast<int32_t>(bg - static_cast<int64_t>(b) * a.Hkv);
+    const int32_t off = a.offset(b), L = a.length(b), rows = a.group * a.Sq;
+    // Row r of a tile is query row r / group of shared head r % group: neighbouring rows keep nearly the same keys.
+    auto head_of = [&](int32_t r) { return hk * a.group + (tile * kSplitRows + r) % a.group; };
+    auto row_of = [&](int32_t r) { return (tile * kSplitRows + r) / a.group; };
+    auto exists = [&](int32_t r) { return tile * kSplitRows + r < rows; };
+
+    int32_t c0[2] = {0, 0}, c1[2] = {0, 0}, lo = INT32_MAX, hi = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int32_t r = g + 8 * k;
+        if (exists(r))
+            a.kept(off + row_of(r), L, c0[k], c1[k]);
+        if (c0[k] < c1[k]) {
+            lo = c0[k] < lo ? c0[k] : lo;
+            hi = c1[k] > hi ? c1[k] : hi;
+        }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        const int32_t x = __shfl_xor_sync(0xffffffffu, lo, o), y = __shfl_xor_sync(0xffffffffu, hi, o);
+        lo = x < lo ? x : lo;
+        hi = y > hi ? y : hi;
+    }
+
+    // q into shared memory; rows that do not exist are zero.
+    for (int32_t i = threadIdx.x; i < kSplitRows * (D / 8); i += kSplitThreads) {
+        const int32_t r = i / (D / 8), x = i % (D / 8);
+        sh.q[r][x] = exists(r) ? *(reinterpret_cast<const uint4*>(a.q.row<T>(b, head_of(r), row_of(r))) + x) : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+
+    // This CTA's share of the 16-key blocks, contiguous; its warps take them in turn.
+    const int32_t first = hi > 0 ? lo / kSplitKeys : 0, blocks = hi > 0 ? (hi + kSplitKeys - 1) / kSplitKeys - first : 0;
+    const int32_t per = (blocks + ranks - 1) / ranks;
+    const int32_t end = first + (per * (rank + 1) < blocks ? per * (rank + 1) : blocks);
+    int32_t blk = first + per * rank + warp;
+
+    const T* kbase = a.k.row<T>(b, hk, 0) + 8 * t;
+    const T* vbase = a.v.row<T>(b, hk, 0) + 8 * g;
+    uint4 kr[2][D / 32], vr[4][D / 64];
+    auto load_k = [&](int32_t n) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int32_t key = n * kSplitKeys + 8 * k + g;
+            const bool use = n < end && key >= lo && key < hi;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+                kr[k][x] = load_once(kbase + key * a.k.ss + 32 * x, use);
+        }
+    };
+    auto load_v = [&](int32_t n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t key = n * kSplitKeys + 2 * t + (k & 1) + 8 * (k >> 1);
+            const bool use = n < end && key >= lo && key < hi;
+#pragma unroll
+            for (int y = 0; y < D / 64; ++y)
+                vr[k][y] = load_once(vbase + key * a.v.ss + 64 * y, use);
+        }
+    };
+
+    const float c = a.scale * kLog2e;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[D / 64][8][4];
+#pragma unroll
+    for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[y][j][k] = 0.0f;
+
+    load_k(blk);
+    load_v(blk);
+    for (; blk < end; blk += kSplitWarps) {
+        float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            const uint4 qa = sh.q[g][4 * x + t], qb = sh.q[g + 8][4 * x + t];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mma_16816<T>(s[k], qa.x, qb.x, qa.y, qb.y, kr[k][x].x, kr[k][x].y);
+                mma_16816<T>(s[k], qa.z, qb.z, qa.w, qb.w, kr[k][x].z, kr[k][x].w);
+            }
+        }
+        load_k(blk + kSplitWarps);
+        const int32_t key0 = blk * kSplitKeys + 2 * t;
+        uint32_t p[2][2];   // [row half][key half]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int32_t key = key0 + (k & 1) + 8 * (k >> 1);
+                x[k] = key >= c0[h] && key < c1[h] ? s[k >> 1][2 * h + (k & 1)] * c : -INFINITY;
+            }
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (top > m[h]) {
+                const float f = exp2_approx(m[h] - top);   // 0 from -inf
+                m[h] = top;
+                l[h] *= f;
+#pragma unroll
+                for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[y][j][2 * h] *= f;
+                        o[y][j][2 * h + 1] *= f;
+                    }
+            }
+            const float shift = m[h] == -INFINITY ? 0.0f : m[h];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = exp2_approx(x[k] - shift);
+                l[h] += x[k];
+            }
+            p[h][0] = pack2<T>(x[0], x[1]);
+            p[h][1] = pack2<T>(x[2], x[3]);
+        }
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) {
+            const uint32_t r[4][4] = {{vr[0][y].x, vr[0][y].y, vr[0][y].z, vr[0][y].w}, {vr[1][y].x, vr[1][y].y, vr[1][y].z, vr[1][y].w},
+                                      {vr[2][y].x, vr[2][y].y, vr[2][y].z, vr[2][y].w}, {vr[3][y].x, vr[3][y].y, vr[3][y].z, vr[3][y].w}};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                mma_16816<T>(o[y][j], p[0][0], p[1][0], p[0][1], p[1][1], __byte_perm(r[0][j / 2], r[1][j / 2], sel),
+                             __byte_perm(r[2][j / 2], r[3][j / 2], sel));
+            }
+        }
+        load_v(blk + kSplitWarps);
+    }
+
+    // Join the warps: row sums over the quad, then every warp brings its O to the CTA's maximum.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (t == 0) {
+            sh.m[warp][g + 8 * h] = m[h];
+            sh.l[warp][g + 8 * h] = l[h];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int32_t r = g + 8 * h;
+        float top = sh.m[0][r];
+#pragma unroll
+        for (int w = 1; w < kSplitWarps; ++w)
+            top = fmaxf(top, sh.m[w][r]);
+        const float base = top == -INFINITY ? 0.0f : top, f = exp2_approx(m[h] - base);
+        if (warp == 0 && t == 0) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kSplitWarps; ++w)
+                sum += sh.l[w][r] * exp2_approx(sh.m[w][r] - base);
+            sh.cta_m[r] = top;
+            sh.cta_l[r] = sum;
+        }
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    *reinterpret_cast<float4*>(&sh.o[warp][r][64 * y + 16 * t + 8 * n + j]) =
+                        make_float4(o[y][j][2 * h + n] * f, o[y][j + 1][2 * h + n] * f, o[y][j + 2][2 * h + n] * f,
+                                    o[y][j + 3][2 * h + n] * f);
+    }
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < kSplitRows * D; i += kSplitThreads) {
+        float sum = sh.o[0][i / D][i % D];
+#pragma unroll
+        for (int w = 1; w < kSplitWarps; ++w)
+            sum += sh.o[w][i / D][i % D];
+        sh.o[0][i / D][i % D] = sum;
+    }
+    if (ranks > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+
+    // Join the CTAs: each writes its share of the rows' element pairs.
+    for (int32_t i = rank * kSplitThreads + threadIdx.x; i < kSplitRows * (D / 2); i += ranks * kSplitThreads) {
+        const int32_t r = i / (D / 2), d = 2 * (i % (D / 2));
+        if (!exists(r))
+            break;   // rows come in order
+        float top = -INFINITY;
+        for (int32_t k = 0; k < ranks; ++k)
+            top = fmaxf(top, *cluster.map_shared_rank(&sh.cta_m[r], k));
+        int32_t k0, k1;
+        a.kept(off + row_of(r), L, k0, k1);
+        const bool live = k0 < k1;
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, x = 0.0f, y = 0.0f;
+        for (int32_t k = 0; k < ranks && live; ++k) {
+            const float f = exp2_approx(*cluster.map_shared_rank(&sh.cta_m[r], k) - base);
+            const float2 e = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&sh.o[0][r][d], k));
+            sum += f * *cluster.map_shared_rank(&sh.cta_l[r], k);
+            x += f * e.x;
+            y += f * e.y;
+        }
+        const float inv = live ? 1.0f / sum : 0.0f;
+        *reinterpret_cast<uint32_t*>(a.o.row<T>(b, head_of(r), row_of(r)) + d) = live ? pack2<T>(x * inv, y * inv) : 0u;
+        if (a.lse && d == 0)
+            a.lse[(static_cast<int64_t>(b) * a.Hq + head_of(r)) * a.Sq + row_of(r)] =
+                live ? top * 0.6931471805599453f + logf(sum) : -INFINITY;
+    }
+    if (ranks > 1)
+        cluster.sync();   // the others may still be reading this CTA's shared memory
+}
+
+template <typename T, int D>
+cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
+{
+    const int nsm = sm_count();
+    if (nsm <= 0)
+        return cudaErrorUnknown;
+    const int32_t tiles = (a.group * a.Sq + kSplitRows - 1) / kSplitRows;
+    const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * tiles;
+    // Split until there are about four CTAs to a multiprocessor, but leave every warp two blocks of keys.
+    int ranks = 1;
+    while (ranks < kSplitMaxCluster && units * ranks < 4 * nsm &&
+           static_cast<int64_t>(ranks) * 4 * kSplitWarps * kSplitKeys <= a.Skv)
+        ranks *= 2;
+    auto* kern = gtms_attention_split_kernel<T, D>;
+    constexpr int smem = static_cast<int>(sizeof(SplitShared<D>));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    if (units * ranks > INT32_MAX)
+        return cudaErrorNotSupported;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units * ranks));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, tiles);
+}
+
+}  // namespace gtms
