@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from ._build import LIB_PATH, build_library  # noqa: F401  (re-exported for build scripts)
@@ -498,60 +499,69 @@ def grouped_tril_mask_softmax(x, seq_lens, scale: float = 1.0):
 # Attention and rotary positions: strided [B, H, S, head_dim] tensors.
 # ---------------------------------------------------------------------------
 
-def _check_heads(name, t, like=None):
+_pack_heads = struct.Struct("@P3q").pack            # gtms_heads
+_pack_shape = struct.Struct("@7q2if4x").pack        # gtms_attention_shape
+_direct_calls: dict = {}
+
+
+def _direct(name):
+    """The entry point taking its structures as packed bytes (building ctypes objects costs more than a launch)."""
+    fn = _direct_calls.get(name)
+    if fn is None:
+        lib = load_library()
+        fn = lib[name]
+        plain = getattr(lib, name).argtypes
+        fn.argtypes = [ctypes.c_void_p if hasattr(t, "contents") else t for t in plain]
+        fn.restype = ctypes.c_int
+        _direct_calls[name] = fn
+    return fn
+
+
+def _heads(name, t, dtype, device):
+    """Packed ``gtms_heads`` of a tensor, after the checks that only the tensor itself allows."""
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, H, S, head_dim], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be of the same dtype as the others")
+    sb, sh, ss, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must match the first tensor in dtype and device")
+    return _pack_heads(t.data_ptr(), sb, sh, ss)
 
 
-def _heads(t):
-    s = t.stride()
-    return Heads(t.data_ptr(), s[0], s[1], s[2])
-
-
-class _On:
-    """The tensors' device as the current one, where it is not already."""
-
-    def __init__(self, device):
-        import torch
-
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
-
-
-def _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status):
+def _int32(name, t, shape, device):
+    """Address of an optional contiguous int32 tensor."""
     import torch
 
-    _check_heads("q", q)
-    _check_heads("k", k, q)
-    _check_heads("v", v, q)
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {tuple(shape)} on the same device")
+    return t.data_ptr()
+
+
+def _launch(fn, device, *args):
+    """The call on the current stream of the tensors' device, made the current one where it is not already."""
+    import torch
+
+    call, stream = _direct(fn), torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        rc = call(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, stream)
+    if rc != GTMS_OK:
+        raise GtmsError(fn, rc)
+
+
+def _attention_shape(q, k, v, scale, mask_kind, window):
     B, Hq, Sq, d = q.shape
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
-        raise ValueError(f"k and v must be [B, Hkv, Skv, head_dim] matching q, got {tuple(k.shape)} and {tuple(v.shape)}")
-    Hkv, Skv = k.shape[1], k.shape[2]
-    _check_lens(seq_lens, B, q.device)
-    if q_offsets is not None and (q_offsets.dtype != torch.int32 or q_offsets.shape != (B,)
-                                  or q_offsets.device != q.device or not q_offsets.is_contiguous()):
-        raise ValueError("q_offsets must be a contiguous int32 CUDA tensor of shape [B] on q's device")
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != q.device):
-        raise ValueError("status must be an int32 CUDA tensor of one element on q's device")
-    return AttentionShape(B, Hq, Hkv, Sq, Skv, d, int(window), int(mask_kind), _dtype_code(q), float(scale))
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    kb, Hkv, Skv, kd = ks = k.shape
+    if ks != v.shape or kb != B or kd != d:
+        raise ValueError(f"k and v must be [B, Hkv, Skv, head_dim] matching q, got {tuple(ks)} and {tuple(v.shape)}")
+    return B, Sq, _pack_shape(B, Hq, Hkv, Sq, Skv, d, int(window), int(mask_kind), _dtype_code(q), scale)
 
 
 def attention_forward(q, k, v, seq_lens, scale: float = 1.0, out=None, mask_kind: int = GTMS_MASK_GROUPED_TRIL,
@@ -565,19 +575,19 @@ def attention_forward(q, k, v, seq_lens, scale: float = 1.0, out=None, mask_kind
     nothing give o = 0 and lse = -inf. ``status`` as in ``attention_softmax_backward``."""
     import torch
 
-    shape = _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status)
-    o = torch.empty_like(q) if out is None else out
-    _check_heads("out", o, q)
-    if o.shape != q.shape:
+    dtype, dev = q.dtype, q.get_device()
+    q_, k_, v_ = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
+    B, Sq, shape = _attention_shape(q, k, v, scale, mask_kind, window)
+    lens, off = _int32("seq_lens", seq_lens, (B,), dev), _int32("q_offsets", q_offsets, (B,), dev)
+    status = _int32("status", status, (1,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
         raise ValueError("out must match q in shape")
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    with _On(q.device):
-        rc = gtms_attention_forward(shape, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
-                                    seq_lens.data_ptr(), _ptr(q_offsets), _ptr(status),
-                                    torch.cuda.current_stream(q.device).cuda_stream)
-    if rc != GTMS_OK:
-        raise GtmsError("gtms_attention_forward", rc)
-    return o, lse
+    lse = torch.empty((B, q.shape[1], Sq), dtype=torch.float32, device=q.device)
+    _launch("gtms_attention_forward", dev, shape, q_, k_, v_, _heads("out", out, dtype, dev), lse.data_ptr(), lens, off,
+            status)
+    return out, lse
 
 
 def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=None,
@@ -587,30 +597,28 @@ def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=
     optional triple of tensors to write to."""
     import torch
 
-    shape = _attention_shape(q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status)
-    for name, t in (("o", o), ("dout", dout)):
-        _check_heads(name, t, q)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} must match q in shape")
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device or not lse.is_contiguous():
+    dtype, dev, shape4 = q.dtype, q.get_device(), q.shape
+    q_, k_, v_ = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
+    B, _, shape = _attention_shape(q, k, v, scale, mask_kind, window)
+    lens, off = _int32("seq_lens", seq_lens, (B,), dev), _int32("q_offsets", q_offsets, (B,), dev)
+    status = _int32("status", status, (1,), dev)
+    if o.shape != shape4 or dout.shape != shape4:
+        raise ValueError("o and dout must match q in shape")
+    if lse.dtype is not torch.float32 or lse.shape != shape4[:3] or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq] on q's device")
-    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v)) if out is None else out
-    for name, t, of in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_heads(name, t, q)
-        if t.shape != of.shape:
-            raise ValueError(f"{name} must match {name[1:]} in shape")
+    if out is None:
+        out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dq, dk, dv = out
+    if dq.shape != shape4 or dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("dq, dk and dv must match q, k and v in shape")
     need = ctypes.c_uint64()
-    rc = gtms_attention_backward_workspace(shape, ctypes.byref(need))
+    rc = _direct("gtms_attention_backward_workspace")(shape, ctypes.byref(need))
     if rc != GTMS_OK:
         raise GtmsError("gtms_attention_backward_workspace", rc)
-    with _On(q.device):
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-        rc = gtms_attention_backward(shape, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(), _heads(dout),
-                                     _heads(dq), _heads(dk), _heads(dv), seq_lens.data_ptr(), _ptr(q_offsets),
-                                     workspace.data_ptr(), need.value, _ptr(status),
-                                     torch.cuda.current_stream(q.device).cuda_stream)
-    if rc != GTMS_OK:
-        raise GtmsError("gtms_attention_backward", rc)
+    workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    _launch("gtms_attention_backward", dev, shape, q_, k_, v_, _heads("o", o, dtype, dev), lse.data_ptr(),
+            _heads("dout", dout, dtype, dev), _heads("dq", dq, dtype, dev), _heads("dk", dk, dtype, dev),
+            _heads("dv", dv, dtype, dev), lens, off, workspace.data_ptr(), need.value, status)
     return dq, dk, dv
 
 
@@ -631,37 +639,35 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = GTMS_
 def _rotary(x, positions, inv_freq, other, interleaved, amplitude, out, out_other, inverse):
     import torch
 
-    _check_heads("x", x)
-    B, H, S, d = x.shape
-    dtype = _dtype_code(x)
-    if positions.dtype != torch.int32 or positions.device != x.device or not positions.is_contiguous() \
-            or positions.shape not in ((S,), (1, S), (B, S)):
-        raise ValueError("positions must be a contiguous int32 CUDA tensor [S] or [B, S] on x's device")
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != x.device \
-            or not inv_freq.is_contiguous() or 2 * inv_freq.numel() > d:
+    dtype, dev = x.dtype, x.get_device()
+    x_ = _heads("x", x, dtype, dev)
+    B, H, S, d = shape = x.shape
+    pairs = inv_freq.numel()
+    rows = 1 if positions.dim() == 1 else positions.shape[0]
+    if rows != 1 and rows != B:
+        raise ValueError(f"positions must be [S] or [B, S], got {tuple(positions.shape)}")
+    pos = _int32("positions", positions, (S,) if positions.dim() == 1 else (rows, S), dev)
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != dev \
+            or not inv_freq.is_contiguous() or 2 * pairs > d:
         raise ValueError("inv_freq must be a contiguous fp32 CUDA tensor of at most head_dim / 2 elements on x's device")
-    y = torch.empty_like(x) if out is None else out
-    _check_heads("out", y, x)
-    if y.shape != x.shape:
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != shape:
         raise ValueError("out must match x in shape")
-    y2, H2, x2_ref, y2_ref = None, 0, None, None
+    H2, other_, out2_ = 0, None, None
     if other is not None:
-        _check_heads("other", other, x)
-        if other.shape[0] != B or other.shape[2:] != x.shape[2:]:
+        other_ = _heads("other", other, dtype, dev)
+        b2, H2, s2, d2 = other.shape
+        if b2 != B or s2 != S or d2 != d:
             raise ValueError("other must match x in every dimension but the heads")
-        y2 = torch.empty_like(other) if out_other is None else out_other
-        _check_heads("out_other", y2, x)
-        if y2.shape != other.shape:
+        if out_other is None:
+            out_other = torch.empty_like(other)
+        elif out_other.shape != other.shape:
             raise ValueError("out_other must match other in shape")
-        H2, x2_ref, y2_ref = other.shape[1], _heads(other), _heads(y2)
-    with _On(x.device):
-        rc = gtms_rotary(_heads(x), _heads(y), x2_ref, y2_ref, B, H, H2, S, d, 2 * inv_freq.numel(),
-                         positions.data_ptr(), B if positions.dim() == 2 and positions.shape[0] == B else 1,
-                         inv_freq.data_ptr(), int(interleaved), float(amplitude), int(inverse), dtype,
-                         torch.cuda.current_stream(x.device).cuda_stream)
-    if rc != GTMS_OK:
-        raise GtmsError("gtms_rotary", rc)
-    return y if other is None else (y, y2)
+        out2_ = _heads("out_other", out_other, dtype, dev)
+    _launch("gtms_rotary", dev, x_, _heads("out", out, dtype, dev), other_, out2_, B, H, H2, S, d, 2 * pairs, pos, rows,
+            inv_freq.data_ptr(), bool(interleaved), amplitude, inverse, _dtype_code(x))
+    return out if other is None else (out, out_other)
 
 
 def rotary_forward(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0, out=None,

@@ -909,7 +909,7 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
     AttentionArgs a = args;
     if (!bind_context())
         return cudaErrorUnknown;
-    const int nsm = sm_count();
+    const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, kv_heads = static_cast<int64_t>(a.B) * a.Hkv;
@@ -935,7 +935,7 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         auto* kern = gtms_attention_dkv_kernel<T, D>;
         constexpr int smem = static_cast<int>(DkvTile<D>::smem);
         const int64_t items = kv_heads * ((a.Skv + kTile - 1) / kTile);
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = allow_smem<gtms_attention_dkv_kernel<T, D>>(smem);
         if (e == cudaSuccess)
             e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
                               kv_heads, items, wait_ns);
@@ -945,7 +945,7 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         constexpr int smem = static_cast<int>(DqTile<D>::smem);
         const int32_t blocks = a.Sq_pad / kTile;
         const int64_t items = heads * blocks;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = allow_smem<gtms_attention_dq_kernel<T, D>>(smem);
         if (e == cudaSuccess)
             e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
                               heads, blocks, wait_ns);

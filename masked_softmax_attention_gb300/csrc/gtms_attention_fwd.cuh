@@ -431,12 +431,12 @@ cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uin
         return cudaErrorInvalidValue;
     auto* kern = gtms_attention_fwd_kernel<T, D>;
     constexpr int smem = static_cast<int>(FwdTile<D>::smem);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D>>(smem);
     if (e != cudaSuccess)
         return e;
     const int32_t blocks = (a.Sq + kFwdRows - 1) / kFwdRows;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, items = heads * blocks;
-    const int nsm = sm_count();
+    const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
     return launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kFwdThreads, smem, st, mq, mk, mv, a, heads,

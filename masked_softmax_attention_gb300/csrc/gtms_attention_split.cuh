@@ -66,7 +66,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int32_t ranks = static_cast<int32_t>(cluster.num_blocks()), rank = static_cast<int32_t>(cluster.block_rank());
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     SplitShared<D>& sh = *reinterpret_cast<SplitShared<D>*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
@@ -291,7 +291,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
 template <typename T, int D>
 cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
 {
-    const int nsm = sm_count();
+    const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
     const int32_t tiles = (a.group * a.Sq + kSplitRows - 1) / kSplitRows;
@@ -303,7 +303,7 @@ cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
         ranks *= 2;
     auto* kern = gtms_attention_split_kernel<T, D>;
     constexpr int smem = static_cast<int>(sizeof(SplitShared<D>));
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D>>(smem);
     if (e != cudaSuccess)
         return e;
     if (units * ranks > INT32_MAX)

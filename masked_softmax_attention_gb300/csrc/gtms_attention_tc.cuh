@@ -8,6 +8,7 @@
 
 #include "gtms_attention.h"
 #include "gtms_attn_tma.cuh"
+#include "gtms_device.h"
 #include "gtms_tcgen05.cuh"
 
 namespace gtms {
