@@ -188,8 +188,8 @@ struct DkvItem {
         const int32_t bg = static_cast<int32_t>(item % heads);
         b = bg / a.Hkv;
         g = bg - b * a.Hkv;
-        off = a.offset(b);
-        L = a.length(b);
+        off = warp_value(a.offset(b));
+        L = warp_value(a.length(b));
         lo = hi = 0;
         const int32_t ca = j * kTile, cb = (ca + kTile < L ? ca + kTile : L) - 1;   // live keys
         if (ca > cb)
@@ -217,7 +217,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     constexpr int ST = TL::stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DkvShared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
@@ -241,7 +241,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = sh.tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + D;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + D;
 
     if (warp >= kBwdMmaWarp) {
         tc::regs_lower<kBwdOtherRegs>();
@@ -342,7 +342,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (nraw)
                     tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
-        } else if (warp == kBwdMmaWarp && lane == 0) {
+        } else if (warp == kBwdMmaWarp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
             uint32_t gq = 0, gt = 0, nk = 0;   // query tiles, element-wise hand-offs, items
             bool ok = true;
@@ -351,7 +351,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks) {
                     const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
-                    tc::mma_f16_ts(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
+                    tc::mma_f16_ts_warp(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
                 }
             };
             for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
@@ -360,64 +360,64 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (n == 0)
                     continue;
                 auto scores = [&](uint32_t q) {
-                    ok = up.wait(&sh.qfull[q % ST], (q / ST) & 1u);
+                    ok = up.warp_wait(&sh.qfull[q % ST], (q / ST) & 1u);
                     if (!ok)
                         return;
                     tc::fence_after_sync();
                     mma_abt<T, D>(t_s, base + TL::off_k, base + TL::off_q + (q % ST) * TL::bytes);
-                    tc::commit(&sh.sfull);
+                    tc::commit_warp(&sh.sfull);
                 };
                 auto products = [&](uint32_t q) {
-                    ok = up.wait(&sh.dofull[q % ST], (q / ST) & 1u);
+                    ok = up.warp_wait(&sh.dofull[q % ST], (q / ST) & 1u);
                     if (!ok)
                         return;
                     tc::fence_after_sync();
                     mma_abt<T, D>(t_dp, base + TL::off_v, base + TL::off_do + (q % ST) * TL::bytes);
-                    tc::commit(&sh.dpfull);
+                    tc::commit_warp(&sh.dpfull);
                 };
-                ok = up.wait(&sh.kfull, nk & 1u);
+                ok = up.warp_wait(&sh.kfull, nk & 1u);
                 if (ok)
                     scores(gq);
                 if (ok && n == 1)
-                    tc::commit(&sh.kempty);
+                    tc::commit_warp(&sh.kempty);
                 if (ok)
-                    ok = up.wait(&sh.vfull, nk & 1u);
+                    ok = up.warp_wait(&sh.vfull, nk & 1u);
                 if (ok)
                     products(gq);
                 if (ok && n == 1)
-                    tc::commit(&sh.vempty);
+                    tc::commit_warp(&sh.vempty);
                 for (int32_t k = 0; k < n && ok; ++k, ++gq, ++gt) {
-                    ok = up.wait(&sh.pready, gt & 1u);
+                    ok = up.warp_wait(&sh.pready, gt & 1u);
                     if (ok && k == 0)
-                        ok = up.wait(&sh.accempty, (nk & 1u) ^ 1u);
+                        ok = up.warp_wait(&sh.accempty, (nk & 1u) ^ 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
                     accumulate(t_dv, t_s, base + TL::off_do + (gq % ST) * TL::bytes, k > 0);
-                    tc::commit(&sh.doempty[gq % ST]);
+                    tc::commit_warp(&sh.doempty[gq % ST]);
                     if (k + 1 < n) {
                         scores(gq + 1);
                         if (ok && k + 2 == n)
-                            tc::commit(&sh.kempty);
+                            tc::commit_warp(&sh.kempty);
                     }
                     if (ok)
-                        ok = up.wait(&sh.dsready, gt & 1u);
+                        ok = up.warp_wait(&sh.dsready, gt & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
                     accumulate(t_dk, t_dp, base + TL::off_q + (gq % ST) * TL::bytes, k > 0);
-                    tc::commit(&sh.qempty[gq % ST]);
+                    tc::commit_warp(&sh.qempty[gq % ST]);
                     if (k + 1 < n) {
                         products(gq + 1);
                         if (ok && k + 2 == n)
-                            tc::commit(&sh.vempty);
+                            tc::commit_warp(&sh.vempty);
                     }
                 }
                 if (ok)
-                    tc::commit(&sh.accfull);
+                    tc::commit_warp(&sh.accfull);
                 ++nk;
             }
-            tc::commit(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
+            tc::commit_warp(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
             tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {
@@ -593,8 +593,8 @@ struct DqItem {
         i0 = (blocks - 1 - static_cast<int32_t>(item / heads)) * kTile;
         b = bh / a.Hq;
         h = bh - b * a.Hq;
-        off = a.offset(b);
-        L = a.length(b);
+        off = warp_value(a.offset(b));
+        L = warp_value(a.length(b));
         const int32_t last = i0 + kTile < a.Sq ? i0 + kTile : a.Sq;
         const int32_t ra = off + i0 > 0 ? off + i0 : 0, rb = (off + last < L ? off + last : L) - 1;
         lo = hi = full0 = full1 = 0;
@@ -620,7 +620,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     constexpr int KS = TL::k_stages, VS = TL::v_stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DqShared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
@@ -647,7 +647,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = sh.tmem_slot, t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
 
     if (warp >= kBwdMmaWarp) {
         tc::regs_lower<kBwdOtherRegs>();
@@ -719,7 +719,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 if (nraw)
                     tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
-        } else if (warp == kBwdMmaWarp && lane == 0) {
+        } else if (warp == kBwdMmaWarp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
             uint32_t g = 0, ni = 0;   // key tiles, items
             bool ok = true;
@@ -729,39 +729,39 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 if (n == 0)
                     continue;
                 auto scores = [&](uint32_t k, bool last) {
-                    ok = up.wait(&sh.kfull[k % KS], (k / KS) & 1u) && up.wait(&sh.sempty[k & 1u], ((k >> 1) & 1u) ^ 1u);
+                    ok = up.warp_wait(&sh.kfull[k % KS], (k / KS) & 1u) && up.warp_wait(&sh.sempty[k & 1u], ((k >> 1) & 1u) ^ 1u);
                     if (!ok)
                         return;
                     tc::fence_after_sync();
                     mma_abt<T, D>(tmem + (k & 1u) * kTile, base + TL::off_q, base + TL::off_k + (k % KS) * TL::bytes);
-                    tc::commit(&sh.sfull[k & 1u]);
+                    tc::commit_warp(&sh.sfull[k & 1u]);
                     if (last)
-                        tc::commit(&sh.qempty);
+                        tc::commit_warp(&sh.qempty);
                 };
                 auto products = [&](uint32_t k, bool last) {
-                    ok = up.wait(&sh.vfull[k % VS], (k / VS) & 1u);
+                    ok = up.warp_wait(&sh.vfull[k % VS], (k / VS) & 1u);
                     if (!ok)
                         return;
                     tc::fence_after_sync();
                     mma_abt<T, D>(t_dp, base + TL::off_do, base + TL::off_v + (k % VS) * TL::bytes);
-                    tc::commit(&sh.dpfull);
-                    tc::commit(&sh.vempty[k % VS]);
+                    tc::commit_warp(&sh.dpfull);
+                    tc::commit_warp(&sh.vempty[k % VS]);
                     if (last)
-                        tc::commit(&sh.doempty);
+                        tc::commit_warp(&sh.doempty);
                 };
-                ok = up.wait(&sh.qfull, ni & 1u);
+                ok = up.warp_wait(&sh.qfull, ni & 1u);
                 if (ok)
                     scores(g, n == 1);
                 if (ok)
-                    ok = up.wait(&sh.dofull, ni & 1u);
+                    ok = up.warp_wait(&sh.dofull, ni & 1u);
                 if (ok)
                     products(g, n == 1);
                 if (ok && n > 1)
                     scores(g + 1, n == 2);
                 for (int32_t k = 0; k < n && ok; ++k, ++g) {
-                    ok = up.wait(&sh.dsready, g & 1u);
+                    ok = up.warp_wait(&sh.dsready, g & 1u);
                     if (ok && k == 0)
-                        ok = up.wait(&sh.accempty, (ni & 1u) ^ 1u);
+                        ok = up.warp_wait(&sh.accempty, (ni & 1u) ^ 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
@@ -769,19 +769,19 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
 #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks) {
                         const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
-                        tc::mma_f16_ts(t_dq, t_dp + at, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc, k > 0 || ks > 0);
+                        tc::mma_f16_ts_warp(t_dq, t_dp + at, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc, k > 0 || ks > 0);
                     }
-                    tc::commit(&sh.kempty[g % KS]);
+                    tc::commit_warp(&sh.kempty[g % KS]);
                     if (k + 1 < n)
                         products(g + 1, k + 2 == n);
                     if (ok && k + 2 < n)
                         scores(g + 2, k + 3 == n);
                 }
                 if (ok)
-                    tc::commit(&sh.accfull);
+                    tc::commit_warp(&sh.accfull);
                 ++ni;
             }
-            tc::commit(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
+            tc::commit_warp(&sh.mma_done);   // nothing may be in flight when the tensor memory is freed
             tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {

@@ -12,7 +12,7 @@
 //   columns 256..511  O of tile 0 and 1 (fp32, head_dim columns each).
 // Roles:
 //   load (1 warp)     TMA: the query tiles, then K and V tiles into one ring;
-//   MMA (1 lane)      S_w = Q_w K^T and O_w += P_w V with P_w read from tensor
+//   MMA (1 warp)      S_w = Q_w K^T and O_w += P_w V with P_w read from tensor
 //                     memory. The two tiles alternate, so one's products run while
 //                     the other's softmax does;
 //   softmax (2 x 4 warps) a thread owns one row: it reads its 128 scores, so the
@@ -56,7 +56,7 @@ struct FwdShared {
     int flag;
 };
 
-// Work item: 256 rows of one head, costliest row blocks first.
+// Work item: 256 rows of one head, costliest row blocks first (a whole warp calls).
 struct FwdItem {
     int32_t b, h, i0, off, L;
     int32_t lo[2], hi[2];       // key tiles [lo, hi) of each query tile
@@ -69,8 +69,8 @@ struct FwdItem {
         b = bh / a.Hq;
         h = bh - b * a.Hq;
         i0 = blk * kFwdRows;
-        off = a.offset(b);
-        L = a.length(b);
+        off = warp_value(a.offset(b));
+        L = warp_value(a.length(b));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             const int32_t i = i0 + w * kTile;
@@ -109,7 +109,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     constexpr int ST = TL::stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ FwdShared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
@@ -139,7 +139,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = sh.tmem_slot;
+    const uint32_t tmem = warp_value(sh.tmem_slot);
 
     if (warp >= kFwdMmaWarp) {
         tc::regs_lower<kFwdOtherRegs>();
@@ -205,84 +205,84 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     tc::mbar_wait(&sh.vraw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
         } else if (warp == kFwdMmaWarp) {
-            if (lane == 0) {
-                    constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
-                uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
-                bool ok = true;
-                for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                    const FwdItem it(a, item, heads, blocks);
-                    const int32_t top = it.top(), bottom = it.bottom();
-                    if (top == 0)
-                        continue;
-                    // S_w of tile t, whose K is ring entry 2 n' (its arrival has been waited for).
-                    auto scores = [&](int w, int32_t t, uint32_t tile_n) {
-                        if (t == it.hi[w] - 1) {
-                            ok = up.wait(&sh.qfull[w], nq[w] & 1u);
-                            ++nq[w];
-                            if (!ok)
-                                return;
-                            tc::fence_after_sync();
-                        }
-                        const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
-                        mma_abt<T, D>(tmem + w * kTile, q0, k0);
-                        tc::commit(&sh.sfull[w]);
-                        if (t == it.lo[w])
-                            tc::commit(&sh.qempty[w]);
-                    };
-                    auto output = [&](int w, int32_t t) {
-                        const bool first = t == it.hi[w] - 1;
-                        ok = up.wait(&sh.pready[w], np[w] & 1u);
-                        ++np[w];
-                        if (ok && first)
-                            ok = up.wait(&sh.oempty[w], (no[w] & 1u) ^ 1u);
+            constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
+            uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
+            bool ok = true;
+            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
+                const FwdItem it(a, item, heads, blocks);
+                const int32_t top = it.top(), bottom = it.bottom();
+                if (top == 0)
+                    continue;
+                // S_w of tile t, whose K is ring entry 2 n' (its arrival has been waited for).
+                auto scores = [&](int w, int32_t t, uint32_t tile_n) {
+                    if (t == it.hi[w] - 1) {
+                        ok = up.warp_wait(&sh.qfull[w], nq[w] & 1u);
+                        ++nq[w];
                         if (!ok)
                             return;
                         tc::fence_after_sync();
-                        const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
-    #pragma unroll
-                        for (int ks = 0; ks < kTile / 16; ++ks)
-                            tc::mma_f16_ts(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
-                                           tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
-                        if (t == it.lo[w]) {
-                            tc::commit(&sh.ofull[w]);
-                            ++no[w];
-                        }
-                    };
-                    auto arrived = [&](uint32_t e) {
-                        ok = up.wait(&sh.kvfull[e % ST], (e / ST) & 1u);
-                        tc::fence_after_sync();
-                    };
-                    arrived(2 * n);
-                    for (int w = 0; w < 2 && ok; ++w)
-                        if (it.has(w, top - 1))
-                            scores(w, top - 1, n);
-                    if (!ok)
-                        break;
-                    tc::commit(&sh.kvempty[(2 * n) % ST]);
-                    for (int32_t t = top - 1; t >= bottom && ok; --t, ++n) {
-                        bool next = false;   // K of the next tile has arrived
-                        arrived(2 * n + 1);
-                        for (int w = 0; w < 2 && ok; ++w) {
-                            if (it.has(w, t))
-                                output(w, t);
-                            if (ok && w == 1)
-                                tc::commit(&sh.kvempty[(2 * n + 1) % ST]);
-                            if (ok && t > bottom && it.has(w, t - 1)) {
-                                if (!next)
-                                    arrived(2 * n + 2);
-                                next = true;
-                                if (ok)
-                                    scores(w, t - 1, n + 1);
-                            }
-                        }
-                        if (ok && next)
-                            tc::commit(&sh.kvempty[(2 * n + 2) % ST]);
                     }
+                    const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
+                    mma_abt<T, D>(tmem + w * kTile, q0, k0);
+                    tc::commit_warp(&sh.sfull[w]);
+                    if (t == it.lo[w])
+                        tc::commit_warp(&sh.qempty[w]);
+                };
+                auto output = [&](int w, int32_t t) {
+                    const bool first = t == it.hi[w] - 1;
+                    ok = up.warp_wait(&sh.pready[w], np[w] & 1u);
+                    ++np[w];
+                    if (ok && first)
+                        ok = up.warp_wait(&sh.oempty[w], (no[w] & 1u) ^ 1u);
+                    if (!ok)
+                        return;
+                    tc::fence_after_sync();
+                    const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        tc::mma_f16_ts_warp(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
+                                            tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
+                    if (t == it.lo[w]) {
+                        tc::commit_warp(&sh.ofull[w]);
+                        ++no[w];
+                    }
+                };
+                auto arrived = [&](uint32_t e) {
+                    ok = up.warp_wait(&sh.kvfull[e % ST], (e / ST) & 1u);
+                    tc::fence_after_sync();
+                };
+                arrived(2 * n);
+#pragma unroll
+                for (int w = 0; w < 2 && ok; ++w)
+                    if (it.has(w, top - 1))
+                        scores(w, top - 1, n);
+                if (!ok)
+                    break;
+                tc::commit_warp(&sh.kvempty[(2 * n) % ST]);
+                for (int32_t t = top - 1; t >= bottom && ok; --t, ++n) {
+                    bool next = false;   // K of the next tile has arrived
+                    arrived(2 * n + 1);
+#pragma unroll
+                    for (int w = 0; w < 2 && ok; ++w) {
+                        if (it.has(w, t))
+                            output(w, t);
+                        if (ok && w == 1)
+                            tc::commit_warp(&sh.kvempty[(2 * n + 1) % ST]);
+                        if (ok && t > bottom && it.has(w, t - 1)) {
+                            if (!next)
+                                arrived(2 * n + 2);
+                            next = true;
+                            if (ok)
+                                scores(w, t - 1, n + 1);
+                        }
+                    }
+                    if (ok && next)
+                        tc::commit_warp(&sh.kvempty[(2 * n + 2) % ST]);
                 }
-                // Nothing may be in flight when the tensor memory is freed.
-                tc::commit(&sh.mma_done);
-                tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
             }
+            // Nothing may be in flight when the tensor memory is freed.
+            tc::commit_warp(&sh.mma_done);
+            tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {
         tc::regs_raise<kFwdSoftmaxRegs>();

@@ -108,6 +108,9 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int3
             *reinterpret_cast<uint4*>(tile + x * kTile * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// The value of lane 0, for the compiler a warp's one value.
+__device__ __forceinline__ int warp_value(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Work item of this CTA's round n: the items come costliest first, and every
 // other round takes them the other way round, so that a CTA with a costly item
 // in one round gets a cheap one in the next.
@@ -117,7 +120,7 @@ __device__ __forceinline__ int64_t snake_item(int64_t n)
     return n * g + i;
 }
 
-// S (or dP) = A B^T: two K-major operands of 128 rows x D.
+// S (or dP) = A B^T: two K-major operands of 128 rows x D (a whole warp calls).
 template <typename T, int D>
 __device__ __forceinline__ void mma_abt(uint32_t d, uint32_t a, uint32_t b)
 {
@@ -125,7 +128,7 @@ __device__ __forceinline__ void mma_abt(uint32_t d, uint32_t a, uint32_t b)
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t at = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;   // 16 columns of a swizzled 64-column box
-        tc::mma_f16(d, tc::smem_desc_sw128(a + at, 1024), tc::smem_desc_sw128(b + at, 1024), idesc, ks > 0);
+        tc::mma_f16_warp(d, tc::smem_desc_sw128(a + at, 1024), tc::smem_desc_sw128(b + at, 1024), idesc, ks > 0);
     }
 }
 
