@@ -20,7 +20,8 @@ namespace gtms {
 constexpr int kBwdGroups = 2;                            // warpgroups that share a tile's columns
 constexpr int kBwdWarps = 4 * kBwdGroups;                // element-wise warps
 constexpr int kBwdCols = kTile / kBwdGroups;             // columns of a tile per thread
-constexpr int kBwdMmaWarp = kBwdWarps, kBwdLoadWarp = kBwdWarps + 1;
+constexpr int kBwdMmaWarp = kBwdWarps, kBwdLoadWarp = kBwdWarps + 1, kBwdDealWarp = kBwdWarps + 2;
+constexpr uint32_t kBwdStage = 2048;                     // shared memory per element-wise warp for its results
 constexpr int kBwdThreads = 32 * (kBwdWarps + 4);
 constexpr int kBwdRegs = 168, kBwdElemRegs = 208, kBwdOtherRegs = 88;
 static_assert(kBwdGroups * kBwdElemRegs + kBwdOtherRegs <= (kBwdGroups + 1) * kBwdRegs, "register shares of one block");
@@ -152,6 +153,29 @@ __device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, f
     return gradient_factor(shared2[0], shared2[1]);
 }
 
+// A warp's 32 rows x COLS columns of an accumulator at `acc` (zeros where there is
+// none), scaled by f; the lanes' rows that are not live are zero. A zero comes out
+// as +0.0.
+template <typename T, int COLS>
+__device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t acc, bool any, bool live, float f, T* out)
+{
+#pragma unroll 1
+    for (int k = 0; k < COLS; k += 32) {
+        uint32_t r[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            r[j] = 0;
+        if (any) {
+            float o[32];
+            tc::tmem_ld32(acc + k, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                r[j] = live ? pack2<T>(o[2 * j] * f + 0.0f, o[2 * j + 1] * f + 0.0f) : 0u;
+        }
+        store_rows<32>(stage, lane, r, out ? out + k : nullptr);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // dk, dv. Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T
 // and dS^T are in tensor memory as the A operands of dV += P^T dO and
@@ -166,30 +190,22 @@ struct DkvTile {
     static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
     static constexpr uint32_t off_k = 0, off_v = bytes, off_q = 2 * bytes, off_do = (2 + stages) * bytes;
     static constexpr uint32_t off_rows = (2 + 2 * stages) * bytes;           // per stage: 128 lse2, 128 D
-    static constexpr uint32_t smem = off_rows + stages * 2 * kTile * 4 + 1024;
-};
-
-struct DkvShared {
-    uint64_t kfull, kempty, vfull, vempty;
-    uint64_t qfull[2], qempty[2], dofull[2], doempty[2], raw;
-    uint64_t sfull, pready, dpfull, dsready, accfull, accempty, mma_done;
-    uint32_t tmem_slot;
-    int flag;
-    float norm[2];
+    static constexpr uint32_t off_out = off_rows + stages * 2 * kTile * 4;
+    static constexpr uint32_t smem = off_out + kBwdWarps * kBwdStage + 1024;   // slack to align the base
 };
 
 struct DkvItem {
     int32_t b, g, j, off, L, lo, hi;   // key tile j of head g; query tiles [lo, hi)
 
-    __device__ __forceinline__ DkvItem(const AttentionArgs& a, int64_t item, int64_t heads)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads)
     {
         // Under a causal mask the first key tiles are kept by the most rows.
         j = static_cast<int32_t>(item / heads);
         const int32_t bg = static_cast<int32_t>(item % heads);
         b = bg / a.Hkv;
         g = bg - b * a.Hkv;
-        off = warp_value(a.offset(b));
-        L = warp_value(a.length(b));
+        off = a.offset(b);
+        L = a.length(b);
         lo = hi = 0;
         const int32_t ca = j * kTile, cb = (ca + kTile < L ? ca + kTile : L) - 1;   // live keys
         if (ca > cb)
@@ -207,11 +223,21 @@ struct DkvItem {
     }
 };
 
+struct DkvShared {
+    uint64_t kfull, kempty, vfull, vempty;
+    uint64_t qfull[2], qempty[2], dofull[2], doempty[2], raw;
+    uint64_t sfull, pready, dpfull, dsready, accfull, accempty, mma_done;
+    ItemSlot<DkvItem> items;
+    uint32_t tmem_slot;
+    int flag;
+    float norm[2];
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
-                          const __grid_constant__ AttentionArgs a, int64_t heads, int64_t items, uint64_t wait_ns)
+                          const __grid_constant__ AttentionArgs a, uint32_t heads, uint64_t wait_ns)
 {
     using TL = DkvTile<D>;
     constexpr int ST = TL::stages;
@@ -231,6 +257,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         tc::mbar_init(&sh.pready, kBwdWarps);
         tc::mbar_init(&sh.dsready, kBwdWarps);
         tc::mbar_init(&sh.accempty, kBwdWarps);
+        init_items(sh.items, kBwdWarps + 2);   // load, MMA and element-wise warps
         sh.flag = 0;
     }
     if (warp == kBwdMmaWarp) {
@@ -245,12 +272,19 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 
     if (warp >= kBwdMmaWarp) {
         tc::regs_lower<kBwdOtherRegs>();
-        if (warp == kBwdLoadWarp) {
+        if (warp == kBwdDealWarp) {
+            deal_items(sh.items, up, lane, [&](int32_t index) {
+                DkvItem it;
+                it.set(a, index, heads);
+                return it;
+            });
+        } else if (warp == kBwdLoadWarp) {
             uint32_t gq = 0, nk = 0, nraw = 0;
+            uint32_t taken = 0;
+            DkvItem it;
             uint32_t issued_q = 0, issued_do = 0, issued_k = 0, issued_v = 0;
             bool ok = true;
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const DkvItem it(a, item, heads);
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
                 if (it.lo == it.hi)
                     continue;
                 // A 128-row tile of queries or output gradients; rows that keep nothing may hold
@@ -344,7 +378,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             }
         } else if (warp == kBwdMmaWarp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
-            uint32_t gq = 0, gt = 0, nk = 0;   // query tiles, element-wise hand-offs, items
+            uint32_t gq = 0, gt = 0, nk = 0, taken = 0;   // query tiles, element-wise hand-offs, items
+            DkvItem it;
             bool ok = true;
             // acc += A B, A (16 bits, in tensor memory, a part of it per warpgroup) and B a tile of rows.
             auto accumulate = [&](uint32_t acc, uint32_t t_a, uint32_t rows, bool more) {
@@ -354,9 +389,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     tc::mma_f16_ts_warp(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
                 }
             };
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const DkvItem it(a, item, heads);
-                const int32_t n = (it.hi - it.lo) * a.group;
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
+                const int32_t n = warp_value((it.hi - it.lo) * a.group);
                 if (n == 0)
                     continue;
                 auto scores = [&](uint32_t q) {
@@ -428,10 +462,10 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
-        uint32_t gt = 0, nk = 0;
+        uint32_t gt = 0, nk = 0, taken = 0;
+        DkvItem it;
         bool ok = true;
-        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-            const DkvItem it(a, item, heads);
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t key = it.j * kTile + row;
             const bool any = it.lo != it.hi;
             for (int32_t h = 0; h < (any ? a.group : 0) && ok; ++h)
@@ -516,38 +550,22 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             const bool is_dk = part >= kBwdGroups / 2;
             constexpr int cols = D / (kBwdGroups / 2);
             const int col0 = (part % (kBwdGroups / 2)) * cols;
-            T* out = (is_dk ? a.dk : a.dv).row<T>(it.b, it.g, key) + col0;
+            T* out = key < a.Skv ? (is_dk ? a.dk : a.dv).row<T>(it.b, it.g, key) + col0 : nullptr;
             if (any) {
                 ok = up.warp_wait(&sh.accfull, nk & 1u);
                 ++nk;
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
-#pragma unroll 1
-                for (int k = 0; k < cols; k += 32) {
-                    float o[32];
-                    tc::tmem_ld32((is_dk ? t_dk : t_dv) + lanes + col0 + k, o);
-                    if (key < a.Skv) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (key < it.L)
-                                v = make_uint4(pack2<T>(o[j] * f + 0.0f, o[j + 1] * f + 0.0f),
-                                               pack2<T>(o[j + 2] * f + 0.0f, o[j + 3] * f + 0.0f),
-                                               pack2<T>(o[j + 4] * f + 0.0f, o[j + 5] * f + 0.0f),
-                                               pack2<T>(o[j + 6] * f + 0.0f, o[j + 7] * f + 0.0f));
-                            *reinterpret_cast<uint4*>(out + k + j) = v;
-                        }
-                    }
-                }
+            }
+            const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
+            write_rows<T, cols>(smem + TL::off_out + warp * kBwdStage, lane, (is_dk ? t_dk : t_dv) + lanes + col0, any,
+                                key < it.L, f, out);
+            if (any) {
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(&sh.accempty);
-            } else if (key < a.Skv) {
-                for (int k = 0; k < cols; k += 8)
-                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -569,32 +587,24 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 // ---------------------------------------------------------------------------
 template <int D>
 struct DqTile {
-    static constexpr int k_stages = 3, v_stages = 2;
+    static constexpr int k_stages = 3, v_stages = D == 64 ? 2 : 1;
     static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
     static constexpr uint32_t off_q = 0, off_do = bytes, off_k = 2 * bytes, off_v = (2 + k_stages) * bytes;
-    static constexpr uint32_t smem = (2 + k_stages + v_stages) * bytes + 1024;
-};
-
-struct DqShared {
-    uint64_t qfull, qempty, dofull, doempty;
-    uint64_t kfull[3], kempty[3], vfull[2], vempty[2], raw;
-    uint64_t sfull[2], sempty[2], dpfull, dsready, accfull, accempty, mma_done;
-    uint32_t tmem_slot;
-    int flag;
-    float norm[2];
+    static constexpr uint32_t off_out = (2 + k_stages + v_stages) * bytes;
+    static constexpr uint32_t smem = off_out + kBwdWarps * kBwdStage + 1024;   // slack to align the base
 };
 
 struct DqItem {
     int32_t b, h, i0, off, L, lo, hi, full0, full1;
 
-    __device__ __forceinline__ DqItem(const AttentionArgs& a, int64_t item, int64_t heads, int32_t blocks)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks)
     {
         const int32_t bh = static_cast<int32_t>(item % heads);
         i0 = (blocks - 1 - static_cast<int32_t>(item / heads)) * kTile;
         b = bh / a.Hq;
         h = bh - b * a.Hq;
-        off = warp_value(a.offset(b));
-        L = warp_value(a.length(b));
+        off = a.offset(b);
+        L = a.length(b);
         const int32_t last = i0 + kTile < a.Sq ? i0 + kTile : a.Sq;
         const int32_t ra = off + i0 > 0 ? off + i0 : 0, rb = (off + last < L ? off + last : L) - 1;
         lo = hi = full0 = full1 = 0;
@@ -610,11 +620,21 @@ struct DqItem {
     }
 };
 
+struct DqShared {
+    uint64_t qfull, qempty, dofull, doempty;
+    uint64_t kfull[3], kempty[3], vfull[2], vempty[2], raw;
+    uint64_t sfull[2], sempty[2], dpfull, dsready, accfull, accempty, mma_done;
+    ItemSlot<DqItem> items;
+    uint32_t tmem_slot;
+    int flag;
+    float norm[2];
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                          const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
-                         const __grid_constant__ AttentionArgs a, int64_t heads, int32_t blocks, uint64_t wait_ns)
+                         const __grid_constant__ AttentionArgs a, uint32_t heads, int32_t blocks, uint64_t wait_ns)
 {
     using TL = DqTile<D>;
     constexpr int KS = TL::k_stages, VS = TL::v_stages;
@@ -624,7 +644,6 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
-    const int64_t items = heads * blocks;
 
     if (threadIdx.x == 0) {
         uint64_t* const one[] = {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull[0], &sh.sfull[1],
@@ -637,6 +656,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
         tc::mbar_init(&sh.sempty[1], kBwdWarps);
         tc::mbar_init(&sh.dsready, kBwdWarps);
         tc::mbar_init(&sh.accempty, kBwdWarps);
+        init_items(sh.items, kBwdWarps + 2);   // load, MMA and element-wise warps
         sh.flag = 0;
     }
     if (warp == kBwdMmaWarp) {
@@ -651,11 +671,17 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
 
     if (warp >= kBwdMmaWarp) {
         tc::regs_lower<kBwdOtherRegs>();
-        if (warp == kBwdLoadWarp) {
-            uint32_t gk = 0, gv = 0, nq = 0, ndo = 0, nraw = 0;
+        if (warp == kBwdDealWarp) {
+            deal_items(sh.items, up, lane, [&](int32_t index) {
+                DqItem it;
+                it.set(a, index, heads, blocks);
+                return it;
+            });
+        } else if (warp == kBwdLoadWarp) {
+            uint32_t gk = 0, gv = 0, nq = 0, ndo = 0, nraw = 0, taken = 0;
+            DqItem it;
             bool ok = true;
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const DqItem it(a, item, heads, blocks);
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
                 if (it.lo == it.hi)
                     continue;
                 const int32_t hk = it.h / a.group;
@@ -721,11 +747,11 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             }
         } else if (warp == kBwdMmaWarp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
-            uint32_t g = 0, ni = 0;   // key tiles, items
+            uint32_t g = 0, ni = 0, taken = 0;   // key tiles, items
+            DqItem it;
             bool ok = true;
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const DqItem it(a, item, heads, blocks);
-                const int32_t n = it.hi - it.lo;
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
+                const int32_t n = warp_value(it.hi - it.lo);
                 if (n == 0)
                     continue;
                 auto scores = [&](uint32_t k, bool last) {
@@ -792,10 +818,10 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
-        uint32_t g = 0, ni = 0;
+        uint32_t g = 0, ni = 0, taken = 0;
+        DqItem it;
         bool ok = true;
-        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-            const DqItem it(a, item, heads, blocks);
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t i = it.i0 + row;
             int32_t c0, c1;
             a.kept(it.off + i, it.L, c0, c1);
@@ -858,38 +884,22 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             if (!ok)
                 break;
             constexpr int cols = D / kBwdGroups;
-            T* out = a.dq.row<T>(it.b, it.h, i) + part * cols;
-            if (it.lo != it.hi) {
+            T* out = i < a.Sq ? a.dq.row<T>(it.b, it.h, i) + part * cols : nullptr;
+            const bool any = it.lo != it.hi;
+            if (any) {
                 ok = up.warp_wait(&sh.accfull, ni & 1u);
                 ++ni;
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                const float f = a.scale / factor;
-#pragma unroll 1
-                for (int k = 0; k < cols; k += 32) {
-                    float o[32];
-                    tc::tmem_ld32(t_dq + lanes + part * cols + k, o);
-                    if (i < a.Sq) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (live)
-                                v = make_uint4(pack2<T>(o[j] * f + 0.0f, o[j + 1] * f + 0.0f),
-                                               pack2<T>(o[j + 2] * f + 0.0f, o[j + 3] * f + 0.0f),
-                                               pack2<T>(o[j + 4] * f + 0.0f, o[j + 5] * f + 0.0f),
-                                               pack2<T>(o[j + 6] * f + 0.0f, o[j + 7] * f + 0.0f));
-                            *reinterpret_cast<uint4*>(out + k + j) = v;
-                        }
-                    }
-                }
+            }
+            write_rows<T, cols>(smem + TL::off_out + warp * kBwdStage, lane, t_dq + lanes + part * cols, any, live,
+                                a.scale / factor, out);
+            if (any) {
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(&sh.accempty);
-            } else if (i < a.Sq) {
-                for (int k = 0; k < cols; k += 8)
-                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -908,9 +918,6 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
 {
     AttentionArgs a = args;
     if (!bind_context())
-        return cudaErrorUnknown;
-    const int nsm = device_sms();
-    if (nsm <= 0)
         return cudaErrorUnknown;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, kv_heads = static_cast<int64_t>(a.B) * a.Hkv;
     // Where one side has no rows its tensors may be null: nothing of them is loaded, and the other side's
@@ -931,24 +938,23 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         a.norm_blocks = static_cast<int32_t>(blocks);
         e = launch_kernel(gtms_attention_bwd_prep_kernel<T, D>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, a, n, m);
     }
+    // One CTA per item; the running ones take over the others' (see ItemSlot).
     if (e == cudaSuccess && keys) {
         auto* kern = gtms_attention_dkv_kernel<T, D>;
         constexpr int smem = static_cast<int>(DkvTile<D>::smem);
-        const int64_t items = kv_heads * ((a.Skv + kTile - 1) / kTile);
         e = allow_smem<gtms_attention_dkv_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
-                              kv_heads, items, wait_ns);
+            e = launch_kernel(kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)), kBwdThreads, smem, st, mq,
+                              mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
     }
     if (e == cudaSuccess && rows) {
         auto* kern = gtms_attention_dq_kernel<T, D>;
         constexpr int smem = static_cast<int>(DqTile<D>::smem);
         const int32_t blocks = a.Sq_pad / kTile;
-        const int64_t items = heads * blocks;
         e = allow_smem<gtms_attention_dq_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
-                              heads, blocks, wait_ns);
+            e = launch_kernel(kern, static_cast<unsigned>(heads * blocks), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
+                              static_cast<uint32_t>(heads), blocks, wait_ns);
     }
     return e;
 }

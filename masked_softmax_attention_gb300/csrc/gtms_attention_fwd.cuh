@@ -3,7 +3,7 @@
 //   s_ic = scale q_i . k_c,  o_i = sum_c exp(s_ic - m_i) v_c / l_i,
 //   l_i = sum_c exp(s_ic - m_i),  lse_i = m_i + log l_i   over the kept c.
 //
-// One persistent CTA per SM works on 256 query rows at a time, as two tiles of
+// A CTA, one per SM, works on 256 query rows at a time, as two tiles of
 // 128, and walks over the 128-key tiles that hold kept entries, last first (so
 // that the tiles a causal mask cuts come first and the maximum settles early).
 // Scores, probabilities and both output accumulators stay in tensor memory:
@@ -11,6 +11,7 @@
 //                     over the first half of its own S;
 //   columns 256..511  O of tile 0 and 1 (fp32, head_dim columns each).
 // Roles:
+//   deal (1 warp)     the work items (see ItemSlot);
 //   load (1 warp)     TMA: the query tiles, then K and V tiles into one ring;
 //   MMA (1 warp)      S_w = Q_w K^T and O_w += P_w V with P_w read from tensor
 //                     memory. The two tiles alternate, so one's products run while
@@ -18,11 +19,15 @@
 //   softmax (2 x 4 warps) a thread owns one row: it reads its 128 scores, so the
 //                     maximum and the sum need no exchange, writes P back, and at
 //                     the end divides O and stores it.
-// The running maximum is only raised, and O and l rescaled, when it would grow by
-// more than 8 in log2 units: p stays below 2^8, which 16-bit and fp32 hold as
-// well, and the rescaling of O leaves the loop for almost every tile. The thread
-// that owns the row rescales: S_w of a tile completes after every earlier product
-// into O_w, so no other hand-off is needed.
+// The running maximum is only raised, and O and l rescaled, when a tile exceeds it
+// by more than 12 in log2 units: p stays below 2^12, which fp16, bf16 and fp32
+// hold as well as numbers below 1. Almost no tile but a row's first does, so the
+// exponentials do not wait for the tile's maximum: the first half of the row is
+// exponentiated while the maximum is found, and done again in the rare other
+// case. The thread that owns the row rescales: S_w of a tile completes after
+// every earlier product into O_w, so no other hand-off is needed. P is handed
+// over in two halves, so that the first half's product runs while the second
+// half is exponentiated.
 #pragma once
 
 #include "gtms_attention_tc.cuh"
@@ -30,47 +35,38 @@
 namespace gtms {
 
 constexpr int kFwdRows = 2 * kTile;                 // query rows of one work item
-constexpr int kFwdMmaWarp = 8, kFwdLoadWarp = 9;    // warps 0..7 are the softmax warps
-constexpr int kFwdThreads = 32 * 12;                // two warps idle: register shares go by warpgroup
+constexpr int kFwdMmaWarp = 8, kFwdLoadWarp = 9, kFwdDealWarp = 10;   // warps 0..7 are the softmax warps
+constexpr int kFwdThreads = 32 * 12;                // one warp idle: register shares go by warpgroup
 // 168 registers a thread at launch (three warps to each SM quarter), shared out as
 // 208 for a softmax thread, which holds a row of 128 scores, and 88 for the rest.
 constexpr int kFwdRegs = 168, kFwdSoftmaxRegs = 208, kFwdOtherRegs = 88;
 static_assert(2 * kFwdSoftmaxRegs + kFwdOtherRegs <= 3 * kFwdRegs, "register shares of one block");
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRaiseLog2 = 12.0f;
 
 template <int D>
 struct FwdTile {
-    static constexpr int stages = D == 64 ? 8 : 5;
+    static constexpr int stages = D == 64 ? 8 : 4;
     static constexpr uint32_t bytes = kTile * D * 2;          // one 128-row tile
     static constexpr uint32_t box = kTile * 128;              // one swizzled 64-column box of it
-    static constexpr uint32_t off_ring = 2 * bytes;
-    static constexpr uint32_t smem = (2 + stages) * bytes + 1024;   // + slack to align the base
+    static constexpr uint32_t off_ring = 2 * bytes, off_out = (2 + stages) * bytes;
+    static constexpr uint32_t smem = off_out + 8 * 4096 + 1024;   // 4 KB per softmax warp; slack to align the base
 };
 
-struct FwdShared {
-    uint64_t qfull[2], qempty[2];
-    uint64_t kvfull[8], kvempty[8], vraw;
-    uint64_t sfull[2], pready[2], ofull[2], oempty[2];
-    uint64_t mma_done;
-    uint32_t tmem_slot;
-    int flag;
-};
-
-// Work item: 256 rows of one head, costliest row blocks first (a whole warp calls).
+// Work item: 256 rows of one head, costliest row blocks first.
 struct FwdItem {
     int32_t b, h, i0, off, L;
     int32_t lo[2], hi[2];       // key tiles [lo, hi) of each query tile
     int32_t full0[2], full1[2]; // columns [full0, full1) that every live row of the tile keeps
 
-    __device__ __forceinline__ FwdItem(const AttentionArgs& a, int64_t item, int64_t heads, int32_t blocks)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks)
     {
         const int32_t blk = blocks - 1 - static_cast<int32_t>(item / heads);
         const int32_t bh = static_cast<int32_t>(item % heads);
         b = bh / a.Hq;
         h = bh - b * a.Hq;
         i0 = blk * kFwdRows;
-        off = warp_value(a.offset(b));
-        L = warp_value(a.length(b));
+        off = a.offset(b);
+        L = a.length(b);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             const int32_t i = i0 + w * kTile;
@@ -99,10 +95,20 @@ struct FwdItem {
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
 };
 
+struct FwdShared {
+    uint64_t qfull[2], qempty[2];
+    uint64_t kvfull[8], kvempty[8], vraw;
+    uint64_t sfull[2], phalf[2], pready[2], ofull[2], oempty[2];
+    ItemSlot<FwdItem> items;
+    uint64_t mma_done;
+    uint32_t tmem_slot;
+    int flag;
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
-                          const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, int64_t heads,
+                          const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, uint32_t heads,
                           int32_t blocks, uint64_t wait_ns)
 {
     using TL = FwdTile<D>;
@@ -113,13 +119,13 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
-    const int64_t items = heads * blocks;
 
     if (threadIdx.x == 0) {
         for (int w = 0; w < 2; ++w) {
             tc::mbar_init(&sh.qfull[w], 1);
             tc::mbar_init(&sh.qempty[w], 1);
             tc::mbar_init(&sh.sfull[w], 1);
+            tc::mbar_init(&sh.phalf[w], 4);
             tc::mbar_init(&sh.pready[w], 4);
             tc::mbar_init(&sh.ofull[w], 1);
             tc::mbar_init(&sh.oempty[w], 4);
@@ -130,6 +136,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         }
         tc::mbar_init(&sh.vraw, 1);
         tc::mbar_init(&sh.mma_done, 1);
+        init_items(sh.items, 10);   // load, MMA and softmax warps
         sh.flag = 0;
     }
     if (warp == kFwdMmaWarp) {
@@ -143,11 +150,17 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 
     if (warp >= kFwdMmaWarp) {
         tc::regs_lower<kFwdOtherRegs>();
-        if (warp == kFwdLoadWarp) {
-            uint32_t g = 0, nq[2] = {0, 0}, nraw = 0;
+        if (warp == kFwdDealWarp) {
+            deal_items(sh.items, up, lane, [&](int32_t index) {
+                FwdItem it;
+                it.set(a, index, heads, blocks);
+                return it;
+            });
+        } else if (warp == kFwdLoadWarp) {
+            uint32_t g = 0, nq[2] = {0, 0}, nraw = 0, taken = 0;
+            FwdItem it;
             bool ok = true;
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const FwdItem it(a, item, heads, blocks);
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
                 const int32_t hk = it.h / a.group;
                 auto tile = [&](const HeadsMap& m, int32_t t, bool tail) {
                     const uint32_t s = g % ST;
@@ -206,10 +219,15 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             }
         } else if (warp == kFwdMmaWarp) {
             constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
-            uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
+            uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, taken = 0;
+            FwdItem it;
             bool ok = true;
-            for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-                const FwdItem it(a, item, heads, blocks);
+            while (take_item(sh.items, up, lane, taken, it, ok)) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    it.lo[w] = warp_value(it.lo[w]);
+                    it.hi[w] = warp_value(it.hi[w]);
+                }
                 const int32_t top = it.top(), bottom = it.bottom();
                 if (top == 0)
                     continue;
@@ -230,18 +248,21 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 };
                 auto output = [&](int w, int32_t t) {
                     const bool first = t == it.hi[w] - 1;
-                    ok = up.warp_wait(&sh.pready[w], np[w] & 1u);
-                    ++np[w];
-                    if (ok && first)
-                        ok = up.warp_wait(&sh.oempty[w], (no[w] & 1u) ^ 1u);
-                    if (!ok)
-                        return;
-                    tc::fence_after_sync();
                     const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        tc::mma_f16_ts_warp(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
-                                            tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
+                    for (int half = 0; half < 2; ++half) {
+                        ok = up.warp_wait(half ? &sh.pready[w] : &sh.phalf[w], np[w] & 1u);
+                        if (ok && first && half == 0)
+                            ok = up.warp_wait(&sh.oempty[w], (no[w] & 1u) ^ 1u);
+                        if (!ok)
+                            return;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int ks = half * (kTile / 32); ks < (half + 1) * (kTile / 32); ++ks)
+                            tc::mma_f16_ts_warp(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
+                                                tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
+                    }
+                    ++np[w];
                     if (t == it.lo[w]) {
                         tc::commit_warp(&sh.ofull[w]);
                         ++no[w];
@@ -260,24 +281,22 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     break;
                 tc::commit_warp(&sh.kvempty[(2 * n) % ST]);
                 for (int32_t t = top - 1; t >= bottom && ok; --t, ++n) {
-                    bool next = false;   // K of the next tile has arrived
+                    // What the loads bring is waited for first: the hand-overs of P are the ones that matter.
                     arrived(2 * n + 1);
+                    if (ok && t > bottom)
+                        arrived(2 * n + 2);
 #pragma unroll
-                    for (int w = 0; w < 2 && ok; ++w) {
-                        if (it.has(w, t))
+                    for (int w = 0; w < 2; ++w) {
+                        if (ok && it.has(w, t))
                             output(w, t);
-                        if (ok && w == 1)
-                            tc::commit_warp(&sh.kvempty[(2 * n + 1) % ST]);
-                        if (ok && t > bottom && it.has(w, t - 1)) {
-                            if (!next)
-                                arrived(2 * n + 2);
-                            next = true;
-                            if (ok)
-                                scores(w, t - 1, n + 1);
-                        }
+                        if (ok && it.has(w, t - 1))
+                            scores(w, t - 1, n + 1);
                     }
-                    if (ok && next)
-                        tc::commit_warp(&sh.kvempty[(2 * n + 2) % ST]);
+                    if (ok) {
+                        tc::commit_warp(&sh.kvempty[(2 * n + 1) % ST]);
+                        if (t > bottom)
+                            tc::commit_warp(&sh.kvempty[(2 * n + 2) % ST]);
+                    }
                 }
             }
             // Nothing may be in flight when the tensor memory is freed.
@@ -292,10 +311,10 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         // exp(scale x) = exp2(c x) with c > 0: a negative scale flips the scores, a zero one clears them.
         const float c = a.scale == 0.0f ? kLog2e : fabsf(a.scale) * kLog2e;
         const float pre = a.scale > 0.0f ? 1.0f : (a.scale < 0.0f ? -1.0f : 0.0f);
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, no = 0, taken = 0;
+        FwdItem it;
         bool ok = true;
-        for (int64_t round = 0, item; ok && (item = snake_item(round)) < items; ++round) {
-            const FwdItem it(a, item, heads, blocks);
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t i = it.i0 + w * kTile + (warp & 3) * 32 + lane;
             int32_t c0, c1;
             a.kept(it.off + i, it.L, c0, c1);
@@ -314,11 +333,17 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     for (int j = 0; j < kTile; ++j)
                         s[j] *= pre;
                 }
-                if (t * kTile < it.full0[w] || (t + 1) * kTile > it.full1[w]) {
-                    const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
+                if ((t + 1) * kTile > it.full1[w]) {
+                    const int32_t k1 = c1 - t * kTile;
 #pragma unroll
                     for (int j = 0; j < kTile; ++j)
-                        s[j] = j >= k0 && j < k1 ? s[j] : -INFINITY;
+                        s[j] = j < k1 ? s[j] : -INFINITY;
+                }
+                if (t * kTile < it.full0[w]) {
+                    const int32_t k0 = c0 - t * kTile;
+#pragma unroll
+                    for (int j = 0; j < kTile; ++j)
+                        s[j] = j >= k0 ? s[j] : -INFINITY;
                 }
                 float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -327,14 +352,31 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     for (int k = 0; k < 4; ++k)
                         x[k] = j + 4 + k < kTile ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
                 const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-                if (t == it.hi[w] - 1) {
-                    m = top;
-                } else {
-                    const bool raise = (top - m) * c > kRescaleLog2;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float f = raise ? exp2_approx((m - top) * c) : 1.0f;
-                        m = raise ? top : m;
-                        l *= f;
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, rounded to 16 bits.
+                auto exponentiate = [&](int k, float shift, uint32_t(&r)[16]) {
+                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float2 e = __ffma2_rn(make_float2(s[k + 2 * j], s[k + 2 * j + 1]), c2, shift2);
+                        e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                        r[j] = pack2<T>(e.x, e.y);
+                    }
+                };
+                float shift = m == -INFINITY ? 0.0f : -m * c;
+                uint32_t r0[16], r1[16];
+                const bool opening = t == it.hi[w] - 1;
+                if (!opening) {
+                    exponentiate(0, shift, r0);
+                    exponentiate(32, shift, r1);
+                }
+                const bool raise = (top - m) * c > kRaiseLog2;   // a row's first kept tile: infinity
+                if (__any_sync(0xffffffffu, raise) || opening) {
+                    const float f = raise ? exp2_approx((m - top) * c) : 1.0f;
+                    m = raise ? top : m;
+                    l *= f;
+                    if (!opening) {
 #pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
                             float o[32];
@@ -346,61 +388,61 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             tc::tmem_st32(to + k, r);
                         }
                     }
+                    shift = m == -INFINITY ? 0.0f : -m * c;
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                    exponentiate(0, shift, r0);
+                    exponentiate(32, shift, r1);
                 }
-                const float shift = m == -INFINITY ? 0.0f : -m * c;
-                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int k = 0; k < kTile; k += 32) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float2 e = __ffma2_rn(make_float2(s[k + 2 * j], s[k + 2 * j + 1]), c2, shift2);
-                        e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                        r[j] = pack2<T>(e.x, e.y);
-                    }
-                    tc::tmem_st16(ts + k / 2, r);
-                }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.pready[w]);
+                auto hand_over = [&](uint64_t* bar) {
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(bar);
+                };
+                tc::tmem_st16(ts, r0);
+                tc::tmem_st16(ts + 16, r1);
+                hand_over(&sh.phalf[w]);
+                exponentiate(64, shift, r0);
+                tc::tmem_st16(ts + 32, r0);
+                exponentiate(96, shift, r1);
+                tc::tmem_st16(ts + 48, r1);
+                hand_over(&sh.pready[w]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok)
                 break;
-            T* out = a.o.row<T>(it.b, it.h, i);
+            T* out = i < a.Sq ? a.o.row<T>(it.b, it.h, i) : nullptr;
+            uint8_t* stage = smem + TL::off_out + warp * 4096;
             const float inv = live ? 1.0f / l : 0.0f;
-            if (it.hi[w] > it.lo[w]) {
+            const bool any = it.hi[w] > it.lo[w];
+            if (any) {
                 ok = up.warp_wait(&sh.ofull[w], no & 1u);
                 ++no;
                 if (!ok)
                     break;
                 tc::fence_after_sync();
+            }
 #pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
-                    tc::tmem_ld32(to + k, o);
-                    if (i < a.Sq) {
+            for (int k = 0; k < D; k += 64) {
+                uint32_t r[32];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (live)
-                                v = make_uint4(pack2<T>(o[j] * inv, o[j + 1] * inv), pack2<T>(o[j + 2] * inv, o[j + 3] * inv),
-                                               pack2<T>(o[j + 4] * inv, o[j + 5] * inv), pack2<T>(o[j + 6] * inv, o[j + 7] * inv));
-                            *reinterpret_cast<uint4*>(out + k + j) = v;
-                        }
-                    }
+                for (int j = 0; j < 32; ++j)
+                    r[j] = 0;
+                if (any) {
+                    float o[64];
+                    tc::tmem_ld64(to + k, o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = live ? pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
                 }
+                store_rows<64>(stage, lane, r, out ? out + k : nullptr);
+            }
+            if (any) {
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(&sh.oempty[w]);
-            } else if (i < a.Sq) {
-                for (int k = 0; k < D; k += 8)
-                    *reinterpret_cast<uint4*>(out + k) = make_uint4(0, 0, 0, 0);
             }
             if (a.lse && i < a.Sq)
                 a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq + i] =
@@ -436,10 +478,7 @@ cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uin
         return e;
     const int32_t blocks = (a.Sq + kFwdRows - 1) / kFwdRows;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, items = heads * blocks;
-    const int nsm = device_sms();
-    if (nsm <= 0)
-        return cudaErrorUnknown;
-    return launch_kernel(kern, static_cast<unsigned>(items < nsm ? items : nsm), kFwdThreads, smem, st, mq, mk, mv, a, heads,
+    return launch_kernel(kern, static_cast<unsigned>(items), kFwdThreads, smem, st, mq, mk, mv, a, static_cast<uint32_t>(heads),
                          blocks, wait_ns);
 }
 

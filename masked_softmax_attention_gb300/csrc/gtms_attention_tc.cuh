@@ -111,13 +111,102 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int3
 // The value of lane 0, for the compiler a warp's one value.
 __device__ __forceinline__ int warp_value(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Work item of this CTA's round n: the items come costliest first, and every
-// other round takes them the other way round, so that a CTA with a costly item
-// in one round gets a cheap one in the next.
-__device__ __forceinline__ int64_t snake_item(int64_t n)
+// Work items. The grid has one CTA per item, costliest first, but only as many run
+// as the multiprocessors hold: each, its own item handed out, asks the hardware
+// for another CTA's in its place, so that whoever is done first takes the next one
+// (a static deal leaves CTAs idle when lengths differ), and its pipelines run on
+// from item to item. One warp works the items out and deals them to the others
+// through shared memory, one item ahead of their use, which keeps the index
+// arithmetic and the loads of lengths out of their way.
+template <typename Item>
+struct ItemSlot {
+    __align__(16) uint4 response;
+    uint64_t full, empty, answered;
+    Item item;
+};
+
+template <typename Item>
+__device__ __forceinline__ void init_items(ItemSlot<Item>& s, int readers)
 {
-    const int64_t g = gridDim.x, i = n & 1 ? g - 1 - blockIdx.x : blockIdx.x;
-    return n * g + i;
+    tc::mbar_init(&s.full, 1);
+    tc::mbar_init(&s.empty, readers);
+    tc::mbar_init(&s.answered, 1);
+}
+
+// The dealing warp: make(index) is the item of a CTA index; an item with b < 0 ends
+// the deal. The next item is asked for once every reader has taken the last.
+template <typename Item, typename Make>
+__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, Make make)
+{
+    int32_t index = blockIdx.x;
+    for (uint32_t n = 0; index >= 0; ++n) {
+        if (n > 0) {
+            if (!up.warp_wait(&s.empty, (n - 1) & 1u))
+                return;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&s.answered, 16);
+                tc::next_cta_request(tc::smem_u32(&s.response), &s.answered);
+            }
+            __syncwarp();
+            // A request is always waited for, also when another role has given up.
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.answered, (n - 1) & 1u, kAttnDrainWaitNs))) {
+                up.raise();
+                return;
+            }
+            index = tc::next_cta_index(tc::smem_u32(&s.response));
+            tc::fence_smem_for_async();   // the response has been read before the next one may land
+            __syncwarp();
+        }
+        Item it;
+        it.b = -1;
+        if (index >= 0)
+            it = make(index);
+        if (lane == 0) {
+            s.item = it;
+            tc::mbar_arrive(&s.full);
+        }
+    }
+}
+
+// The next item, for a reading warp (n counts its items); false at the end of the deal or where a role gave up.
+template <typename Item>
+__device__ __forceinline__ bool take_item(ItemSlot<Item>& s, const GiveUp& up, int lane, uint32_t& n, Item& it, bool& ok)
+{
+    ok = ok && up.warp_wait(&s.full, n & 1u);
+    if (!ok)
+        return false;
+    it = s.item;
+    __syncwarp();
+    if (lane == 0)
+        tc::mbar_arrive(&s.empty);
+    ++n;
+    return it.b >= 0;
+}
+
+// A warp's 32 rows x COLS columns of results, 16 bits each, through shared memory
+// (64 COLS bytes, 16-byte chunks swizzled by row) so that neighbouring lanes write
+// a row's bytes together: straight from the rows' owners every store would touch
+// 32 lines. `row` is the address of this lane's row's columns, null where it is
+// not written.
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint32_t (&v)[COLS / 2], void* row)
+{
+    constexpr int CH = COLS / 8, ROWS = 32 / CH;   // chunks of a row, rows of one store
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+        *reinterpret_cast<uint4*>(stage + lane * (16 * CH) + ((j ^ (lane % 8 * CH / 8)) << 4)) =
+            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const uint64_t mine = reinterpret_cast<uint64_t>(row);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const int r = ROWS * k + lane / CH, j = lane % CH;
+        const uint64_t to = __shfl_sync(0xffffffffu, mine, r);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * (16 * CH) + ((j ^ (r % 8 * CH / 8)) << 4));
+        if (to)
+            *reinterpret_cast<uint4*>(to + 16 * j) = x;
+    }
 }
 
 // S (or dP) = A B^T: two K-major operands of 128 rows x D (a whole warp calls).

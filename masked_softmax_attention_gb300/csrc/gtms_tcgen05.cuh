@@ -405,6 +405,29 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Ask the hardware for a CTA of this grid that has not been launched yet, to be run
+// by this one in its place: 16 bytes arrive at `response`, signalled on the mbarrier
+// as transaction bytes. Once no CTA was left, it is not asked again.
+__device__ __forceinline__ void next_cta_request(uint32_t response, uint64_t* mbar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 :: "r"(response), "r"(smem_u32(mbar)) : "memory");
+}
+
+// The index (x) of the CTA that the response hands over, or -1.
+__device__ __forceinline__ int32_t next_cta_index(uint32_t response)
+{
+    int32_t x;
+    asm volatile("{\n.reg .b128 h;\n.reg .pred p;\n.reg .b32 a, b, c, d;\n"
+                 "ld.shared.b128 h, [%1];\n"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+                 "mov.b32 %0, -1;\n"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, h;\n"
+                 "@p mov.b32 %0, a;\n}\n"
+                 : "=r"(x) : "r"(response) : "memory");
+    return x;
+}
+
 // Nanoseconds of the GPU's global timer.
 __device__ __forceinline__ uint64_t globaltimer_ns()
 {
