@@ -64,8 +64,8 @@ struct AttentionArgs {
 #endif
 };
 
-// The backward's workspace: per query row, padded to whole tiles of 128, lse in
-// base 2 and D; then the partial maxima of the norms of dout and v.
+// The backward's workspace: per query row, padded to whole tiles of 128, -lse in
+// base 2 and -D; then the partial maxima of the norms of dout and v.
 constexpr int64_t kWorkspaceNorms = 2 * 1024;
 
 inline int64_t attention_padded_rows(int64_t B, int64_t Hq, int64_t Sq) { return B * Hq * ((Sq + 127) / 128 * 128); }

@@ -17,14 +17,17 @@
 
 namespace gtms {
 
-constexpr int kBwdGroups = 2;                            // warpgroups that share a tile's columns
-constexpr int kBwdWarps = 4 * kBwdGroups;                // element-wise warps
-constexpr int kBwdCols = kTile / kBwdGroups;             // columns of a tile per thread
-constexpr int kBwdMmaWarp = kBwdWarps, kBwdLoadWarp = kBwdWarps + 1, kBwdDealWarp = kBwdWarps + 2;
-constexpr uint32_t kBwdStage = 2048;                     // shared memory per element-wise warp for its results
-constexpr int kBwdThreads = 32 * (kBwdWarps + 4);
-constexpr int kBwdRegs = 168, kBwdElemRegs = 208, kBwdOtherRegs = 88;
-static_assert(kBwdGroups * kBwdElemRegs + kBwdOtherRegs <= (kBwdGroups + 1) * kBwdRegs, "register shares of one block");
+// The warpgroups that share a tile's columns, and the block around them.
+template <int D>
+struct BwdShape {
+    static constexpr int groups = D == 64 ? 4 : 2;
+    static constexpr int warps = 4 * groups, cols = kTile / groups;         // element-wise warps; columns of a thread
+    static constexpr int mma_warp = warps, load_warp = warps + 1, deal_warp = warps + 2;
+    static constexpr int threads = 32 * (warps + 4);
+    static constexpr int regs = groups == 4 ? 96 : 168, elem_regs = groups == 4 ? 104 : 208, other_regs = groups == 4 ? 64 : 88;
+    static_assert(groups * elem_regs + other_regs <= (groups + 1) * regs, "register shares of one block");
+    static constexpr uint32_t stage = 2048;                                 // shared memory per element-wise warp for its results
+};
 
 constexpr int kPrepThreads = 256, kPrepMaxBlocks = 1024;
 
@@ -45,77 +48,99 @@ __device__ __forceinline__ float gradient_factor(float do_norm, float v_norm)
     return exp2f(static_cast<float>(e));
 }
 
-// Per padded query row: lse log2(e) - kPShift (+inf where nothing is kept, which
-// makes every p of the row zero) and D. For fp16 also the largest norms of the
+// Per padded query row: kPShift - lse log2(e) (-inf where nothing is kept, which
+// makes every p of the row zero) and -D, so that both are added. For fp16 also the largest norms of the
 // live rows of do and of the live keys of v, one partial maximum per block.
-// D / 8 lanes hold a row.
+// A block takes 128 rows of one head at a time, D / 8 lanes to a row, and has the
+// loads of four rows in flight per thread.
 template <typename T, int D>
 __global__ void __launch_bounds__(kPrepThreads)
-gtms_attention_bwd_prep_kernel(const AttentionArgs a, int64_t rows, int64_t keys)
+gtms_attention_bwd_prep_kernel(const AttentionArgs a, int64_t row_tiles, int64_t key_tiles)
 {
-    constexpr int LANES = D / 8, PER = kPrepThreads / LANES;
+    constexpr int LANES = D / 8, PER = kPrepThreads / LANES, N = 4;
     constexpr bool norms = std::is_same<T, __half>::value;
-    const int sub = threadIdx.x % LANES;
+    const int sub = threadIdx.x % LANES, first = threadIdx.x / LANES;
     float do_norm = 0.0f, v_norm = 0.0f;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * PER;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * PER; base < rows; base += step) {
-        const int64_t w = base + threadIdx.x / LANES;
-        float dot = 0.0f, sq = 0.0f;
-        bool live = false;
-        int64_t bh = 0;
-        int32_t i = 0;
-        if (w < rows) {
-            bh = w / a.Sq_pad;
-            i = static_cast<int32_t>(w - bh * a.Sq_pad);
-            const int32_t b = static_cast<int32_t>(bh / a.Hq), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.Hq);
-            int32_t c0 = 0, c1 = 0;
-            if (i < a.Sq)
-                a.kept(a.offset(b) + i, a.length(b), c0, c1);
-            live = c0 < c1;
-            if (live) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.dout.row<T>(b, h, i)) + sub);
-                const uint4 y = __ldg(reinterpret_cast<const uint4*>(a.o.row<T>(b, h, i)) + sub);
-                const T* xe = reinterpret_cast<const T*>(&x);
-                const T* ye = reinterpret_cast<const T*>(&y);
+    const int32_t tiles_q = a.Sq_pad / kTile, tiles_k = (a.Skv + kTile - 1) / kTile;
+    for (int64_t w = blockIdx.x; w < row_tiles; w += gridDim.x) {
+        const int64_t bh = w / tiles_q;
+        const int32_t i0 = static_cast<int32_t>(w - bh * tiles_q) * kTile;
+        const int32_t b = static_cast<int32_t>(bh / a.Hq), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.Hq);
+        const int32_t off = a.offset(b), L = a.length(b);
+        const T* px = a.dout.row<T>(b, h, i0) + 8 * sub;
+        const T* py = a.o.row<T>(b, h, i0) + 8 * sub;
+        for (int32_t r0 = first; r0 < kTile; r0 += N * PER) {
+            uint4 x[N], y[N];
+            float lse[N];
+            bool live[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int32_t r = r0 + n * PER;
+                int32_t c0 = 0, c1 = 0;
+                if (i0 + r < a.Sq)
+                    a.kept(off + i0 + r, L, c0, c1);
+                live[n] = c0 < c1;
+                x[n] = y[n] = make_uint4(0, 0, 0, 0);
+                lse[n] = -INFINITY;
+                if (live[n]) {
+                    x[n] = __ldg(reinterpret_cast<const uint4*>(px + r * a.dout.ss));
+                    y[n] = __ldg(reinterpret_cast<const uint4*>(py + r * a.o.ss));
+                    if (sub == 0)
+                        lse[n] = kPShift<T> - __ldg(a.lse + bh * a.Sq + i0 + r) * kLog2e;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const T* xe = reinterpret_cast<const T*>(&x[n]);
+                const T* ye = reinterpret_cast<const T*>(&y[n]);
+                float dot = 0.0f, sq = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float f = static_cast<float>(xe[k]);
                     dot += f * static_cast<float>(ye[k]);
                     sq += f * f;
                 }
-            }
-        }
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (norms)
-                sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        }
-        do_norm = fmaxf(do_norm, sq);
-        if (sub == 0 && w < rows) {
-            a.delta[w] = dot;
-            a.lse2[w] = live ? a.lse[bh * a.Sq + i] * kLog2e - kPShift<T> : INFINITY;
+                for (int o = LANES / 2; o > 0; o >>= 1) {
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                    if (norms)
+                        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                }
+                do_norm = fmaxf(do_norm, sq);
+                if (sub == 0) {
+                    const int64_t at = bh * a.Sq_pad + i0 + r0 + n * PER;
+                    a.delta[at] = -dot;
+                    a.lse2[at] = lse[n];
+                }
+            }
         }
     }
     if constexpr (norms) {
-        for (int64_t base = static_cast<int64_t>(blockIdx.x) * PER; base < keys; base += step) {
-            const int64_t w = base + threadIdx.x / LANES;
-            float sq = 0.0f;
-            if (w < keys) {
-                const int64_t bg = w / a.Skv;
-                const int32_t c = static_cast<int32_t>(w - bg * a.Skv), b = static_cast<int32_t>(bg / a.Hkv);
-                if (c < a.length(b)) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.v.row<T>(b, bg - static_cast<int64_t>(b) * a.Hkv, c)) + sub);
-                    const T* xe = reinterpret_cast<const T*>(&x);
+        for (int64_t w = blockIdx.x; w < key_tiles; w += gridDim.x) {
+            const int64_t bg = w / tiles_k;
+            const int32_t c0 = static_cast<int32_t>(w - bg * tiles_k) * kTile, b = static_cast<int32_t>(bg / a.Hkv);
+            const int32_t L = a.length(b);
+            const T* pv = a.v.row<T>(b, bg - static_cast<int64_t>(b) * a.Hkv, c0) + 8 * sub;
+            for (int32_t r0 = first; r0 < kTile; r0 += N * PER) {
+                uint4 x[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int32_t r = r0 + n * PER;
+                    x[n] = c0 + r < L ? __ldg(reinterpret_cast<const uint4*>(pv + r * a.v.ss)) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const T* xe = reinterpret_cast<const T*>(&x[n]);
+                    float sq = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         sq += static_cast<float>(xe[k]) * static_cast<float>(xe[k]);
+#pragma unroll
+                    for (int o = LANES / 2; o > 0; o >>= 1)
+                        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    v_norm = fmaxf(v_norm, sq);
                 }
             }
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o >>= 1)
-                sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            v_norm = fmaxf(v_norm, sq);
         }
         __shared__ float part[2][kPrepThreads / 32];
         do_norm = team_max<32>(do_norm, nullptr);
@@ -152,6 +177,9 @@ __device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, f
     __syncthreads();
     return gradient_factor(shared2[0], shared2[1]);
 }
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[64]) { tc::tmem_ld64(taddr, v); }
 
 // A warp's 32 rows x COLS columns of an accumulator at `acc` (zeros where there is
 // none), scaled by f; the lanes' rows that are not live are zero. A zero comes out
@@ -191,7 +219,7 @@ struct DkvTile {
     static constexpr uint32_t off_k = 0, off_v = bytes, off_q = 2 * bytes, off_do = (2 + stages) * bytes;
     static constexpr uint32_t off_rows = (2 + 2 * stages) * bytes;           // per stage: 128 lse2, 128 D
     static constexpr uint32_t off_out = off_rows + stages * 2 * kTile * 4;
-    static constexpr uint32_t smem = off_out + kBwdWarps * kBwdStage + 1024;   // slack to align the base
+    static constexpr uint32_t smem = off_out + BwdShape<D>::warps * BwdShape<D>::stage + 1024;   // slack to align the base
 };
 
 struct DkvItem {
@@ -234,12 +262,13 @@ struct DkvShared {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(BwdShape<D>::threads, 1)
 gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
                           const __grid_constant__ AttentionArgs a, uint32_t heads, uint64_t wait_ns)
 {
     using TL = DkvTile<D>;
+    using SH = BwdShape<D>;
     constexpr int ST = TL::stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DkvShared sh;
@@ -254,13 +283,13 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                                  &sh.dofull[1], &sh.doempty[0], &sh.doempty[1]};
         for (uint64_t* m : one)
             tc::mbar_init(m, 1);
-        tc::mbar_init(&sh.pready, kBwdWarps);
-        tc::mbar_init(&sh.dsready, kBwdWarps);
-        tc::mbar_init(&sh.accempty, kBwdWarps);
-        init_items(sh.items, kBwdWarps + 2);   // load, MMA and element-wise warps
+        tc::mbar_init(&sh.pready, SH::warps);
+        tc::mbar_init(&sh.dsready, SH::warps);
+        tc::mbar_init(&sh.accempty, SH::warps);
+        init_items(sh.items, SH::warps + 2);   // load, MMA and element-wise warps
         sh.flag = 0;
     }
-    if (warp == kBwdMmaWarp) {
+    if (warp == SH::mma_warp) {
         __syncwarp();
         tc::tmem_alloc<512>(&sh.tmem_slot);
     }
@@ -270,15 +299,15 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_after_sync();
     const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + D;
 
-    if (warp >= kBwdMmaWarp) {
-        tc::regs_lower<kBwdOtherRegs>();
-        if (warp == kBwdDealWarp) {
+    if (warp >= SH::mma_warp) {
+        tc::regs_lower<SH::other_regs>();
+        if (warp == SH::deal_warp) {
             deal_items(sh.items, up, lane, [&](int32_t index) {
                 DkvItem it;
                 it.set(a, index, heads);
                 return it;
             });
-        } else if (warp == kBwdLoadWarp) {
+        } else if (warp == SH::load_warp) {
             uint32_t gq = 0, nk = 0, nraw = 0;
             uint32_t taken = 0;
             DkvItem it;
@@ -376,7 +405,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (nraw)
                     tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
-        } else if (warp == kBwdMmaWarp) {
+        } else if (warp == SH::mma_warp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
             uint32_t gq = 0, gt = 0, nk = 0, taken = 0;   // query tiles, element-wise hand-offs, items
             DkvItem it;
@@ -385,7 +414,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             auto accumulate = [&](uint32_t acc, uint32_t t_a, uint32_t rows, bool more) {
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks) {
-                    const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
+                    const uint32_t at = (ks * 16 / SH::cols) * SH::cols + (ks * 16 % SH::cols) / 2;
                     tc::mma_f16_ts_warp(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
                 }
             };
@@ -455,10 +484,10 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {
-        tc::regs_raise<kBwdElemRegs>();
+        tc::regs_raise<SH::elem_regs>();
         const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-        const uint32_t my_s = t_s + lanes + part * kBwdCols, my_dp = t_dp + lanes + part * kBwdCols;
+        const uint32_t my_s = t_s + lanes + part * SH::cols, my_dp = t_dp + lanes + part * SH::cols;
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
@@ -475,15 +504,15 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    const float* lse2 = reinterpret_cast<const float*>(smem + TL::off_rows + s * 2 * kTile * 4) + part * kBwdCols;
+                    const float* lse2 = reinterpret_cast<const float*>(smem + TL::off_rows + s * 2 * kTile * 4) + part * SH::cols;
                     const float* delta = lse2 + kTile;
-                    float p[kBwdCols];
-                    tc::tmem_ld64(my_s, p);
+                    float p[SH::cols];
+                    tmem_ld(my_s, p);
 #pragma unroll
-                    for (int j = 0; j < kBwdCols; j += 4) {
+                    for (int j = 0; j < SH::cols; j += 4) {
                         const float4 e = *reinterpret_cast<const float4*>(lse2 + j);
-                        const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, make_float2(-e.x, -e.y));
-                        const float2 y = __ffma2_rn(make_float2(p[j + 2], p[j + 3]), c2, make_float2(-e.z, -e.w));
+                        const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, make_float2(e.x, e.y));
+                        const float2 y = __ffma2_rn(make_float2(p[j + 2], p[j + 3]), c2, make_float2(e.z, e.w));
                         p[j] = exp2_approx(x.x);
                         p[j + 1] = exp2_approx(x.y);
                         p[j + 2] = exp2_approx(y.x);
@@ -493,14 +522,14 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (a.mask_kind != GTMS_MASK_LENGTH &&
                         (r0 < it.j * kTile + kTile - 1 ||
                          (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && r0 + kTile - 1 >= it.j * kTile + a.window))) {
-                        const int32_t k0 = key - r0 - part * kBwdCols;
+                        const int32_t k0 = key - r0 - part * SH::cols;
                         const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : kTile;
 #pragma unroll
-                        for (int j = 0; j < kBwdCols; ++j)
+                        for (int j = 0; j < SH::cols; ++j)
                             p[j] = j >= k0 && j < k1 ? p[j] : 0.0f;
                     }
 #pragma unroll
-                    for (int k = 0; k < kBwdCols; k += 32) {
+                    for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -516,17 +545,17 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    float ds[kBwdCols];
-                    tc::tmem_ld64(my_dp, ds);
+                    float ds[SH::cols];
+                    tmem_ld(my_dp, ds);
 #pragma unroll
-                    for (int k = 0; k < kBwdCols; k += 32) {
+                    for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const int at = k + 2 * j;
                             const float4 e = *reinterpret_cast<const float4*>(delta + at);
-                            float2 x = __fadd2_rn(make_float2(ds[at], ds[at + 1]), make_float2(-e.x, -e.y));
-                            float2 y = __fadd2_rn(make_float2(ds[at + 2], ds[at + 3]), make_float2(-e.z, -e.w));
+                            float2 x = __fadd2_rn(make_float2(ds[at], ds[at + 1]), make_float2(e.x, e.y));
+                            float2 y = __fadd2_rn(make_float2(ds[at + 2], ds[at + 3]), make_float2(e.z, e.w));
                             if (kPShift<T> != 0) {
                                 x = __fmul2_rn(x, make_float2(fk, fk));
                                 y = __fmul2_rn(y, make_float2(fk, fk));
@@ -547,9 +576,9 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             if (!ok)
                 break;
             // Half of the warpgroups write dV, the others dK: a row each, its share of the columns.
-            const bool is_dk = part >= kBwdGroups / 2;
-            constexpr int cols = D / (kBwdGroups / 2);
-            const int col0 = (part % (kBwdGroups / 2)) * cols;
+            const bool is_dk = part >= SH::groups / 2;
+            constexpr int cols = D / (SH::groups / 2);
+            const int col0 = (part % (SH::groups / 2)) * cols;
             T* out = key < a.Skv ? (is_dk ? a.dk : a.dv).row<T>(it.b, it.g, key) + col0 : nullptr;
             if (any) {
                 ok = up.warp_wait(&sh.accfull, nk & 1u);
@@ -559,7 +588,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 tc::fence_after_sync();
             }
             const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
-            write_rows<T, cols>(smem + TL::off_out + warp * kBwdStage, lane, (is_dk ? t_dk : t_dv) + lanes + col0, any,
+            write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, (is_dk ? t_dk : t_dv) + lanes + col0, any,
                                 key < it.L, f, out);
             if (any) {
                 tc::fence_before_sync();
@@ -573,7 +602,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kBwdMmaWarp) {
+    if (warp == SH::mma_warp) {
         __syncwarp();
         tc::tmem_free<512>(tmem);
     }
@@ -591,7 +620,7 @@ struct DqTile {
     static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
     static constexpr uint32_t off_q = 0, off_do = bytes, off_k = 2 * bytes, off_v = (2 + k_stages) * bytes;
     static constexpr uint32_t off_out = (2 + k_stages + v_stages) * bytes;
-    static constexpr uint32_t smem = off_out + kBwdWarps * kBwdStage + 1024;   // slack to align the base
+    static constexpr uint32_t smem = off_out + BwdShape<D>::warps * BwdShape<D>::stage + 1024;   // slack to align the base
 };
 
 struct DqItem {
@@ -631,12 +660,13 @@ struct DqShared {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(BwdShape<D>::threads, 1)
 gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                          const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
                          const __grid_constant__ AttentionArgs a, uint32_t heads, int32_t blocks, uint64_t wait_ns)
 {
     using TL = DqTile<D>;
+    using SH = BwdShape<D>;
     constexpr int KS = TL::k_stages, VS = TL::v_stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DqShared sh;
@@ -652,14 +682,14 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                                  &sh.vempty[1]};
         for (uint64_t* m : one)
             tc::mbar_init(m, 1);
-        tc::mbar_init(&sh.sempty[0], kBwdWarps);
-        tc::mbar_init(&sh.sempty[1], kBwdWarps);
-        tc::mbar_init(&sh.dsready, kBwdWarps);
-        tc::mbar_init(&sh.accempty, kBwdWarps);
-        init_items(sh.items, kBwdWarps + 2);   // load, MMA and element-wise warps
+        tc::mbar_init(&sh.sempty[0], SH::warps);
+        tc::mbar_init(&sh.sempty[1], SH::warps);
+        tc::mbar_init(&sh.dsready, SH::warps);
+        tc::mbar_init(&sh.accempty, SH::warps);
+        init_items(sh.items, SH::warps + 2);   // load, MMA and element-wise warps
         sh.flag = 0;
     }
-    if (warp == kBwdMmaWarp) {
+    if (warp == SH::mma_warp) {
         __syncwarp();
         tc::tmem_alloc<512>(&sh.tmem_slot);
     }
@@ -669,15 +699,15 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     tc::fence_after_sync();
     const uint32_t tmem = warp_value(sh.tmem_slot), t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
 
-    if (warp >= kBwdMmaWarp) {
-        tc::regs_lower<kBwdOtherRegs>();
-        if (warp == kBwdDealWarp) {
+    if (warp >= SH::mma_warp) {
+        tc::regs_lower<SH::other_regs>();
+        if (warp == SH::deal_warp) {
             deal_items(sh.items, up, lane, [&](int32_t index) {
                 DqItem it;
                 it.set(a, index, heads, blocks);
                 return it;
             });
-        } else if (warp == kBwdLoadWarp) {
+        } else if (warp == SH::load_warp) {
             uint32_t gk = 0, gv = 0, nq = 0, ndo = 0, nraw = 0, taken = 0;
             DqItem it;
             bool ok = true;
@@ -745,7 +775,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 if (nraw)
                     tc::mbar_wait(&sh.raw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
-        } else if (warp == kBwdMmaWarp) {
+        } else if (warp == SH::mma_warp) {
             constexpr uint32_t idesc_acc = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
             uint32_t g = 0, ni = 0, taken = 0;   // key tiles, items
             DqItem it;
@@ -794,7 +824,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     const uint32_t k0 = base + TL::off_k + (g % KS) * TL::bytes;
 #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks) {
-                        const uint32_t at = (ks * 16 / kBwdCols) * kBwdCols + (ks * 16 % kBwdCols) / 2;
+                        const uint32_t at = (ks * 16 / SH::cols) * SH::cols + (ks * 16 % SH::cols) / 2;
                         tc::mma_f16_ts_warp(t_dq, t_dp + at, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc, k > 0 || ks > 0);
                     }
                     tc::commit_warp(&sh.kempty[g % KS]);
@@ -811,10 +841,10 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {
-        tc::regs_raise<kBwdElemRegs>();
+        tc::regs_raise<SH::elem_regs>();
         const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-        const uint32_t my_dp = t_dp + lanes + part * kBwdCols;
+        const uint32_t my_dp = t_dp + lanes + part * SH::cols;
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
@@ -827,21 +857,21 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             a.kept(it.off + i, it.L, c0, c1);
             const bool live = c0 < c1 && i < a.Sq;
             const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq_pad + i;
-            const float neg_lse = -__ldg(a.lse2 + at), neg_delta = -__ldg(a.delta + at);
+            const float neg_lse = __ldg(a.lse2 + at), neg_delta = __ldg(a.delta + at);
             const float2 lse2 = make_float2(neg_lse, neg_lse), delta2 = make_float2(neg_delta, neg_delta);
             for (int32_t t = it.lo; t < it.hi; ++t, ++g) {
                 ok = up.warp_wait(&sh.sfull[g & 1u], (g >> 1) & 1u);
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                float p[kBwdCols];
-                tc::tmem_ld64(tmem + (g & 1u) * kTile + lanes + part * kBwdCols, p);
+                float p[SH::cols];
+                tmem_ld(tmem + (g & 1u) * kTile + lanes + part * SH::cols, p);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(&sh.sempty[g & 1u]);
 #pragma unroll
-                for (int j = 0; j < kBwdCols; j += 2) {
+                for (int j = 0; j < SH::cols; j += 2) {
                     const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, lse2);
                     p[j] = exp2_approx(x.x);
                     p[j + 1] = exp2_approx(x.y);
@@ -850,10 +880,10 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                float ds[kBwdCols];
-                tc::tmem_ld64(my_dp, ds);
+                float ds[SH::cols];
+                tmem_ld(my_dp, ds);
 #pragma unroll
-                for (int j = 0; j < kBwdCols; j += 2) {
+                for (int j = 0; j < SH::cols; j += 2) {
                     float2 x = __fadd2_rn(make_float2(ds[j], ds[j + 1]), delta2);
                     if (kPShift<T> != 0)
                         x = __fmul2_rn(x, make_float2(fk, fk));
@@ -862,13 +892,13 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     ds[j + 1] = x.y;
                 }
                 if (t * kTile < it.full0 || (t + 1) * kTile > it.full1) {
-                    const int32_t k0 = c0 - t * kTile - part * kBwdCols, k1 = c1 - t * kTile - part * kBwdCols;
+                    const int32_t k0 = c0 - t * kTile - part * SH::cols, k1 = c1 - t * kTile - part * SH::cols;
 #pragma unroll
-                    for (int j = 0; j < kBwdCols; ++j)
+                    for (int j = 0; j < SH::cols; ++j)
                         ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
                 }
 #pragma unroll
-                for (int k = 0; k < kBwdCols; k += 32) {
+                for (int k = 0; k < SH::cols; k += 32) {
                     uint32_t r[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -883,7 +913,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             }
             if (!ok)
                 break;
-            constexpr int cols = D / kBwdGroups;
+            constexpr int cols = D / SH::groups < 32 ? 32 : D / SH::groups;   // of dQ; some warpgroups have none
             T* out = i < a.Sq ? a.dq.row<T>(it.b, it.h, i) + part * cols : nullptr;
             const bool any = it.lo != it.hi;
             if (any) {
@@ -893,8 +923,9 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     break;
                 tc::fence_after_sync();
             }
-            write_rows<T, cols>(smem + TL::off_out + warp * kBwdStage, lane, t_dq + lanes + part * cols, any, live,
-                                a.scale / factor, out);
+            if (part * cols < D)
+                write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, t_dq + lanes + part * cols, any, live,
+                                    a.scale / factor, out);
             if (any) {
                 tc::fence_before_sync();
                 __syncwarp();
@@ -907,7 +938,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kBwdMmaWarp) {
+    if (warp == SH::mma_warp) {
         __syncwarp();
         tc::tmem_free<512>(tmem);
     }
@@ -931,12 +962,14 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     {
-        constexpr int per = kPrepThreads / (D / 8);
-        const int64_t n = heads * a.Sq_pad, m = std::is_same<T, __half>::value ? kv_heads * a.Skv : 0;
-        int64_t blocks = ((n > m ? n : m) + per - 1) / per;
-        blocks = blocks < 1 ? 1 : (blocks > kPrepMaxBlocks ? kPrepMaxBlocks : blocks);
+        constexpr bool norms = std::is_same<T, __half>::value;
+        const int64_t n = heads * (a.Sq_pad / kTile), m = norms ? kv_heads * ((a.Skv + kTile - 1) / kTile) : 0;
+        int64_t blocks = n > m ? n : m;
+        if (norms && blocks > kPrepMaxBlocks)
+            blocks = kPrepMaxBlocks;   // one partial maximum each
         a.norm_blocks = static_cast<int32_t>(blocks);
-        e = launch_kernel(gtms_attention_bwd_prep_kernel<T, D>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, a, n, m);
+        if (blocks > 0)
+            e = launch_kernel(gtms_attention_bwd_prep_kernel<T, D>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, a, n, m);
     }
     // One CTA per item; the running ones take over the others' (see ItemSlot).
     if (e == cudaSuccess && keys) {
@@ -944,7 +977,7 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         constexpr int smem = static_cast<int>(DkvTile<D>::smem);
         e = allow_smem<gtms_attention_dkv_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)), kBwdThreads, smem, st, mq,
+            e = launch_kernel(kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)), BwdShape<D>::threads, smem, st, mq,
                               mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
     }
     if (e == cudaSuccess && rows) {
@@ -953,7 +986,7 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         const int32_t blocks = a.Sq_pad / kTile;
         e = allow_smem<gtms_attention_dq_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(heads * blocks), kBwdThreads, smem, st, mq, mk, mv, mdo, a,
+            e = launch_kernel(kern, static_cast<unsigned>(heads * blocks), BwdShape<D>::threads, smem, st, mq, mk, mv, mdo, a,
                               static_cast<uint32_t>(heads), blocks, wait_ns);
     }
     return e;
