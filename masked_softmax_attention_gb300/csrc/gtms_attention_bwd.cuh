@@ -207,15 +207,28 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t ac
 // ---------------------------------------------------------------------------
 // dk, dv. Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T
 // and dS^T are in tensor memory as the A operands of dV += P^T dO and
-// dK += dS^T Q. Tensor memory: S^T, dP^T (128 columns each; P^T and dS^T, 16 bits,
-// over them, each warpgroup's part over its own scores), dV, dK (head_dim each).
-// While the element-wise warps form dS of one query tile the tensor cores run
-// dV of that tile and S of the next, and while they form P of the next, dK and dP.
+// dK += dS^T Q. Tensor memory: S^T, dP^T (128 columns each), P^T and dS^T (16
+// bits), dV, dK (head_dim each). At head dim 64 they all fit, and S and dP of the
+// next query tile are formed as soon as this one's have been read. At 128 P^T and
+// dS^T are written over S^T and dP^T, each warpgroup's part over its own scores:
+// while the element-wise warps form dS of one query tile the tensor cores run dV
+// of that tile and S of the next, and while they form P of the next, dK and dP.
 // ---------------------------------------------------------------------------
 template <int D>
 struct DkvTile {
-    static constexpr int stages = 2;
+    static constexpr int stages = D == 64 ? 4 : 2;
     static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
+    // Tensor memory columns. At head dim 64 there is room for P and dS beside the scores.
+    static constexpr bool roomy = D == 64;
+    static constexpr uint32_t t_s = 0, t_dp = kTile, t_p = roomy ? 2 * kTile : t_s, t_ds = roomy ? t_p + kTile / 2 : t_dp;
+    static constexpr uint32_t t_dv = roomy ? t_ds + kTile / 2 : 2 * kTile, t_dk = t_dv + D;
+    static_assert(t_dk + D <= 512, "tensor memory");
+    // First column of the 16-bit operand's columns k on: packed, or each warpgroup's over its own scores.
+    static constexpr uint32_t packed(int k)
+    {
+        constexpr int c = BwdShape<D>::cols;
+        return roomy ? k / 2 : k / c * c + k % c / 2;
+    }
     static constexpr uint32_t off_k = 0, off_v = bytes, off_q = 2 * bytes, off_do = (2 + stages) * bytes;
     static constexpr uint32_t off_rows = (2 + 2 * stages) * bytes;           // per stage: 128 lse2, 128 D
     static constexpr uint32_t off_out = off_rows + stages * 2 * kTile * 4;
@@ -253,8 +266,8 @@ struct DkvItem {
 
 struct DkvShared {
     uint64_t kfull, kempty, vfull, vempty;
-    uint64_t qfull[2], qempty[2], dofull[2], doempty[2], raw;
-    uint64_t sfull, pready, dpfull, dsready, accfull, accempty, mma_done;
+    uint64_t qfull[4], qempty[4], dofull[4], doempty[4], raw;
+    uint64_t sfull, sread, pready, dpfull, dpread, dsready, accfull, accempty, mma_done;
     ItemSlot<DkvItem> items;
     uint32_t tmem_slot;
     int flag;
@@ -279,10 +292,14 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 
     if (threadIdx.x == 0) {
         uint64_t* const one[] = {&sh.kfull, &sh.kempty, &sh.vfull, &sh.vempty, &sh.raw, &sh.sfull, &sh.dpfull, &sh.accfull,
-                                 &sh.mma_done, &sh.qfull[0], &sh.qfull[1], &sh.qempty[0], &sh.qempty[1], &sh.dofull[0],
-                                 &sh.dofull[1], &sh.doempty[0], &sh.doempty[1]};
+                                 &sh.mma_done};
         for (uint64_t* m : one)
             tc::mbar_init(m, 1);
+        for (int s = 0; s < ST; ++s)
+            for (uint64_t* m : {&sh.qfull[s], &sh.qempty[s], &sh.dofull[s], &sh.doempty[s]})
+                tc::mbar_init(m, 1);
+        tc::mbar_init(&sh.sread, SH::warps);
+        tc::mbar_init(&sh.dpread, SH::warps);
         tc::mbar_init(&sh.pready, SH::warps);
         tc::mbar_init(&sh.dsready, SH::warps);
         tc::mbar_init(&sh.accempty, SH::warps);
@@ -297,7 +314,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + D;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem + TL::t_s, t_dp = tmem + TL::t_dp, t_p = tmem + TL::t_p,
+                   t_ds = tmem + TL::t_ds, t_dv = tmem + TL::t_dv, t_dk = tmem + TL::t_dk;
 
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
@@ -410,13 +428,12 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             uint32_t gq = 0, gt = 0, nk = 0, taken = 0;   // query tiles, element-wise hand-offs, items
             DkvItem it;
             bool ok = true;
-            // acc += A B, A (16 bits, in tensor memory, a part of it per warpgroup) and B a tile of rows.
+            // acc += A B, A 16 bits in tensor memory and B a tile of rows.
             auto accumulate = [&](uint32_t acc, uint32_t t_a, uint32_t rows, bool more) {
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks) {
-                    const uint32_t at = (ks * 16 / SH::cols) * SH::cols + (ks * 16 % SH::cols) / 2;
-                    tc::mma_f16_ts_warp(acc, t_a + at, tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc, more || ks > 0);
-                }
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    tc::mma_f16_ts_warp(acc, t_a + TL::packed(16 * ks), tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc,
+                                        more || ks > 0);
             };
             while (take_item(sh.items, up, lane, taken, it, ok)) {
                 const int32_t n = warp_value((it.hi - it.lo) * a.group);
@@ -450,31 +467,47 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (ok && n == 1)
                     tc::commit_warp(&sh.vempty);
                 for (int32_t k = 0; k < n && ok; ++k, ++gq, ++gt) {
-                    ok = up.warp_wait(&sh.pready, gt & 1u);
+                    const bool next = k + 1 < n, last_next = k + 2 == n;
+                    auto next_scores = [&] {
+                        scores(gq + 1);
+                        if (ok && last_next)
+                            tc::commit_warp(&sh.kempty);
+                    };
+                    auto next_products = [&] {
+                        products(gq + 1);
+                        if (ok && last_next)
+                            tc::commit_warp(&sh.vempty);
+                    };
+                    if (TL::roomy && next) {   // the scores only have to have been read
+                        ok = up.warp_wait(&sh.sread, gt & 1u);
+                        if (ok)
+                            next_scores();
+                    }
+                    ok = ok && up.warp_wait(&sh.pready, gt & 1u);
                     if (ok && k == 0)
                         ok = up.warp_wait(&sh.accempty, (nk & 1u) ^ 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    accumulate(t_dv, t_s, base + TL::off_do + (gq % ST) * TL::bytes, k > 0);
+                    accumulate(t_dv, t_p, base + TL::off_do + (gq % ST) * TL::bytes, k > 0);
                     tc::commit_warp(&sh.doempty[gq % ST]);
-                    if (k + 1 < n) {
-                        scores(gq + 1);
-                        if (ok && k + 2 == n)
-                            tc::commit_warp(&sh.kempty);
+                    if (next) {
+                        if (TL::roomy) {
+                            ok = up.warp_wait(&sh.dpread, gt & 1u);
+                            if (ok)
+                                next_products();
+                        } else {               // P has gone: its columns take the next scores
+                            next_scores();
+                        }
                     }
-                    if (ok)
-                        ok = up.warp_wait(&sh.dsready, gt & 1u);
+                    ok = ok && up.warp_wait(&sh.dsready, gt & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    accumulate(t_dk, t_dp, base + TL::off_q + (gq % ST) * TL::bytes, k > 0);
+                    accumulate(t_dk, t_ds, base + TL::off_q + (gq % ST) * TL::bytes, k > 0);
                     tc::commit_warp(&sh.qempty[gq % ST]);
-                    if (k + 1 < n) {
-                        products(gq + 1);
-                        if (ok && k + 2 == n)
-                            tc::commit_warp(&sh.vempty);
-                    }
+                    if (!TL::roomy && next)
+                        next_products();
                 }
                 if (ok)
                     tc::commit_warp(&sh.accfull);
@@ -488,12 +521,26 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t my_s = t_s + lanes + part * SH::cols, my_dp = t_dp + lanes + part * SH::cols;
+        const uint32_t my_p = t_p + lanes + TL::packed(part * SH::cols), my_ds = t_ds + lanes + TL::packed(part * SH::cols);
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
         uint32_t gt = 0, nk = 0, taken = 0;
         DkvItem it;
         bool ok = true;
+        auto arrive = [&](uint64_t* bar) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(bar);
+        };
+        // Where P and dS stand beside the scores: their columns are free once the last tile's products are done,
+        // which its stage's release says too.
+        auto released = [&](uint64_t* empty) {
+            if (TL::roomy && gt > 0)
+                ok = up.warp_wait(&empty[(gt - 1) % ST], ((gt - 1) / ST) & 1u);
+            return ok;
+        };
         while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t key = it.j * kTile + row;
             const bool any = it.lo != it.hi;
@@ -508,6 +555,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     const float* delta = lse2 + kTile;
                     float p[SH::cols];
                     tmem_ld(my_s, p);
+                    if (TL::roomy)
+                        arrive(&sh.sread);
 #pragma unroll
                     for (int j = 0; j < SH::cols; j += 4) {
                         const float4 e = *reinterpret_cast<const float4*>(lse2 + j);
@@ -528,25 +577,28 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         for (int j = 0; j < SH::cols; ++j)
                             p[j] = j >= k0 && j < k1 ? p[j] : 0.0f;
                     }
+                    if (!released(sh.doempty))
+                        break;
 #pragma unroll
                     for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             r[j] = pack2<T>(p[k + 2 * j], p[k + 2 * j + 1]);
-                        tc::tmem_st16(my_s + k / 2, r);
+                        tc::tmem_st16(my_p + k / 2, r);
                     }
                     tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(&sh.pready);
+                    arrive(&sh.pready);
                     ok = up.warp_wait(&sh.dpfull, gt & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
                     float ds[SH::cols];
                     tmem_ld(my_dp, ds);
+                    if (TL::roomy)
+                        arrive(&sh.dpread);
+                    if (!released(sh.qempty))
+                        break;
 #pragma unroll
                     for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
@@ -565,13 +617,10 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             r[j] = pack2<T>(x.x, x.y);
                             r[j + 1] = pack2<T>(y.x, y.y);
                         }
-                        tc::tmem_st16(my_dp + k / 2, r);
+                        tc::tmem_st16(my_ds + k / 2, r);
                     }
                     tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(&sh.dsready);
+                    arrive(&sh.dsready);
                 }
             if (!ok)
                 break;
@@ -590,12 +639,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
             write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, (is_dk ? t_dk : t_dv) + lanes + col0, any,
                                 key < it.L, f, out);
-            if (any) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.accempty);
-            }
+            if (any)
+                arrive(&sh.accempty);
         }
     }
 
@@ -609,10 +654,10 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// dq. S = Q K^T twice buffered, dP = dO V^T (dS, 16 bits, over it, each
-// warpgroup's part over its own columns) and dQ in tensor memory. While the
-// element-wise warps form P of one key tile the tensor cores run dQ of the last,
-// dP of this one and S of the next.
+// dq. S = Q K^T, dP = dO V^T (128 columns of tensor memory each), dS (16 bits,
+// twice) and dQ. P never leaves the registers, so S and dP of the next key tile are
+// formed as soon as this one's have been read, and dQ of this one as soon as dS is
+// written.
 // ---------------------------------------------------------------------------
 template <int D>
 struct DqTile {
@@ -652,7 +697,7 @@ struct DqItem {
 struct DqShared {
     uint64_t qfull, qempty, dofull, doempty;
     uint64_t kfull[3], kempty[3], vfull[2], vempty[2], raw;
-    uint64_t sfull[2], sempty[2], dpfull, dsready, accfull, accempty, mma_done;
+    uint64_t sfull, sread, dpfull, dpread, dsready, accfull, accempty, mma_done;
     ItemSlot<DqItem> items;
     uint32_t tmem_slot;
     int flag;
@@ -676,14 +721,14 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     const GiveUp up{&sh.flag, a.status, wait_ns};
 
     if (threadIdx.x == 0) {
-        uint64_t* const one[] = {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull[0], &sh.sfull[1],
-                                 &sh.dpfull, &sh.accfull, &sh.mma_done, &sh.kfull[0], &sh.kfull[1], &sh.kfull[2],
+        uint64_t* const one[] = {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull, &sh.dpfull,
+                                  &sh.accfull, &sh.mma_done, &sh.kfull[0], &sh.kfull[1], &sh.kfull[2],
                                  &sh.kempty[0], &sh.kempty[1], &sh.kempty[2], &sh.vfull[0], &sh.vfull[1], &sh.vempty[0],
                                  &sh.vempty[1]};
         for (uint64_t* m : one)
             tc::mbar_init(m, 1);
-        tc::mbar_init(&sh.sempty[0], SH::warps);
-        tc::mbar_init(&sh.sempty[1], SH::warps);
+        tc::mbar_init(&sh.sread, SH::warps);
+        tc::mbar_init(&sh.dpread, SH::warps);
         tc::mbar_init(&sh.dsready, SH::warps);
         tc::mbar_init(&sh.accempty, SH::warps);
         init_items(sh.items, SH::warps + 2);   // load, MMA and element-wise warps
@@ -697,7 +742,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = warp_value(sh.tmem_slot), t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem, t_dp = tmem + kTile, t_ds = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
 
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
@@ -785,12 +830,12 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 if (n == 0)
                     continue;
                 auto scores = [&](uint32_t k, bool last) {
-                    ok = up.warp_wait(&sh.kfull[k % KS], (k / KS) & 1u) && up.warp_wait(&sh.sempty[k & 1u], ((k >> 1) & 1u) ^ 1u);
+                    ok = up.warp_wait(&sh.kfull[k % KS], (k / KS) & 1u);
                     if (!ok)
                         return;
                     tc::fence_after_sync();
-                    mma_abt<T, D>(tmem + (k & 1u) * kTile, base + TL::off_q, base + TL::off_k + (k % KS) * TL::bytes);
-                    tc::commit_warp(&sh.sfull[k & 1u]);
+                    mma_abt<T, D>(t_s, base + TL::off_q, base + TL::off_k + (k % KS) * TL::bytes);
+                    tc::commit_warp(&sh.sfull);
                     if (last)
                         tc::commit_warp(&sh.qempty);
                 };
@@ -812,26 +857,27 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     ok = up.warp_wait(&sh.dofull, ni & 1u);
                 if (ok)
                     products(g, n == 1);
-                if (ok && n > 1)
-                    scores(g + 1, n == 2);
                 for (int32_t k = 0; k < n && ok; ++k, ++g) {
-                    ok = up.warp_wait(&sh.dsready, g & 1u);
+                    if (k + 1 < n) {
+                        ok = up.warp_wait(&sh.sread, g & 1u);
+                        if (ok)
+                            scores(g + 1, k + 2 == n);
+                        ok = ok && up.warp_wait(&sh.dpread, g & 1u);
+                        if (ok)
+                            products(g + 1, k + 2 == n);
+                    }
+                    ok = ok && up.warp_wait(&sh.dsready, g & 1u);
                     if (ok && k == 0)
                         ok = up.warp_wait(&sh.accempty, (ni & 1u) ^ 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    const uint32_t k0 = base + TL::off_k + (g % KS) * TL::bytes;
+                    const uint32_t k0 = base + TL::off_k + (g % KS) * TL::bytes, ds = t_ds + (g & 1u) * (kTile / 2);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks) {
-                        const uint32_t at = (ks * 16 / SH::cols) * SH::cols + (ks * 16 % SH::cols) / 2;
-                        tc::mma_f16_ts_warp(t_dq, t_dp + at, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc, k > 0 || ks > 0);
-                    }
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        tc::mma_f16_ts_warp(t_dq, ds + ks * 8, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc,
+                                            k > 0 || ks > 0);
                     tc::commit_warp(&sh.kempty[g % KS]);
-                    if (k + 1 < n)
-                        products(g + 1, k + 2 == n);
-                    if (ok && k + 2 < n)
-                        scores(g + 2, k + 3 == n);
                 }
                 if (ok)
                     tc::commit_warp(&sh.accfull);
@@ -844,13 +890,20 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
         tc::regs_raise<SH::elem_regs>();
         const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-        const uint32_t my_dp = t_dp + lanes + part * SH::cols;
+        const uint32_t my_s = t_s + lanes + part * SH::cols, my_dp = t_dp + lanes + part * SH::cols;
+        const uint32_t my_ds = t_ds + lanes + part * (SH::cols / 2);
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
         uint32_t g = 0, ni = 0, taken = 0;
         DqItem it;
         bool ok = true;
+        auto arrive = [&](uint64_t* bar) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(bar);
+        };
         while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t i = it.i0 + row;
             int32_t c0, c1;
@@ -860,16 +913,13 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             const float neg_lse = __ldg(a.lse2 + at), neg_delta = __ldg(a.delta + at);
             const float2 lse2 = make_float2(neg_lse, neg_lse), delta2 = make_float2(neg_delta, neg_delta);
             for (int32_t t = it.lo; t < it.hi; ++t, ++g) {
-                ok = up.warp_wait(&sh.sfull[g & 1u], (g >> 1) & 1u);
+                ok = up.warp_wait(&sh.sfull, g & 1u);
                 if (!ok)
                     break;
                 tc::fence_after_sync();
                 float p[SH::cols];
-                tmem_ld(tmem + (g & 1u) * kTile + lanes + part * SH::cols, p);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.sempty[g & 1u]);
+                tmem_ld(my_s, p);
+                arrive(&sh.sread);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
                     const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, lse2);
@@ -882,6 +932,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 tc::fence_after_sync();
                 float ds[SH::cols];
                 tmem_ld(my_dp, ds);
+                arrive(&sh.dpread);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
                     float2 x = __fadd2_rn(make_float2(ds[j], ds[j + 1]), delta2);
@@ -897,19 +948,21 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     for (int j = 0; j < SH::cols; ++j)
                         ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
                 }
+                // The columns of dS are free once dQ of the tile before last is done, which its keys' release says too.
+                if (g > 1)
+                    ok = up.warp_wait(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u);
+                if (!ok)
+                    break;
 #pragma unroll
                 for (int k = 0; k < SH::cols; k += 32) {
                     uint32_t r[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         r[j] = pack2<T>(ds[k + 2 * j], ds[k + 2 * j + 1]);
-                    tc::tmem_st16(my_dp + k / 2, r);
+                    tc::tmem_st16(my_ds + (g & 1u) * (kTile / 2) + k / 2, r);
                 }
                 tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.dsready);
+                arrive(&sh.dsready);
             }
             if (!ok)
                 break;
@@ -926,12 +979,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             if (part * cols < D)
                 write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, t_dq + lanes + part * cols, any, live,
                                     a.scale / factor, out);
-            if (any) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.accempty);
-            }
+            if (any)
+                arrive(&sh.accempty);
         }
     }
 
