@@ -17,16 +17,25 @@
 
 namespace gtms {
 
-// The warpgroups that share a tile's columns, and the block around them.
+// Both kernels own 128 rows of one side and walk over the other side in inner tiles.
+// At head dim 128 the tensor cores bound them: inner tiles of 128, two warpgroups
+// on a tile's columns, one CTA per SM with all of the tensor memory. At 64 the
+// products take half as long and the element-wise chain of a tile (read the scores,
+// exponentiate, hand over, read dP, form dS, hand over) bounds them: inner tiles of
+// 64, one warpgroup, and two CTAs per SM, whose chains fill each other's gaps
+// ([32,16,2048,64] bf16: OLD us with one CTA per SM and 128 x 128 tiles, NEW so).
 template <int D>
 struct BwdShape {
-    static constexpr int groups = D == 64 ? 4 : 2;
-    static constexpr int warps = 4 * groups, cols = kTile / groups;         // element-wise warps; columns of a thread
+    static constexpr int inner = D == 64 ? 64 : 128, groups = inner / 64, ctas = D == 64 ? 2 : 1;
+    static constexpr int warps = 4 * groups, cols = 64;                     // element-wise warps; columns of a thread
     static constexpr int mma_warp = warps, load_warp = warps + 1, deal_warp = warps + 2;
     static constexpr int threads = 32 * (warps + 4);
-    static constexpr int regs = groups == 4 ? 96 : 168, elem_regs = groups == 4 ? 104 : 208, other_regs = groups == 4 ? 64 : 88;
+    static constexpr int regs = D == 64 ? 128 : 168, elem_regs = D == 64 ? 176 : 208, other_regs = D == 64 ? 80 : 88;
     static_assert(groups * elem_regs + other_regs <= (groups + 1) * regs, "register shares of one block");
+    static constexpr int tmem = 512 / ctas;
     static constexpr uint32_t stage = 2048;                                 // shared memory per element-wise warp for its results
+    static constexpr uint32_t bytes = kTile * D * 2, inner_bytes = inner * D * 2;   // a tile of the owned side, an inner tile
+    static constexpr uint32_t box = inner * 128;                            // 64 columns of an inner tile
 };
 
 constexpr int kPrepThreads = 256, kPrepMaxBlocks = 1024;
@@ -178,9 +187,6 @@ __device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, f
     return gradient_factor(shared2[0], shared2[1]);
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::tmem_ld32(taddr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[64]) { tc::tmem_ld64(taddr, v); }
-
 // A warp's 32 rows x COLS columns of an accumulator at `acc` (zeros where there is
 // none), scaled by f; the lanes' rows that are not live are zero. A zero comes out
 // as +0.0.
@@ -207,38 +213,31 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t ac
 // ---------------------------------------------------------------------------
 // dk, dv. Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T
 // and dS^T are in tensor memory as the A operands of dV += P^T dO and
-// dK += dS^T Q. Tensor memory: S^T, dP^T (128 columns each), P^T and dS^T (16
-// bits), dV, dK (head_dim each). At head dim 64 they all fit, and S and dP of the
-// next query tile are formed as soon as this one's have been read. At 128 P^T and
-// dS^T are written over S^T and dP^T, each warpgroup's part over its own scores:
-// while the element-wise warps form dS of one query tile the tensor cores run dV
-// of that tile and S of the next, and while they form P of the next, dK and dP.
+// dK += dS^T Q. Tensor memory: S^T, dP^T (P^T and dS^T, 16 bits, over them, each
+// warpgroup's part over its own scores), dV, dK (head_dim columns each). While the
+// element-wise warps form dS of one query tile the tensor cores run dV of that
+// tile and S of the next, and while they form P of the next, dK and dP.
 // ---------------------------------------------------------------------------
 template <int D>
 struct DkvTile {
+    using SH = BwdShape<D>;
     static constexpr int stages = D == 64 ? 4 : 2;
-    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
-    // Tensor memory columns. At head dim 64 there is room for P and dS beside the scores.
-    static constexpr bool roomy = D == 64;
-    static constexpr uint32_t t_s = 0, t_dp = kTile, t_p = roomy ? 2 * kTile : t_s, t_ds = roomy ? t_p + kTile / 2 : t_dp;
-    static constexpr uint32_t t_dv = roomy ? t_ds + kTile / 2 : 2 * kTile, t_dk = t_dv + D;
-    static_assert(t_dk + D <= 512, "tensor memory");
-    // First column of the 16-bit operand's columns k on: packed, or each warpgroup's over its own scores.
-    static constexpr uint32_t packed(int k)
-    {
-        constexpr int c = BwdShape<D>::cols;
-        return roomy ? k / 2 : k / c * c + k % c / 2;
-    }
-    static constexpr uint32_t off_k = 0, off_v = bytes, off_q = 2 * bytes, off_do = (2 + stages) * bytes;
-    static constexpr uint32_t off_rows = (2 + 2 * stages) * bytes;           // per stage: 128 lse2, 128 D
-    static constexpr uint32_t off_out = off_rows + stages * 2 * kTile * 4;
-    static constexpr uint32_t smem = off_out + BwdShape<D>::warps * BwdShape<D>::stage + 1024;   // slack to align the base
+    static constexpr uint32_t off_k = 0, off_v = SH::bytes, off_q = 2 * SH::bytes, off_do = off_q + stages * SH::inner_bytes;
+    static constexpr uint32_t off_rows = off_do + stages * SH::inner_bytes;   // per stage: lse2 and D of the inner rows
+    static constexpr uint32_t rows_bytes = 2 * SH::inner * 4;
+    static constexpr uint32_t off_out = off_rows + stages * rows_bytes;
+    static constexpr uint32_t smem = off_out + SH::warps * SH::stage + 1024;   // slack to align the base
+    // Tensor memory columns.
+    static constexpr uint32_t t_s = 0, t_dp = SH::inner, t_dv = 2 * SH::inner, t_dk = t_dv + D;
+    static_assert(t_dk + D <= SH::tmem, "tensor memory");
+    // First column of the 16-bit operand's columns k on: each warpgroup's part over its own scores.
+    static constexpr uint32_t packed(int k) { return k / SH::cols * SH::cols + k % SH::cols / 2; }
 };
 
 struct DkvItem {
-    int32_t b, g, j, off, L, lo, hi;   // key tile j of head g; query tiles [lo, hi)
+    int32_t b, g, j, off, L, lo, hi;   // key tile j of head g; inner query tiles [lo, hi)
 
-    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t inner)
     {
         // Under a causal mask the first key tiles are kept by the most rows.
         j = static_cast<int32_t>(item / heads);
@@ -258,8 +257,8 @@ struct DkvItem {
         ia = ia > 0 ? ia : 0;
         ib = ib < a.Sq - 1 ? ib : a.Sq - 1;
         if (ia <= ib) {
-            lo = ia / kTile;
-            hi = ib / kTile + 1;
+            lo = ia / inner;
+            hi = ib / inner + 1;
         }
     }
 };
@@ -267,7 +266,7 @@ struct DkvItem {
 struct DkvShared {
     uint64_t kfull, kempty, vfull, vempty;
     uint64_t qfull[4], qempty[4], dofull[4], doempty[4], raw;
-    uint64_t sfull, sread, pready, dpfull, dpread, dsready, accfull, accempty, mma_done;
+    uint64_t sfull, pready, dpfull, dsready, accfull, accempty, mma_done;
     ItemSlot<DkvItem> items;
     uint32_t tmem_slot;
     int flag;
@@ -275,7 +274,7 @@ struct DkvShared {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(BwdShape<D>::threads, 1)
+__global__ void __launch_bounds__(BwdShape<D>::threads, BwdShape<D>::ctas)
 gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
                           const __grid_constant__ AttentionArgs a, uint32_t heads, uint64_t wait_ns)
@@ -298,8 +297,6 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         for (int s = 0; s < ST; ++s)
             for (uint64_t* m : {&sh.qfull[s], &sh.qempty[s], &sh.dofull[s], &sh.doempty[s]})
                 tc::mbar_init(m, 1);
-        tc::mbar_init(&sh.sread, SH::warps);
-        tc::mbar_init(&sh.dpread, SH::warps);
         tc::mbar_init(&sh.pready, SH::warps);
         tc::mbar_init(&sh.dsready, SH::warps);
         tc::mbar_init(&sh.accempty, SH::warps);
@@ -308,21 +305,21 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     }
     if (warp == SH::mma_warp) {
         __syncwarp();
-        tc::tmem_alloc<512>(&sh.tmem_slot);
+        tc::tmem_alloc<SH::tmem>(&sh.tmem_slot);
     }
     const float factor = block_gradient_factor<T>(a, sh.norm);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem + TL::t_s, t_dp = tmem + TL::t_dp, t_p = tmem + TL::t_p,
-                   t_ds = tmem + TL::t_ds, t_dv = tmem + TL::t_dv, t_dk = tmem + TL::t_dk;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem + TL::t_s, t_dp = tmem + TL::t_dp, t_dv = tmem + TL::t_dv,
+                   t_dk = tmem + TL::t_dk;
 
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
         if (warp == SH::deal_warp) {
             deal_items(sh.items, up, lane, [&](int32_t index) {
                 DkvItem it;
-                it.set(a, index, heads);
+                it.set(a, index, heads, SH::inner);
                 return it;
             });
         } else if (warp == SH::load_warp) {
@@ -334,22 +331,22 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             while (take_item(sh.items, up, lane, taken, it, ok)) {
                 if (it.lo == it.hi)
                     continue;
-                // A 128-row tile of queries or output gradients; rows that keep nothing may hold
+                // An inner tile of queries or output gradients; rows that keep nothing may hold
                 // anything, and 0 x NaN is NaN: they are zeroed before the tensor cores see them.
                 auto rows = [&](const HeadsMap& m, uint32_t dst, int32_t i, int32_t h, uint64_t* full, uint32_t extra,
                                 uint32_t rows_dst, int64_t at) {
-                    const int32_t i0 = i * kTile;
-                    const int32_t n = a.Sq - i0 < kTile ? a.Sq - i0 : kTile;
+                    const int32_t i0 = i * SH::inner;
+                    const int32_t n = a.Sq - i0 < SH::inner ? a.Sq - i0 : SH::inner;
                     const int32_t za = -it.off - i0 > 0 ? -it.off - i0 : 0;
                     const int32_t zb = it.L - it.off - i0 < n ? it.L - it.off - i0 : n;
                     const bool patch = za > 0 || zb < n;
                     uint64_t* bar = patch ? &sh.raw : full;
                     if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(bar, TL::bytes + extra);
-                        load_tile<D, kTile>(base + dst, m, i0, h, it.b, bar);
+                        tc::mbar_arrive_expect_tx(bar, SH::inner_bytes + extra);
+                        load_tile<D, SH::inner>(base + dst, m, i0, h, it.b, bar);
                         if (extra) {
-                            tc::bulk_load_1d(base + rows_dst, a.lse2 + at, kTile * 4, bar);
-                            tc::bulk_load_1d(base + rows_dst + kTile * 4, a.delta + at, kTile * 4, bar);
+                            tc::bulk_load_1d(base + rows_dst, a.lse2 + at, extra / 2, bar);
+                            tc::bulk_load_1d(base + rows_dst + extra / 2, a.delta + at, extra / 2, bar);
                         }
                     }
                     if (patch) {
@@ -357,8 +354,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D>(smem + dst, 0, za, lane);
-                        zero_tile_rows<D>(smem + dst, zb, n, lane);
+                        zero_tile_rows<D, SH::inner>(smem + dst, 0, za, lane);
+                        zero_tile_rows<D, SH::inner>(smem + dst, zb, n, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -369,21 +366,21 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 for (int32_t h = it.g * a.group; h < (it.g + 1) * a.group && ok; ++h)
                     for (int32_t i = it.lo; i < it.hi && ok; ++i) {
                         const uint32_t s = gq % ST, ph = ((gq / ST) & 1u) ^ 1u;
-                        const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + h) * a.Sq_pad + i * kTile;
+                        const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + h) * a.Sq_pad + i * SH::inner;
                         if (first) {
                             ok = up.warp_wait(&sh.kempty, (nk & 1u) ^ 1u);
                             if (!ok)
                                 break;
                             if (lane == 0) {
-                                tc::mbar_arrive_expect_tx(&sh.kfull, TL::bytes);
-                                load_tile<D, kTile>(base + TL::off_k, mk, it.j * kTile, it.g, it.b, &sh.kfull);
+                                tc::mbar_arrive_expect_tx(&sh.kfull, SH::bytes);
+                                load_tile<D, kTile, SH::inner>(base + TL::off_k, mk, it.j * kTile, it.g, it.b, &sh.kfull);
                             }
                             issued_k = nk + 1;
                         }
                         ok = up.warp_wait(&sh.qempty[s], ph);
                         if (!ok)
                             break;
-                        rows(mq, TL::off_q + s * TL::bytes, i, h, &sh.qfull[s], 2 * kTile * 4, TL::off_rows + s * 2 * kTile * 4, at);
+                        rows(mq, TL::off_q + s * SH::inner_bytes, i, h, &sh.qfull[s], TL::rows_bytes, TL::off_rows + s * TL::rows_bytes, at);
                         if (!ok)
                             break;
                         issued_q = gq + 1;
@@ -392,8 +389,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             if (!ok)
                                 break;
                             if (lane == 0) {
-                                tc::mbar_arrive_expect_tx(&sh.vfull, TL::bytes);
-                                load_tile<D, kTile>(base + TL::off_v, mv, it.j * kTile, it.g, it.b, &sh.vfull);
+                                tc::mbar_arrive_expect_tx(&sh.vfull, SH::bytes);
+                                load_tile<D, kTile, SH::inner>(base + TL::off_v, mv, it.j * kTile, it.g, it.b, &sh.vfull);
                             }
                             issued_v = nk + 1;
                             first = false;
@@ -401,7 +398,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ok = up.warp_wait(&sh.doempty[s], ph);
                         if (!ok)
                             break;
-                        rows(mdo, TL::off_do + s * TL::bytes, i, h, &sh.dofull[s], 0, 0, 0);
+                        rows(mdo, TL::off_do + s * SH::inner_bytes, i, h, &sh.dofull[s], 0, 0, 0);
                         if (!ok)
                             break;
                         issued_do = gq + 1;
@@ -431,8 +428,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             // acc += A B, A 16 bits in tensor memory and B a tile of rows.
             auto accumulate = [&](uint32_t acc, uint32_t t_a, uint32_t rows, bool more) {
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    tc::mma_f16_ts_warp(acc, t_a + TL::packed(16 * ks), tc::smem_desc_sw128_mn(rows + ks * 2048, TL::box), idesc_acc,
+                for (int ks = 0; ks < SH::inner / 16; ++ks)
+                    tc::mma_f16_ts_warp(acc, t_a + TL::packed(16 * ks), tc::smem_desc_sw128_mn(rows + ks * 2048, SH::box), idesc_acc,
                                         more || ks > 0);
             };
             while (take_item(sh.items, up, lane, taken, it, ok)) {
@@ -444,7 +441,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (!ok)
                         return;
                     tc::fence_after_sync();
-                    mma_abt<T, D>(t_s, base + TL::off_k, base + TL::off_q + (q % ST) * TL::bytes);
+                    mma_abt<T, D, SH::inner>(t_s, base + TL::off_k, base + TL::off_q + (q % ST) * SH::inner_bytes);
                     tc::commit_warp(&sh.sfull);
                 };
                 auto products = [&](uint32_t q) {
@@ -452,7 +449,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (!ok)
                         return;
                     tc::fence_after_sync();
-                    mma_abt<T, D>(t_dp, base + TL::off_v, base + TL::off_do + (q % ST) * TL::bytes);
+                    mma_abt<T, D, SH::inner>(t_dp, base + TL::off_v, base + TL::off_do + (q % ST) * SH::inner_bytes);
                     tc::commit_warp(&sh.dpfull);
                 };
                 ok = up.warp_wait(&sh.kfull, nk & 1u);
@@ -478,35 +475,23 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         if (ok && last_next)
                             tc::commit_warp(&sh.vempty);
                     };
-                    if (TL::roomy && next) {   // the scores only have to have been read
-                        ok = up.warp_wait(&sh.sread, gt & 1u);
-                        if (ok)
-                            next_scores();
-                    }
                     ok = ok && up.warp_wait(&sh.pready, gt & 1u);
                     if (ok && k == 0)
                         ok = up.warp_wait(&sh.accempty, (nk & 1u) ^ 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    accumulate(t_dv, t_p, base + TL::off_do + (gq % ST) * TL::bytes, k > 0);
+                    accumulate(t_dv, t_s, base + TL::off_do + (gq % ST) * SH::inner_bytes, k > 0);
                     tc::commit_warp(&sh.doempty[gq % ST]);
-                    if (next) {
-                        if (TL::roomy) {
-                            ok = up.warp_wait(&sh.dpread, gt & 1u);
-                            if (ok)
-                                next_products();
-                        } else {               // P has gone: its columns take the next scores
-                            next_scores();
-                        }
-                    }
+                    if (next)   // P has gone: its columns take the next scores
+                        next_scores();
                     ok = ok && up.warp_wait(&sh.dsready, gt & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    accumulate(t_dk, t_ds, base + TL::off_q + (gq % ST) * TL::bytes, k > 0);
+                    accumulate(t_dk, t_dp, base + TL::off_q + (gq % ST) * SH::inner_bytes, k > 0);
                     tc::commit_warp(&sh.qempty[gq % ST]);
-                    if (!TL::roomy && next)
+                    if (next)
                         next_products();
                 }
                 if (ok)
@@ -521,7 +506,6 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t my_s = t_s + lanes + part * SH::cols, my_dp = t_dp + lanes + part * SH::cols;
-        const uint32_t my_p = t_p + lanes + TL::packed(part * SH::cols), my_ds = t_ds + lanes + TL::packed(part * SH::cols);
         const float c = a.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         const float fk = factor * exp2f(static_cast<float>(-kPShift<T>));
@@ -534,29 +518,21 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             if (lane == 0)
                 tc::mbar_arrive(bar);
         };
-        // Where P and dS stand beside the scores: their columns are free once the last tile's products are done,
-        // which its stage's release says too.
-        auto released = [&](uint64_t* empty) {
-            if (TL::roomy && gt > 0)
-                ok = up.warp_wait(&empty[(gt - 1) % ST], ((gt - 1) / ST) & 1u);
-            return ok;
-        };
         while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t key = it.j * kTile + row;
             const bool any = it.lo != it.hi;
             for (int32_t h = 0; h < (any ? a.group : 0) && ok; ++h)
                 for (int32_t i = it.lo; i < it.hi; ++i, ++gt) {
                     const uint32_t s = gt % ST;
-                    ok = up.warp_wait(&sh.qfull[s], (gt / ST) & 1u) && up.warp_wait(&sh.sfull, gt & 1u);
+                    // S says that the queries' tile has arrived, and lse2 and D with it on the same barrier.
+                    ok = up.warp_wait(&sh.sfull, gt & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    const float* lse2 = reinterpret_cast<const float*>(smem + TL::off_rows + s * 2 * kTile * 4) + part * SH::cols;
-                    const float* delta = lse2 + kTile;
+                    const float* lse2 = reinterpret_cast<const float*>(smem + TL::off_rows + s * TL::rows_bytes) + part * SH::cols;
+                    const float* delta = lse2 + SH::inner;
                     float p[SH::cols];
-                    tmem_ld(my_s, p);
-                    if (TL::roomy)
-                        arrive(&sh.sread);
+                    tc::tmem_ld64(my_s, p);
 #pragma unroll
                     for (int j = 0; j < SH::cols; j += 4) {
                         const float4 e = *reinterpret_cast<const float4*>(lse2 + j);
@@ -567,25 +543,23 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         p[j + 2] = exp2_approx(y.x);
                         p[j + 3] = exp2_approx(y.y);
                     }
-                    const int32_t r0 = it.off + i * kTile;   // the tile's first position
+                    const int32_t r0 = it.off + i * SH::inner;   // the tile's first position
                     if (a.mask_kind != GTMS_MASK_LENGTH &&
                         (r0 < it.j * kTile + kTile - 1 ||
-                         (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && r0 + kTile - 1 >= it.j * kTile + a.window))) {
+                         (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && r0 + SH::inner - 1 >= it.j * kTile + a.window))) {
                         const int32_t k0 = key - r0 - part * SH::cols;
-                        const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : kTile;
+                        const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : SH::cols;
 #pragma unroll
                         for (int j = 0; j < SH::cols; ++j)
                             p[j] = j >= k0 && j < k1 ? p[j] : 0.0f;
                     }
-                    if (!released(sh.doempty))
-                        break;
 #pragma unroll
                     for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             r[j] = pack2<T>(p[k + 2 * j], p[k + 2 * j + 1]);
-                        tc::tmem_st16(my_p + k / 2, r);
+                        tc::tmem_st16(my_s + k / 2, r);
                     }
                     tc::tmem_wait_st();
                     arrive(&sh.pready);
@@ -594,11 +568,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         break;
                     tc::fence_after_sync();
                     float ds[SH::cols];
-                    tmem_ld(my_dp, ds);
-                    if (TL::roomy)
-                        arrive(&sh.dpread);
-                    if (!released(sh.qempty))
-                        break;
+                    tc::tmem_ld64(my_dp, ds);
 #pragma unroll
                     for (int k = 0; k < SH::cols; k += 32) {
                         uint32_t r[16];
@@ -617,18 +587,13 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             r[j] = pack2<T>(x.x, x.y);
                             r[j + 1] = pack2<T>(y.x, y.y);
                         }
-                        tc::tmem_st16(my_ds + k / 2, r);
+                        tc::tmem_st16(my_dp + k / 2, r);
                     }
                     tc::tmem_wait_st();
                     arrive(&sh.dsready);
                 }
             if (!ok)
                 break;
-            // Half of the warpgroups write dV, the others dK: a row each, its share of the columns.
-            const bool is_dk = part >= SH::groups / 2;
-            constexpr int cols = D / (SH::groups / 2);
-            const int col0 = (part % (SH::groups / 2)) * cols;
-            T* out = key < a.Skv ? (is_dk ? a.dk : a.dv).row<T>(it.b, it.g, key) + col0 : nullptr;
             if (any) {
                 ok = up.warp_wait(&sh.accfull, nk & 1u);
                 ++nk;
@@ -636,9 +601,14 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     break;
                 tc::fence_after_sync();
             }
-            const float f = is_dk ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>));
-            write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, (is_dk ? t_dk : t_dv) + lanes + col0, any,
-                                key < it.L, f, out);
+            // A row each of dV and of dK: two warpgroups take one of them each.
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
+                if (SH::groups == 1 || part == which) {
+                    T* out = key < a.Skv ? (which ? a.dk : a.dv).row<T>(it.b, it.g, key) : nullptr;
+                    write_rows<T, D>(smem + TL::off_out + warp * SH::stage, lane, (which ? t_dk : t_dv) + lanes, any,
+                                     key < it.L, which ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>)), out);
+                }
             if (any)
                 arrive(&sh.accempty);
         }
@@ -649,7 +619,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_after_sync();
     if (warp == SH::mma_warp) {
         __syncwarp();
-        tc::tmem_free<512>(tmem);
+        tc::tmem_free<SH::tmem>(tmem);
     }
 }
 
@@ -661,17 +631,20 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 // ---------------------------------------------------------------------------
 template <int D>
 struct DqTile {
-    static constexpr int k_stages = 3, v_stages = D == 64 ? 2 : 1;
-    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;
-    static constexpr uint32_t off_q = 0, off_do = bytes, off_k = 2 * bytes, off_v = (2 + k_stages) * bytes;
-    static constexpr uint32_t off_out = (2 + k_stages + v_stages) * bytes;
-    static constexpr uint32_t smem = off_out + BwdShape<D>::warps * BwdShape<D>::stage + 1024;   // slack to align the base
+    using SH = BwdShape<D>;
+    static constexpr int k_stages = D == 64 ? 4 : 3, v_stages = D == 64 ? 3 : 1;
+    static constexpr uint32_t off_q = 0, off_do = SH::bytes, off_k = 2 * SH::bytes, off_v = off_k + k_stages * SH::inner_bytes;
+    static constexpr uint32_t off_out = off_v + v_stages * SH::inner_bytes;
+    static constexpr uint32_t smem = off_out + SH::warps * SH::stage + 1024;   // slack to align the base
+    // Tensor memory columns; dS twice.
+    static constexpr uint32_t t_s = 0, t_dp = SH::inner, t_ds = 2 * SH::inner, t_dq = 3 * SH::inner;
+    static_assert(t_dq + D <= SH::tmem, "tensor memory");
 };
 
 struct DqItem {
     int32_t b, h, i0, off, L, lo, hi, full0, full1;
 
-    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks, int32_t inner)
     {
         const int32_t bh = static_cast<int32_t>(item % heads);
         i0 = (blocks - 1 - static_cast<int32_t>(item / heads)) * kTile;
@@ -686,8 +659,8 @@ struct DqItem {
             int32_t a0, a1, b0, b1;
             a.kept(ra, L, a0, a1);
             a.kept(rb, L, b0, b1);
-            lo = a0 / kTile;
-            hi = (b1 + kTile - 1) / kTile;
+            lo = a0 / inner;
+            hi = (b1 + inner - 1) / inner;
             full0 = b0;
             full1 = a1;
         }
@@ -696,7 +669,7 @@ struct DqItem {
 
 struct DqShared {
     uint64_t qfull, qempty, dofull, doempty;
-    uint64_t kfull[3], kempty[3], vfull[2], vempty[2], raw;
+    uint64_t kfull[4], kempty[4], vfull[3], vempty[3], raw;
     uint64_t sfull, sread, dpfull, dpread, dsready, accfull, accempty, mma_done;
     ItemSlot<DqItem> items;
     uint32_t tmem_slot;
@@ -705,7 +678,7 @@ struct DqShared {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(BwdShape<D>::threads, 1)
+__global__ void __launch_bounds__(BwdShape<D>::threads, BwdShape<D>::ctas)
 gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                          const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
                          const __grid_constant__ AttentionArgs a, uint32_t heads, int32_t blocks, uint64_t wait_ns)
@@ -721,12 +694,17 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     const GiveUp up{&sh.flag, a.status, wait_ns};
 
     if (threadIdx.x == 0) {
-        uint64_t* const one[] = {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull, &sh.dpfull,
-                                  &sh.accfull, &sh.mma_done, &sh.kfull[0], &sh.kfull[1], &sh.kfull[2],
-                                 &sh.kempty[0], &sh.kempty[1], &sh.kempty[2], &sh.vfull[0], &sh.vfull[1], &sh.vempty[0],
-                                 &sh.vempty[1]};
-        for (uint64_t* m : one)
+        for (uint64_t* m : {&sh.qfull, &sh.qempty, &sh.dofull, &sh.doempty, &sh.raw, &sh.sfull, &sh.dpfull, &sh.accfull,
+                            &sh.mma_done})
             tc::mbar_init(m, 1);
+        for (int s = 0; s < KS; ++s) {
+            tc::mbar_init(&sh.kfull[s], 1);
+            tc::mbar_init(&sh.kempty[s], 1);
+        }
+        for (int s = 0; s < VS; ++s) {
+            tc::mbar_init(&sh.vfull[s], 1);
+            tc::mbar_init(&sh.vempty[s], 1);
+        }
         tc::mbar_init(&sh.sread, SH::warps);
         tc::mbar_init(&sh.dpread, SH::warps);
         tc::mbar_init(&sh.dsready, SH::warps);
@@ -736,20 +714,21 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     }
     if (warp == SH::mma_warp) {
         __syncwarp();
-        tc::tmem_alloc<512>(&sh.tmem_slot);
+        tc::tmem_alloc<SH::tmem>(&sh.tmem_slot);
     }
     const float factor = block_gradient_factor<T>(a, sh.norm);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem, t_dp = tmem + kTile, t_ds = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;
+    const uint32_t tmem = warp_value(sh.tmem_slot), t_s = tmem + TL::t_s, t_dp = tmem + TL::t_dp, t_ds = tmem + TL::t_ds,
+                   t_dq = tmem + TL::t_dq;
 
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
         if (warp == SH::deal_warp) {
             deal_items(sh.items, up, lane, [&](int32_t index) {
                 DqItem it;
-                it.set(a, index, heads, blocks);
+                it.set(a, index, heads, blocks, SH::inner);
                 return it;
             });
         } else if (warp == SH::load_warp) {
@@ -765,8 +744,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     if (!ok)
                         return;
                     if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(full, TL::bytes);
-                        load_tile<D, kTile>(base + dst, m, it.i0, it.h, it.b, full);
+                        tc::mbar_arrive_expect_tx(full, SH::bytes);
+                        load_tile<D, kTile, SH::inner>(base + dst, m, it.i0, it.h, it.b, full);
                     }
                     ++count;
                 };
@@ -777,15 +756,15 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                         return;
                     uint64_t* bar = tail ? &sh.raw : full;
                     if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(bar, TL::bytes);
-                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, it.b, bar);
+                        tc::mbar_arrive_expect_tx(bar, SH::inner_bytes);
+                        load_tile<D, SH::inner>(base + dst, m, t * SH::inner, hk, it.b, bar);
                     }
                     if (tail) {   // keys behind the length meet a zero ds in dQ: they must be numbers
                         ok = up.warp_wait(&sh.raw, nraw & 1u);
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D>(smem + dst, it.L - t * kTile, kTile, lane);
+                        zero_tile_rows<D, SH::inner>(smem + dst, it.L - t * SH::inner, SH::inner, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -796,14 +775,14 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     if (t == it.lo)
                         queries(mq, TL::off_q, &sh.qfull, &sh.qempty, nq);
                     if (ok) {
-                        keys(mk, TL::off_k + (gk % KS) * TL::bytes, t, &sh.kfull[gk % KS], &sh.kempty[gk % KS], (gk / KS) & 1u,
-                             (t + 1) * kTile > it.L && it.L < a.Skv);
+                        keys(mk, TL::off_k + (gk % KS) * SH::inner_bytes, t, &sh.kfull[gk % KS], &sh.kempty[gk % KS], (gk / KS) & 1u,
+                             (t + 1) * SH::inner > it.L && it.L < a.Skv);
                         gk += ok;
                     }
                     if (ok && t == it.lo)
                         queries(mdo, TL::off_do, &sh.dofull, &sh.doempty, ndo);
                     if (ok) {
-                        keys(mv, TL::off_v + (gv % VS) * TL::bytes, t, &sh.vfull[gv % VS], &sh.vempty[gv % VS], (gv / VS) & 1u, false);
+                        keys(mv, TL::off_v + (gv % VS) * SH::inner_bytes, t, &sh.vfull[gv % VS], &sh.vempty[gv % VS], (gv / VS) & 1u, false);
                         gv += ok;
                     }
                 }
@@ -834,7 +813,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     if (!ok)
                         return;
                     tc::fence_after_sync();
-                    mma_abt<T, D>(t_s, base + TL::off_q, base + TL::off_k + (k % KS) * TL::bytes);
+                    mma_abt<T, D, SH::inner>(t_s, base + TL::off_q, base + TL::off_k + (k % KS) * SH::inner_bytes);
                     tc::commit_warp(&sh.sfull);
                     if (last)
                         tc::commit_warp(&sh.qempty);
@@ -844,7 +823,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     if (!ok)
                         return;
                     tc::fence_after_sync();
-                    mma_abt<T, D>(t_dp, base + TL::off_do, base + TL::off_v + (k % VS) * TL::bytes);
+                    mma_abt<T, D, SH::inner>(t_dp, base + TL::off_do, base + TL::off_v + (k % VS) * SH::inner_bytes);
                     tc::commit_warp(&sh.dpfull);
                     tc::commit_warp(&sh.vempty[k % VS]);
                     if (last)
@@ -872,10 +851,10 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     if (!ok)
                         break;
                     tc::fence_after_sync();
-                    const uint32_t k0 = base + TL::off_k + (g % KS) * TL::bytes, ds = t_ds + (g & 1u) * (kTile / 2);
+                    const uint32_t k0 = base + TL::off_k + (g % KS) * SH::inner_bytes, ds = t_ds + (g & 1u) * (SH::inner / 2);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        tc::mma_f16_ts_warp(t_dq, ds + ks * 8, tc::smem_desc_sw128_mn(k0 + ks * 2048, TL::box), idesc_acc,
+                    for (int ks = 0; ks < SH::inner / 16; ++ks)
+                        tc::mma_f16_ts_warp(t_dq, ds + ks * 8, tc::smem_desc_sw128_mn(k0 + ks * 2048, SH::box), idesc_acc,
                                             k > 0 || ks > 0);
                     tc::commit_warp(&sh.kempty[g % KS]);
                 }
@@ -918,7 +897,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     break;
                 tc::fence_after_sync();
                 float p[SH::cols];
-                tmem_ld(my_s, p);
+                tc::tmem_ld64(my_s, p);
                 arrive(&sh.sread);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
@@ -931,7 +910,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     break;
                 tc::fence_after_sync();
                 float ds[SH::cols];
-                tmem_ld(my_dp, ds);
+                tc::tmem_ld64(my_dp, ds);
                 arrive(&sh.dpread);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
@@ -942,8 +921,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     ds[j] = x.x;
                     ds[j + 1] = x.y;
                 }
-                if (t * kTile < it.full0 || (t + 1) * kTile > it.full1) {
-                    const int32_t k0 = c0 - t * kTile - part * SH::cols, k1 = c1 - t * kTile - part * SH::cols;
+                if (t * SH::inner < it.full0 || (t + 1) * SH::inner > it.full1) {
+                    const int32_t k0 = c0 - t * SH::inner - part * SH::cols, k1 = c1 - t * SH::inner - part * SH::cols;
 #pragma unroll
                     for (int j = 0; j < SH::cols; ++j)
                         ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
@@ -959,14 +938,14 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         r[j] = pack2<T>(ds[k + 2 * j], ds[k + 2 * j + 1]);
-                    tc::tmem_st16(my_ds + (g & 1u) * (kTile / 2) + k / 2, r);
+                    tc::tmem_st16(my_ds + (g & 1u) * (SH::inner / 2) + k / 2, r);
                 }
                 tc::tmem_wait_st();
                 arrive(&sh.dsready);
             }
             if (!ok)
                 break;
-            constexpr int cols = D / SH::groups < 32 ? 32 : D / SH::groups;   // of dQ; some warpgroups have none
+            constexpr int cols = D / SH::groups;
             T* out = i < a.Sq ? a.dq.row<T>(it.b, it.h, i) + part * cols : nullptr;
             const bool any = it.lo != it.hi;
             if (any) {
@@ -976,9 +955,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     break;
                 tc::fence_after_sync();
             }
-            if (part * cols < D)
-                write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, t_dq + lanes + part * cols, any, live,
-                                    a.scale / factor, out);
+            write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, t_dq + lanes + part * cols, any, live,
+                                a.scale / factor, out);
             if (any)
                 arrive(&sh.accempty);
         }
@@ -989,13 +967,14 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     tc::fence_after_sync();
     if (warp == SH::mma_warp) {
         __syncwarp();
-        tc::tmem_free<512>(tmem);
+        tc::tmem_free<SH::tmem>(tmem);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
 {
+    using SH = BwdShape<D>;
     AttentionArgs a = args;
     if (!bind_context())
         return cudaErrorUnknown;
@@ -1004,10 +983,10 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
     // stand in for them in the maps.
     const bool rows = a.Sq > 0, keys = a.Skv > 0;
     HeadsMap mq, mk, mv, mdo;
-    if (!encode_heads<T>(mq, rows ? a.q : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, kTile) ||
-        !encode_heads<T>(mdo, rows ? a.dout : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, kTile) ||
-        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
-        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile))
+    if (!encode_heads<T>(mq, rows ? a.q : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, SH::inner) ||
+        !encode_heads<T>(mdo, rows ? a.dout : a.k, a.B, a.Hq, rows ? a.Sq : 1, D, SH::inner) ||
+        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, SH::inner) ||
+        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, SH::inner))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     {

@@ -179,7 +179,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D>(smem + dst, it.L - t * kTile, kTile, lane);
+                        zero_tile_rows<D, kTile>(smem + dst, it.L - t * kTile, kTile, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -241,7 +241,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         tc::fence_after_sync();
                     }
                     const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
-                    mma_abt<T, D>(tmem + w * kTile, q0, k0);
+                    mma_abt<T, D, kTile>(tmem + w * kTile, q0, k0);
                     tc::commit_warp(&sh.sfull[w]);
                     if (t == it.lo[w])
                         tc::commit_warp(&sh.qempty[w]);

@@ -51,13 +51,16 @@ inline bool encode_heads(HeadsMap& m, const HeadsRef& t, int64_t B, int64_t H, i
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows row0 .. row0 + ROWS - 1 of head (h, b): D / 64 boxes of ROWS x 128 bytes.
-template <int D, int ROWS>
+// Rows row0 .. row0 + ROWS - 1 of head (h, b), as 64-column blocks of ROWS x 128
+// bytes; the map's boxes are BOX rows high.
+template <int D, int ROWS, int BOX = ROWS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const HeadsMap& m, int32_t row0, int32_t h, int32_t b, uint64_t* bar)
 {
 #pragma unroll
     for (int x = 0; x < D / 64; ++x)
-        tc::tma_load_4d(dst + x * ROWS * 128, &m.map, x * 64, row0, h * m.mh, b * m.mb, bar);
+#pragma unroll
+        for (int y = 0; y < ROWS; y += BOX)
+            tc::tma_load_4d(dst + (x * ROWS + y) * 128, &m.map, x * 64, row0 + y, h * m.mh, b * m.mb, bar);
 }
 
 // Every wait of these kernels is bounded: one that runs out raises the flag and
@@ -99,13 +102,13 @@ struct GiveUp {
     }
 };
 
-// Zeroes rows [from, to) of a swizzled 128-row tile of D / 64 boxes (a whole warp works).
-template <int D>
+// Zeroes rows [from, to) of a swizzled tile of ROWS rows (a whole warp works).
+template <int D, int ROWS>
 __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int32_t to, int lane)
 {
     for (int32_t x = 0; x < D / 64; ++x)
         for (int32_t i = from * 8 + lane; i < to * 8; i += 32)   // 16-byte chunks, 8 to a row
-            *reinterpret_cast<uint4*>(tile + x * kTile * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tile + x * ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // The value of lane 0, for the compiler a warp's one value.
@@ -209,15 +212,16 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
     }
 }
 
-// S (or dP) = A B^T: two K-major operands of 128 rows x D (a whole warp calls).
-template <typename T, int D>
+// S (or dP) = A B^T: K-major operands of 128 and N rows x D (a whole warp calls).
+template <typename T, int D, int N>
 __device__ __forceinline__ void mma_abt(uint32_t d, uint32_t a, uint32_t b)
 {
-    constexpr uint32_t idesc = tc::idesc_f16<T>(kTile, kTile);
+    constexpr uint32_t idesc = tc::idesc_f16<T>(kTile, N);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t at = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;   // 16 columns of a swizzled 64-column box
-        tc::mma_f16_warp(d, tc::smem_desc_sw128(a + at, 1024), tc::smem_desc_sw128(b + at, 1024), idesc, ks > 0);
+    for (int ks = 0; ks < D / 16; ++ks) {   // 16 columns of a swizzled 64-column block
+        const uint32_t at = (ks & 3) * 32;
+        tc::mma_f16_warp(d, tc::smem_desc_sw128(a + (ks >> 2) * (kTile * 128) + at, 1024),
+                         tc::smem_desc_sw128(b + (ks >> 2) * (N * 128) + at, 1024), idesc, ks > 0);
     }
 }
 
