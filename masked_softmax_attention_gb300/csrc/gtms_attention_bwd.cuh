@@ -524,7 +524,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             for (int32_t h = 0; h < (any ? a.group : 0) && ok; ++h)
                 for (int32_t i = it.lo; i < it.hi; ++i, ++gt) {
                     const uint32_t s = gt % ST;
-                    // S says that the queries' tile has arrived, and lse2 and D with it on the same barrier.
+                    // S says that the queries' tile has arrived, and the rows' lse2 and D with it on the same barrier.
                     ok = up.warp_wait(&sh.sfull, gt & 1u);
                     if (!ok)
                         break;
@@ -533,6 +533,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     const float* delta = lse2 + SH::inner;
                     float p[SH::cols];
                     tc::tmem_ld64(my_s, p);
+                    const bool multiplied = up.ask(&sh.dpfull, gt & 1u);
 #pragma unroll
                     for (int j = 0; j < SH::cols; j += 4) {
                         const float4 e = *reinterpret_cast<const float4*>(lse2 + j);
@@ -563,7 +564,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     }
                     tc::tmem_wait_st();
                     arrive(&sh.pready);
-                    ok = up.warp_wait(&sh.dpfull, gt & 1u);
+                    ok = up.warp_wait(&sh.dpfull, gt & 1u, multiplied);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
@@ -891,27 +892,31 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq_pad + i;
             const float neg_lse = __ldg(a.lse2 + at), neg_delta = __ldg(a.delta + at);
             const float2 lse2 = make_float2(neg_lse, neg_lse), delta2 = make_float2(neg_delta, neg_delta);
+            bool scored = false;
             for (int32_t t = it.lo; t < it.hi; ++t, ++g) {
-                ok = up.warp_wait(&sh.sfull, g & 1u);
+                ok = up.warp_wait(&sh.sfull, g & 1u, scored);
                 if (!ok)
                     break;
                 tc::fence_after_sync();
                 float p[SH::cols];
                 tc::tmem_ld64(my_s, p);
                 arrive(&sh.sread);
+                const bool multiplied = up.ask(&sh.dpfull, g & 1u);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
                     const float2 x = __ffma2_rn(make_float2(p[j], p[j + 1]), c2, lse2);
                     p[j] = exp2_approx(x.x);
                     p[j + 1] = exp2_approx(x.y);
                 }
-                ok = up.warp_wait(&sh.dpfull, g & 1u);
+                ok = up.warp_wait(&sh.dpfull, g & 1u, multiplied);
                 if (!ok)
                     break;
                 tc::fence_after_sync();
                 float ds[SH::cols];
                 tc::tmem_ld64(my_dp, ds);
                 arrive(&sh.dpread);
+                // The columns of dS are free once dQ of the tile before last is done, which its keys' release says too.
+                const bool released = g < 2 || up.ask(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u);
 #pragma unroll
                 for (int j = 0; j < SH::cols; j += 2) {
                     float2 x = __fadd2_rn(make_float2(ds[j], ds[j + 1]), delta2);
@@ -927,9 +932,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     for (int j = 0; j < SH::cols; ++j)
                         ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
                 }
-                // The columns of dS are free once dQ of the tile before last is done, which its keys' release says too.
-                if (g > 1)
-                    ok = up.warp_wait(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u);
+                ok = up.warp_wait(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u, released);
                 if (!ok)
                     break;
 #pragma unroll
@@ -940,6 +943,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                         r[j] = pack2<T>(ds[k + 2 * j], ds[k + 2 * j + 1]);
                     tc::tmem_st16(my_ds + (g & 1u) * (SH::inner / 2) + k / 2, r);
                 }
+                scored = t + 1 < it.hi && up.ask(&sh.sfull, (g + 1) & 1u);
                 tc::tmem_wait_st();
                 arrive(&sh.dsready);
             }

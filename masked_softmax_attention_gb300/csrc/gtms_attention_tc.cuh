@@ -94,6 +94,15 @@ struct GiveUp {
             }
         }
     }
+    // Beside busy tensor cores shared memory answers slowly, and even a wait for a
+    // phase that has long completed stalls a warp for 100 to 200 cycles. So a phase
+    // that is expected to have completed is asked after ahead of the work that
+    // precedes its use, and only the answer is looked at there.
+    __device__ __forceinline__ bool ask(uint64_t* bar, uint32_t parity) const { return tc::mbar_test(bar, parity); }
+    __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool asked) const
+    {
+        return __all_sync(0xffffffffu, asked) || warp_wait(bar, parity);
+    }
     // All 32 lanes wait; the verdict is the warp's, so that warp-collective
     // instructions that follow stay converged.
     __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) const

@@ -444,6 +444,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* mbar, uint32_t parity)
     return done != 0;
 }
 
+// Whether the mbarrier's phase `parity` has completed, without waiting at all
+// (try_wait may suspend the thread for a while before it says no).
+__device__ __forceinline__ bool mbar_test(uint64_t* mbar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done) : "r"(smem_u32(mbar)), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // Wait until the mbarrier's phase `parity` has completed, giving up once
 // `limit_ns` nanoseconds of the global timer have passed since the first poll
 // failed (each poll may itself suspend the thread for a short, hardware-chosen
