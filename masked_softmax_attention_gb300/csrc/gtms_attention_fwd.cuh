@@ -333,17 +333,15 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     for (int j = 0; j < kTile; ++j)
                         s[j] *= pre;
                 }
-                if ((t + 1) * kTile > it.full1[w]) {
-                    const int32_t k1 = c1 - t * kTile;
+                if ((t + 1) * kTile > it.full1[w] || t * kTile < it.full0[w]) {
+                    const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j)
-                        s[j] = j < k1 ? s[j] : -INFINITY;
-                }
-                if (t * kTile < it.full0[w]) {
-                    const int32_t k0 = c0 - t * kTile;
+                    for (int k = 0; k < kTile; k += 32) {
+                        const uint32_t keep = bits_below(k1 - k) & ~bits_below(k0 - k);
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j)
-                        s[j] = j >= k0 ? s[j] : -INFINITY;
+                        for (int j = 0; j < 32; ++j)
+                            s[k + j] = keep & (1u << j) ? s[k + j] : -INFINITY;
+                    }
                 }
                 float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll

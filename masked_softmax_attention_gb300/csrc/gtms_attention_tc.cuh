@@ -249,6 +249,12 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The lowest n bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t bits_below(int32_t n)
+{
+    return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
+
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
