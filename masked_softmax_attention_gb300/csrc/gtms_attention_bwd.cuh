@@ -187,6 +187,18 @@ __device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, f
     return gradient_factor(shared2[0], shared2[1]);
 }
 
+// Zeroes what stands outside [k0, k1).
+__device__ __forceinline__ void keep_range(float (&v)[64], int32_t k0, int32_t k1)
+{
+#pragma unroll
+    for (int k = 0; k < 64; k += 32) {
+        const uint32_t keep = bits_below(k1 - k) & ~bits_below(k0 - k);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[k + j] = keep & (1u << j) ? v[k + j] : 0.0f;
+    }
+}
+
 // A warp's 32 rows x COLS columns of an accumulator at `acc` (zeros where there is
 // none), scaled by f; the lanes' rows that are not live are zero. A zero comes out
 // as +0.0.
@@ -545,14 +557,13 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         p[j + 3] = exp2_approx(y.y);
                     }
                     const int32_t r0 = it.off + i * SH::inner;   // the tile's first position
-                    if (a.mask_kind != GTMS_MASK_LENGTH &&
-                        (r0 < it.j * kTile + kTile - 1 ||
-                         (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && r0 + SH::inner - 1 >= it.j * kTile + a.window))) {
+                    if (__builtin_expect(a.mask_kind != GTMS_MASK_LENGTH &&
+                                             (r0 < it.j * kTile + kTile - 1 ||
+                                              (a.mask_kind == GTMS_MASK_SLIDING_WINDOW &&
+                                               r0 + SH::inner - 1 >= it.j * kTile + a.window)), 0)) {
                         const int32_t k0 = key - r0 - part * SH::cols;
                         const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : SH::cols;
-#pragma unroll
-                        for (int j = 0; j < SH::cols; ++j)
-                            p[j] = j >= k0 && j < k1 ? p[j] : 0.0f;
+                        keep_range(p, k0, k1);
                     }
 #pragma unroll
                     for (int k = 0; k < SH::cols; k += 32) {
@@ -926,12 +937,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                     ds[j] = x.x;
                     ds[j + 1] = x.y;
                 }
-                if (t * SH::inner < it.full0 || (t + 1) * SH::inner > it.full1) {
-                    const int32_t k0 = c0 - t * SH::inner - part * SH::cols, k1 = c1 - t * SH::inner - part * SH::cols;
-#pragma unroll
-                    for (int j = 0; j < SH::cols; ++j)
-                        ds[j] = j >= k0 && j < k1 ? ds[j] : 0.0f;
-                }
+                if (__builtin_expect(t * SH::inner < it.full0 || (t + 1) * SH::inner > it.full1, 0))
+                    keep_range(ds, c0 - t * SH::inner - part * SH::cols, c1 - t * SH::inner - part * SH::cols);
                 ok = up.warp_wait(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u, released);
                 if (!ok)
                     break;

@@ -328,12 +328,12 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 tc::fence_after_sync();
                 float s[kTile];
                 tc::tmem_ld128(ts, s);
-                if (pre != 1.0f) {
+                if (__builtin_expect(pre != 1.0f, 0)) {
 #pragma unroll
                     for (int j = 0; j < kTile; ++j)
                         s[j] *= pre;
                 }
-                if ((t + 1) * kTile > it.full1[w] || t * kTile < it.full0[w]) {
+                if (__builtin_expect((t + 1) * kTile > it.full1[w] || t * kTile < it.full0[w], 0)) {
                     const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
 #pragma unroll
                     for (int k = 0; k < kTile; k += 32) {
@@ -370,7 +370,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     exponentiate(32, shift, r1);
                 }
                 const bool raise = (top - m) * c > kRaiseLog2;   // a row's first kept tile: infinity
-                if (__any_sync(0xffffffffu, raise) || opening) {
+                if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
                     const float f = raise ? exp2_approx((m - top) * c) : 1.0f;
                     m = raise ? top : m;
                     l *= f;
