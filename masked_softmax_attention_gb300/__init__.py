@@ -226,13 +226,18 @@ def device_pointer_of_host(host_ptr: int) -> int:
 # Tensor API (torch provides device memory and the stream, nothing else).
 # ---------------------------------------------------------------------------
 
-def _dtype_code(t) -> int:
-    import torch
+_dtype_codes: dict = {}
 
-    codes = {torch.float32: GTMS_F32, torch.bfloat16: GTMS_BF16, torch.float16: GTMS_F16}
-    if t.dtype not in codes:
+
+def _dtype_code(t) -> int:
+    if not _dtype_codes:
+        import torch
+
+        _dtype_codes.update({torch.float32: GTMS_F32, torch.bfloat16: GTMS_BF16, torch.float16: GTMS_F16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}; expected float32, bfloat16 or float16")
-    return codes[t.dtype]
+    return code
 
 
 def _check_scores(name, t):
@@ -519,25 +524,31 @@ def _direct(name):
 
 def _heads(name, t, dtype, device):
     """Packed ``gtms_heads`` of a tensor, after the checks that only the tensor itself allows."""
-    if t.dim() != 4:
+    strides = t.stride()
+    if len(strides) != 4:
         raise ValueError(f"{name} must be [B, H, S, head_dim], got {tuple(t.shape)}")
     if t.get_device() != device or device < 0:
         raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be of the same dtype as the others")
-    sb, sh, ss, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
+    if strides[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _pack_heads(t.data_ptr(), sb, sh, ss)
+    return _pack_heads(t.data_ptr(), strides[0], strides[1], strides[2])
+
+
+_int32_dtype = None
 
 
 def _int32(name, t, shape, device):
     """Address of an optional contiguous int32 tensor."""
-    import torch
-
+    global _int32_dtype
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if _int32_dtype is None:
+        import torch
+
+        _int32_dtype = torch.int32
+    if t.dtype is not _int32_dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {tuple(shape)} on the same device")
     return t.data_ptr()
 
@@ -546,13 +557,14 @@ def _launch(fn, device, *args):
     """The call on the current stream of the tensors' device, made the current one where it is not already."""
     import torch
 
-    call, stream = _direct(fn), torch._C._cuda_getCurrentRawStream(device)
-    if torch._C._cuda_getDevice() == device:
+    call, c = _direct_calls.get(fn) or _direct(fn), torch._C
+    stream = c._cuda_getCurrentRawStream(device)
+    if c._cuda_getDevice() == device:
         rc = call(*args, stream)
     else:
         with torch.cuda.device(device):
             rc = call(*args, stream)
-    if rc != GTMS_OK:
+    if rc:
         raise GtmsError(fn, rc)
 
 
