@@ -34,29 +34,40 @@
 
 namespace gtms {
 
-constexpr int kFwdRows = 2 * kTile;                 // query rows of one work item
-constexpr int kFwdMmaWarp = 8, kFwdLoadWarp = 9, kFwdDealWarp = 10;   // warps 0..7 are the softmax warps
-constexpr int kFwdThreads = 32 * 12;                // one warp idle: register shares go by warpgroup
-// 168 registers a thread at launch (three warps to each SM quarter), shared out as
-// 208 for a softmax thread, which holds a row of 128 scores, and 88 for the rest.
-constexpr int kFwdRegs = 168, kFwdSoftmaxRegs = 208, kFwdOtherRegs = 88;
-static_assert(2 * kFwdSoftmaxRegs + kFwdOtherRegs <= 3 * kFwdRegs, "register shares of one block");
 constexpr float kRaiseLog2 = 12.0f;
 
-template <int D>
+// W query tiles of 128 rows to a CTA, key tiles of `inner`.
+//   W = 2, inner 128: head dim 128, whose accumulators and scores then fill the
+//     tensor memory; and head dim 64 where there are few rows (see launch).
+//   W = 4, inner 64: head dim 64, whose products take half as long, so that the
+//     softmax bounds it: twice the softmax warps, with half a row each, hide each
+//     other's latencies, and their loop is half as long to fetch
+//     ([32,16,2048,64] bf16: OLD us with W = 2, NEW us so).
+template <int D, int W>
 struct FwdTile {
+    static constexpr int inner = W == 4 ? 64 : 128, halves = inner / 64;   // P goes over 64 columns at a time
+    static constexpr int rows = W * kTile;                                 // query rows of one work item
+    static constexpr int mma_warp = 4 * W, load_warp = mma_warp + 1, deal_warp = mma_warp + 2;   // after the softmax warps
+    static constexpr int threads = 32 * (4 * W + 4);                       // one warp idle: register shares go by warpgroup
+    // Registers a thread at launch, shared out so that a softmax thread holds its row of scores.
+    static constexpr int regs = W == 4 ? 96 : 168, softmax_regs = W == 4 ? 104 : 208, other_regs = W == 4 ? 64 : 88;
+    static_assert(W * softmax_regs + other_regs <= (W + 1) * regs, "register shares of one block");
     static constexpr int stages = D == 64 ? 8 : 4;
-    static constexpr uint32_t bytes = kTile * D * 2;          // one 128-row tile
-    static constexpr uint32_t box = kTile * 128;              // one swizzled 64-column box of it
-    static constexpr uint32_t off_ring = 2 * bytes, off_out = (2 + stages) * bytes;
-    static constexpr uint32_t smem = off_out + 8 * 4096 + 1024;   // 4 KB per softmax warp; slack to align the base
+    static constexpr uint32_t q_bytes = kTile * D * 2, bytes = inner * D * 2;   // a query tile, a key tile
+    static constexpr uint32_t box = inner * 128;                                // 64 columns of a key tile
+    static constexpr uint32_t t_o = W * inner;                                  // tensor memory: S (and P), then O
+    static_assert(t_o + W * D <= 512, "tensor memory");
+    static constexpr uint32_t stage = W == 4 ? 2048 : 4096, out_cols = stage / 64;   // results: 32 rows x out_cols a time
+    static constexpr uint32_t off_ring = W * q_bytes, off_out = off_ring + stages * bytes;
+    static constexpr uint32_t smem = off_out + 4 * W * stage + 1024;            // slack to align the base
 };
 
-// Work item: 256 rows of one head, costliest row blocks first.
+// Work item: W query tiles of one head, costliest row blocks first.
+template <int W, int INNER>
 struct FwdItem {
     int32_t b, h, i0, off, L;
-    int32_t lo[2], hi[2];       // key tiles [lo, hi) of each query tile
-    int32_t full0[2], full1[2]; // columns [full0, full1) that every live row of the tile keeps
+    int32_t lo[W], hi[W];       // key tiles [lo, hi) of each query tile
+    int32_t full0[W], full1[W]; // columns [full0, full1) that every live row of the tile keeps
 
     __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks)
     {
@@ -64,11 +75,11 @@ struct FwdItem {
         const int32_t bh = static_cast<int32_t>(item % heads);
         b = bh / a.Hq;
         h = bh - b * a.Hq;
-        i0 = blk * kFwdRows;
+        i0 = blk * W * kTile;
         off = a.offset(b);
         L = a.length(b);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < W; ++w) {
             const int32_t i = i0 + w * kTile;
             const int32_t last = i + kTile < a.Sq ? i + kTile : a.Sq;
             const int32_t ra = off + i > 0 ? off + i : 0, rb = (off + last < L ? off + last : L) - 1;
@@ -78,55 +89,67 @@ struct FwdItem {
                 int32_t a0, a1, b0, b1;
                 a.kept(ra, L, a0, a1);
                 a.kept(rb, L, b0, b1);
-                lo[w] = a0 / kTile;
-                hi[w] = (b1 + kTile - 1) / kTile;
+                lo[w] = a0 / INNER;
+                hi[w] = (b1 + INNER - 1) / INNER;
                 full0[w] = b0;
                 full1[w] = a1;
             }
         }
     }
-    __device__ __forceinline__ int32_t top() const { return hi[0] > hi[1] ? hi[0] : hi[1]; }
+    __device__ __forceinline__ int32_t top() const
+    {
+        int32_t t = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            t = hi[w] > t ? hi[w] : t;
+        return t;
+    }
     __device__ __forceinline__ int32_t bottom() const
     {
-        if (hi[0] == 0)
-            return lo[1];
-        return hi[1] == 0 || lo[0] < lo[1] ? lo[0] : lo[1];
+        int32_t t = INT32_MAX;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            t = hi[w] > 0 && lo[w] < t ? lo[w] : t;
+        return t;
     }
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
 };
 
+template <int D, int W>
 struct FwdShared {
-    uint64_t qfull[2], qempty[2];
+    using TL = FwdTile<D, W>;
+    uint64_t qfull[W], qempty[W];
     uint64_t kvfull[8], kvempty[8], vraw;
-    uint64_t sfull[2], phalf[2], pready[2], ofull[2], oempty[2];
-    ItemSlot<FwdItem> items;
+    uint64_t sfull[W], pready[W][TL::halves], ofull[W], oempty[W];
+    ItemSlot<FwdItem<W, TL::inner>> items;
     uint64_t mma_done;
     uint32_t tmem_slot;
     int flag;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(FwdTile<D, W>::threads, 1)
 gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, uint32_t heads,
                           int32_t blocks, uint64_t wait_ns)
 {
-    using TL = FwdTile<D>;
+    using TL = FwdTile<D, W>;
+    using Item = FwdItem<W, TL::inner>;
     constexpr int ST = TL::stages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ FwdShared sh;
+    __shared__ FwdShared<D, W> sh;
     const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const GiveUp up{&sh.flag, a.status, wait_ns};
 
     if (threadIdx.x == 0) {
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < W; ++w) {
             tc::mbar_init(&sh.qfull[w], 1);
             tc::mbar_init(&sh.qempty[w], 1);
             tc::mbar_init(&sh.sfull[w], 1);
-            tc::mbar_init(&sh.phalf[w], 4);
-            tc::mbar_init(&sh.pready[w], 4);
+            for (int k = 0; k < TL::halves; ++k)
+                tc::mbar_init(&sh.pready[w][k], 4);
             tc::mbar_init(&sh.ofull[w], 1);
             tc::mbar_init(&sh.oempty[w], 4);
         }
@@ -136,10 +159,10 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         }
         tc::mbar_init(&sh.vraw, 1);
         tc::mbar_init(&sh.mma_done, 1);
-        init_items(sh.items, 10);   // load, MMA and softmax warps
+        init_items(sh.items, 4 * W + 2);   // load, MMA and softmax warps
         sh.flag = 0;
     }
-    if (warp == kFwdMmaWarp) {
+    if (warp == TL::mma_warp) {
         __syncwarp();
         tc::tmem_alloc<512>(&sh.tmem_slot);
     }
@@ -148,17 +171,17 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_after_sync();
     const uint32_t tmem = warp_value(sh.tmem_slot);
 
-    if (warp >= kFwdMmaWarp) {
-        tc::regs_lower<kFwdOtherRegs>();
-        if (warp == kFwdDealWarp) {
+    if (warp >= TL::mma_warp) {
+        tc::regs_lower<TL::other_regs>();
+        if (warp == TL::deal_warp) {
             deal_items(sh.items, up, lane, [&](int32_t index) {
-                FwdItem it;
+                Item it;
                 it.set(a, index, heads, blocks);
                 return it;
             });
-        } else if (warp == kFwdLoadWarp) {
-            uint32_t g = 0, nq[2] = {0, 0}, nraw = 0, taken = 0;
-            FwdItem it;
+        } else if (warp == TL::load_warp) {
+            uint32_t g = 0, asked = 0, odd = 0, nraw = 0, taken = 0;   // bits w: queries loaded at all, an odd number of times
+            Item it;
             bool ok = true;
             while (take_item(sh.items, up, lane, taken, it, ok)) {
                 const int32_t hk = it.h / a.group;
@@ -171,7 +194,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     uint64_t* bar = tail ? &sh.vraw : &sh.kvfull[s];
                     if (lane == 0) {
                         tc::mbar_arrive_expect_tx(bar, TL::bytes);
-                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, it.b, bar);
+                        load_tile<D, TL::inner>(base + dst, m, t * TL::inner, hk, it.b, bar);
                     }
                     if (tail) {
                         // Keys behind the length may hold anything, and 0 x NaN is NaN: zero their rows of V.
@@ -179,7 +202,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D, kTile>(smem + dst, it.L - t * kTile, kTile, lane);
+                        zero_tile_rows<D, TL::inner>(smem + dst, it.L - t * TL::inner, TL::inner, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -188,43 +211,48 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     ++g;
                 };
                 auto queries = [&](int w) {
-                    ok = up.warp_wait(&sh.qempty[w], (nq[w] & 1u) ^ 1u);
-                    if (ok && lane == 0) {
-                        tc::mbar_arrive_expect_tx(&sh.qfull[w], TL::bytes);
-                        load_tile<D, kTile>(base + w * TL::bytes, mq, it.i0 + w * kTile, it.h, it.b, &sh.qfull[w]);
+                    ok = up.warp_wait(&sh.qempty[w], ((odd >> w) & 1u) ^ 1u);
+                    if (!ok)
+                        return;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&sh.qfull[w], TL::q_bytes);
+                        load_tile<D, kTile, TL::inner>(base + w * TL::q_bytes, mq, it.i0 + w * kTile, it.h, it.b, &sh.qfull[w]);
                     }
-                    nq[w] += ok;
+                    odd ^= 1u << w;
+                    asked |= 1u << w;
                 };
-                bool loaded[2] = {it.hi[0] == 0, it.hi[1] == 0};
+                uint32_t loaded = 0;
                 for (int32_t t = it.top() - 1; t >= it.bottom() && ok; --t) {
-                    for (int w = 0; w < 2 && ok; ++w)
-                        if (!loaded[w] && it.has(w, t)) {
-                            loaded[w] = true;
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        if (ok && !(loaded & (1u << w)) && it.has(w, t)) {
+                            loaded |= 1u << w;
                             queries(w);
                         }
                     if (ok)
                         tile(mk, t, false);
                     if (ok)
-                        tile(mv, t, (t + 1) * kTile > it.L && it.L < a.Skv);
+                        tile(mv, t, (t + 1) * TL::inner > it.L && it.L < a.Skv);
                 }
             }
             if (!ok) {   // let the copies already issued land before the CTA can exit
                 for (uint32_t k = 0; k < static_cast<uint32_t>(ST) && k < g; ++k)
                     tc::mbar_wait(&sh.kvfull[(g - 1 - k) % ST], ((g - 1 - k) / ST) & 1u, kAttnDrainWaitNs);
-                for (int w = 0; w < 2; ++w)
-                    if (nq[w])
-                        tc::mbar_wait(&sh.qfull[w], (nq[w] - 1) & 1u, kAttnDrainWaitNs);
+                for (int w = 0; w < W; ++w)
+                    if (asked & (1u << w))
+                        tc::mbar_wait(&sh.qfull[w], ((odd >> w) & 1u) ^ 1u, kAttnDrainWaitNs);
                 if (nraw)
                     tc::mbar_wait(&sh.vraw, (nraw - 1) & 1u, kAttnDrainWaitNs);
             }
-        } else if (warp == kFwdMmaWarp) {
+        } else if (warp == TL::mma_warp) {
             constexpr uint32_t idesc_o = tc::idesc_f16<T>(kTile, D) | tc::kIdescBMnMajor;
-            uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, taken = 0;
-            FwdItem it;
+            // n counts key tiles; bits w: parities of the queries, the hand-overs of P and the outputs of tile w.
+            uint32_t n = 0, nq = 0, np = 0, no = 0, taken = 0;
+            Item it;
             bool ok = true;
             while (take_item(sh.items, up, lane, taken, it, ok)) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
+                for (int w = 0; w < W; ++w) {
                     it.lo[w] = warp_value(it.lo[w]);
                     it.hi[w] = warp_value(it.hi[w]);
                 }
@@ -234,14 +262,14 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 // S_w of tile t, whose K is ring entry 2 n' (its arrival has been waited for).
                 auto scores = [&](int w, int32_t t, uint32_t tile_n) {
                     if (t == it.hi[w] - 1) {
-                        ok = up.warp_wait(&sh.qfull[w], nq[w] & 1u);
-                        ++nq[w];
+                        ok = up.warp_wait(&sh.qfull[w], (nq >> w) & 1u);
+                        nq ^= 1u << w;
                         if (!ok)
                             return;
                         tc::fence_after_sync();
                     }
-                    const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
-                    mma_abt<T, D, kTile>(tmem + w * kTile, q0, k0);
+                    const uint32_t q0 = base + w * TL::q_bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
+                    mma_abt<T, D, TL::inner>(tmem + w * TL::inner, q0, k0);
                     tc::commit_warp(&sh.sfull[w]);
                     if (t == it.lo[w])
                         tc::commit_warp(&sh.qempty[w]);
@@ -250,22 +278,22 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     const bool first = t == it.hi[w] - 1;
                     const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = up.warp_wait(half ? &sh.pready[w] : &sh.phalf[w], np[w] & 1u);
+                    for (int half = 0; half < TL::halves; ++half) {
+                        ok = up.warp_wait(&sh.pready[w][half], (np >> w) & 1u);
                         if (ok && first && half == 0)
-                            ok = up.warp_wait(&sh.oempty[w], (no[w] & 1u) ^ 1u);
+                            ok = up.warp_wait(&sh.oempty[w], ((no >> w) & 1u) ^ 1u);
                         if (!ok)
                             return;
                         tc::fence_after_sync();
 #pragma unroll
-                        for (int ks = half * (kTile / 32); ks < (half + 1) * (kTile / 32); ++ks)
-                            tc::mma_f16_ts_warp(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
+                        for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                            tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * TL::inner + ks * 8,
                                                 tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
                     }
-                    ++np[w];
+                    np ^= 1u << w;
                     if (t == it.lo[w]) {
                         tc::commit_warp(&sh.ofull[w]);
-                        ++no[w];
+                        no ^= 1u << w;
                     }
                 };
                 auto arrived = [&](uint32_t e) {
@@ -274,8 +302,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 };
                 arrived(2 * n);
 #pragma unroll
-                for (int w = 0; w < 2 && ok; ++w)
-                    if (it.has(w, top - 1))
+                for (int w = 0; w < W; ++w)
+                    if (ok && it.has(w, top - 1))
                         scores(w, top - 1, n);
                 if (!ok)
                     break;
@@ -286,7 +314,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (ok && t > bottom)
                         arrived(2 * n + 2);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
+                    for (int w = 0; w < W; ++w) {
                         if (ok && it.has(w, t))
                             output(w, t);
                         if (ok && it.has(w, t - 1))
@@ -304,39 +332,47 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
         }
     } else {
-        tc::regs_raise<kFwdSoftmaxRegs>();
+        tc::regs_raise<TL::softmax_regs>();
         const int w = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 tensor-memory lanes per warp, lane in bits 16..
-        const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + 2 * kTile + w * D;
+        const uint32_t ts = tmem + lanes + w * TL::inner, to = tmem + lanes + TL::t_o + w * D;
         // exp(scale x) = exp2(c x) with c > 0: a negative scale flips the scores, a zero one clears them.
         const float c = a.scale == 0.0f ? kLog2e : fabsf(a.scale) * kLog2e;
         const float pre = a.scale > 0.0f ? 1.0f : (a.scale < 0.0f ? -1.0f : 0.0f);
         uint32_t ns = 0, no = 0, taken = 0;
-        FwdItem it;
         bool ok = true;
-        while (take_item(sh.items, up, lane, taken, it, ok)) {
-            const int32_t i = it.i0 + w * kTile + (warp & 3) * 32 + lane;
-            int32_t c0, c1;
+        int32_t b = 0, h = 0, i = 0, c0 = 0, c1 = 0, lo = 0, hi = 0, full0 = 0, full1 = 0;
+        auto read = [&](const Item& it) {
+            b = it.b;
+            h = it.h;
+            i = it.i0 + w * kTile + (warp & 3) * 32 + lane;
             a.kept(it.off + i, it.L, c0, c1);
+            lo = it.lo[w];
+            hi = it.hi[w];
+            full0 = it.full0[w];
+            full1 = it.full1[w];
+        };
+        while (take_item(sh.items, up, lane, taken, ok, read)) {
             const bool live = c0 < c1 && i < a.Sq;
             float m = -INFINITY, l = 0.0f;
-            for (int32_t t = it.hi[w] - 1; t >= it.lo[w]; --t) {
+            for (int32_t t = hi - 1; t >= lo; --t) {
                 ok = up.warp_wait(&sh.sfull[w], ns & 1u);
                 ++ns;
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                float s[kTile];
-                tc::tmem_ld128(ts, s);
+                constexpr int N = TL::inner;
+                float s[N];
+                tmem_ld(ts, s);
                 if (__builtin_expect(pre != 1.0f, 0)) {
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j)
+                    for (int j = 0; j < N; ++j)
                         s[j] *= pre;
                 }
-                if (__builtin_expect((t + 1) * kTile > it.full1[w] || t * kTile < it.full0[w], 0)) {
-                    const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
+                if (__builtin_expect((t + 1) * N > full1 || t * N < full0, 0)) {
+                    const int32_t k0 = c0 - t * N, k1 = c1 - t * N;
 #pragma unroll
-                    for (int k = 0; k < kTile; k += 32) {
+                    for (int k = 0; k < N; k += 32) {
                         const uint32_t keep = bits_below(k1 - k) & ~bits_below(k0 - k);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -345,10 +381,10 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 }
                 float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int j = 4; j < kTile; j += 8)
+                for (int j = 4; j < N; j += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] = j + 4 + k < kTile ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
+                        x[k] = j + 4 + k < N ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % N]) : fmaxf(x[k], s[j + k]);
                 const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, rounded to 16 bits.
@@ -362,35 +398,26 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         r[j] = pack2<T>(e.x, e.y);
                     }
                 };
-                float shift = m == -INFINITY ? 0.0f : -m * c;
-                uint32_t r0[16], r1[16];
-                const bool opening = t == it.hi[w] - 1;
-                if (!opening) {
-                    exponentiate(0, shift, r0);
-                    exponentiate(32, shift, r1);
-                }
+                const bool opening = t == hi - 1;   // nothing to rescale yet
                 const bool raise = (top - m) * c > kRaiseLog2;   // a row's first kept tile: infinity
-                if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
+                auto raised = [&] {
                     const float f = raise ? exp2_approx((m - top) * c) : 1.0f;
                     m = raise ? top : m;
                     l *= f;
                     if (!opening) {
 #pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            float o[32];
-                            uint32_t r[32];
-                            tc::tmem_ld32(to + k, o);
+                        for (int k = 0; k < D; k += 16) {
+                            float o[16];
+                            uint32_t r[16];
+                            tc::tmem_ld16(to + k, o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < 16; ++j)
                                 r[j] = __float_as_uint(o[j] * f);
-                            tc::tmem_st32(to + k, r);
+                            tc::tmem_st16(to + k, r);
                         }
                     }
-                    shift = m == -INFINITY ? 0.0f : -m * c;
-                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                    exponentiate(0, shift, r0);
-                    exponentiate(32, shift, r1);
-                }
+                };
+                auto shift_of = [&] { return m == -INFINITY ? 0.0f : -m * c; };
                 auto hand_over = [&](uint64_t* bar) {
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
@@ -398,22 +425,49 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (lane == 0)
                         tc::mbar_arrive(bar);
                 };
-                tc::tmem_st16(ts, r0);
-                tc::tmem_st16(ts + 16, r1);
-                hand_over(&sh.phalf[w]);
-                exponentiate(64, shift, r0);
-                tc::tmem_st16(ts + 32, r0);
-                exponentiate(96, shift, r1);
-                tc::tmem_st16(ts + 48, r1);
-                hand_over(&sh.pready[w]);
+                uint32_t r0[16];
+                if constexpr (TL::halves == 2) {
+                    // Two warps to a scheduler: the first half is exponentiated while the maximum is found, and
+                    // again where that raises it.
+                    uint32_t r1[16];
+                    if (!opening) {
+                        exponentiate(0, shift_of(), r0);
+                        exponentiate(32, shift_of(), r1);
+                    }
+                    if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
+                        raised();
+                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                        exponentiate(0, shift_of(), r0);
+                        exponentiate(32, shift_of(), r1);
+                    }
+                    const float shift = shift_of();
+                    tc::tmem_st16(ts, r0);
+                    tc::tmem_st16(ts + 16, r1);
+                    hand_over(&sh.pready[w][0]);
+                    exponentiate(64, shift, r0);
+                    tc::tmem_st16(ts + 32, r0);
+                    exponentiate(96, shift, r1);
+                    tc::tmem_st16(ts + 48, r1);
+                    hand_over(&sh.pready[w][1]);
+                } else {
+                    // Four warps to a scheduler hide the maximum's latency, and have no registers for more.
+                    if (__builtin_expect(__any_sync(0xffffffffu, raise), 0))
+                        raised();
+                    const float shift = shift_of();
+                    exponentiate(0, shift, r0);
+                    tc::tmem_st16(ts, r0);
+                    exponentiate(32, shift, r0);
+                    tc::tmem_st16(ts + 16, r0);
+                    hand_over(&sh.pready[w][0]);
+                }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok)
                 break;
-            T* out = i < a.Sq ? a.o.row<T>(it.b, it.h, i) : nullptr;
-            uint8_t* stage = smem + TL::off_out + warp * 4096;
+            T* out = i < a.Sq ? a.o.row<T>(b, h, i) : nullptr;
+            uint8_t* stage = smem + TL::off_out + warp * TL::stage;
             const float inv = live ? 1.0f / l : 0.0f;
-            const bool any = it.hi[w] > it.lo[w];
+            const bool any = hi > lo;
             if (any) {
                 ok = up.warp_wait(&sh.ofull[w], no & 1u);
                 ++no;
@@ -421,20 +475,21 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     break;
                 tc::fence_after_sync();
             }
+            constexpr int OC = TL::out_cols;
 #pragma unroll 1
-            for (int k = 0; k < D; k += 64) {
-                uint32_t r[32];
+            for (int k = 0; k < D; k += OC) {
+                uint32_t r[OC / 2];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < OC / 2; ++j)
                     r[j] = 0;
                 if (any) {
-                    float o[64];
-                    tc::tmem_ld64(to + k, o);
+                    float o[OC];
+                    tmem_ld(to + k, o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < OC / 2; ++j)
                         r[j] = live ? pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
                 }
-                store_rows<64>(stage, lane, r, out ? out + k : nullptr);
+                store_rows<OC>(stage, lane, r, out ? out + k : nullptr);
             }
             if (any) {
                 tc::fence_before_sync();
@@ -443,7 +498,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     tc::mbar_arrive(&sh.oempty[w]);
             }
             if (a.lse && i < a.Sq)
-                a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq + i] =
+                a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + i] =
                     live ? (a.scale == 0.0f ? m : m * fabsf(a.scale)) + logf(l) : -INFINITY;
         }
     }
@@ -451,10 +506,31 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kFwdMmaWarp) {
+    if (warp == TL::mma_warp) {
         __syncwarp();
         tc::tmem_free<512>(tmem);
     }
+}
+
+template <typename T, int D, int W>
+cudaError_t launch_attention_fwd_w(const AttentionArgs& a, cudaStream_t st, uint64_t wait_ns)
+{
+    using TL = FwdTile<D, W>;
+    // Without keys no tile is loaded, and q stands in for k and v in the maps.
+    const bool keys = a.Skv > 0;
+    HeadsMap mq, mk, mv;
+    if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, TL::inner) ||
+        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, TL::inner) ||
+        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, TL::inner))
+        return cudaErrorInvalidValue;
+    constexpr int smem = static_cast<int>(TL::smem);
+    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D, W>>(smem);
+    if (e != cudaSuccess)
+        return e;
+    const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
+    return launch_kernel(gtms_attention_fwd_kernel<T, D, W>, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk,
+                         mv, a, static_cast<uint32_t>(heads), blocks, wait_ns);
 }
 
 template <typename T, int D>
@@ -462,22 +538,13 @@ cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uin
 {
     if (!bind_context())
         return cudaErrorUnknown;
-    // Without keys no tile is loaded, and q stands in for k and v in the maps.
-    const bool keys = a.Skv > 0;
-    HeadsMap mq, mk, mv;
-    if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, kTile) ||
-        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
-        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile))
-        return cudaErrorInvalidValue;
-    auto* kern = gtms_attention_fwd_kernel<T, D>;
-    constexpr int smem = static_cast<int>(FwdTile<D>::smem);
-    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D>>(smem);
-    if (e != cudaSuccess)
-        return e;
-    const int32_t blocks = (a.Sq + kFwdRows - 1) / kFwdRows;
-    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, items = heads * blocks;
-    return launch_kernel(kern, static_cast<unsigned>(items), kFwdThreads, smem, st, mq, mk, mv, a, static_cast<uint32_t>(heads),
-                         blocks, wait_ns);
+    if constexpr (D == 64) {
+        // Blocks of 512 rows where that still makes two items for every multiprocessor.
+        const int64_t items = static_cast<int64_t>(a.B) * a.Hq * ((a.Sq + 4 * kTile - 1) / (4 * kTile));
+        if (items >= 2 * device_sms())
+            return launch_attention_fwd_w<T, D, 4>(a, st, wait_ns);
+    }
+    return launch_attention_fwd_w<T, D, 2>(a, st, wait_ns);
 }
 
 }  // namespace gtms

@@ -180,19 +180,27 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
     }
 }
 
-// The next item, for a reading warp (n counts its items); false at the end of the deal or where a role gave up.
-template <typename Item>
-__device__ __forceinline__ bool take_item(ItemSlot<Item>& s, const GiveUp& up, int lane, uint32_t& n, Item& it, bool& ok)
+// The next item, for a reading warp (n counts its items), handed to read() while it
+// stands in shared memory; false at the end of the deal or where a role gave up.
+template <typename Item, typename Read>
+__device__ __forceinline__ bool take_item(ItemSlot<Item>& s, const GiveUp& up, int lane, uint32_t& n, bool& ok, Read read)
 {
     ok = ok && up.warp_wait(&s.full, n & 1u);
     if (!ok)
         return false;
-    it = s.item;
+    const bool more = s.item.b >= 0;
+    if (more)
+        read(s.item);
     __syncwarp();
     if (lane == 0)
         tc::mbar_arrive(&s.empty);
     ++n;
-    return it.b >= 0;
+    return more;
+}
+template <typename Item>
+__device__ __forceinline__ bool take_item(ItemSlot<Item>& s, const GiveUp& up, int lane, uint32_t& n, Item& it, bool& ok)
+{
+    return take_item(s, up, lane, n, ok, [&](const Item& x) { it = x; });
 }
 
 // A warp's 32 rows x COLS columns of results, 16 bits each, through shared memory
@@ -220,6 +228,10 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
             *reinterpret_cast<uint4*>(to + 16 * j) = x;
     }
 }
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[64]) { tc::tmem_ld64(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[128]) { tc::tmem_ld128(taddr, v); }
 
 // S (or dP) = A B^T: K-major operands of 128 and N rows x D (a whole warp calls).
 template <typename T, int D, int N>
