@@ -340,7 +340,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             DkvItem it;
             uint32_t issued_q = 0, issued_do = 0, issued_k = 0, issued_v = 0;
             bool ok = true;
-            while (take_item(sh.items, up, lane, taken, it, ok)) {
+            while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
                 if (it.lo == it.hi)
                     continue;
                 // An inner tile of queries or output gradients; rows that keep nothing may hold
@@ -747,7 +747,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             uint32_t gk = 0, gv = 0, nq = 0, ndo = 0, nraw = 0, taken = 0;
             DqItem it;
             bool ok = true;
-            while (take_item(sh.items, up, lane, taken, it, ok)) {
+            while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
                 if (it.lo == it.hi)
                     continue;
                 const int32_t hk = it.h / a.group;

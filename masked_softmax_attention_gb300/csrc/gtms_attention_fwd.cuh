@@ -3,20 +3,19 @@
 //   s_ic = scale q_i . k_c,  o_i = sum_c exp(s_ic - m_i) v_c / l_i,
 //   l_i = sum_c exp(s_ic - m_i),  lse_i = m_i + log l_i   over the kept c.
 //
-// A CTA, one per SM, works on 256 query rows at a time, as two tiles of
-// 128, and walks over the 128-key tiles that hold kept entries, last first (so
-// that the tiles a causal mask cuts come first and the maximum settles early).
-// Scores, probabilities and both output accumulators stay in tensor memory:
-//   columns 0..255    S of tile 0 and 1 (fp32); P, rounded to 16 bits, is written
-//                     over the first half of its own S;
-//   columns 256..511  O of tile 0 and 1 (fp32, head_dim columns each).
+// A CTA works on one or two tiles of 128 query rows (see FwdTile) and walks over the
+// 128-key tiles that hold kept entries, last first (so that the tiles a causal mask
+// cuts come first and the maximum settles early). Scores, probabilities and the
+// output accumulators stay in tensor memory: S of each query tile (128 fp32
+// columns; P, rounded to 16 bits, is written over the first half of it), then O
+// (head_dim fp32 columns each).
 // Roles:
 //   deal (1 warp)     the work items (see ItemSlot);
 //   load (1 warp)     TMA: the query tiles, then K and V tiles into one ring;
 //   MMA (1 warp)      S_w = Q_w K^T and O_w += P_w V with P_w read from tensor
 //                     memory. The two tiles alternate, so one's products run while
 //                     the other's softmax does;
-//   softmax (2 x 4 warps) a thread owns one row: it reads its 128 scores, so the
+//   softmax (4 warps a tile) a thread owns one row: it reads its 128 scores, so the
 //                     maximum and the sum need no exchange, writes P back, and at
 //                     the end divides O and stores it.
 // The running maximum is only raised, and O and l rescaled, when a tile exceeds it
@@ -36,34 +35,33 @@ namespace gtms {
 
 constexpr float kRaiseLog2 = 12.0f;
 
-// W query tiles of 128 rows to a CTA, key tiles of `inner`.
-//   W = 2, inner 128: head dim 128, whose accumulators and scores then fill the
-//     tensor memory; and head dim 64 where there are few rows (see launch).
-//   W = 4, inner 64: head dim 64, whose products take half as long, so that the
-//     softmax bounds it: twice the softmax warps, with half a row each, hide each
-//     other's latencies, and their loop is half as long to fetch
-//     ([32,16,2048,64] bf16: OLD us with W = 2, NEW us so).
-template <int D, int W>
+// Query tiles (W) of a CTA and CTAs of a multiprocessor: two tiles work side by side
+// on each. At head dim 128 they share a CTA, and so the keys and values in shared
+// memory, which their tiles fill, as their scores and outputs fill the tensor
+// memory. At 64 there is room for two CTAs of one tile, which run into each
+// other's starts and ends of items and have an MMA warp each ([32,16,2048,64] bf16:
+// 252 us with two tiles to a CTA, 264 with four tiles and keys by 64, 248 so;
+// 24 heads of 333 rows: 9.4 -> 8.4 us).
+template <int D>
 struct FwdTile {
-    static constexpr int inner = W == 4 ? 64 : 128, halves = inner / 64;   // P goes over 64 columns at a time
+    static constexpr int W = D == 64 ? 1 : 2, ctas = 2 / W, tmem = 512 / ctas;
     static constexpr int rows = W * kTile;                                 // query rows of one work item
     static constexpr int mma_warp = 4 * W, load_warp = mma_warp + 1, deal_warp = mma_warp + 2;   // after the softmax warps
     static constexpr int threads = 32 * (4 * W + 4);                       // one warp idle: register shares go by warpgroup
-    // Registers a thread at launch, shared out so that a softmax thread holds its row of scores.
-    static constexpr int regs = W == 4 ? 96 : 168, softmax_regs = W == 4 ? 104 : 208, other_regs = W == 4 ? 64 : 88;
+    // Registers a thread at launch, shared out so that a softmax thread holds its row of 128 scores.
+    static constexpr int regs = W == 1 ? 128 : 168, softmax_regs = W == 1 ? 192 : 208, other_regs = W == 1 ? 64 : 88;
     static_assert(W * softmax_regs + other_regs <= (W + 1) * regs, "register shares of one block");
-    static constexpr int stages = D == 64 ? 8 : 4;
-    static constexpr uint32_t q_bytes = kTile * D * 2, bytes = inner * D * 2;   // a query tile, a key tile
-    static constexpr uint32_t box = inner * 128;                                // 64 columns of a key tile
-    static constexpr uint32_t t_o = W * inner;                                  // tensor memory: S (and P), then O
-    static_assert(t_o + W * D <= 512, "tensor memory");
-    static constexpr uint32_t stage = W == 4 ? 2048 : 4096, out_cols = stage / 64;   // results: 32 rows x out_cols a time
-    static constexpr uint32_t off_ring = W * q_bytes, off_out = off_ring + stages * bytes;
-    static constexpr uint32_t smem = off_out + 4 * W * stage + 1024;            // slack to align the base
+    static constexpr int stages = 4;                                       // of the ring of K and V tiles
+    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;    // a 128-row tile, 64 columns of it
+    static constexpr uint32_t t_o = W * kTile;                             // tensor memory: S (and P), then O
+    static_assert(t_o + W * D <= tmem, "tensor memory");
+    static constexpr uint32_t stage = 4096;                                // per softmax warp: 32 rows x 64 columns of results
+    static constexpr uint32_t off_ring = W * bytes, off_out = off_ring + stages * bytes;
+    static constexpr uint32_t smem = off_out + 4 * W * stage + 1024;       // slack to align the base
 };
 
 // Work item: W query tiles of one head, costliest row blocks first.
-template <int W, int INNER>
+template <int W>
 struct FwdItem {
     int32_t b, h, i0, off, L;
     int32_t lo[W], hi[W];       // key tiles [lo, hi) of each query tile
@@ -89,8 +87,8 @@ struct FwdItem {
                 int32_t a0, a1, b0, b1;
                 a.kept(ra, L, a0, a1);
                 a.kept(rb, L, b0, b1);
-                lo[w] = a0 / INNER;
-                hi[w] = (b1 + INNER - 1) / INNER;
+                lo[w] = a0 / kTile;
+                hi[w] = (b1 + kTile - 1) / kTile;
                 full0[w] = b0;
                 full1[w] = a1;
             }
@@ -115,29 +113,28 @@ struct FwdItem {
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
 };
 
-template <int D, int W>
+template <int W>
 struct FwdShared {
-    using TL = FwdTile<D, W>;
     uint64_t qfull[W], qempty[W];
-    uint64_t kvfull[8], kvempty[8], vraw;
-    uint64_t sfull[W], pready[W][TL::halves], ofull[W], oempty[W];
-    ItemSlot<FwdItem<W, TL::inner>> items;
+    uint64_t kvfull[4], kvempty[4], vraw;
+    uint64_t sfull[W], pready[W][2], ofull[W], oempty[W];
+    ItemSlot<FwdItem<W>> items;
     uint64_t mma_done;
     uint32_t tmem_slot;
     int flag;
 };
 
-template <typename T, int D, int W>
-__global__ void __launch_bounds__(FwdTile<D, W>::threads, 1)
+template <typename T, int D>
+__global__ void __launch_bounds__(FwdTile<D>::threads, FwdTile<D>::ctas)
 gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, uint32_t heads,
                           int32_t blocks, uint64_t wait_ns)
 {
-    using TL = FwdTile<D, W>;
-    using Item = FwdItem<W, TL::inner>;
-    constexpr int ST = TL::stages;
+    using TL = FwdTile<D>;
+    constexpr int ST = TL::stages, W = TL::W;
+    using Item = FwdItem<W>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ FwdShared<D, W> sh;
+    __shared__ FwdShared<W> sh;
     const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
@@ -148,7 +145,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             tc::mbar_init(&sh.qfull[w], 1);
             tc::mbar_init(&sh.qempty[w], 1);
             tc::mbar_init(&sh.sfull[w], 1);
-            for (int k = 0; k < TL::halves; ++k)
+            for (int k = 0; k < 2; ++k)
                 tc::mbar_init(&sh.pready[w][k], 4);
             tc::mbar_init(&sh.ofull[w], 1);
             tc::mbar_init(&sh.oempty[w], 4);
@@ -164,7 +161,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     }
     if (warp == TL::mma_warp) {
         __syncwarp();
-        tc::tmem_alloc<512>(&sh.tmem_slot);
+        tc::tmem_alloc<TL::tmem>(&sh.tmem_slot);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -183,7 +180,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             uint32_t g = 0, asked = 0, odd = 0, nraw = 0, taken = 0;   // bits w: queries loaded at all, an odd number of times
             Item it;
             bool ok = true;
-            while (take_item(sh.items, up, lane, taken, it, ok)) {
+            while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
                 const int32_t hk = it.h / a.group;
                 auto tile = [&](const HeadsMap& m, int32_t t, bool tail) {
                     const uint32_t s = g % ST;
@@ -194,7 +191,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     uint64_t* bar = tail ? &sh.vraw : &sh.kvfull[s];
                     if (lane == 0) {
                         tc::mbar_arrive_expect_tx(bar, TL::bytes);
-                        load_tile<D, TL::inner>(base + dst, m, t * TL::inner, hk, it.b, bar);
+                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, it.b, bar);
                     }
                     if (tail) {
                         // Keys behind the length may hold anything, and 0 x NaN is NaN: zero their rows of V.
@@ -202,7 +199,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D, TL::inner>(smem + dst, it.L - t * TL::inner, TL::inner, lane);
+                        zero_tile_rows<D, kTile>(smem + dst, it.L - t * kTile, kTile, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -215,8 +212,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (!ok)
                         return;
                     if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(&sh.qfull[w], TL::q_bytes);
-                        load_tile<D, kTile, TL::inner>(base + w * TL::q_bytes, mq, it.i0 + w * kTile, it.h, it.b, &sh.qfull[w]);
+                        tc::mbar_arrive_expect_tx(&sh.qfull[w], TL::bytes);
+                        load_tile<D, kTile>(base + w * TL::bytes, mq, it.i0 + w * kTile, it.h, it.b, &sh.qfull[w]);
                     }
                     odd ^= 1u << w;
                     asked |= 1u << w;
@@ -232,7 +229,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (ok)
                         tile(mk, t, false);
                     if (ok)
-                        tile(mv, t, (t + 1) * TL::inner > it.L && it.L < a.Skv);
+                        tile(mv, t, (t + 1) * kTile > it.L && it.L < a.Skv);
                 }
             }
             if (!ok) {   // let the copies already issued land before the CTA can exit
@@ -268,8 +265,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             return;
                         tc::fence_after_sync();
                     }
-                    const uint32_t q0 = base + w * TL::q_bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
-                    mma_abt<T, D, TL::inner>(tmem + w * TL::inner, q0, k0);
+                    const uint32_t q0 = base + w * TL::bytes, k0 = base + TL::off_ring + ((2 * tile_n) % ST) * TL::bytes;
+                    mma_abt<T, D, kTile>(tmem + w * kTile, q0, k0);
                     tc::commit_warp(&sh.sfull[w]);
                     if (t == it.lo[w])
                         tc::commit_warp(&sh.qempty[w]);
@@ -278,7 +275,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     const bool first = t == it.hi[w] - 1;
                     const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
 #pragma unroll
-                    for (int half = 0; half < TL::halves; ++half) {
+                    for (int half = 0; half < 2; ++half) {
                         ok = up.warp_wait(&sh.pready[w][half], (np >> w) & 1u);
                         if (ok && first && half == 0)
                             ok = up.warp_wait(&sh.oempty[w], ((no >> w) & 1u) ^ 1u);
@@ -287,7 +284,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         tc::fence_after_sync();
 #pragma unroll
                         for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                            tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * TL::inner + ks * 8,
+                            tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * kTile + ks * 8,
                                                 tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
                     }
                     np ^= 1u << w;
@@ -335,7 +332,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         tc::regs_raise<TL::softmax_regs>();
         const int w = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 tensor-memory lanes per warp, lane in bits 16..
-        const uint32_t ts = tmem + lanes + w * TL::inner, to = tmem + lanes + TL::t_o + w * D;
+        const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + TL::t_o + w * D;
         // exp(scale x) = exp2(c x) with c > 0: a negative scale flips the scores, a zero one clears them.
         const float c = a.scale == 0.0f ? kLog2e : fabsf(a.scale) * kLog2e;
         const float pre = a.scale > 0.0f ? 1.0f : (a.scale < 0.0f ? -1.0f : 0.0f);
@@ -361,18 +358,17 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (!ok)
                     break;
                 tc::fence_after_sync();
-                constexpr int N = TL::inner;
-                float s[N];
-                tmem_ld(ts, s);
+                float s[kTile];
+                tc::tmem_ld128(ts, s);
                 if (__builtin_expect(pre != 1.0f, 0)) {
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
+                    for (int j = 0; j < kTile; ++j)
                         s[j] *= pre;
                 }
-                if (__builtin_expect((t + 1) * N > full1 || t * N < full0, 0)) {
-                    const int32_t k0 = c0 - t * N, k1 = c1 - t * N;
+                if (__builtin_expect((t + 1) * kTile > full1 || t * kTile < full0, 0)) {
+                    const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
 #pragma unroll
-                    for (int k = 0; k < N; k += 32) {
+                    for (int k = 0; k < kTile; k += 32) {
                         const uint32_t keep = bits_below(k1 - k) & ~bits_below(k0 - k);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -381,10 +377,10 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 }
                 float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int j = 4; j < N; j += 8)
+                for (int j = 4; j < kTile; j += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] = j + 4 + k < N ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % N]) : fmaxf(x[k], s[j + k]);
+                        x[k] = j + 4 + k < kTile ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
                 const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, rounded to 16 bits.
@@ -425,41 +421,27 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     if (lane == 0)
                         tc::mbar_arrive(bar);
                 };
-                uint32_t r0[16];
-                if constexpr (TL::halves == 2) {
-                    // Two warps to a scheduler: the first half is exponentiated while the maximum is found, and
-                    // again where that raises it.
-                    uint32_t r1[16];
-                    if (!opening) {
-                        exponentiate(0, shift_of(), r0);
-                        exponentiate(32, shift_of(), r1);
-                    }
-                    if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
-                        raised();
-                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                        exponentiate(0, shift_of(), r0);
-                        exponentiate(32, shift_of(), r1);
-                    }
-                    const float shift = shift_of();
-                    tc::tmem_st16(ts, r0);
-                    tc::tmem_st16(ts + 16, r1);
-                    hand_over(&sh.pready[w][0]);
-                    exponentiate(64, shift, r0);
-                    tc::tmem_st16(ts + 32, r0);
-                    exponentiate(96, shift, r1);
-                    tc::tmem_st16(ts + 48, r1);
-                    hand_over(&sh.pready[w][1]);
-                } else {
-                    // Four warps to a scheduler hide the maximum's latency, and have no registers for more.
-                    if (__builtin_expect(__any_sync(0xffffffffu, raise), 0))
-                        raised();
-                    const float shift = shift_of();
-                    exponentiate(0, shift, r0);
-                    tc::tmem_st16(ts, r0);
-                    exponentiate(32, shift, r0);
-                    tc::tmem_st16(ts + 16, r0);
-                    hand_over(&sh.pready[w][0]);
+                uint32_t r0[16], r1[16];
+                // The first half is exponentiated while the maximum is found, and again where that raises it.
+                if (!opening) {
+                    exponentiate(0, shift_of(), r0);
+                    exponentiate(32, shift_of(), r1);
                 }
+                if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
+                    raised();
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                    exponentiate(0, shift_of(), r0);
+                    exponentiate(32, shift_of(), r1);
+                }
+                const float shift = shift_of();
+                tc::tmem_st16(ts, r0);
+                tc::tmem_st16(ts + 16, r1);
+                hand_over(&sh.pready[w][0]);
+                exponentiate(64, shift, r0);
+                tc::tmem_st16(ts + 32, r0);
+                exponentiate(96, shift, r1);
+                tc::tmem_st16(ts + 48, r1);
+                hand_over(&sh.pready[w][1]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok)
@@ -475,21 +457,20 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     break;
                 tc::fence_after_sync();
             }
-            constexpr int OC = TL::out_cols;
 #pragma unroll 1
-            for (int k = 0; k < D; k += OC) {
-                uint32_t r[OC / 2];
+            for (int k = 0; k < D; k += 64) {
+                uint32_t r[32];
 #pragma unroll
-                for (int j = 0; j < OC / 2; ++j)
+                for (int j = 0; j < 32; ++j)
                     r[j] = 0;
                 if (any) {
-                    float o[OC];
-                    tmem_ld(to + k, o);
+                    float o[64];
+                    tc::tmem_ld64(to + k, o);
 #pragma unroll
-                    for (int j = 0; j < OC / 2; ++j)
+                    for (int j = 0; j < 32; ++j)
                         r[j] = live ? pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
                 }
-                store_rows<OC>(stage, lane, r, out ? out + k : nullptr);
+                store_rows<64>(stage, lane, r, out ? out + k : nullptr);
             }
             if (any) {
                 tc::fence_before_sync();
@@ -508,43 +489,32 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_after_sync();
     if (warp == TL::mma_warp) {
         __syncwarp();
-        tc::tmem_free<512>(tmem);
+        tc::tmem_free<TL::tmem>(tmem);
     }
-}
-
-template <typename T, int D, int W>
-cudaError_t launch_attention_fwd_w(const AttentionArgs& a, cudaStream_t st, uint64_t wait_ns)
-{
-    using TL = FwdTile<D, W>;
-    // Without keys no tile is loaded, and q stands in for k and v in the maps.
-    const bool keys = a.Skv > 0;
-    HeadsMap mq, mk, mv;
-    if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, TL::inner) ||
-        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, TL::inner) ||
-        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, TL::inner))
-        return cudaErrorInvalidValue;
-    constexpr int smem = static_cast<int>(TL::smem);
-    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D, W>>(smem);
-    if (e != cudaSuccess)
-        return e;
-    const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
-    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
-    return launch_kernel(gtms_attention_fwd_kernel<T, D, W>, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk,
-                         mv, a, static_cast<uint32_t>(heads), blocks, wait_ns);
 }
 
 template <typename T, int D>
 cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
 {
+    using TL = FwdTile<D>;
     if (!bind_context())
         return cudaErrorUnknown;
-    if constexpr (D == 64) {
-        // Blocks of 512 rows where that still makes two items for every multiprocessor.
-        const int64_t items = static_cast<int64_t>(a.B) * a.Hq * ((a.Sq + 4 * kTile - 1) / (4 * kTile));
-        if (items >= 2 * device_sms())
-            return launch_attention_fwd_w<T, D, 4>(a, st, wait_ns);
-    }
-    return launch_attention_fwd_w<T, D, 2>(a, st, wait_ns);
+    // Without keys no tile is loaded, and q stands in for k and v in the maps.
+    const bool keys = a.Skv > 0;
+    HeadsMap mq, mk, mv;
+    if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, kTile) ||
+        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
+        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile))
+        return cudaErrorInvalidValue;
+    constexpr int smem = static_cast<int>(TL::smem);
+    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D>>(smem);
+    if (e != cudaSuccess)
+        return e;
+    // One CTA per item; the running ones take over the others' (see ItemSlot).
+    const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
+    return launch_kernel(gtms_attention_fwd_kernel<T, D>, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv,
+                         a, static_cast<uint32_t>(heads), blocks, wait_ns);
 }
 
 }  // namespace gtms

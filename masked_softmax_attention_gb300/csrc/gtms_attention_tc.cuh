@@ -146,21 +146,22 @@ __device__ __forceinline__ void init_items(ItemSlot<Item>& s, int readers)
 }
 
 // The dealing warp: make(index) is the item of a CTA index; an item with b < 0 ends
-// the deal. The next item is asked for once every reader has taken the last.
+// the deal. The next item is asked for once every reader has taken the last. Where
+// a role has given up, the CTAs that are left are taken over all the same and
+// dropped, so that a grid that cannot make progress ends at once and not CTA by CTA.
 template <typename Item, typename Make>
 __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, Make make)
 {
     int32_t index = blockIdx.x;
+    bool ok = true;
     for (uint32_t n = 0; index >= 0; ++n) {
         if (n > 0) {
-            if (!up.warp_wait(&s.empty, (n - 1) & 1u))
-                return;
+            ok = ok && up.warp_wait(&s.empty, (n - 1) & 1u);
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&s.answered, 16);
                 tc::next_cta_request(tc::smem_u32(&s.response), &s.answered);
             }
             __syncwarp();
-            // A request is always waited for, also when another role has given up.
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.answered, (n - 1) & 1u, kAttnDrainWaitNs))) {
                 up.raise();
                 return;
@@ -169,6 +170,8 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
             tc::fence_smem_for_async();   // the response has been read before the next one may land
             __syncwarp();
         }
+        if (!ok)
+            continue;
         Item it;
         it.b = -1;
         if (index >= 0)
@@ -228,10 +231,6 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
             *reinterpret_cast<uint4*>(to + 16 * j) = x;
     }
 }
-
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::tmem_ld32(taddr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[64]) { tc::tmem_ld64(taddr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[128]) { tc::tmem_ld128(taddr, v); }
 
 // S (or dP) = A B^T: K-major operands of 128 and N rows x D (a whole warp calls).
 template <typename T, int D, int N>

@@ -504,3 +504,61 @@ def test_layer_step_captured_without_autograd_nodes(dev):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     alive.backward(c.dout)
     assert torch.equal(leaf.grad, want[0])
+
+
+# ---------------------------------------------------------------------------
+# Giving up
+# ---------------------------------------------------------------------------
+
+def _build_give_up_probe():
+    """tests/attention_give_up_probe.cu (the attention kernels without their copies) as a library of its own."""
+    import ctypes
+    import os
+    import subprocess
+
+    from masked_softmax_attention_gb300 import _build as b
+
+    src = os.path.join(b.ROOT, "tests", "attention_give_up_probe.cu")
+    out_dir = os.path.join(b.ROOT, "_build", "test_probe")
+    os.makedirs(out_dir, exist_ok=True)
+    path = os.path.join(out_dir, "libgtms_attention_give_up_probe.so")
+    deps = [src] + [os.path.join(b.CSRC, f) for f in os.listdir(b.CSRC)] + [os.path.join(b.INCLUDE, "gtms.h")]
+    if not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps):
+        tmp = path + f".{os.getpid()}.tmp"
+        subprocess.run([b.nvcc_path(), *b.ARCH, *b.NVCC_FLAGS, "-shared", src, "-o", tmp], check=True,
+                       capture_output=True, text=True)
+        os.replace(tmp, path)
+    fn = ctypes.CDLL(path).gtms_test_attention_no_loads
+    vp, i32 = ctypes.c_void_p, ctypes.c_int32
+    fn.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, vp, ctypes.c_uint64]
+    fn.restype = ctypes.c_int
+    return fn
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_kernels_give_up_when_their_waits_run_out(dev, d):
+    """Failure detection without a GPU fault: where no copy is issued, every wait runs out (after 200 us here).
+    The launches must succeed, the grid must end promptly, also the CTAs that had not started, with
+    GTMS_ERR_TIMEOUT in the status word, and a normal call right after it is exact."""
+    import ctypes
+    import time
+
+    probe = _build_give_up_probe()
+    B, H, S = 8, 16, 1000
+    c = Case(B, H, H, S, S, d, BF16, (S,) * B)
+    o, lse = c.forward()
+    grads = [torch.zeros_like(t) for t in (c.q, c.k, c.v)]
+    tensors = (ctypes.c_void_p * 8)(*(t.data_ptr() for t in (c.q, c.k, c.v, o.clone(), c.dout, *grads)))
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    work = torch.empty(1 << 22, dtype=torch.uint8, device=dev)
+    for workspace in (None, work.data_ptr()):
+        status.zero_()
+        torch.cuda.synchronize()
+        t0 = time.monotonic()
+        rc = probe(tensors, lse.clone().data_ptr(), c.lens.data_ptr(), B, H, S, d, c.scale, status.data_ptr(), workspace,
+                   torch.cuda.current_stream().cuda_stream, 200_000)
+        torch.cuda.synchronize()
+        assert rc == 0 and int(status.item()) == gtms.GTMS_ERR_TIMEOUT and time.monotonic() - t0 < 5.0
+    o2, lse2 = c.forward()
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    c.backward(o, lse)
