@@ -269,11 +269,13 @@ typedef struct {
  *   status   as in gtms_attention_softmax_backward.
  * k and v at c >= L and q at r >= L are never used: anything may stand there,
  * NaN too. Inside the live length a NaN or infinity in k stays in the rows that
- * keep it; one in v can reach other rows of the same tile of up to 256 rows.
+ * keep it; one in v can reach the other rows of its 128-key tile that come before
+ * it (a masked probability is an exact zero, but the tile's product multiplies it).
  * Sums, maxima and accumulators are fp32; probabilities are rounded once to
  * `dtype` for the product with v, and o once on its way out.
  * dtype GTMS_BF16 or GTMS_F16, head_dim 64 or 128. Data 16-byte aligned,
- * strides multiples of 8 elements. o must not overlap the inputs.
+ * strides multiples of 8 elements, below 2^40 bytes and not below head_dim, save
+ * for the strides of 0 of a broadcast batch or head. o must not overlap the inputs.
  * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, Hq not a
  * multiple of Hkv, a non-finite scale, a window below 1 with the sliding window,
  * overlaps, an output that repeats itself, misaligned lse, seq_lens, q_offsets
@@ -300,7 +302,8 @@ int gtms_attention_forward(const gtms_attention_shape* shape, const gtms_heads* 
  * The sums run in a fixed order (no atomics on the gradients): the same inputs
  * give the same bits. p and ds are rounded once to `dtype` for their products.
  * q, o, lse and dout of rows that keep nothing, and k and v at c >= L, are never
- * used. The three gradients must not overlap each other or any input. Otherwise
+ * used; a NaN or infinity in a live row or key can reach the gradients of the rows
+ * and keys that share a 128 x 128 tile with it. The three gradients must not overlap each other or any input. Otherwise
  * as gtms_attention_forward.
  */
 int gtms_attention_backward(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,

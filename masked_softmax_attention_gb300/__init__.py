@@ -699,7 +699,7 @@ def rotary_backward(dy, positions, inv_freq, other=None, interleaved: bool = Fal
 def _usable(t):
     """A gradient as the kernels take it: one that autograd expanded or sliced is copied."""
     aligned = 16 // t.element_size()
-    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(n <= 1 or s % aligned == 0
+    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(n <= 1 or (s % aligned == 0 and s >= t.shape[3])
                                                             for n, s in zip(t.shape[:3], t.stride()[:3]))
     return t if ok else t.contiguous()
 

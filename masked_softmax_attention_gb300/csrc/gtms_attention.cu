@@ -8,7 +8,7 @@ namespace gtms {
 template <typename T, int D>
 cudaError_t launch_attention_forward(const AttentionArgs& a, cudaStream_t st)
 {
-    if (a.group * static_cast<int64_t>(a.Sq) <= kSplitRows)
+    if (prefer_split<D>(a))
         return launch_attention_split<T, D>(a, st);
     return launch_attention_fwd_tc<T, D>(a, st);
 }

@@ -72,6 +72,16 @@ int check_shape(const gtms_attention_shape* p, int64_t* rows)
     return GTMS_OK;
 }
 
+// Strides that a tensor map holds: a row's stride steps over the row, the others are 0 (a broadcast) or step
+// over it too, all below 2^40 bytes.
+int check_mapped(const HeadsSpan& t)
+{
+    for (int i = 0; i < 3; ++i)
+        if (t.ext[i] > 1 && ((t.stride[i] < t.row && (i == 2 || t.stride[i] != 0)) || t.stride[i] >= (int64_t(1) << 40)))
+            return GTMS_ERR_UNSUPPORTED;
+    return GTMS_OK;
+}
+
 // One strided operand: pointer, alignment, strides, distinct elements of outputs.
 int check_heads(const gtms_heads* t, int64_t B, int64_t H, int64_t S, int64_t D, int elem, int align, bool output,
                 HeadsSpan& span)
@@ -87,7 +97,7 @@ int check_heads(const gtms_heads* t, int64_t B, int64_t H, int64_t S, int64_t D,
     for (int i = 0; i < 3; ++i)
         if (span.stride[i] % align != 0)
             return GTMS_ERR_UNSUPPORTED;
-    return GTMS_OK;
+    return align == 16 ? check_mapped(span) : GTMS_OK;   // 16: the attention calls
 }
 
 bool hits(const HeadsSpan& t, const void* p, uint64_t bytes)

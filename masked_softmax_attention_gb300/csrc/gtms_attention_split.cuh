@@ -24,9 +24,11 @@
 
 namespace gtms {
 
-constexpr int kSplitWarps = 4, kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitRows = 16, kSplitKeys = 16;   // rows of a tile; keys a warp takes at a time
 constexpr int kSplitMaxCluster = 8;               // the largest portable cluster
+// Warps of a CTA: four, three CTAs to a multiprocessor; eight where the grid has a
+// CTA for at most every other multiprocessor (one token, 8 key/value heads of 8192
+// keys, head dim 128, 64 CTAs: 25.1 -> 18.0 us; 128 CTAs of twice the rows: 26.1 -> 32.2).
 
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -51,23 +53,25 @@ __device__ __forceinline__ uint4 load_once(const T* p, bool use)
     return v;
 }
 
-template <int D>
+template <int D, int WARPS>
 struct SplitShared {
     uint4 q[kSplitRows][D / 8 + 1];                  // + 1: rows start in different banks
-    float m[kSplitWarps][kSplitRows], l[kSplitWarps][kSplitRows];
-    float o[kSplitWarps][kSplitRows][D + 4];
+    float m[WARPS][kSplitRows], l[WARPS][kSplitRows];
+    float o[WARPS][kSplitRows][D + 4];
     float cta_m[kSplitRows], cta_l[kSplitRows];      // joined over the warps; o[0] then holds the CTA's O
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSplitThreads, 3)
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 3 : 1)
 gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
 {
     namespace cg = cooperative_groups;
+    constexpr int THREADS = 32 * WARPS;
     const cg::cluster_group cluster = cg::this_cluster();
     const int32_t ranks = static_cast<int32_t>(cluster.num_blocks()), rank = static_cast<int32_t>(cluster.block_rank());
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    SplitShared<D>& sh = *reinterpret_cast<SplitShared<D>*>(smem_raw);
+    using Shared = SplitShared<D, WARPS>;
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
     const int64_t unit = blockIdx.x / ranks;
@@ -99,7 +103,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
     }
 
     // q into shared memory; rows that do not exist are zero.
-    for (int32_t i = threadIdx.x; i < kSplitRows * (D / 8); i += kSplitThreads) {
+    for (int32_t i = threadIdx.x; i < kSplitRows * (D / 8); i += THREADS) {
         const int32_t r = i / (D / 8), x = i % (D / 8);
         sh.q[r][x] = exists(r) ? *(reinterpret_cast<const uint4*>(a.q.row<T>(b, head_of(r), row_of(r))) + x) : make_uint4(0, 0, 0, 0);
     }
@@ -148,7 +152,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
 
     load_k(blk);
     load_v(blk);
-    for (; blk < end; blk += kSplitWarps) {
+    for (; blk < end; blk += WARPS) {
         float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
@@ -159,7 +163,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
                 mma_16816<T>(s[k], qa.z, qb.z, qa.w, qb.w, kr[k][x].z, kr[k][x].w);
             }
         }
-        load_k(blk + kSplitWarps);
+        load_k(blk + WARPS);
         const int32_t key0 = blk * kSplitKeys + 2 * t;
         uint32_t p[2][2];   // [row half][key half]
 #pragma unroll
@@ -205,7 +209,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
                              __byte_perm(r[2][j / 2], r[3][j / 2], sel));
             }
         }
-        load_v(blk + kSplitWarps);
+        load_v(blk + WARPS);
     }
 
     // Join the warps: row sums over the quad, then every warp brings its O to the CTA's maximum.
@@ -224,13 +228,13 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
         const int32_t r = g + 8 * h;
         float top = sh.m[0][r];
 #pragma unroll
-        for (int w = 1; w < kSplitWarps; ++w)
+        for (int w = 1; w < WARPS; ++w)
             top = fmaxf(top, sh.m[w][r]);
         const float base = top == -INFINITY ? 0.0f : top, f = exp2_approx(m[h] - base);
         if (warp == 0 && t == 0) {
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kSplitWarps; ++w)
+            for (int w = 0; w < WARPS; ++w)
                 sum += sh.l[w][r] * exp2_approx(sh.m[w][r] - base);
             sh.cta_m[r] = top;
             sh.cta_l[r] = sum;
@@ -246,10 +250,10 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
                                     o[y][j + 3][2 * h + n] * f);
     }
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < kSplitRows * D; i += kSplitThreads) {
+    for (int32_t i = threadIdx.x; i < kSplitRows * D; i += THREADS) {
         float sum = sh.o[0][i / D][i % D];
 #pragma unroll
-        for (int w = 1; w < kSplitWarps; ++w)
+        for (int w = 1; w < WARPS; ++w)
             sum += sh.o[w][i / D][i % D];
         sh.o[0][i / D][i % D] = sum;
     }
@@ -259,7 +263,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
         __syncthreads();
 
     // Join the CTAs: each writes its share of the rows' element pairs.
-    for (int32_t i = rank * kSplitThreads + threadIdx.x; i < kSplitRows * (D / 2); i += ranks * kSplitThreads) {
+    for (int32_t i = rank * THREADS + threadIdx.x; i < kSplitRows * (D / 2); i += ranks * THREADS) {
         const int32_t r = i / (D / 2), d = 2 * (i % (D / 2));
         if (!exists(r))
             break;   // rows come in order
@@ -288,38 +292,83 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles)
         cluster.sync();   // the others may still be reading this CTA's shared memory
 }
 
+// CTAs that share a unit's keys: until there are about four to a multiprocessor, but
+// every warp of four is left two blocks of keys.
+inline int split_ranks(int64_t units, int64_t keys, int nsm)
+{
+    int ranks = 1;
+    while (ranks < kSplitMaxCluster && units * ranks < 4 * nsm && ranks * int64_t(16) * kSplitKeys <= keys)
+        ranks *= 2;
+    return ranks;
+}
+
+inline int64_t split_units(const AttentionArgs& a)
+{
+    return static_cast<int64_t>(a.B) * a.Hkv * ((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
+}
+
+// Whether to split: always where the rows of a key/value head fill one tile, so that
+// the keys are read once; otherwise where the waves of its CTAs take less time than
+// those of the tensor-memory kernel, whose CTAs (128 rows of one head at head dim
+// 64, 256 at 128) walk over all keys by themselves. Microseconds, from measurements
+// (bf16, keys at least half filled; split / tensor-memory kernel):
+//   32 / 8 heads d 128, 8192 keys, 1 sequence:   8 tokens 26 / 84, 16: 28 / 84, 32: 64 / 84, 64: 103 / 84
+//   the same, 4096 keys:  4 sequences, 8 tokens 32 / 46, 32: 76 / 46;  16 sequences, 8: 83 / 132, 16: 142 / 134
+//   16 / 16 heads d 64, 4096 keys, 32 tokens:    1 sequence 12 / 38, 8: 47 / 40
+//   8 / 8 heads d 64, 33 of 33 rows, 32 sequences: 13 / 7
+template <int D>
+bool prefer_split(const AttentionArgs& a)
+{
+    const int64_t rows = static_cast<int64_t>(a.group) * a.Sq;
+    if (rows <= kSplitRows)
+        return true;
+    const int nsm = device_sms();
+    if (rows > 16 * kSplitRows || nsm <= 0)
+        return false;
+    const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + a.Sq < a.Skv ? a.window + a.Sq : a.Skv;
+    const int64_t units = split_units(a), ranks = split_ranks(units, keys, nsm);
+    const double split = static_cast<double>((units * ranks + 3 * nsm - 1) / (3 * nsm)) *
+                         (6.0 + 1.4 * static_cast<double>((keys + ranks * 64 - 1) / (ranks * 64)));
+    const int64_t items = static_cast<int64_t>(a.B) * a.Hq * ((a.Sq + FwdTile<D>::rows - 1) / FwdTile<D>::rows);
+    const int64_t slots = static_cast<int64_t>(nsm) * FwdTile<D>::ctas;
+    const double whole = static_cast<double>((items + slots - 1) / slots) * (5.0 + 1.2 * static_cast<double>((keys + 127) / 128));
+    return split < whole;
+}
+
+template <typename T, int D, int WARPS>
+cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
+{
+    constexpr int smem = static_cast<int>(sizeof(SplitShared<D, WARPS>));
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>>(smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int32_t tiles = static_cast<int32_t>((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
+    return cudaLaunchKernelEx(&cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles);
+}
+
 template <typename T, int D>
 cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
 {
     const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
-    const int32_t tiles = (a.group * a.Sq + kSplitRows - 1) / kSplitRows;
-    const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * tiles;
-    // Split until there are about four CTAs to a multiprocessor, but leave every warp two blocks of keys.
-    int ranks = 1;
-    while (ranks < kSplitMaxCluster && units * ranks < 4 * nsm &&
-           static_cast<int64_t>(ranks) * 4 * kSplitWarps * kSplitKeys <= a.Skv)
-        ranks *= 2;
-    auto* kern = gtms_attention_split_kernel<T, D>;
-    constexpr int smem = static_cast<int>(sizeof(SplitShared<D>));
-    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D>>(smem);
-    if (e != cudaSuccess)
-        return e;
+    const int64_t units = split_units(a);
+    const int ranks = split_ranks(units, a.Skv, nsm);
     if (units * ranks > INT32_MAX)
         return cudaErrorNotSupported;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(units * ranks));
-    cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, tiles);
+    return 2 * units * ranks <= nsm ? launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st)
+                                : launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
 }
 
 }  // namespace gtms

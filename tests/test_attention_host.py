@@ -84,6 +84,10 @@ def test_alignment_and_strides(call):
     assert call(k=heads(K, 2, 300, strides=(2 * 300 * 64, 300 * 64, 68))) == UNSUPPORTED
     assert call(k=heads(K, 2, 300, strides=(-64, 300 * 64, 64))) == INVALID
     assert call(o=heads(O, strides=(1 << 62, 1 << 62, 64))) == INVALID       # the range overflows
+    assert call(k=heads(K, 2, 300, strides=(2 * 300 * 64, 300 * 64, 0))) == UNSUPPORTED    # one row for every key
+    assert call(k=heads(K, 2, 300, strides=(2 * 300 * 64, 300 * 64, 32))) == UNSUPPORTED   # rows that overlap
+    assert call(v=heads(V, 2, 300, strides=(8, 300 * 64, 64))) == UNSUPPORTED
+    assert call(v=heads(V, 2, 300, strides=(1 << 40, 300 * 64, 64))) == UNSUPPORTED        # a stride of 2^41 bytes
     assert call(lens=LENS + 2) == INVALID and call(off=OFF + 1) == INVALID and call(status=ST + 2) == INVALID
     assert call(lse=LSE + 2) == INVALID
 
@@ -111,7 +115,7 @@ def test_overlaps():
 
 
 def test_parts_of_a_fused_projection_do_not_overlap():
-    """The overlap test knows interleaved parts apart: with a misaligned length behind them only the last check fails."""
+    """Parts that run into each other are told from parts that do not (test_attention_gpu.py runs the latter)."""
     H, S, d, B = 8, 200, 64, 2
     st = (S * H * d, d, H * d)
     part = lambda base, h: heads(base + 2 * h * d, strides=st)  # noqa: E731
@@ -121,7 +125,7 @@ def test_parts_of_a_fused_projection_do_not_overlap():
     assert gtms.gtms_attention_backward_workspace(shape(**sh), ctypes.byref(bad)) == OK
     need = bad.value
     assert need >= B * 4 * S * 4
-    # all of these reach the workspace check, which comes before the overlaps: too small is refused
+    # a workspace that is too small is refused
     assert bwd(q=q, k=k, v=v, o=o, dq=part(DQ, 0), dk=part(DQ, 4), dv=part(DQ, 6), size=need - 1, **sh) == INVALID
     # parts that do run into each other are refused as overlaps with a workspace that is large enough
     assert bwd(q=q, k=k, v=v, o=o, dq=part(DQ, 0), dk=part(DQ, 3), dv=part(DQ, 6), size=need, **sh) == INVALID
