@@ -2,9 +2,11 @@
 // angle = position * inv_freq (see gtms_rotary in include/gtms.h).
 //
 // The work is one read and one write of every element, so memory bounds it. The
-// sine and cosine are the same for every head of a token: a block takes a few
-// tokens and forms their rotations once, in shared memory; a thread then takes
-// those of one 16-byte unit of one token into registers and walks over the heads.
+// sine and cosine are the same for every head of a token: a block takes one token,
+// asks for its rows in L2, forms its rotations in shared memory meanwhile, and each
+// thread then takes those of one 16-byte unit into registers and walks over the
+// heads. q and k [4,40,4096,128] bf16: 52 us, 6.5 TB/s (70 without the L2 prefetch
+// and with four tokens to a block of 128 threads).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -68,68 +70,55 @@ struct __align__(sizeof(T) * VEC) Unit {
     T e[VEC];
 };
 
-// Blocks of 128 threads (six to a multiprocessor), four tokens each, two heads in
-// flight per thread: of 128 to 512 threads, 2 to 5 heads and 2 to 8 tokens the
-// best over the three measured sizes (q and k [4,40,4096,128] bf16 68 us, 4.9 TB/s;
-// fewer, larger blocks hide less of the sines, more heads in flight cost occupancy).
-constexpr int kRotaryThreads = 128;
+// 64 threads, 16 blocks to a multiprocessor, two heads in flight per thread: of 32 to
+// 256 threads, 1 to 5 heads and 1 to 8 tokens the best at the size above (52 us;
+// 128 threads 68, one head in flight 54, three 71, two tokens 60).
+constexpr int kRotaryThreads = 64, kRotaryBlocks = 16;
 constexpr int kRotaryUnroll = 2;      // heads whose loads are in flight together
-constexpr int kRotaryBlocks = 6;
-constexpr int kRotaryMaxTokens = 4;   // tokens of a block
 
 // Units [0, n_rot) of a head hold rotated pairs (VEC pairs from two places in the
 // half layout, VEC / 2 neighbours in the interleaved one), the rest are copied. A
-// block takes 2^tokens_log tokens and heads_per_block heads; consecutive threads
-// take the units of a token, then the tokens, then the heads.
+// block takes one token and heads_per_block heads; consecutive threads take the
+// units, then the heads.
 template <typename T, int VEC, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks)
-gtms_rotary_kernel(const RotaryArgs a, int32_t units, int32_t n_rot, int32_t tokens_log, int32_t heads_per_block)
+gtms_rotary_kernel(const RotaryArgs a, int32_t units, int32_t n_rot, int32_t heads_per_block)
 {
     using U = Unit<T, VEC>;
     constexpr int PAIRS = INTERLEAVED ? (VEC > 1 ? VEC / 2 : 1) : VEC;
     constexpr bool TWO = !INTERLEAVED || VEC == 1;   // the pairs' elements come from two units
-    extern __shared__ __align__(16) float2 turn[];   // [token][pair]: amplitude cos, amplitude sin
-    __shared__ int64_t at[kRotaryMaxTokens][4];      // the token's offsets in x[0], y[0], x[1], y[1]
-    const int32_t tokens = 1 << tokens_log, half = a.R / 2;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) << tokens_log, all = static_cast<int64_t>(a.B) * a.S;
-    const int32_t live = all - first < tokens ? static_cast<int32_t>(all - first) : tokens;
-    for (int32_t i = threadIdx.x; i < tokens * half; i += kRotaryThreads) {
-        const int32_t k = i / half, j = i - k * half;
-        if (k < live) {
-            const int64_t b = (first + k) / a.S, s = first + k - b * a.S;
-            float c, sn;
-            rotation(__ldg(a.positions + b * a.position_stride + s), __ldg(a.inv_freq + j), c, sn);
-            turn[i] = make_float2(c * a.amplitude, sn * (a.inverse ? -a.amplitude : a.amplitude));
-        }
+    extern __shared__ __align__(16) float2 turn[];   // [pair]: amplitude cos, amplitude sin
+    const int32_t half = a.R / 2, heads = a.H[0] + a.H[1], h0 = blockIdx.y * heads_per_block;
+    const int32_t h1 = h0 + heads_per_block < heads ? h0 + heads_per_block : heads;
+    const int64_t b = blockIdx.x / a.S, s = blockIdx.x - b * a.S;
+    auto row = [&](const HeadsRef& x, int32_t h) { return static_cast<T*>(x.data) + b * x.sb + s * x.ss + h * x.sh; };
+
+    const int32_t lines = (a.D * static_cast<int32_t>(sizeof(T)) + 127) / 128;
+    for (int32_t i = threadIdx.x; i < (h1 - h0) * lines; i += kRotaryThreads) {
+        const int32_t n = i / lines, h = h0 + n, t = h >= a.H[0];
+        const char* p = reinterpret_cast<const char*>(row(a.x[t], t ? h - a.H[0] : h)) + (i - n * lines) * 128;
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
     }
-    if (threadIdx.x < live) {
-        const int64_t b = (first + threadIdx.x) / a.S, s = first + threadIdx.x - b * a.S;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            at[threadIdx.x][2 * k] = b * a.x[k].sb + s * a.x[k].ss;
-            at[threadIdx.x][2 * k + 1] = b * a.y[k].sb + s * a.y[k].ss;
-        }
+    const int32_t position = __ldg(a.positions + b * a.position_stride + s);
+    for (int32_t j = threadIdx.x; j < half; j += kRotaryThreads) {
+        float c, sn;
+        rotation(position, __ldg(a.inv_freq + j), c, sn);
+        turn[j] = make_float2(c * a.amplitude, sn * (a.inverse ? -a.amplitude : a.amplitude));
     }
     __syncthreads();
 
-    const int32_t heads = a.H[0] + a.H[1], h0 = blockIdx.y * heads_per_block;
-    const int32_t h1 = h0 + heads_per_block < heads ? h0 + heads_per_block : heads;
-    // A thread keeps one unit of one token, its rotations in registers, and walks over the heads.
-    const int32_t places = units << tokens_log, lanes = places < kRotaryThreads ? kRotaryThreads / places : 1;
-    const int32_t lane = threadIdx.x / places;
+    // A thread keeps one unit, its rotations in registers, and walks over the heads.
+    const int32_t lanes = units < kRotaryThreads ? kRotaryThreads / units : 1, lane = threadIdx.x / units;
     if (lane >= lanes)
         return;
-    for (int32_t place = threadIdx.x - lane * places; place < places; place += kRotaryThreads) {
-        const int32_t k = place / units, unit = place - k * units;
-        if (k >= live)
-            break;
+    for (int32_t unit = threadIdx.x - lane * units; unit < units; unit += kRotaryThreads) {
         const bool turned = unit < n_rot;
         const int32_t e = turned ? (INTERLEAVED ? 2 * PAIRS : PAIRS) * unit : a.R + (unit - n_rot) * VEC;
         float2 r[PAIRS];
         if (turned) {
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i)
-                r[i] = turn[k * half + unit * PAIRS + i];
+                r[i] = turn[unit * PAIRS + i];
         }
         const int32_t gap = INTERLEAVED ? 1 : half;   // from a pair's first element to its second
 #pragma unroll
@@ -139,8 +128,8 @@ gtms_rotary_kernel(const RotaryArgs a, int32_t units, int32_t n_rot, int32_t tok
             const int32_t last = h1 - before < a.H[t] ? h1 - before : a.H[t];
             int32_t h = (h0 > before ? h0 - before : 0) + lane;
             const int64_t in_step = lanes * a.x[t].sh, out_step = lanes * a.y[t].sh;
-            const T* in = static_cast<const T*>(a.x[t].data) + at[k][2 * t] + h * a.x[t].sh + e;
-            T* out = static_cast<T*>(a.y[t].data) + at[k][2 * t + 1] + h * a.y[t].sh + e;
+            const T* in = row(a.x[t], h) + e;
+            T* out = row(a.y[t], h) + e;
             auto walk = [&](auto count) {   // `count` heads, their loads in flight together
                 constexpr int N = decltype(count)::value;
                 U u[N], w[N];
@@ -189,24 +178,21 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t st)
     const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
-    // Four tokens to a block; fewer, and then fewer heads, where that leaves multiprocessors without work.
+    // A block a token; where that leaves multiprocessors without work, the heads are split.
     const int32_t heads = a.H[0] + a.H[1];
     const int64_t tokens = static_cast<int64_t>(a.B) * a.S;
-    int32_t tokens_log = 2, splits = 1;
-    while (tokens_log > 0 && ((tokens - 1) >> tokens_log) + 1 < 4 * nsm)
-        --tokens_log;
-    const int64_t grid_x = ((tokens - 1) >> tokens_log) + 1;
-    while (grid_x * splits < nsm && (heads / splits) * units > kRotaryThreads)
+    int32_t splits = 1;
+    while (tokens * splits < nsm && (heads / splits) * units > kRotaryThreads)
         splits *= 2;
-    if (grid_x > INT32_MAX)
+    if (tokens > INT32_MAX)
         return cudaErrorNotSupported;
     const int32_t per = (heads + splits - 1) / splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid_x), static_cast<unsigned>((heads + per - 1) / per));
+    cfg.gridDim = dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((heads + per - 1) / per));
     cfg.blockDim = dim3(kRotaryThreads);
-    cfg.dynamicSmemBytes = (static_cast<size_t>(a.R / 2) << tokens_log) * sizeof(float2);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.R / 2) * sizeof(float2);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, gtms_rotary_kernel<T, VEC, INTERLEAVED>, a, units, n_rot, tokens_log, per);
+    return cudaLaunchKernelEx(&cfg, gtms_rotary_kernel<T, VEC, INTERLEAVED>, a, units, n_rot, per);
 }
 
 }  // namespace
