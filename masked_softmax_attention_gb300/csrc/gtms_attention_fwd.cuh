@@ -380,7 +380,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 for (int j = 4; j < kTile; j += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] = j + 4 + k < kTile ? fmaxf(fmaxf(x[k], s[j + k]), s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
+                        x[k] = j + 4 + k < kTile ? max3(x[k], s[j + k], s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
                 const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, rounded to 16 bits.
