@@ -20,13 +20,17 @@
 //                     the end divides O and stores it.
 // The running maximum is only raised, and O and l rescaled, when a tile exceeds it
 // by more than 12 in log2 units: p stays below 2^12, which fp16, bf16 and fp32
-// hold as well as numbers below 1. Almost no tile but a row's first does, so the
-// exponentials do not wait for the tile's maximum: the first half of the row is
-// exponentiated while the maximum is found, and done again in the rare other
-// case. The thread that owns the row rescales: S_w of a tile completes after
-// every earlier product into O_w, so no other hand-off is needed. P is handed
-// over in two halves, so that the first half's product runs while the second
-// half is exponentiated.
+// hold as well as numbers below 1, and almost no tile but a row's first does. The
+// thread that owns the row rescales: S_w of a tile completes after every earlier
+// product into O_w, so no other hand-off is needed.
+// What bounds it: at head dim 128 the tensor cores, 66 % busy on a full-length
+// case of 32 heads (a softmax thread's chain of scores, maximum, exponentials and
+// hand-over and the two products it waits for take 2400 cycles a tile, and the two
+// tiles' chains overlap): [4,32/8,4096,128] bf16 245 us, 1500 TFLOP/s. At 64 the
+// softmax warps' instructions, 43 % of the issue slots, and their fetching: what
+// made their loop shorter made it faster (masks as 32-bit words 267 -> 258 us, no
+// second copy of the exponentials 251 -> 245 and 247 -> 237 us; two MMA warps,
+// whose code evicts theirs, cost 70 %): [32,16,2048,64] 235 us.
 #pragma once
 
 #include "gtms_attention_tc.cuh"
@@ -45,6 +49,9 @@ constexpr float kRaiseLog2 = 12.0f;
 template <int D>
 struct FwdTile {
     static constexpr int W = D == 64 ? 1 : 2, ctas = 2 / W, tmem = 512 / ctas;
+    // Parts in which P is handed over: halves at head dim 128, where the tensor cores bound the kernel and the first
+    // half's product starts early (252 -> 245 us); at 64 the hand-over costs more than it gives (237 -> 235).
+    static constexpr int parts = W;
     static constexpr int rows = W * kTile;                                 // query rows of one work item
     static constexpr int mma_warp = 4 * W, load_warp = mma_warp + 1, deal_warp = mma_warp + 2;   // after the softmax warps
     static constexpr int threads = 32 * (4 * W + 4);                       // one warp idle: register shares go by warpgroup
@@ -275,15 +282,15 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     const bool first = t == it.hi[w] - 1;
                     const uint32_t v0 = base + TL::off_ring + ((2 * n + 1) % ST) * TL::bytes;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = up.warp_wait(&sh.pready[w][half], (np >> w) & 1u);
-                        if (ok && first && half == 0)
+                    for (int part = 0; part < TL::parts; ++part) {
+                        ok = up.warp_wait(&sh.pready[w][part], (np >> w) & 1u);
+                        if (ok && first && part == 0)
                             ok = up.warp_wait(&sh.oempty[w], ((no >> w) & 1u) ^ 1u);
                         if (!ok)
                             return;
                         tc::fence_after_sync();
 #pragma unroll
-                        for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                        for (int ks = part * (8 / TL::parts); ks < (part + 1) * (8 / TL::parts); ++ks)
                             tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * kTile + ks * 8,
                                                 tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
                     }
@@ -413,7 +420,9 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         }
                     }
                 };
-                auto shift_of = [&] { return m == -INFINITY ? 0.0f : -m * c; };
+                if (__builtin_expect(__any_sync(0xffffffffu, raise), 0))
+                    raised();
+                const float shift = m == -INFINITY ? 0.0f : -m * c;
                 auto hand_over = [&](uint64_t* bar) {
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
@@ -422,26 +431,17 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         tc::mbar_arrive(bar);
                 };
                 uint32_t r0[16], r1[16];
-                // The first half is exponentiated while the maximum is found, and again where that raises it.
-                if (!opening) {
-                    exponentiate(0, shift_of(), r0);
-                    exponentiate(32, shift_of(), r1);
-                }
-                if (__builtin_expect(__any_sync(0xffffffffu, raise) || opening, 0)) {
-                    raised();
-                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                    exponentiate(0, shift_of(), r0);
-                    exponentiate(32, shift_of(), r1);
-                }
-                const float shift = shift_of();
+                exponentiate(0, shift, r0);
+                exponentiate(32, shift, r1);
                 tc::tmem_st16(ts, r0);
                 tc::tmem_st16(ts + 16, r1);
-                hand_over(&sh.pready[w][0]);
+                if (TL::parts == 2)
+                    hand_over(&sh.pready[w][0]);
                 exponentiate(64, shift, r0);
                 tc::tmem_st16(ts + 32, r0);
                 exponentiate(96, shift, r1);
                 tc::tmem_st16(ts + 48, r1);
-                hand_over(&sh.pready[w][1]);
+                hand_over(&sh.pready[w][TL::parts - 1]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok)
