@@ -566,14 +566,11 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         const int32_t k1 = a.mask_kind == GTMS_MASK_SLIDING_WINDOW ? k0 + a.window : SH::cols;
                         keep_range(p, k0, k1);
                     }
+                    uint32_t r[32];
 #pragma unroll
-                    for (int k = 0; k < SH::cols; k += 32) {
-                        uint32_t r[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            r[j] = pack2<T>(p[k + 2 * j], p[k + 2 * j + 1]);
-                        tc::tmem_st16(my_s + k / 2, r);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = pack2<T>(p[2 * j], p[2 * j + 1]);
+                    tc::tmem_st32(my_s, r);
                     tc::tmem_wait_st();
                     arrive(&sh.pready);
                     ok = up.warp_wait(&sh.dpfull, gt & 1u, multiplied);
@@ -583,25 +580,21 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     float ds[SH::cols];
                     tc::tmem_ld64(my_dp, ds);
 #pragma unroll
-                    for (int k = 0; k < SH::cols; k += 32) {
-                        uint32_t r[16];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const int at = k + 2 * j;
-                            const float4 e = *reinterpret_cast<const float4*>(delta + at);
-                            float2 x = __fadd2_rn(make_float2(ds[at], ds[at + 1]), make_float2(e.x, e.y));
-                            float2 y = __fadd2_rn(make_float2(ds[at + 2], ds[at + 3]), make_float2(e.z, e.w));
-                            if (kPShift<T> != 0) {
-                                x = __fmul2_rn(x, make_float2(fk, fk));
-                                y = __fmul2_rn(y, make_float2(fk, fk));
-                            }
-                            x = __fmul2_rn(x, make_float2(p[at], p[at + 1]));
-                            y = __fmul2_rn(y, make_float2(p[at + 2], p[at + 3]));
-                            r[j] = pack2<T>(x.x, x.y);
-                            r[j + 1] = pack2<T>(y.x, y.y);
+                    for (int j = 0; j < 32; j += 2) {
+                        const int at = 2 * j;
+                        const float4 e = *reinterpret_cast<const float4*>(delta + at);
+                        float2 x = __fadd2_rn(make_float2(ds[at], ds[at + 1]), make_float2(e.x, e.y));
+                        float2 y = __fadd2_rn(make_float2(ds[at + 2], ds[at + 3]), make_float2(e.z, e.w));
+                        if (kPShift<T> != 0) {
+                            x = __fmul2_rn(x, make_float2(fk, fk));
+                            y = __fmul2_rn(y, make_float2(fk, fk));
                         }
-                        tc::tmem_st16(my_dp + k / 2, r);
+                        x = __fmul2_rn(x, make_float2(p[at], p[at + 1]));
+                        y = __fmul2_rn(y, make_float2(p[at + 2], p[at + 3]));
+                        r[j] = pack2<T>(x.x, x.y);
+                        r[j + 1] = pack2<T>(y.x, y.y);
                     }
+                    tc::tmem_st32(my_dp, r);
                     tc::tmem_wait_st();
                     arrive(&sh.dsready);
                 }
@@ -943,14 +936,11 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 ok = up.warp_wait(&sh.kempty[(g - 2) % KS], ((g - 2) / KS) & 1u, released);
                 if (!ok)
                     break;
+                uint32_t r[32];
 #pragma unroll
-                for (int k = 0; k < SH::cols; k += 32) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        r[j] = pack2<T>(ds[k + 2 * j], ds[k + 2 * j + 1]);
-                    tc::tmem_st16(my_ds + (g & 1u) * (SH::inner / 2) + k / 2, r);
-                }
+                for (int j = 0; j < 32; ++j)
+                    r[j] = pack2<T>(ds[2 * j], ds[2 * j + 1]);
+                tc::tmem_st32(my_ds + (g & 1u) * (SH::inner / 2), r);
                 scored = t + 1 < it.hi && up.ask(&sh.sfull, (g + 1) & 1u);
                 tc::tmem_wait_st();
                 arrive(&sh.dsready);
