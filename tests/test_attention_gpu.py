@@ -134,16 +134,29 @@ TOKENS = [
     (5, 2, 1, 1, 1, 64, BF16, (1, 1, 0, 1, 1), TRIL, 0, None, "bhsd"),
     (1, 64, 1, 2, 300, 128, F16, (300,), TRIL, 0, (298,), "bhsd"),
     (1, 8, 1, 16, 5000, 128, BF16, (5000,), TRIL, 0, (4984,), "bshd"),
+    # several tiles of 16 packed rows share the keys of a key/value head
+    (1, 8, 2, 9, 3000, 64, F16, (2990,), TRIL, 0, (2981,), "bhsd"),
+    (2, 12, 1, 5, 4001, 128, BF16, (4001, 7), WINDOW, 700, (3996, 2), "sliced"),
+    (3, 4, 4, 33, 2500, 64, BF16, (2500, 33, 1200), LENGTH, 0, (2467, 0, 1167), "bshd"),
+]
+# longer sequences: many tiles to an item, many items to a multiprocessor
+LONG = [
+    (1, 4, 2, 2300, 2300, 128, BF16, (2190,), TRIL, 0, None, "bshd"),
+    (1, 4, 1, 2300, 2300, 64, F16, (2300,), TRIL, 0, None, "bhsd"),
+    (1, 2, 2, 2500, 2500, 64, BF16, (2500,), WINDOW, 300, None, "bshd"),
+    (1, 2, 1, 2500, 2500, 128, F16, (2431,), LENGTH, 0, None, "bhsd"),
+    (60, 16, 8, 20, 20, 64, BF16, tuple(1 + (7 * b) % 20 for b in range(60)), TRIL, 0, None, "bhsd"),
+    (60, 16, 8, 150, 150, 128, F16, tuple((37 * b) % 151 for b in range(60)), TRIL, 0, None, "bshd"),
 ]
 
 
-@pytest.mark.parametrize("case", SHAPES + TOKENS, ids=str)
+@pytest.mark.parametrize("case", SHAPES + TOKENS + LONG, ids=str)
 def test_forward_matches_reference(dev, case):
     c = Case(*case)
     c.check_forward(*c.forward())
 
 
-@pytest.mark.parametrize("case", SHAPES + TOKENS[:5], ids=str)
+@pytest.mark.parametrize("case", SHAPES + TOKENS[:5] + LONG, ids=str)
 def test_backward_matches_reference(dev, case):
     c = Case(*case, dstd=0.01)
     ref, ref_lse, _, _ = forward(c.q, c.k, c.v, c.keep, c.scale)
@@ -279,6 +292,60 @@ def test_on_a_side_stream(dev):
     s.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+def test_calls_at_the_same_time(dev):
+    """Calls on several streams at once, each with its own tensors, give what they give alone."""
+    cases = [Case(*s, seed=i) for i, s in enumerate((SHAPES[9], SHAPES[7], SHAPES[8], TOKENS[1], LONG[0], LONG[1]))]
+    want = []
+    for c in cases:
+        o, lse = c.forward()
+        want.append((o, lse, *c.backward(o, lse)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for c, s, g in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                o, lse = gtms.attention_forward(c.q, c.k, c.v, c.lens, c.scale, **c.options)
+                g.append((o, lse, *gtms.attention_backward(c.q, c.k, c.v, o, lse, c.dout, c.lens, c.scale, **c.options)))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for one in g:
+            assert all(torch.equal(a, b) for a, b in zip(one, w))
+
+
+_FIRST_CALL = """
+import sys; sys.path.insert(0, {root!r})
+import torch
+import masked_softmax_attention_gb300 as gtms
+q = torch.randn(1, 4, 200, 64, device="cuda").to(torch.bfloat16)
+lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+pos = torch.arange(200, dtype=torch.int32, device="cuda")
+f = gtms.rotary_frequencies(64, device="cuda")
+def step():
+    x, y = gtms.rotary_forward(q, pos, f, other=q)
+    o, lse = gtms.attention_forward(x, y, q, lens, 0.125)
+    return o, *gtms.attention_backward(x, y, q, o, lse, o, lens, 0.125)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured(dev):
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", _FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "same" in res.stdout, res.stderr[-2000:]
 
 
 @pytest.mark.parametrize("case", [SHAPES[9], TOKENS[1]], ids=str)
