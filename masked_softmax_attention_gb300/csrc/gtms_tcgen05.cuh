@@ -1,6 +1,6 @@
 // gtms_tcgen05.cuh -- the few sm_100+ tensor-core (tcgen05), tensor-memory,
-// mbarrier and asynchronous-copy instructions the fused attention-backward step
-// uses, as inline PTX.
+// mbarrier and asynchronous-copy instructions that the attention kernels use, as
+// inline PTX.
 //
 // Operands live in shared memory in the canonical K-major layout without
 // swizzle: the matrix is cut into core matrices of 8 rows x 16 bytes (8 x 8
@@ -146,20 +146,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
         v[j] = __uint_as_float(r[j]);
 }
 
-// D (tensor memory) = A * B^T (+ D when accumulate != 0) with the A operand in
-// tensor memory: row i in lane i, two consecutive 16-bit K elements to a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate)
-{
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-                 :: "r"(tmem_d), "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-// The same instructions issued by one elected lane of a converged warp. All lanes
-// run the code around them, so that the operands can stay in uniform registers,
-// which the instruction reads: from inside a one-lane branch each costs moves, and
-// 8 products of 128 x 128 x 16 took about 800 cycles to issue where they run in 512.
+// mma_f16 and commit issued by one elected lane of a converged warp. All lanes run
+// the code around them, so that the operands can stay in uniform registers, which
+// the instruction reads: from inside a one-lane branch each costs moves, and 8
+// products of 128 x 128 x 16 took about 800 cycles to issue where they run in 512.
+// _ts: the A operand in tensor memory, row i in lane i, two consecutive 16-bit K
+// elements to a column.
 __device__ __forceinline__ void mma_f16_warp(uint32_t tmem_d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate)
 {
