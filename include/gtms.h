@@ -269,8 +269,9 @@ typedef struct {
  *   status   as in gtms_attention_softmax_backward.
  * k and v at c >= L and q at r >= L are never used: anything may stand there,
  * NaN too. Inside the live length a NaN or infinity in k stays in the rows that
- * keep it; one in v can reach the other rows of its 128-key tile that come before
- * it (a masked probability is an exact zero, but the tile's product multiplies it).
+ * keep it; one in v can also reach rows that mask it, those within 127 rows of one
+ * that keeps a key of the same 128-key tile (a masked probability is an exact zero,
+ * but the tile's product multiplies it).
  * Sums, maxima and accumulators are fp32; probabilities are rounded once to
  * `dtype` for the product with v, and o once on its way out.
  * dtype GTMS_BF16 or GTMS_F16, head_dim 64 or 128. Data 16-byte aligned,
@@ -303,8 +304,8 @@ int gtms_attention_forward(const gtms_attention_shape* shape, const gtms_heads* 
  * give the same bits. p and ds are rounded once to `dtype` for their products.
  * q, o, lse and dout of rows that keep nothing, and k and v at c >= L, are never
  * used; a NaN or infinity in a live row or key can reach the gradients of the rows
- * and keys that share a 128 x 128 tile with it. The three gradients must not overlap each other or any input. Otherwise
- * as gtms_attention_forward.
+ * and keys that share a 128 x 128 tile with it. The three gradients must not overlap
+ * each other or any input. Otherwise as gtms_attention_forward.
  */
 int gtms_attention_backward(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,
                             const gtms_heads* v, const gtms_heads* o, const float* lse, const gtms_heads* dout,
@@ -335,8 +336,8 @@ int gtms_attention_backward_workspace(const gtms_attention_shape* shape, uint64_
  * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, an odd or too
  * large rot_dim, a non-finite amplitude, misaligned pointers, an output that
  * repeats itself or overlaps an input other than as its exact alias.
- * GTMS_ERR_UNSUPPORTED: an unknown dtype, head_dim above 1024, S above
- * GTMS_ATTENTION_MAX_S.
+ * GTMS_ERR_UNSUPPORTED: an unknown dtype, head_dim above 1024, S or H + H2 above
+ * GTMS_ATTENTION_MAX_S, more tokens (B * S) than a grid holds.
  */
 int gtms_rotary(const gtms_heads* x, const gtms_heads* y, const gtms_heads* x2, const gtms_heads* y2, int64_t B,
                 int64_t H, int64_t H2, int64_t S, int64_t head_dim, int64_t rot_dim, const int32_t* positions,

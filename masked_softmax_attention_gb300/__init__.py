@@ -765,6 +765,6 @@ def attention(q, k, v, seq_lens, scale: float = 1.0, mask_kind: int = GTMS_MASK_
 
 
 def rotary(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0):
-    """Differentiable ``rotary_forward``: y, or (y, y_other)."""
+    """Differentiable ``rotary_forward``: y, or (y, y_other). Gradients reach ``x`` and ``other`` alone."""
     rest = () if other is None else (other,)
     return _attention_fn(1).apply(positions, inv_freq, bool(interleaved), float(amplitude), x, *rest)

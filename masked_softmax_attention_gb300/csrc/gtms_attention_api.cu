@@ -276,11 +276,12 @@ GTMS_EXPORT int gtms_rotary(const gtms_heads* x, const gtms_heads* y, const gtms
         return GTMS_ERR_UNSUPPORTED;
     int64_t heads = 0, vectors = 0;
     if (__builtin_add_overflow(H, H2, &heads) || __builtin_mul_overflow(heads, B, &vectors) ||
-        __builtin_mul_overflow(vectors, S, &vectors) || vectors > (int64_t(1) << 40) || B > INT32_MAX ||
-        heads > INT32_MAX)
+        __builtin_mul_overflow(vectors, S, &vectors) || vectors > (int64_t(1) << 40) || heads > GTMS_ATTENTION_MAX_S)
         return GTMS_ERR_UNSUPPORTED;
     if (vectors == 0 || head_dim == 0)
         return GTMS_OK;
+    if (B * S > INT32_MAX)   // a block each
+        return GTMS_ERR_UNSUPPORTED;
     if (!positions || !aligned_to(positions, 4) || (position_batches != 1 && position_batches != B) ||
         (rot_dim > 0 && !inv_freq) || !aligned_to(inv_freq, 4))
         return GTMS_ERR_INVALID_ARG;

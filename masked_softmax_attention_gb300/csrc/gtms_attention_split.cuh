@@ -18,6 +18,7 @@
 // with byte permutations: column n of product j is element 64 y + 8 n + j.
 #pragma once
 
+#include <atomic>
 #include <cooperative_groups.h>
 
 #include "gtms_attention_tc.cuh"
@@ -26,6 +27,7 @@ namespace gtms {
 
 constexpr int kSplitRows = 16, kSplitKeys = 16;   // rows of a tile; keys a warp takes at a time
 constexpr int kSplitMaxCluster = 8;               // the largest portable cluster
+constexpr int kSplitLarge[] = {16, 12};           // larger ones, where the chip has room for all of them at once
 // Warps of a CTA: four, three CTAs to a multiprocessor; eight where the grid has a
 // CTA for at most every other multiprocessor (one token, 8 key/value heads of 8192
 // keys, head dim 128, 64 CTAs: 25.1 -> 18.0 us; 128 CTAs of twice the rows: 26.1 -> 32.2).
@@ -335,26 +337,75 @@ bool prefer_split(const AttentionArgs& a)
     return split < whole;
 }
 
+template <int WARPS>
+struct SplitConfig {
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = {};
+
+    SplitConfig(int64_t ctas, int ranks, int smem, cudaStream_t st)
+    {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(32 * WARPS);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+};
+
+// Clusters of `ranks` CTAs that the current device runs at once: fewer than its
+// multiprocessors would hold, since a cluster keeps to one part of the chip, and not
+// the same on every chip. Asked once per device and process; 0 where it cannot be.
+template <typename T, int D, int WARPS>
+int clusters_at_once(int ranks, int smem)
+{
+    static std::atomic<int> known[64][32];   // plus one; 0: not asked yet
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    if (dev < 64 && (n = known[dev][ranks].load(std::memory_order_relaxed)) > 0)
+        return n - 1;
+    const SplitConfig<WARPS> cfg(ranks, ranks, smem, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, WARPS>, &cfg.cfg) != cudaSuccess) {
+        cudaGetLastError();   // no such clusters here
+        n = 0;
+    }
+    if (dev < 64)
+        known[dev][ranks].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Few units over many keys leave most of the chip idle with clusters of 8: larger
+// ones, if they all run at once, from this many keys on (two blocks to each of 8
+// warps of 16 CTAs). bf16, one sequence, a key/value head of four query heads and of
+// 32768 keys each, head dim 128: 8 heads 46 us with clusters of 8, 36 of 12 (54 of 16,
+// which do not all run at once); 1 head of 16384 keys 24, 16; head dim 64, 4 heads of
+// 16384 keys 16.3, 11.4, of 4200 keys 8.0, 7.4.
+constexpr int64_t kSplitLargeKeys = 4096;
+
 template <typename T, int D, int WARPS>
 cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
 {
     constexpr int smem = static_cast<int>(sizeof(SplitShared<D, WARPS>));
-    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>>(smem);
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>, WARPS == 8>(smem);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(32 * WARPS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    if (WARPS == 8 && ranks == kSplitMaxCluster) {
+        const int64_t units = ctas / ranks;
+        const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window < a.Skv ? a.window : a.Skv;
+        for (int large : kSplitLarge)
+            if (keys >= kSplitLargeKeys && units <= clusters_at_once<T, D, WARPS>(large, smem)) {
+                ranks = large;
+                ctas = units * large;
+                break;
+            }
+    }
+    SplitConfig<WARPS> cfg(ctas, ranks, smem, st);
     const int32_t tiles = static_cast<int32_t>((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
-    return cudaLaunchKernelEx(&cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles);
+    return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles);
 }
 
 template <typename T, int D>

@@ -8,7 +8,8 @@ namespace gtms {
 
 // What a launch needs to know once per device and process, and never changes:
 // the number of multiprocessors, and that the kernel may use `smem` bytes of
-// dynamic shared memory. Devices from 64 on ask every time.
+// dynamic shared memory and, where it wants them, run in clusters of more than
+// eight CTAs. Devices from 64 on ask every time.
 inline int device_sms()
 {
     static std::atomic<int> known[64];
@@ -25,7 +26,7 @@ inline int device_sms()
     return n;
 }
 
-template <auto Kernel>
+template <auto Kernel, bool LargeClusters = false>
 inline cudaError_t allow_smem(int smem)
 {
     static std::atomic<bool> done[64];
@@ -34,6 +35,8 @@ inline cudaError_t allow_smem(int smem)
     if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed)))
         return e;
     e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && LargeClusters)
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && dev < 64)
         done[dev].store(true, std::memory_order_relaxed);
     return e;

@@ -184,8 +184,6 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t st)
     int32_t splits = 1;
     while (tokens * splits < nsm && (heads / splits) * units > kRotaryThreads)
         splits *= 2;
-    if (tokens > INT32_MAX)
-        return cudaErrorNotSupported;
     const int32_t per = (heads + splits - 1) / splits;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((heads + per - 1) / per));

@@ -138,6 +138,11 @@ TOKENS = [
     (1, 8, 2, 9, 3000, 64, F16, (2990,), TRIL, 0, (2981,), "bhsd"),
     (2, 12, 1, 5, 4001, 128, BF16, (4001, 7), WINDOW, 700, (3996, 2), "sliced"),
     (3, 4, 4, 33, 2500, 64, BF16, (2500, 33, 1200), LENGTH, 0, (2467, 0, 1167), "bshd"),
+    # few key/value heads over many keys: clusters of more than eight
+    (1, 8, 8, 1, 4500, 128, F16, (4499,), TRIL, 0, (4498,), "bshd"),
+    (7, 2, 1, 1, 4700, 64, BF16, (4700, 0, 9, 4096, 1, 3000, 193), TRIL, 0, (4699, -1, 8, 4095, 0, 2999, 192), "bhsd"),
+    (4, 4, 1, 2, 9000, 128, BF16, (9000, 5, 4095, 6000), WINDOW, 5000, (8998, 3, 4093, 5998), "sliced"),
+    (1, 3, 1, 4, 16000, 64, F16, (15990,), LENGTH, 0, (15986,), "bhsd"),
 ]
 # longer sequences: many tiles to an item, many items to a multiprocessor
 LONG = [
@@ -172,6 +177,29 @@ def test_masked_places_may_hold_anything(dev, case):
     dead = ~c.keep.any(-1).expand_as(lse)
     o, lse = o.masked_fill(dead[..., None], math.nan), lse.masked_fill(dead, math.nan)
     c.check_backward(c.backward(o, lse))
+
+
+@pytest.mark.parametrize("d,Sq,window,mask", [(64, 900, 40, WINDOW), (128, 900, 40, WINDOW), (128, 900, 0, TRIL),
+                                              (64, 24, 9, WINDOW)])
+def test_how_far_a_live_nan_reaches(dev, d, Sq, window, mask):
+    """One in v: the rows that keep it, and at most those within 127 rows of one that keeps a key of its tile. One in
+    k: the rows that keep it alone."""
+    Skv, at = 900, 880 if Sq < 900 else 300
+    c = Case(1, 2, 1, Sq, Skv, d, BF16, (Skv,), mask, window, (Skv - Sq,), "bhsd", seed=17)
+    clean, _ = c.forward()
+    keeps = c.keep.any(1)[0]                                                   # [Sq, Skv]
+    near = keeps[:, at // 128 * 128:at // 128 * 128 + 128].any(1).nonzero()
+    row = torch.arange(Sq, device="cuda")
+    far = (row < near.min() - 127) | (row > near.max() + 127)
+    for t, safe in ((c.v, far), (c.k, ~keeps[:, at])):
+        old = t[:, :, at].clone()
+        t[:, :, at] = math.nan
+        o, _ = c.forward()
+        t[:, :, at] = old
+        assert bool(torch.isnan(o[:, :, keeps[:, at]]).all())
+        assert bool(torch.isfinite(o[:, :, safe]).all())
+        if t is c.v:                                                           # the scores are the same, and so are the bits
+            assert torch.equal(o[:, :, safe], clean[:, :, safe])
 
 
 @pytest.mark.parametrize("scale,std", [(-0.2, 1.0), (0.0, 1.0), (1.0, 3.0), (0.125, 20.0)])

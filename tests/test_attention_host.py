@@ -167,6 +167,12 @@ def test_rotary_errors():
     assert rot(B=1 << 40) == UNSUPPORTED
 
 
+def test_rotary_extents():
+    many = gtms.GTMS_ATTENTION_MAX_S + 1
+    assert rot(B=1, H=many, S=1, sx=(0, 64, 64), sy=(0, 64, 64), pb=1) == UNSUPPORTED
+    assert rot(B=1 << 16, H=1, S=1 << 15, sx=(0, 0, 64), sy=(0, 64, 64), pb=1) == UNSUPPORTED   # 2^31 tokens
+
+
 def test_rotary_frequencies():
     d, base = 128, 500000.0
     want = base ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
