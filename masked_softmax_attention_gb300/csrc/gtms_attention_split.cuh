@@ -27,10 +27,10 @@ namespace gtms {
 
 constexpr int kSplitRows = 16, kSplitKeys = 16;   // rows of a tile; keys a warp takes at a time
 constexpr int kSplitMaxCluster = 8;               // the largest portable cluster
-constexpr int kSplitLarge[] = {16, 12};           // larger ones, where the chip has room for all of them at once
-// Warps of a CTA: four, three CTAs to a multiprocessor; eight where the grid has a
-// CTA for at most every other multiprocessor (one token, 8 key/value heads of 8192
-// keys, head dim 128, 64 CTAs: 25.1 -> 18.0 us; 128 CTAs of twice the rows: 26.1 -> 32.2).
+constexpr int kSplitLarge[] = {16, 12, 10};          // larger ones, where the chip has room for all of them at once
+// Warps of a CTA: four, three CTAs to a multiprocessor; eight and one CTA where all
+// clusters then run at once (one token, 10 key/value heads of 8192 keys, 80 CTAs: head
+// dim 128 23.8 -> 17.5 us, 64 16.5 -> 11.6; 16 heads, whose 128 CTAs do not: 27.9, 32.4).
 
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -339,28 +339,30 @@ bool prefer_split(const AttentionArgs& a)
 
 template <int WARPS>
 struct SplitConfig {
+    template <int D>
+    static constexpr int smem = static_cast<int>(sizeof(SplitShared<D, WARPS>));
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
 
-    SplitConfig(int64_t ctas, int ranks, int smem, cudaStream_t st)
+    SplitConfig(int64_t ctas, int ranks, int bytes, cudaStream_t st)
     {
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = static_cast<unsigned>(ranks);
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         cfg.blockDim = dim3(32 * WARPS);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = bytes;
         cfg.stream = st;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
     }
 };
 
-// Clusters of `ranks` CTAs that the current device runs at once: fewer than its
-// multiprocessors would hold, since a cluster keeps to one part of the chip, and not
-// the same on every chip. Asked once per device and process; 0 where it cannot be.
-template <typename T, int D, int WARPS>
-int clusters_at_once(int ranks, int smem)
+// Clusters of `ranks` CTAs of eight warps that the current device runs at once: fewer
+// than its multiprocessors would hold, since a cluster keeps to one part of the chip,
+// and not the same on every chip. Asked once per device and process; 0 where it cannot be.
+template <typename T, int D>
+int clusters_at_once(int ranks)
 {
     static std::atomic<int> known[64][32];   // plus one; 0: not asked yet
     int dev = 0, n = 0;
@@ -368,8 +370,10 @@ int clusters_at_once(int ranks, int smem)
         return 0;
     if (dev < 64 && (n = known[dev][ranks].load(std::memory_order_relaxed)) > 0)
         return n - 1;
-    const SplitConfig<WARPS> cfg(ranks, ranks, smem, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, WARPS>, &cfg.cfg) != cudaSuccess) {
+    constexpr int smem = SplitConfig<8>::template smem<D>;
+    const SplitConfig<8> cfg(ranks, ranks, smem, nullptr);
+    if (allow_smem<gtms_attention_split_kernel<T, D, 8>, true>(smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, 8>, &cfg.cfg) != cudaSuccess) {
         cudaGetLastError();   // no such clusters here
         n = 0;
     }
@@ -382,27 +386,17 @@ int clusters_at_once(int ranks, int smem)
 // ones, if they all run at once, from this many keys on (two blocks to each of 8
 // warps of 16 CTAs). bf16, one sequence, a key/value head of four query heads and of
 // 32768 keys each, head dim 128: 8 heads 46 us with clusters of 8, 36 of 12 (54 of 16,
-// which do not all run at once); 1 head of 16384 keys 24, 16; head dim 64, 4 heads of
-// 16384 keys 16.3, 11.4, of 4200 keys 8.0, 7.4.
+// which do not all run at once), 13 of 8192 keys 18.0, 17.2 of 10; 1 head of 16384 keys
+// 24, 16 of 16; head dim 64, 4 heads of 16384 keys 16.3, 11.4, of 4200 keys 8.0, 7.4.
 constexpr int64_t kSplitLargeKeys = 4096;
 
 template <typename T, int D, int WARPS>
 cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
 {
-    constexpr int smem = static_cast<int>(sizeof(SplitShared<D, WARPS>));
+    constexpr int smem = SplitConfig<WARPS>::template smem<D>;
     const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>, WARPS == 8>(smem);
     if (e != cudaSuccess)
         return e;
-    if (WARPS == 8 && ranks == kSplitMaxCluster) {
-        const int64_t units = ctas / ranks;
-        const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window < a.Skv ? a.window : a.Skv;
-        for (int large : kSplitLarge)
-            if (keys >= kSplitLargeKeys && units <= clusters_at_once<T, D, WARPS>(large, smem)) {
-                ranks = large;
-                ctas = units * large;
-                break;
-            }
-    }
     SplitConfig<WARPS> cfg(ctas, ranks, smem, st);
     const int32_t tiles = static_cast<int32_t>((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
     return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles);
@@ -418,8 +412,15 @@ cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
     const int ranks = split_ranks(units, a.Skv, nsm);
     if (units * ranks > INT32_MAX)
         return cudaErrorNotSupported;
-    return 2 * units * ranks <= nsm ? launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st)
-                                : launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
+    if (units * ranks > nsm)   // more clusters than can run at once
+        return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
+    const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window < a.Skv ? a.window : a.Skv;
+    if (keys >= kSplitLargeKeys)
+        for (int large : kSplitLarge)
+            if (units * large <= nsm && units <= clusters_at_once<T, D>(large))
+                return launch_attention_split_w<T, D, 8>(a, units * large, large, st);
+    return units <= clusters_at_once<T, D>(ranks) ? launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st)
+                                                  : launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
 }
 
 }  // namespace gtms

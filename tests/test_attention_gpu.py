@@ -143,6 +143,9 @@ TOKENS = [
     (7, 2, 1, 1, 4700, 64, BF16, (4700, 0, 9, 4096, 1, 3000, 193), TRIL, 0, (4699, -1, 8, 4095, 0, 2999, 192), "bhsd"),
     (4, 4, 1, 2, 9000, 128, BF16, (9000, 5, 4095, 6000), WINDOW, 5000, (8998, 3, 4093, 5998), "sliced"),
     (1, 3, 1, 4, 16000, 64, F16, (15990,), LENGTH, 0, (15986,), "bhsd"),
+    (11, 2, 1, 1, 4100, 128, BF16, tuple(range(4100, 0, -400)), TRIL, 0, tuple(range(4099, -1, -400)), "bhsd"),
+    (3, 5, 5, 1, 600, 64, BF16, (600, 0, 111), LENGTH, 0, (599, 0, 110), "bshd"),
+    (60, 1, 1, 1, 300, 128, F16, tuple(range(1, 301, 5)), TRIL, 0, tuple(range(0, 300, 5)), "bhsd"),
 ]
 # longer sequences: many tiles to an item, many items to a multiprocessor
 LONG = [
