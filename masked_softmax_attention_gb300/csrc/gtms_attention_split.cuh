@@ -358,10 +358,10 @@ struct SplitConfig {
     }
 };
 
-// Clusters of `ranks` CTAs of eight warps that the current device runs at once: fewer
+// Clusters of `ranks` CTAs that the current device runs at once: fewer
 // than its multiprocessors would hold, since a cluster keeps to one part of the chip,
 // and not the same on every chip. Asked once per device and process; 0 where it cannot be.
-template <typename T, int D>
+template <typename T, int D, int WARPS>
 int clusters_at_once(int ranks)
 {
     static std::atomic<int> known[64][32];   // plus one; 0: not asked yet
@@ -370,10 +370,10 @@ int clusters_at_once(int ranks)
         return 0;
     if (dev < 64 && (n = known[dev][ranks].load(std::memory_order_relaxed)) > 0)
         return n - 1;
-    constexpr int smem = SplitConfig<8>::template smem<D>;
-    const SplitConfig<8> cfg(ranks, ranks, smem, nullptr);
-    if (allow_smem<gtms_attention_split_kernel<T, D, 8>, true>(smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, 8>, &cfg.cfg) != cudaSuccess) {
+    constexpr int smem = SplitConfig<WARPS>::template smem<D>;
+    const SplitConfig<WARPS> cfg(ranks, ranks, smem, nullptr);
+    if (allow_smem<gtms_attention_split_kernel<T, D, WARPS>, true>(smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, WARPS>, &cfg.cfg) != cudaSuccess) {
         cudaGetLastError();   // no such clusters here
         n = 0;
     }
@@ -382,19 +382,21 @@ int clusters_at_once(int ranks)
     return n;
 }
 
-// Few units over many keys leave most of the chip idle with clusters of 8: larger
-// ones, if they all run at once, from this many keys on (two blocks to each of 8
-// warps of 16 CTAs). bf16, one sequence, a key/value head of four query heads and of
-// 32768 keys each, head dim 128: 8 heads 46 us with clusters of 8, 36 of 12 (54 of 16,
-// which do not all run at once), 13 of 8192 keys 18.0, 17.2 of 10; 1 head of 16384 keys
-// 24, 16 of 16; head dim 64, 4 heads of 16384 keys 16.3, 11.4, of 4200 keys 8.0, 7.4.
+// Few units over many keys leave most of the chip's memory pipes idle with clusters of
+// 8: larger ones, if they all run at once, from this many keys on (two blocks to each
+// of 8 warps of 16 CTAs). bf16, one token, key/value heads of four query heads each:
+//   eight warps to a CTA, head dim 128: 8 heads of 32768 keys 46 us with clusters of 8,
+//     36 of 12 (54 of 16, which do not all run at once); 13 of 8192 18.0, 17.2 of 10;
+//     1 of 16384 24, 16 of 16; head dim 64: 4 of 16384 16.3, 11.4, of 4200 8.0, 7.4
+//   four warps, head dim 128, 8192 keys: 16 heads 27.5, 22.1 of 16; 28 heads 30.0, 28.1
+//     of 12; 38 heads 36.1, 32.9 of 10; head dim 64: 16 heads 18.1, 14.2
 constexpr int64_t kSplitLargeKeys = 4096;
 
 template <typename T, int D, int WARPS>
 cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
 {
     constexpr int smem = SplitConfig<WARPS>::template smem<D>;
-    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>, WARPS == 8>(smem);
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>, true>(smem);
     if (e != cudaSuccess)
         return e;
     SplitConfig<WARPS> cfg(ctas, ranks, smem, st);
@@ -412,15 +414,17 @@ cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
     const int ranks = split_ranks(units, a.Skv, nsm);
     if (units * ranks > INT32_MAX)
         return cudaErrorNotSupported;
-    if (units * ranks > nsm)   // more clusters than can run at once
-        return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
     const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window < a.Skv ? a.window : a.Skv;
-    if (keys >= kSplitLargeKeys)
-        for (int large : kSplitLarge)
-            if (units * large <= nsm && units <= clusters_at_once<T, D>(large))
-                return launch_attention_split_w<T, D, 8>(a, units * large, large, st);
-    return units <= clusters_at_once<T, D>(ranks) ? launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st)
-                                                  : launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
+    const bool large = keys >= kSplitLargeKeys;
+    for (int r : kSplitLarge)
+        if (large && units <= clusters_at_once<T, D, 8>(r))
+            return launch_attention_split_w<T, D, 8>(a, units * r, r, st);
+    if (units <= clusters_at_once<T, D, 8>(ranks))
+        return launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st);
+    for (int r : kSplitLarge)
+        if (large && units <= clusters_at_once<T, D, 4>(r))
+            return launch_attention_split_w<T, D, 4>(a, units * r, r, st);
+    return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
 }
 
 }  // namespace gtms
