@@ -392,6 +392,13 @@ int clusters_at_once(int ranks)
 //     of 12; 38 heads 36.1, 32.9 of 10; head dim 64: 16 heads 18.1, 14.2
 constexpr int64_t kSplitLargeKeys = 4096;
 
+// Somewhat smaller ones, where the clusters of 8 would need a second turn and these do
+// not: 64 heads of 8192 keys, head dim 128, 65.4 -> 49.0 us (41.1, 40.5 where the lengths
+// spread from 819 on), 80 heads 71.8 -> 57.1 (48.2, 45.7); head dim 64, 64 heads 40.7 ->
+// 28.7. Below 5 spread lengths lose more than equal ones win (128 heads, 8 -> 3: 107.8,
+// 87.5; 69.7, 77.8).
+constexpr int kSplitSmaller[] = {6, 5};
+
 template <typename T, int D, int WARPS>
 cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
 {
@@ -424,6 +431,10 @@ cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
     for (int r : kSplitLarge)
         if (large && units <= clusters_at_once<T, D, 4>(r))
             return launch_attention_split_w<T, D, 4>(a, units * r, r, st);
+    if (ranks == kSplitMaxCluster && units > clusters_at_once<T, D, 4>(ranks))
+        for (int r : kSplitSmaller)
+            if (units <= clusters_at_once<T, D, 4>(r))
+                return launch_attention_split_w<T, D, 4>(a, units * r, r, st);
     return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
 }
 

@@ -145,6 +145,9 @@ TOKENS = [
     (1, 3, 1, 4, 16000, 64, F16, (15990,), LENGTH, 0, (15986,), "bhsd"),
     (11, 2, 1, 1, 4100, 128, BF16, tuple(range(4100, 0, -400)), TRIL, 0, tuple(range(4099, -1, -400)), "bhsd"),
     (3, 5, 5, 1, 600, 64, BF16, (600, 0, 111), LENGTH, 0, (599, 0, 110), "bshd"),
+    (20, 2, 1, 1, 4200, 64, BF16, tuple(range(200, 4201, 210))[:20], WINDOW, 4150, tuple(range(199, 4200, 210))[:20], "bshd"),
+    (15, 8, 4, 1, 2100, 64, F16, tuple(range(140, 2101, 140)), TRIL, 0, tuple(range(139, 2100, 140)), "bhsd"),
+    (40, 4, 2, 1, 2100, 128, BF16, tuple(range(2100, 0, -53))[:40], TRIL, 0, tuple(range(2099, -1, -53))[:40], "bhsd"),
     (60, 1, 1, 1, 300, 128, F16, tuple(range(1, 301, 5)), TRIL, 0, tuple(range(0, 300, 5)), "bhsd"),
 ]
 # longer sequences: many tiles to an item, many items to a multiprocessor
