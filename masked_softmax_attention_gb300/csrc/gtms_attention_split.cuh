@@ -310,14 +310,17 @@ inline int64_t split_units(const AttentionArgs& a)
 }
 
 // Whether to split: always where the rows of a key/value head fill one tile, so that
-// the keys are read once; otherwise where the waves of its CTAs take less time than
-// those of the tensor-memory kernel, whose CTAs (128 rows of one head at head dim
-// 64, 256 at 128) walk over all keys by themselves. Microseconds, from measurements
-// (bf16, keys at least half filled; split / tensor-memory kernel):
-//   32 / 8 heads d 128, 8192 keys, 1 sequence:   8 tokens 26 / 84, 16: 28 / 84, 32: 64 / 84, 64: 103 / 84
-//   the same, 4096 keys:  4 sequences, 8 tokens 32 / 46, 32: 76 / 46;  16 sequences, 8: 83 / 132, 16: 142 / 134
-//   16 / 16 heads d 64, 4096 keys, 32 tokens:    1 sequence 12 / 38, 8: 47 / 40
-//   8 / 8 heads d 64, 33 of 33 rows, 32 sequences: 13 / 7
+// the keys are read once; otherwise where its CTAs (64 keys in 1 to 2.3 us, three to a
+// multiprocessor) take less time than those of the tensor-memory kernel (128 keys in 1
+// to 1.15 us), which walk over all keys by themselves (128 rows of one head at head
+// dim 64, 256 at 128). Microseconds, measured (bf16, keys at least half filled; split /
+// tensor-memory kernel):
+//   32 / 8 heads d 128, 8192 keys, 1 sequence:   8 tokens 23 / 77, 32: 47 / 77, 48: 70 / 77, 64: 103 / 77
+//   the same, 32768 keys:  32 tokens 155 / 288, 64: 344 / 289
+//   the same, 4096 keys:   4 sequences, 8 tokens 26 / 42, 16: 53 / 42;  16 sequences, 8: 83 / 121, 16: 143 / 123
+//   8 / 8 heads d 128, 2000 keys, 100 tokens, 2 sequences: 34 / 24
+//   16 / 16 heads d 64, 4096 keys, 32 tokens:    1 sequence 12 / 37, 8: 47 / 39
+//   8 / 8 heads d 64, 33 of 33 rows, 32 sequences: 13 / 7;  200 rows, 4096 keys, 1 sequence: 31 / 37
 template <int D>
 bool prefer_split(const AttentionArgs& a)
 {
@@ -329,11 +332,12 @@ bool prefer_split(const AttentionArgs& a)
         return false;
     const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + a.Sq < a.Skv ? a.window + a.Sq : a.Skv;
     const int64_t units = split_units(a), ranks = split_ranks(units, keys, nsm);
-    const double split = static_cast<double>((units * ranks + 3 * nsm - 1) / (3 * nsm)) *
-                         (6.0 + 1.4 * static_cast<double>((keys + ranks * 64 - 1) / (ranks * 64)));
-    const int64_t items = static_cast<int64_t>(a.B) * a.Hq * ((a.Sq + FwdTile<D>::rows - 1) / FwdTile<D>::rows);
-    const int64_t slots = static_cast<int64_t>(nsm) * FwdTile<D>::ctas;
-    const double whole = static_cast<double>((items + slots - 1) / slots) * (5.0 + 1.2 * static_cast<double>((keys + 127) / 128));
+    const double turns = static_cast<double>(units * ranks) / (3 * nsm);   // of three CTAs to a multiprocessor
+    const double block = turns > 1.0 ? (D == 64 ? 1.3 : 2.3) : (D == 64 ? 1.0 : 1.8);
+    const double split = (turns > 1.0 ? turns : 1.0) * (6.0 + block * static_cast<double>((keys + ranks * 64 - 1) / (ranks * 64)));
+    const double items = static_cast<double>(a.B) * a.Hq * ((a.Sq + FwdTile<D>::rows - 1) / FwdTile<D>::rows);
+    const double loads = items / (static_cast<double>(nsm) * FwdTile<D>::ctas);
+    const double whole = (loads > 1.0 ? loads : 1.0) * (5.0 + (D == 64 ? 1.0 : 1.15) * static_cast<double>((keys + 127) / 128));
     return split < whole;
 }
 
