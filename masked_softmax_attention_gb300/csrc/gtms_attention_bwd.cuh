@@ -11,6 +11,9 @@
 // the 5 that one pass with dq summed by atomics would take. In exchange nothing
 // but the results goes through memory, no order of sums depends on timing, and
 // each accumulator stays in tensor memory.
+// The launches overlap: the second starts as the first drains and the third, which
+// needs only the first, as the second runs out of items ([2,32/8,4096,128] bf16: 564
+// us one after the other, 528 so; [1,12/4,2611,128] fp16, window 256: 48, 37).
 #pragma once
 
 #include "gtms_attention_tc.cuh"
@@ -69,6 +72,7 @@ gtms_attention_bwd_prep_kernel(const AttentionArgs a, int64_t row_tiles, int64_t
 {
     constexpr int LANES = D / 8, PER = kPrepThreads / LANES, N = 4;
     constexpr bool norms = std::is_same<T, __half>::value;
+    let_next_launch_start();
     const int sub = threadIdx.x % LANES, first = threadIdx.x / LANES;
     float do_norm = 0.0f, v_norm = 0.0f;
     const int32_t tiles_q = a.Sq_pad / kTile, tiles_k = (a.Skv + kTile - 1) / kTile;
@@ -179,7 +183,7 @@ __device__ __forceinline__ float block_gradient_factor(const AttentionArgs& a, f
     if (warp < 2) {
         float m = 0.0f;
         for (int k = lane; k < a.norm_blocks; k += 32)
-            m = fmaxf(m, __ldg(a.norms + warp * kPrepMaxBlocks + k));
+            m = fmaxf(m, __ldcg(a.norms + warp * kPrepMaxBlocks + k));
         m = team_max<32>(m, nullptr);
         if (lane == 0)
             shared2[warp] = m;
@@ -320,6 +324,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         __syncwarp();
         tc::tmem_alloc<SH::tmem>(&sh.tmem_slot);
     }
+    await_last_launch();       // the row statistics stand in memory
+    let_next_launch_start();   // dq needs them, and nothing of this launch
     const float factor = block_gradient_factor<T>(a, sh.norm);
     tc::fence_before_sync();
     __syncthreads();
@@ -971,6 +977,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
         __syncwarp();
         tc::tmem_free<SH::tmem>(tmem);
     }
+    await_last_launch();   // so that the end of this launch is that of the one before it too
 }
 
 template <typename T, int D>
@@ -1007,8 +1014,8 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         constexpr int smem = static_cast<int>(DkvTile<D>::smem);
         e = allow_smem<gtms_attention_dkv_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)), BwdShape<D>::threads, smem, st, mq,
-                              mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
+            e = launch_beside_last(a.norm_blocks > 0, kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)),
+                                   BwdShape<D>::threads, smem, st, mq, mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
     }
     if (e == cudaSuccess && rows) {
         auto* kern = gtms_attention_dq_kernel<T, D>;
@@ -1016,8 +1023,8 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
         const int32_t blocks = a.Sq_pad / kTile;
         e = allow_smem<gtms_attention_dq_kernel<T, D>>(smem);
         if (e == cudaSuccess)
-            e = launch_kernel(kern, static_cast<unsigned>(heads * blocks), BwdShape<D>::threads, smem, st, mq, mk, mv, mdo, a,
-                              static_cast<uint32_t>(heads), blocks, wait_ns);
+            e = launch_beside_last(keys, kern, static_cast<unsigned>(heads * blocks), BwdShape<D>::threads, smem, st, mq, mk, mv, mdo,
+                                   a, static_cast<uint32_t>(heads), blocks, wait_ns);
     }
     return e;
 }

@@ -111,6 +111,29 @@ struct GiveUp {
     }
 };
 
+// Launches that follow each other in a stream and may overlap: a kernel lets the next
+// one start (once every CTA of its own has said so or has gone), and that one waits
+// for the end of this, with all of its writes, where it needs it.
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_last_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_beside_last(bool beside, void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                                      cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Zeroes rows [from, to) of a swizzled tile of ROWS rows (a whole warp works).
 template <int D, int ROWS>
 __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int32_t from, int32_t to, int lane)

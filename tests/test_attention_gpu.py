@@ -328,6 +328,28 @@ def test_on_a_side_stream(dev):
     assert all(torch.equal(a, b) for a, b in zip(got, grads))
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_calls_one_after_the_other(dev, d, dtype):
+    """The launches of a call overlap (few long items of dk and dv beside many short ones of dq), but what follows in
+    the stream, the next call in the same memory too, stands behind all of them."""
+    cases = [Case(1, 8, 1, S, S, d, dtype, (n,), TRIL, 0, None, "bhsd", seed=s) for s, (S, n) in
+             enumerate([(1500, 1500), (1200, 1100), (900, 900)], 30)]
+    first = []
+    for c in cases:
+        o, lse = c.forward()
+        first.append((o, lse, [t.clone() for t in c.backward(o, lse)]))
+    out = [torch.empty_like(t) for t in (cases[0].q, cases[0].k, cases[0].v)]
+    for _ in range(6):
+        seen = []
+        for c, (o, lse, _g) in zip(cases, first):
+            views = tuple(b.view(-1)[:t.numel()].view(t.shape) for b, t in zip(out, (c.q, c.k, c.v)))
+            gtms.attention_backward(c.q, c.k, c.v, o, lse, c.dout, c.lens, c.scale, out=views, **c.options)
+            seen.append([t.clone() for t in views])
+        for got, (_o, _l, want) in zip(seen, first):
+            for g, w in zip(got, want):
+                assert torch.equal(g, w)
+
+
 def test_calls_at_the_same_time(dev):
     """Calls on several streams at once, each with its own tensors, give what they give alone."""
     cases = [Case(*s, seed=i) for i, s in enumerate((SHAPES[9], SHAPES[7], SHAPES[8], TOKENS[1], LONG[0], LONG[1]))]
