@@ -13,7 +13,7 @@
 // each accumulator stays in tensor memory.
 // The launches overlap: the second starts as the first drains and the third, which
 // needs only the first, as the second runs out of items ([2,32/8,4096,128] bf16: 564
-// us one after the other, 528 so; [1,12/4,2611,128] fp16, window 256: 48, 37).
+// us one after the other, 528 so; [1,12/4,2611,128] fp16, window 256: 48, 38).
 #pragma once
 
 #include "gtms_attention_tc.cuh"
@@ -62,8 +62,9 @@ __device__ __forceinline__ float gradient_factor(float do_norm, float v_norm)
 }
 
 // Per padded query row: kPShift - lse log2(e) (-inf where nothing is kept, which
-// makes every p of the row zero) and -D, so that both are added. For fp16 also the largest norms of the
-// live rows of do and of the live keys of v, one partial maximum per block.
+// makes every p of the row zero) and -D, so that both are added. For fp16 also the
+// largest norms of the live rows of do and of the live keys of v, one partial maximum
+// per block.
 // A block takes 128 rows of one head at a time, D / 8 lanes to a row, and has the
 // loads of four rows in flight per thread.
 template <typename T, int D>
