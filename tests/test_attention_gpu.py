@@ -148,6 +148,11 @@ TOKENS = [
     (20, 2, 1, 1, 4200, 64, BF16, tuple(range(200, 4201, 210))[:20], WINDOW, 4150, tuple(range(199, 4200, 210))[:20], "bshd"),
     (15, 8, 4, 1, 2100, 64, F16, tuple(range(140, 2101, 140)), TRIL, 0, tuple(range(139, 2100, 140)), "bhsd"),
     (40, 4, 2, 1, 2100, 128, BF16, tuple(range(2100, 0, -53))[:40], TRIL, 0, tuple(range(2099, -1, -53))[:40], "bhsd"),
+    # more CTAs than run at once: sequences are taken by length, ties and empty ones among them
+    (70, 8, 8, 1, 600, 64, BF16, tuple((97 * b) % 601 // 3 * 3 for b in range(70)), TRIL, 0,
+     tuple((97 * b) % 601 // 3 * 3 - 1 for b in range(70)), "bshd"),
+    (256, 2, 2, 1, 140, 128, F16, tuple(b % 140 for b in range(256)), LENGTH, 0, (0,) * 256, "bhsd"),
+    (257, 4, 2, 2, 90, 64, BF16, tuple(90 - b % 70 for b in range(257)), WINDOW, 40, tuple(88 - b % 70 for b in range(257)), "bhsd"),
     (60, 1, 1, 1, 300, 128, F16, tuple(range(1, 301, 5)), TRIL, 0, tuple(range(0, 300, 5)), "bhsd"),
 ]
 # longer sequences: many tiles to an item, many items to a multiprocessor
