@@ -343,6 +343,10 @@ inline int64_t split_units(const AttentionArgs& a)
 //   8 / 8 heads d 128, 2000 keys, 100 tokens, 2 sequences: 34 / 24
 //   16 / 16 heads d 64, 4096 keys, 32 tokens:    1 sequence 12 / 37, 8: 47 / 39
 //   8 / 8 heads d 64, 33 of 33 rows, 32 sequences: 13 / 7;  200 rows, 4096 keys, 1 sequence: 31 / 37
+//   4 / 1 heads d 64, 8071 keys, 212 tokens, 1 sequence: 24 / 69;  2 / 1 heads d 128, 7381 keys, 316 tokens, 2: 42 / 80
+//   4 / 1 heads d 128, 3162 keys, 791 tokens, 3 sequences: 102 / 39
+constexpr int64_t kSplitMaxRows = 4096;   // of a key/value head: more are never better split
+
 template <int D>
 bool prefer_split(const AttentionArgs& a)
 {
@@ -350,7 +354,7 @@ bool prefer_split(const AttentionArgs& a)
     if (rows <= kSplitRows)
         return true;
     const int nsm = device_sms();
-    if (rows > 16 * kSplitRows || nsm <= 0)
+    if (rows > kSplitMaxRows || nsm <= 0)
         return false;
     const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + a.Sq < a.Skv ? a.window + a.Sq : a.Skv;
     const int64_t units = split_units(a), ranks = split_ranks(units, keys, nsm);

@@ -148,6 +148,10 @@ TOKENS = [
     (20, 2, 1, 1, 4200, 64, BF16, tuple(range(200, 4201, 210))[:20], WINDOW, 4150, tuple(range(199, 4200, 210))[:20], "bshd"),
     (15, 8, 4, 1, 2100, 64, F16, tuple(range(140, 2101, 140)), TRIL, 0, tuple(range(139, 2100, 140)), "bhsd"),
     (40, 4, 2, 1, 2100, 128, BF16, tuple(range(2100, 0, -53))[:40], TRIL, 0, tuple(range(2099, -1, -53))[:40], "bhsd"),
+    # many rows, but few key/value heads and many keys
+    (1, 4, 1, 150, 4000, 64, F16, (3990,), TRIL, 0, (3840,), "sliced"),
+    (2, 2, 1, 300, 3500, 128, BF16, (3500, 2100), WINDOW, 2000, (3200, 1800), "bhsd"),
+    (1, 1, 1, 700, 6000, 128, F16, (5999,), LENGTH, 0, (5299,), "bshd"),
     # more CTAs than run at once: sequences are taken by length, ties and empty ones among them
     (70, 8, 8, 1, 600, 64, BF16, tuple((97 * b) % 601 // 3 * 3 for b in range(70)), TRIL, 0,
      tuple((97 * b) % 601 // 3 * 3 - 1 for b in range(70)), "bshd"),
@@ -161,6 +165,8 @@ LONG = [
     (1, 4, 1, 2300, 2300, 64, F16, (2300,), TRIL, 0, None, "bhsd"),
     (1, 2, 2, 2500, 2500, 64, BF16, (2500,), WINDOW, 300, None, "bshd"),
     (1, 2, 1, 2500, 2500, 128, F16, (2431,), LENGTH, 0, None, "bhsd"),
+    (6, 16, 4, 300, 900, 128, F16, (900, 450, 301, 0, 777, 899), WINDOW, 200, (600, 150, 1, -300, 477, 599), "bshd"),
+    (4, 16, 4, 260, 700, 64, BF16, (700, 261, 260, 500), TRIL, 0, (440, 1, 0, 240), "sliced"),
     (60, 16, 8, 20, 20, 64, BF16, tuple(1 + (7 * b) % 20 for b in range(60)), TRIL, 0, None, "bhsd"),
     (60, 16, 8, 150, 150, 128, F16, tuple((37 * b) % 151 for b in range(60)), TRIL, 0, None, "bshd"),
 ]
