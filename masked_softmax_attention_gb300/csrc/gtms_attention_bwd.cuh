@@ -687,7 +687,11 @@ struct DqItem {
 struct DqShared {
     uint64_t qfull, qempty, dofull, doempty;
     uint64_t kfull[4], kempty[4], vfull[3], vempty[3], raw;
-    uint64_t sfull, sread, dpfull, dpread, dsready, accfull, accempty, mma_done;
+    uint64_t sfull, sread, dpfull, dpread, accfull, accempty, mma_done;
+    // One for each copy of dS: S and dP of the next tile are formed before the MMA warp waits for this one's dS,
+    // so that a late MMA warp can find dS of both written. On one barrier that is two phases, which a parity bit
+    // does not tell from none.
+    uint64_t dsready[2];
     ItemSlot<DqItem> items;
     uint32_t tmem_slot;
     int flag;
@@ -724,7 +728,8 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
         }
         tc::mbar_init(&sh.sread, SH::warps);
         tc::mbar_init(&sh.dpread, SH::warps);
-        tc::mbar_init(&sh.dsready, SH::warps);
+        tc::mbar_init(&sh.dsready[0], SH::warps);
+        tc::mbar_init(&sh.dsready[1], SH::warps);
         tc::mbar_init(&sh.accempty, SH::warps);
         init_items(sh.items, SH::warps + 2);   // load, MMA and element-wise warps
         sh.flag = 0;
@@ -862,7 +867,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                         if (ok)
                             products(g + 1, k + 2 == n);
                     }
-                    ok = ok && up.warp_wait(&sh.dsready, g & 1u);
+                    ok = ok && up.warp_wait(&sh.dsready[g & 1u], (g >> 1) & 1u);
                     if (ok && k == 0)
                         ok = up.warp_wait(&sh.accempty, (ni & 1u) ^ 1u);
                     if (!ok)
@@ -954,7 +959,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 tc::tmem_st32(my_ds + (g & 1u) * (SH::inner / 2), r);
                 scored = t + 1 < it.hi && up.ask(&sh.sfull, (g + 1) & 1u);
                 tc::tmem_wait_st();
-                arrive(&sh.dsready);
+                arrive(&sh.dsready[g & 1u]);
             }
             if (!ok)
                 break;

@@ -15,6 +15,11 @@ namespace gtms {
 
 constexpr int kTile = 128;   // rows and columns of one score tile
 
+// Where a test build makes chosen warps late: before every wait of theirs.
+#ifndef GTMS_ATTENTION_BEFORE_WAIT
+#define GTMS_ATTENTION_BEFORE_WAIT()
+#endif
+
 // A strided [B, H, S, D] tensor as a 4-D map (d, s, h, b) of 64-column boxes with
 // the 128-byte swizzle. Rows past S read as zero. A broadcast dimension (stride 0)
 // becomes an extent of one, and the kernels' coordinates along it are multiplied
@@ -80,6 +85,7 @@ struct GiveUp {
     }
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const
     {
+        GTMS_ATTENTION_BEFORE_WAIT();
         if (tc::mbar_try_wait(bar, parity))
             return true;
         const uint64_t t0 = tc::globaltimer_ns();
