@@ -266,7 +266,9 @@ typedef struct {
  *   o        [B, Hq, Sq, head_dim], every element written.
  *   lse      fp32 [B, Hq, Sq], contiguous, or NULL.
  *   seq_lens device int32[B]; q_offsets device int32[B] or NULL.
- *   status   as in gtms_attention_softmax_backward.
+ *   status   as in gtms_attention_softmax_backward; the limit of 1 s is that of the
+ *            hand-offs of one tile, and however long the rows are, a call that
+ *            makes progress is not given up.
  * k and v at c >= L and q at r >= L are never used: anything may stand there,
  * NaN too. Inside the live length a NaN or infinity in k stays in the rows that
  * keep it; one in v can also reach rows that mask it, those within 127 rows of one

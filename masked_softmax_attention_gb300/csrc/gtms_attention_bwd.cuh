@@ -283,6 +283,10 @@ struct DkvItem {
             hi = ib / inner + 1;
         }
     }
+    __device__ __forceinline__ uint32_t steps(const AttentionArgs& a) const
+    {
+        return static_cast<uint32_t>(hi - lo) * static_cast<uint32_t>(a.group);
+    }
 };
 
 struct DkvShared {
@@ -341,7 +345,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
         if (warp == SH::deal_warp) {
-            deal_items(sh.items, up, lane, [&](int32_t index) {
+            deal_items(sh.items, up, lane, a, [&](int32_t index) {
                 DkvItem it;
                 it.set(a, index, heads, SH::inner);
                 return it;
@@ -682,6 +686,7 @@ struct DqItem {
             full1 = a1;
         }
     }
+    __device__ __forceinline__ uint32_t steps(const AttentionArgs&) const { return hi - lo; }
 };
 
 struct DqShared {
@@ -748,7 +753,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
     if (warp >= SH::mma_warp) {
         tc::regs_lower<SH::other_regs>();
         if (warp == SH::deal_warp) {
-            deal_items(sh.items, up, lane, [&](int32_t index) {
+            deal_items(sh.items, up, lane, a, [&](int32_t index) {
                 DqItem it;
                 it.set(a, index, heads, blocks, SH::inner);
                 return it;

@@ -117,6 +117,7 @@ struct FwdItem {
             t = hi[w] > 0 && lo[w] < t ? lo[w] : t;
         return t;
     }
+    __device__ __forceinline__ uint32_t steps(const AttentionArgs&) const { return top() > 0 ? top() - bottom() : 0; }
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
 };
 
@@ -178,7 +179,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     if (warp >= TL::mma_warp) {
         tc::regs_lower<TL::other_regs>();
         if (warp == TL::deal_warp) {
-            deal_items(sh.items, up, lane, [&](int32_t index) {
+            deal_items(sh.items, up, lane, a, [&](int32_t index) {
                 Item it;
                 it.set(a, index, heads, blocks);
                 return it;
@@ -360,7 +361,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             const bool live = c0 < c1 && i < a.Sq;
             float m = -INFINITY, l = 0.0f;
             for (int32_t t = hi - 1; t >= lo; --t) {
-                ok = up.warp_wait(&sh.sfull[w], ns & 1u);
+                // The first scores may have to wait while the other tile has a whole item to itself.
+                ok = item_wait(sh.items, up, &sh.sfull[w], ns & 1u);
                 ++ns;
                 if (!ok)
                     break;

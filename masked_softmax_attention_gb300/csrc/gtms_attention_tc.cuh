@@ -68,7 +68,8 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const HeadsMap& m, int32
             tc::tma_load_4d(dst + (x * ROWS + y) * 128, &m.map, x * 64, row0 + y, h * m.mh, b * m.mb, bar);
 }
 
-// Every wait of these kernels is bounded: one that runs out raises the flag and
+// Every wait of these kernels is bounded (limit_ns, or for a whole item that much for
+// each of its tiles, see item_wait): one that runs out raises the flag and
 // the caller's status word, and every other role leaves its loop at the next wait
 // that does not succeed at once.
 struct GiveUp {
@@ -83,7 +84,8 @@ struct GiveUp {
         if (status)
             atomicOr(status, GTMS_ERR_TIMEOUT);
     }
-    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const
+    // With a limit of 4 (*tiles + 1) times limit_ns where `tiles` is given.
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* tiles = nullptr) const
     {
         GTMS_ATTENTION_BEFORE_WAIT();
         if (tc::mbar_try_wait(bar, parity))
@@ -94,7 +96,7 @@ struct GiveUp {
                 return true;
             if (raised())
                 return false;
-            if (tc::globaltimer_ns() - t0 >= limit_ns) {
+            if (tc::globaltimer_ns() - t0 >= (tiles ? 4 * (uint64_t(*tiles) + 1) * limit_ns : limit_ns)) {
                 raise();
                 return false;
             }
@@ -114,6 +116,11 @@ struct GiveUp {
     __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) const
     {
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    }
+    // A wait that lasts as long as work on so many tiles, each with a few hand-offs.
+    __device__ __forceinline__ bool warp_wait_tiles(uint64_t* bar, uint32_t parity, const volatile uint32_t* tiles) const
+    {
+        return __all_sync(0xffffffffu, wait(bar, parity, tiles)) != 0;
     }
 };
 
@@ -163,6 +170,7 @@ template <typename Item>
 struct ItemSlot {
     __align__(16) uint4 response;
     uint64_t full, empty, answered;
+    uint32_t longest;   // tiles of the longest item dealt yet
     Item item;
 };
 
@@ -172,20 +180,34 @@ __device__ __forceinline__ void init_items(ItemSlot<Item>& s, int readers)
     tc::mbar_init(&s.full, 1);
     tc::mbar_init(&s.empty, readers);
     tc::mbar_init(&s.answered, 1);
+    s.longest = 0;
 }
 
-// The dealing warp: make(index) is the item of a CTA index; an item with b < 0 ends
-// the deal. The next item is asked for once every reader has taken the last. Where
-// a role has given up, the CTAs that are left are taken over all the same and
-// dropped, so that a grid that cannot make progress ends at once and not CTA by CTA.
+// Waits for an item to be dealt, for all readers to have taken it, and for its first
+// results by a reader that had no rows in the one before it, last as long as a warp is
+// busy with the one before. An item has as many tiles as rows or keys and shared heads
+// make, so the limit goes by the longest one yet, and is read only once the wait has not
+// succeeded at once; the waits inside an item, whose limit is a hand-off's, end these
+// too where they run out, by the raised flag.
+template <typename Item>
+__device__ __forceinline__ bool item_wait(const ItemSlot<Item>& s, const GiveUp& up, uint64_t* bar, uint32_t parity)
+{
+    return up.warp_wait_tiles(bar, parity, &s.longest);
+}
+
+// The dealing warp: make(index) is the item of a CTA index, whose steps(a) are the
+// tiles that a warp walks over; an item with b < 0 ends the deal. The next item is asked
+// for once every reader has taken the last. Where a role has given up, the CTAs that are
+// left are taken over all the same and dropped, so that a grid that cannot make progress
+// ends at once and not CTA by CTA.
 template <typename Item, typename Make>
-__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, Make make)
+__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, const AttentionArgs& a, Make make)
 {
     int32_t index = blockIdx.x;
     bool ok = true;
     for (uint32_t n = 0; index >= 0; ++n) {
         if (n > 0) {
-            ok = ok && up.warp_wait(&s.empty, (n - 1) & 1u);
+            ok = ok && item_wait(s, up, &s.empty, (n - 1) & 1u);
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&s.answered, 16);
                 tc::next_cta_request(tc::smem_u32(&s.response), &s.answered);
@@ -203,10 +225,15 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
             continue;
         Item it;
         it.b = -1;
-        if (index >= 0)
+        uint32_t steps = 0;
+        if (index >= 0) {
             it = make(index);
+            steps = it.steps(a);
+        }
         if (lane == 0) {
             s.item = it;
+            if (steps > s.longest)
+                *reinterpret_cast<volatile uint32_t*>(&s.longest) = steps;
             tc::mbar_arrive(&s.full);
         }
     }
@@ -217,7 +244,7 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
 template <typename Item, typename Read>
 __device__ __forceinline__ bool take_item(ItemSlot<Item>& s, const GiveUp& up, int lane, uint32_t& n, bool& ok, Read read)
 {
-    ok = ok && up.warp_wait(&s.full, n & 1u);
+    ok = ok && item_wait(s, up, &s.full, n & 1u);
     if (!ok)
         return false;
     const bool more = s.item.b >= 0;

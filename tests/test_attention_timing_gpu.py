@@ -77,3 +77,13 @@ def test_late_warps_change_nothing(probe, backward, d, late):
     bits = {"mma": 1 << n, "load": 2 << n, "deal": 4 << n, "first element-wise": 1, "last element-wise": 1 << (n - 1),
             "mma and load": 3 << n}[late]
     Run(2, 4, 2, 700, d, (700, 613), TRIL).check(probe, backward, bits, 20_000)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("lens,mask", [((50000,), LENGTH), ((50000, 70), TRIL)])
+def test_items_may_outlast_the_limit_of_a_wait(probe, lens, mask, backward, d):
+    """The limit is that of a hand-off inside a tile (1 to 2 us of work), however many tiles an item has: here it is 120
+    us and the items of some 400 tiles take three times that and more. There are more items than CTAs at once, so that
+    the deal waits for whole items, and some in which a warp has no rows."""
+    Run(len(lens), 2, 1, 50000, d, lens, mask).check(probe, backward, wait_ns=120_000)
