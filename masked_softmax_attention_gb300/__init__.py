@@ -710,11 +710,12 @@ def _attention_functions():
 
     class Attention(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, v, seq_lens, q_offsets, scale, mask_kind, window):
+        def forward(ctx, q, k, v, seq_lens, q_offsets, scale, mask_kind, window, status):
             o, lse = attention_forward(q, k, v, seq_lens, scale, mask_kind=mask_kind, window=window,
-                                       q_offsets=q_offsets)
+                                       q_offsets=q_offsets, status=status)
             ctx.save_for_backward(q, k, v, o, lse, seq_lens, q_offsets)
             ctx.options = scale, mask_kind, window
+            ctx.status = status   # written by both calls, so not one of the saved tensors, which must not change
             return o
 
         @staticmethod
@@ -723,8 +724,8 @@ def _attention_functions():
             q, k, v, o, lse, seq_lens, q_offsets = ctx.saved_tensors
             scale, mask_kind, window = ctx.options
             dq, dk, dv = attention_backward(q, k, v, o, lse, _usable(dout), seq_lens, scale, mask_kind=mask_kind,
-                                            window=window, q_offsets=q_offsets)
-            return dq, dk, dv, None, None, None, None, None
+                                            window=window, q_offsets=q_offsets, status=ctx.status)
+            return dq, dk, dv, None, None, None, None, None, None
 
     class Rotary(torch.autograd.Function):
         @staticmethod
@@ -756,12 +757,16 @@ def _attention_fn(i):
 
 
 def attention(q, k, v, seq_lens, scale: float = 1.0, mask_kind: int = GTMS_MASK_GROUPED_TRIL, window: int = 0,
-              q_offsets=None):
+              q_offsets=None, status=None):
     """Differentiable ``attention_forward`` (o alone); the backward is ``attention_backward``.
+
+    ``status``, an int32 CUDA tensor of one element, is handed to both: cleared before the step and read after
+    synchronising, it says whether a wait inside a kernel ran out, so that o or the gradients are incomplete
+    (``GTMS_ERR_TIMEOUT``). Without it nothing says so.
 
     To capture a training step into a CUDA graph, capture ``attention_forward`` and ``attention_backward``
     themselves, which make no autograd nodes."""
-    return _attention_fn(0).apply(q, k, v, seq_lens, q_offsets, float(scale), int(mask_kind), int(window))
+    return _attention_fn(0).apply(q, k, v, seq_lens, q_offsets, float(scale), int(mask_kind), int(window), status)
 
 
 def rotary(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0):

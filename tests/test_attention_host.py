@@ -202,3 +202,24 @@ def test_tensor_api_refusals():
                  lambda: gtms.rotary(z[0], pos, f)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_differentiable_attention_hands_its_status_on(monkeypatch):
+    """A wait that runs out in the forward or in the backward can be seen by the caller of attention()."""
+    q = torch.zeros(1, 2, 3, 64, requires_grad=True)
+    lens, status, seen = torch.ones(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), []
+
+    def fwd_call(q, k, v, seq_lens, scale, status=None, **kw):
+        seen.append(("forward", status))
+        return torch.zeros_like(q), torch.zeros(q.shape[:3])
+
+    def bwd_call(q, k, v, o, lse, dout, seq_lens, scale, status=None, **kw):
+        seen.append(("backward", status))
+        status.add_(4)
+        return torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+
+    monkeypatch.setattr(gtms, "attention_forward", fwd_call)
+    monkeypatch.setattr(gtms, "attention_backward", bwd_call)
+    gtms.attention(q, q.detach(), q.detach(), lens, status=status).sum().backward()
+    assert [n for n, _ in seen] == ["forward", "backward"] and all(t is status for _, t in seen)
+    assert int(status) == 4
