@@ -697,11 +697,13 @@ def rotary_backward(dy, positions, inv_freq, other=None, interleaved: bool = Fal
 
 
 def _usable(t):
-    """A gradient as the kernels take it: one that autograd expanded or sliced is copied."""
+    """A gradient as the kernels take it: one that autograd expanded, or whose data stands at an odd place, is copied."""
+    import torch
+
     aligned = 16 // t.element_size()
     ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(n <= 1 or (s % aligned == 0 and s >= t.shape[3])
                                                             for n, s in zip(t.shape[:3], t.stride()[:3]))
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)   # contiguous() keeps a dense tensor where it is
 
 
 def _attention_functions():

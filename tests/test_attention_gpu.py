@@ -301,6 +301,38 @@ def test_shared_and_broadcast_inputs(dev):
         _close("broadcast", leaf.grad, total, tol)
 
 
+def _odd_gradients(dev, t):
+    """Gradients of t's shape as autograd may hand them over: expanded, transposed, at an odd address, every other one."""
+    B, H, S, d = t.shape
+    rand = lambda *s: torch.randn(*s, device=dev).to(t.dtype)  # noqa: E731
+    return (torch.ones((), dtype=t.dtype, device=dev).expand(t.shape), rand(1, 1, S, d).expand(t.shape),
+            rand(B, H, 1, d).expand(t.shape), rand(B, H, d, S).transpose(2, 3),
+            rand(B * H * S * d + 1)[1:].view(t.shape), rand(B, H, S, d + 4)[..., 4:], rand(B, H, S, 2 * d)[..., ::2])
+
+
+def test_output_gradients_of_any_layout(dev):
+    """autograd hands the backward expanded, transposed and sliced gradients: as good as contiguous ones."""
+    c = Case(2, 4, 2, 70, 70, 64, BF16, (70, 41))
+    f = gtms.rotary_frequencies(64, device=dev)
+    pos = torch.arange(70, dtype=torch.int32, device=dev)
+    leaves = [t.clone().requires_grad_() for t in (c.q, c.k, c.v)]
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    y = gtms.attention(*leaves, c.lens, c.scale, status=status)
+    z = gtms.rotary(leaves[0], pos, f)
+    y.sum().backward(retain_graph=True)
+    first = [t.grad for t in leaves]
+    for i, dy in enumerate(_odd_gradients(dev, y)):
+        c.dout = dy.clone(memory_format=torch.contiguous_format)
+        want = c.backward(*c.forward())
+        got = torch.autograd.grad(y, leaves, dy, retain_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        if i == 0:
+            assert all(torch.equal(a, b) for a, b in zip(got, first))
+        dx, = torch.autograd.grad(z, leaves[:1], dy, retain_graph=True)
+        assert torch.equal(dx, gtms.rotary_backward(c.dout, pos, f))
+    assert int(status) == 0
+
+
 def test_gradients_against_differences(dev):
     """<dq, t> + <dk, t'> + <dv, t''> against central differences of the 64-bit forward pass."""
     c = Case(2, 4, 2, 90, 90, 64, BF16, (90, 55), mask=WINDOW, window=40)
