@@ -357,6 +357,34 @@ def test_gradients_against_differences(dev):
     assert bool(cols.any())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_gradients_along_themselves(dev, dtype):
+    """Each gradient g against a central difference of the 64-bit forward pass along g / |g|, which is |g|: the kernel's
+    may be off by what its elements' bounds add up to along that step (2 to 5 % of |g| in bf16), so a zero gradient, one
+    of the wrong sign or one without the term D is told from the right one."""
+    c = Case(2, 4, 2, 90, 90, 64, dtype, (90, 55), mask=WINDOW, window=40)
+    got = c.backward(*c.forward())
+    refs, tols = backward(c.q, c.k, c.v, c.dout, c.keep, c.scale)
+    rows = c.keep.any(-1)[..., None]
+
+    def loss(q, k, v):
+        s = torch.einsum("bhid,bhcd->bhic", q, k.repeat_interleave(2, 1)) * c.scale
+        p = torch.softmax(torch.where(c.keep, s, -1e300), -1) * rows
+        return float((torch.einsum("bhic,bhcd->bhid", p, v.repeat_interleave(2, 1)) * c.dout.double()).sum())
+
+    for i, (g, ref, tol) in enumerate(zip(got, refs, tols)):
+        step, h, ends = ref / ref.norm(), 1e-3, []
+        for side in (h, -h):
+            x = [t.double() for t in (c.q, c.k, c.v)]
+            x[i] = x[i] + side * step
+            ends.append(loss(*x))
+        want = (ends[0] - ends[1]) / (2 * h)
+        # the difference is off by h^2 / 6 times the third derivative, some 2e-10 of |g|, and by 1e-13 / h of the loss
+        bound = float((tol * step.abs()).sum()) + 1e-6 * want
+        assert bound <= 0.1 * want
+        assert abs(float((g.double() * step).sum()) - want) <= bound
+
+
 def test_on_a_side_stream(dev):
     c = Case(*SHAPES[9])
     want = c.forward()
