@@ -347,6 +347,12 @@ inline int64_t split_units(const AttentionArgs& a)
 //   4 / 1 heads d 128, 3162 keys, 791 tokens, 3 sequences: 102 / 39
 constexpr int64_t kSplitMaxRows = 4096;   // of a key/value head: more are never better split
 
+// Keys that the rows of a call keep at most.
+inline int32_t split_keys(const AttentionArgs& a)
+{
+    return a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + a.Sq < a.Skv ? a.window + a.Sq : a.Skv;
+}
+
 template <int D>
 bool prefer_split(const AttentionArgs& a)
 {
@@ -356,7 +362,7 @@ bool prefer_split(const AttentionArgs& a)
     const int nsm = device_sms();
     if (rows > kSplitMaxRows || nsm <= 0)
         return false;
-    const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + a.Sq < a.Skv ? a.window + a.Sq : a.Skv;
+    const int64_t keys = split_keys(a);
     const int64_t units = split_units(a), ranks = split_ranks(units, keys, nsm);
     const double turns = static_cast<double>(units * ranks) / (3 * nsm);   // of three CTAs to a multiprocessor
     const double block = turns > 1.0 ? (D == 64 ? 1.3 : 2.3) : (D == 64 ? 1.0 : 1.8);
@@ -442,17 +448,27 @@ cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int r
     return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles, ordered);
 }
 
+// The clusters go by the keys that the rows keep, not by the cache: under a sliding
+// window the CTAs without keys would only make more turns of it (one token over 16384
+// keys, window 256: 128 key/value heads of 128, clusters of 8 24.1 us, of 2 10.5; 64:
+// 18.5, 7.8). Where all clusters run at once a window's warps are left with one block of
+// keys instead of two (8 heads of 128, window 256: 7.8 us with clusters of 2, 6.9 of 4,
+// 7.1 of 8; 32 heads 8.4, 7.5, 7.7).
 template <typename T, int D>
 cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
 {
     const int nsm = device_sms();
     if (nsm <= 0)
         return cudaErrorUnknown;
-    const int64_t units = split_units(a);
-    const int ranks = split_ranks(units, a.Skv, nsm);
+    const int64_t units = split_units(a), keys = split_keys(a);
+    int ranks = split_ranks(units, keys, nsm);
+    if (keys < a.Skv) {
+        const int more = split_ranks(units, 2 * keys, nsm);
+        if (units <= clusters_at_once<T, D, 4>(more))
+            ranks = more;
+    }
     if (units * ranks > INT32_MAX)
         return cudaErrorNotSupported;
-    const int64_t keys = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window < a.Skv ? a.window : a.Skv;
     const bool large = keys >= kSplitLargeKeys;
     for (int r : kSplitLarge)
         if (large && units <= clusters_at_once<T, D, 8>(r))

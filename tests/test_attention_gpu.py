@@ -517,6 +517,27 @@ def test_no_rows_or_no_keys(dev):
     assert gtms.attention_forward(z(0, 2, 3, 64), z(0, 2, 3, 64), z(0, 2, 3, 64), lens[:0])[0].numel() == 0
 
 
+@pytest.mark.parametrize("B,Hkv,d,window", [(16, 8, 128, 256), (9, 16, 64, 100)])
+def test_capacity_behind_a_window_does_not_matter(dev, B, Hkv, d, window):
+    """Work under a sliding window is shared out by the keys in it: with many heads, a token over a long cache takes the
+    same launch, and gives the same bits, as over one that is hardly longer than the window."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    n = 500
+    q = torch.randn(B, 2 * Hkv, 1, d, generator=gen, device=dev).to(BF16)
+    k, v = (torch.randn(B, Hkv, n, d, generator=gen, device=dev).to(BF16) for _ in range(2))
+    lens = n - torch.arange(B, dtype=torch.int32, device=dev)
+    got = []
+    for capacity in (n, 9000):
+        ck, cv = (torch.full((B, Hkv, capacity, d), math.nan, dtype=BF16, device=dev) for _ in range(2))
+        ck[:, :, :n], cv[:, :, :n] = k, v
+        got.append(gtms.attention_forward(q, ck, cv, lens, d ** -0.5, mask_kind=WINDOW, window=window, q_offsets=lens - 1))
+    ref, ref_lse, tol, tol_lse = forward(q, k, v, kept(lens, 1, n, WINDOW, window, lens - 1), d ** -0.5)
+    for o, lse in got:
+        _close("o", o, ref, tol)
+        _close("lse", lse, ref_lse, tol_lse)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_cache_beyond_32_bit_offsets(dev):
     """The second sequence of a [2, 16, 2^20, 128] cache stands more than 2^31 elements in."""
     B, Hkv, S, d, L = 2, 16, 1 << 20, 128, 70001
