@@ -655,8 +655,8 @@ def _rotary(x, positions, inv_freq, other, interleaved, amplitude, out, out_othe
     x_ = _heads("x", x, dtype, dev)
     B, H, S, d = shape = x.shape
     pairs = inv_freq.numel()
-    rows = 1 if positions.dim() == 1 else positions.shape[0]
-    if rows != 1 and rows != B:
+    rows = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.dim() not in (1, 2) or rows != 1 and rows != B:
         raise ValueError(f"positions must be [S] or [B, S], got {tuple(positions.shape)}")
     pos = _int32("positions", positions, (S,) if positions.dim() == 1 else (rows, S), dev)
     if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != dev \

@@ -615,6 +615,18 @@ def test_rotary_in_place_and_shared_positions(dev, layout):
     assert got[0].data_ptr() == x.data_ptr() and got[1].data_ptr() == k.data_ptr()
 
 
+def test_rotary_refuses_positions_of_another_shape(dev):
+    x = torch.zeros(3, 2, 4, 64, dtype=BF16, device=dev)
+    f = gtms.rotary_frequencies(64, device=dev)
+    for shape in ((), (3,), (2, 4), (3, 3), (1, 1, 4), (3, 1, 4), (0, 4)):
+        with pytest.raises(ValueError):
+            gtms.rotary_forward(x, torch.zeros(shape, dtype=torch.int32, device=dev), f)
+    for bad in (torch.zeros(4, dtype=torch.int64, device=dev), torch.zeros(4, dtype=torch.int32),
+                torch.zeros(8, dtype=torch.int32, device=dev)[::2]):
+        with pytest.raises(ValueError):
+            gtms.rotary_forward(x, bad, f)
+
+
 def test_rotary_in_place_inside_a_fused_buffer(dev):
     B, S, H, d = 2, 40, 6, 64
     qkv = torch.randn(B, S, H * d, device=dev).to(BF16)
