@@ -278,7 +278,9 @@ typedef struct {
  * `dtype` for the product with v, and o once on its way out.
  * dtype GTMS_BF16 or GTMS_F16, head_dim 64 or 128. Data 16-byte aligned,
  * strides multiples of 8 elements, below 2^40 bytes and not below head_dim, save
- * for the strides of 0 of a broadcast batch or head. o must not overlap the inputs.
+ * for the strides of 0 of a broadcast batch or head. o must not overlap the inputs;
+ * one that lies between another operand's elements is told apart from it where both
+ * repeat with one common period (the parts of one fused projection).
  * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, Hq not a
  * multiple of Hkv, a non-finite scale, a window below 1 with the sliding window,
  * overlaps, an output that repeats itself, misaligned lse, seq_lens, q_offsets

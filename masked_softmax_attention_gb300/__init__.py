@@ -367,7 +367,8 @@ def backward_explicit(y, dy, mask, scale: float = 1.0, out=None):
 def attention_softmax_backward(p, dout, v, seq_lens, scale: float = 1.0, out=None, status=None):
     """dS = scale * P * (dO V^T - rowsum(dO V^T * P)) on the grouped-tril kept entries, with the GEMM on the
     tensor cores; ``p`` [B,M,S,S], ``dout`` / ``v`` [B,M,S,d] (d 64 or 128), bf16 or fp16. ``status`` (an
-    optional int32 CUDA tensor of one element) receives 1 if an internal wait of the kernel ran out."""
+    optional int32 CUDA tensor of one element, cleared before the call) receives ``GTMS_ERR_TIMEOUT`` if an internal
+    wait of the kernel ran out."""
     import torch
 
     _check_scores("p", p)
@@ -580,8 +581,9 @@ def attention_forward(q, k, v, seq_lens, scale: float = 1.0, out=None, mask_kind
                       window: int = 0, q_offsets=None, status=None):
     """(o, lse) of attention under a mask family, the scores staying on the chip (gtms_attention_forward).
 
-    ``q`` [B, Hq, Sq, d], ``k`` / ``v`` [B, Hkv, Skv, d] (bf16 or fp16, d 64 or 128, Hq a multiple of Hkv), any
-    strides with a contiguous last dimension; ``o`` is laid out like ``q``, ``lse`` is fp32 [B, Hq, Sq]. Row i of
+    ``q`` [B, Hq, Sq, d], ``k`` / ``v`` [B, Hkv, Skv, d] (bf16 or fp16, d 64 or 128, Hq a multiple of Hkv) with a
+    contiguous last dimension, strides that are multiples of 8 elements and data on 16 bytes (a batch or head may be
+    expanded); others are refused, not copied. ``o`` is laid out like ``q``, ``lse`` is fp32 [B, Hq, Sq]. Row i of
     batch b stands at position i, or ``q_offsets[b] + i``: for new tokens over a cache pass the cache as ``k`` and
     ``v``, the lengths with the new tokens as ``seq_lens`` and ``seq_lens - Sq`` as ``q_offsets``. Rows that keep
     nothing give o = 0 and lse = -inf. ``status`` as in ``attention_softmax_backward``."""
@@ -767,11 +769,12 @@ def attention(q, k, v, seq_lens, scale: float = 1.0, mask_kind: int = GTMS_MASK_
     (``GTMS_ERR_TIMEOUT``). Without it nothing says so.
 
     To capture a training step into a CUDA graph, capture ``attention_forward`` and ``attention_backward``
-    themselves, which make no autograd nodes."""
+    (``rotary_forward`` and ``rotary_backward``) themselves, which make no autograd nodes."""
     return _attention_fn(0).apply(q, k, v, seq_lens, q_offsets, float(scale), int(mask_kind), int(window), status)
 
 
 def rotary(x, positions, inv_freq, other=None, interleaved: bool = False, amplitude: float = 1.0):
-    """Differentiable ``rotary_forward``: y, or (y, y_other). Gradients reach ``x`` and ``other`` alone."""
+    """Differentiable ``rotary_forward``: y, or (y, y_other). Gradients reach ``x`` and ``other`` alone. For a captured
+    training step see ``attention``."""
     rest = () if other is None else (other,)
     return _attention_fn(1).apply(positions, inv_freq, bool(interleaved), float(amplitude), x, *rest)

@@ -392,7 +392,9 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         x[k] = j + 4 + k < kTile ? max3(x[k], s[j + k], s[(j + 4 + k) % kTile]) : fmaxf(x[k], s[j + k]);
                 const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, rounded to 16 bits.
+                // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, and rounded to 16 bits, the type of
+                // V, with which alone the tensor cores multiply them at full rate (o is off by 1.3 to 1.5 roundings of its
+                // own type instead of 1).
                 auto exponentiate = [&](int k, float shift, uint32_t(&r)[16]) {
                     const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
 #pragma unroll

@@ -219,6 +219,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
                 x[k] = exp2_approx(x[k] - shift);
                 l[h] += x[k];
             }
+            // 16 bits, as the products with V take them; l sums them as they were.
             p[h][0] = pack2<T>(x[0], x[1]);
             p[h][1] = pack2<T>(x[2], x[3]);
         }

@@ -322,6 +322,8 @@ __device__ __forceinline__ uint32_t bits_below(int32_t n)
     return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
 }
 
+// 2^x, off by 2^-22 of it at most, far below the rounding to 16 bits that follows; results below 2^-126 are zero
+// beside a row's largest probability of 1.
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
