@@ -26,11 +26,12 @@
 // What bounds it: at head dim 128 the tensor cores, 66 % busy on a full-length
 // case of 32 heads (a softmax thread's chain of scores, maximum, exponentials and
 // hand-over and the two products it waits for take 2400 cycles a tile, and the two
-// tiles' chains overlap): [4,32/8,4096,128] bf16 245 us, 1500 TFLOP/s. At 64 the
+// tiles' chains overlap): [4,32/8,4096,128] bf16 249 us in a short run of calls, 1480
+// TFLOP/s, 272 us after seconds of work, at lower clocks. At 64 the
 // softmax warps' instructions, 43 % of the issue slots, and their fetching: what
 // made their loop shorter made it faster (masks as 32-bit words 267 -> 258 us, no
 // second copy of the exponentials 251 -> 245 and 247 -> 237 us; two MMA warps,
-// whose code evicts theirs, cost 70 %): [32,16,2048,64] 235 us.
+// whose code evicts theirs, cost 70 %): [32,16,2048,64] 237 and 247 us.
 #pragma once
 
 #include "gtms_attention_tc.cuh"

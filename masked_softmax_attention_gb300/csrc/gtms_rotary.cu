@@ -5,7 +5,7 @@
 // sine and cosine are the same for every head of a token: a block takes one token,
 // asks for its rows in L2, forms its rotations in shared memory meanwhile, and each
 // thread then takes those of one 16-byte unit into registers and walks over the
-// heads. q and k [4,40,4096,128] bf16: 52 us, 6.5 TB/s (70 without the L2 prefetch
+// heads. q and k [4,40,4096,128] bf16: 52 us, 6.4 TB/s (70 without the L2 prefetch
 // and with four tokens to a block of 128 threads).
 #include <cstdint>
 #include <type_traits>
