@@ -275,7 +275,11 @@ typedef struct {
  * that keeps a key of the same 128-key tile (a masked probability is an exact zero,
  * but the tile's product multiplies it).
  * Sums, maxima and accumulators are fp32; probabilities are rounded once to
- * `dtype` for the product with v, and o once on its way out.
+ * `dtype` for the product with v, and o once on its way out. The accumulators of
+ * the tensor cores cut off instead of rounding: a sum is short by up to 2e-4 of its
+ * terms' size in fp16 and 9e-4 in bf16 (half a step of which is 5e-4 and 4e-3), and
+ * no more however long it is: longer ones are formed in parts, between which o
+ * (the backward: dq, dk, dv) holds what 16 bits take of the sum so far.
  * dtype GTMS_BF16 or GTMS_F16, head_dim 64 or 128. Data 16-byte aligned,
  * strides multiples of 8 elements, below 2^40 bytes and not below head_dim, save
  * for the strides of 0 of a broadcast batch or head. o must not overlap the inputs;

@@ -209,11 +209,25 @@ __device__ __forceinline__ void keep_range(float (&v)[64], int32_t k0, int32_t k
     }
 }
 
+// What a long sum of gradients that comes out scaled by f is carried by (see
+// kCarryTerms): units of 1 / f, and none where f leaves no such unit.
+struct Carried {
+    float unit, per_unit;
+
+    __device__ __forceinline__ explicit Carried(float f)
+    {
+        const bool usable = fabsf(f) >= 1e-30f && fabsf(f) <= 1e30f;
+        per_unit = usable ? f : 0.0f;
+        unit = usable ? 1.0f / f : 0.0f;
+    }
+};
+
 // A warp's 32 rows x COLS columns of an accumulator at `acc` (zeros where there is
-// none), scaled by f; the lanes' rows that are not live are zero. A zero comes out
-// as +0.0.
+// none) and, where carried, of what `out` carries, scaled by f; the lanes' rows that are
+// not live are zero. A zero comes out as +0.0.
 template <typename T, int COLS>
-__device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t acc, bool any, bool live, float f, T* out)
+__device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t acc, bool any, bool live, float f, T* out,
+                                           bool carried)
 {
 #pragma unroll 1
     for (int k = 0; k < COLS; k += 32) {
@@ -224,6 +238,8 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, int lane, uint32_t ac
         if (any) {
             float o[32];
             tc::tmem_ld32(acc + k, o);
+            if (carried && live && out)
+                add_carried(o, out + k, Carried(f).unit);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 r[j] = live ? pack2<T>(o[2 * j] * f + 0.0f, o[2 * j + 1] * f + 0.0f) : 0u;
@@ -299,7 +315,7 @@ struct DkvShared {
     float norm[2];
 };
 
-template <typename T, int D>
+template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(BwdShape<D>::threads, BwdShape<D>::ctas)
 gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
@@ -307,7 +323,7 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 {
     using TL = DkvTile<D>;
     using SH = BwdShape<D>;
-    constexpr int ST = TL::stages;
+    constexpr int ST = TL::stages, carry_tiles = kCarryTerms<T> / SH::inner;   // inner tiles of a part of a long sum
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DkvShared sh;
     const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -549,9 +565,25 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         while (take_item(sh.items, up, lane, taken, it, ok)) {
             const int32_t key = it.j * kTile + row;
             const bool any = it.lo != it.hi;
+            const uint32_t first = gt;
             for (int32_t h = 0; h < (any ? a.group : 0) && ok; ++h)
                 for (int32_t i = it.lo; i < it.hi; ++i, ++gt) {
                     const uint32_t s = gt % ST;
+                    if (LONG && (gt - first) % carry_tiles == 0 && gt != first) {
+                        // dP of this tile says that the products into dK are done, and with them those into dV.
+                        ok = up.warp_wait(&sh.dpfull, gt & 1u);
+                        if (!ok)
+                            break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int which = 0; which < 2; ++which)
+                            if (SH::groups == 1 || part == which) {
+                                const Carried c(which ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>)));
+                                carry_accumulator<T, D>((which ? t_dk : t_dv) + lanes,
+                                                        key < a.Skv ? (which ? a.dk : a.dv).row<T>(it.b, it.g, key) : nullptr,
+                                                        gt - first > carry_tiles ? c.unit : 0.0f, c.unit, c.per_unit);
+                            }
+                    }
                     // S says that the queries' tile has arrived, and the rows' lse2 and D with it on the same barrier.
                     ok = up.warp_wait(&sh.sfull, gt & 1u);
                     if (!ok)
@@ -628,7 +660,8 @@ gtms_attention_dkv_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (SH::groups == 1 || part == which) {
                     T* out = key < a.Skv ? (which ? a.dk : a.dv).row<T>(it.b, it.g, key) : nullptr;
                     write_rows<T, D>(smem + TL::off_out + warp * SH::stage, lane, (which ? t_dk : t_dv) + lanes, any,
-                                     key < it.L, which ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>)), out);
+                                     key < it.L, which ? a.scale / factor : exp2f(static_cast<float>(-kPShift<T>)), out,
+                                     LONG && gt - first > carry_tiles);
                 }
             if (any)
                 arrive(&sh.accempty);
@@ -703,7 +736,7 @@ struct DqShared {
     float norm[2];
 };
 
-template <typename T, int D>
+template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(BwdShape<D>::threads, BwdShape<D>::ctas)
 gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                          const __grid_constant__ HeadsMap mv, const __grid_constant__ HeadsMap mdo,
@@ -711,7 +744,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
 {
     using TL = DqTile<D>;
     using SH = BwdShape<D>;
-    constexpr int KS = TL::k_stages, VS = TL::v_stages;
+    constexpr int KS = TL::k_stages, VS = TL::v_stages, carry_tiles = kCarryTerms<T> / SH::inner;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ DqShared sh;
     const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -918,8 +951,19 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Sq_pad + i;
             const float neg_lse = __ldg(a.lse2 + at), neg_delta = __ldg(a.delta + at);
             const float2 lse2 = make_float2(neg_lse, neg_lse), delta2 = make_float2(neg_delta, neg_delta);
+            constexpr int cols = D / SH::groups;
+            T* out = i < a.Sq ? a.dq.row<T>(it.b, it.h, i) + part * cols : nullptr;
             bool scored = false;
             for (int32_t t = it.lo; t < it.hi; ++t, ++g) {
+                if (LONG && (t - it.lo) % carry_tiles == 0 && t != it.lo) {
+                    ok = up.warp_wait(&sh.kempty[(g - 1) % KS], ((g - 1) / KS) & 1u);   // the products into dQ are done
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    const Carried c(a.scale / factor);
+                    carry_accumulator<T, cols>(t_dq + lanes + part * cols, out, t - it.lo > carry_tiles ? c.unit : 0.0f, c.unit,
+                                               c.per_unit);
+                }
                 ok = up.warp_wait(&sh.sfull, g & 1u, scored);
                 if (!ok)
                     break;
@@ -968,8 +1012,6 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
             }
             if (!ok)
                 break;
-            constexpr int cols = D / SH::groups;
-            T* out = i < a.Sq ? a.dq.row<T>(it.b, it.h, i) + part * cols : nullptr;
             const bool any = it.lo != it.hi;
             if (any) {
                 ok = up.warp_wait(&sh.accfull, ni & 1u);
@@ -979,7 +1021,7 @@ gtms_attention_dq_kernel(const __grid_constant__ HeadsMap mq, const __grid_const
                 tc::fence_after_sync();
             }
             write_rows<T, cols>(smem + TL::off_out + warp * SH::stage, lane, t_dq + lanes + part * cols, any, live,
-                                a.scale / factor, out);
+                                a.scale / factor, out, LONG && it.hi - it.lo > carry_tiles);
             if (any)
                 arrive(&sh.accempty);
         }
@@ -1024,23 +1066,28 @@ cudaError_t launch_attention_bwd_tc(const AttentionArgs& args, cudaStream_t st, 
             e = launch_kernel(gtms_attention_bwd_prep_kernel<T, D>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, a, n, m);
     }
     // One CTA per item; the running ones take over the others' (see ItemSlot).
-    if (e == cudaSuccess && keys) {
-        auto* kern = gtms_attention_dkv_kernel<T, D>;
+    auto launch_dkv = [&](auto is_long) {
+        constexpr auto* kern = gtms_attention_dkv_kernel<T, D, is_long()>;
         constexpr int smem = static_cast<int>(DkvTile<D>::smem);
-        e = allow_smem<gtms_attention_dkv_kernel<T, D>>(smem);
-        if (e == cudaSuccess)
-            e = launch_beside_last(a.norm_blocks > 0, kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)),
-                                   BwdShape<D>::threads, smem, st, mq, mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
-    }
-    if (e == cudaSuccess && rows) {
-        auto* kern = gtms_attention_dq_kernel<T, D>;
+        const cudaError_t allowed = allow_smem<kern>(smem);
+        return allowed != cudaSuccess
+                   ? allowed
+                   : launch_beside_last(a.norm_blocks > 0, kern, static_cast<unsigned>(kv_heads * ((a.Skv + kTile - 1) / kTile)),
+                                        BwdShape<D>::threads, smem, st, mq, mk, mv, mdo, a, static_cast<uint32_t>(kv_heads), wait_ns);
+    };
+    auto launch_dq = [&](auto is_long) {
+        constexpr auto* kern = gtms_attention_dq_kernel<T, D, is_long()>;
         constexpr int smem = static_cast<int>(DqTile<D>::smem);
         const int32_t blocks = a.Sq_pad / kTile;
-        e = allow_smem<gtms_attention_dq_kernel<T, D>>(smem);
-        if (e == cudaSuccess)
-            e = launch_beside_last(keys, kern, static_cast<unsigned>(heads * blocks), BwdShape<D>::threads, smem, st, mq, mk, mv, mdo,
-                                   a, static_cast<uint32_t>(heads), blocks, wait_ns);
-    }
+        const cudaError_t allowed = allow_smem<kern>(smem);
+        return allowed != cudaSuccess ? allowed
+                                      : launch_beside_last(keys, kern, static_cast<unsigned>(heads * blocks), BwdShape<D>::threads, smem,
+                                                           st, mq, mk, mv, mdo, a, static_cast<uint32_t>(heads), blocks, wait_ns);
+    };
+    if (e == cudaSuccess && keys)
+        e = kept_at_most(a, a.Sq) * a.group > kCarryTerms<T> ? launch_dkv(std::true_type()) : launch_dkv(std::false_type());
+    if (e == cudaSuccess && rows)
+        e = kept_at_most(a, a.Skv) > kCarryTerms<T> ? launch_dq(std::true_type()) : launch_dq(std::false_type());
     return e;
 }
 

@@ -133,14 +133,14 @@ struct FwdShared {
     int flag;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(FwdTile<D>::threads, FwdTile<D>::ctas)
 gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, uint32_t heads,
                           int32_t blocks, uint64_t wait_ns)
 {
     using TL = FwdTile<D>;
-    constexpr int ST = TL::stages, W = TL::W;
+    constexpr int ST = TL::stages, W = TL::W, carry_tiles = kCarryTerms<T> / kTile;
     using Item = FwdItem<W>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ FwdShared<W> sh;
@@ -361,6 +361,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         while (take_item(sh.items, up, lane, taken, ok, read)) {
             const bool live = c0 < c1 && i < a.Sq;
             float m = -INFINITY, l = 0.0f;
+            float m_carried = -INFINITY, l_carried = 0.0f;   // of the part of O that the row of o carries, in units of l
+            auto carried = [&] { return l_carried > 0.0f ? l_carried * exp2_approx((m_carried - m) * c) : 0.0f; };
             for (int32_t t = hi - 1; t >= lo; --t) {
                 // The first scores may have to wait while the other tile has a whole item to itself.
                 ok = item_wait(sh.items, up, &sh.sfull[w], ns & 1u);
@@ -368,6 +370,12 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (!ok)
                     break;
                 tc::fence_after_sync();
+                if (LONG && (hi - 1 - t) % carry_tiles == 0 && t != hi - 1) {
+                    // The products into O are done, up to the last tile's (see above).
+                    carry_accumulator<T, D>(to, live ? a.o.row<T>(b, h, i) : nullptr, carried(), l, l > 0.0f ? 1.0f / l : 0.0f);
+                    m_carried = m;
+                    l_carried = l;
+                }
                 float s[kTile];
                 tc::tmem_ld128(ts, s);
                 if (__builtin_expect(pre != 1.0f, 0)) {
@@ -471,6 +479,8 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 if (any) {
                     float o[64];
                     tc::tmem_ld64(to + k, o);
+                    if (LONG && hi - lo > carry_tiles && live)
+                        add_carried(o, out + k, carried());
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         r[j] = live ? pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
@@ -511,15 +521,18 @@ cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uin
         !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
         !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile))
         return cudaErrorInvalidValue;
-    constexpr int smem = static_cast<int>(TL::smem);
-    const cudaError_t e = allow_smem<gtms_attention_fwd_kernel<T, D>>(smem);
-    if (e != cudaSuccess)
-        return e;
     // One CTA per item; the running ones take over the others' (see ItemSlot).
     const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
-    return launch_kernel(gtms_attention_fwd_kernel<T, D>, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv,
-                         a, static_cast<uint32_t>(heads), blocks, wait_ns);
+    auto launch = [&](auto is_long) {
+        constexpr auto* kern = gtms_attention_fwd_kernel<T, D, is_long()>;
+        constexpr int smem = static_cast<int>(TL::smem);
+        const cudaError_t e = allow_smem<kern>(smem);
+        return e != cudaSuccess ? e
+                                : launch_kernel(kern, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv, a,
+                                                static_cast<uint32_t>(heads), blocks, wait_ns);
+    };
+    return kept_at_most(a, a.Skv) > kCarryTerms<T> ? launch(std::true_type()) : launch(std::false_type());
 }
 
 }  // namespace gtms

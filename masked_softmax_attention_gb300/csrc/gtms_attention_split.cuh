@@ -69,7 +69,9 @@ struct SplitShared {
     int32_t length[kSplitOrdered], batch;            // of all batches; the one this CTA takes
 };
 
-template <typename T, int D, int WARPS>
+// LONG: where a warp may have more than kCarryTerms keys (code of its own, whose registers
+// the others would spill for).
+template <typename T, int D, int WARPS, bool LONG>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 3 : 1)
 gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordered)
 {
@@ -174,9 +176,54 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
             for (int k = 0; k < 4; ++k)
                 o[y][j][k] = 0.0f;
 
+    // Long sums (see kCarryTerms): the warp's O is added up in fp32 in its place in shared
+    // memory, at the maxima that stand in sh.m.
+    constexpr int kCarryBlocks = kCarryTerms<T> / kSplitKeys;
+    const int32_t start = blk;
+    auto kept_o = [&](int y, int h, int n, int j) { return reinterpret_cast<float4*>(&sh.o[warp][g + 8 * h][64 * y + 16 * t + 8 * n + j]); };
+    auto add_kept = [&] {   // o += what is kept
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float f = m[h] == -INFINITY ? 0.0f : exp2_approx(sh.m[warp][g + 8 * h] - m[h]);
+#pragma unroll
+            for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 x = *kept_o(y, h, n, j);
+                        o[y][j][2 * h + n] += f * x.x;
+                        o[y][j + 1][2 * h + n] += f * x.y;
+                        o[y][j + 2][2 * h + n] += f * x.z;
+                        o[y][j + 3][2 * h + n] += f * x.w;
+                    }
+        }
+    };
+
     load_k(blk);
     load_v(blk);
     for (; blk < end; blk += WARPS) {
+        if (LONG && (blk - start) % (kCarryBlocks * WARPS) == 0 && blk != start) {
+            if (blk - start > kCarryBlocks * WARPS)
+                add_kept();
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (t == 0)
+                    sh.m[warp][g + 8 * h] = m[h];
+#pragma unroll
+                for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            *kept_o(y, h, n, j) = make_float4(o[y][j][2 * h + n], o[y][j + 1][2 * h + n], o[y][j + 2][2 * h + n],
+                                                              o[y][j + 3][2 * h + n]);
+                            o[y][j][2 * h + n] = o[y][j + 1][2 * h + n] = o[y][j + 2][2 * h + n] = o[y][j + 3][2 * h + n] = 0.0f;
+                        }
+            }
+            __syncwarp();
+        }
         float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
@@ -235,6 +282,11 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
             }
         }
         load_v(blk + WARPS);
+    }
+
+    if (LONG && blk - start > kCarryBlocks * WARPS) {
+        add_kept();
+        __syncwarp();   // sh.m is written anew
     }
 
     // Join the warps: row sums over the quad, then every warp brings its O to the CTA's maximum.
@@ -409,8 +461,8 @@ int clusters_at_once(int ranks)
         return n - 1;
     constexpr int smem = SplitConfig<WARPS>::template smem<D>;
     const SplitConfig<WARPS> cfg(ranks, ranks, smem, nullptr);
-    if (allow_smem<gtms_attention_split_kernel<T, D, WARPS>, true>(smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, WARPS>, &cfg.cfg) != cudaSuccess) {
+    if (allow_smem<gtms_attention_split_kernel<T, D, WARPS, false>, true>(smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gtms_attention_split_kernel<T, D, WARPS, false>, &cfg.cfg) != cudaSuccess) {
         cudaGetLastError();   // no such clusters here
         n = 0;
     }
@@ -436,17 +488,26 @@ constexpr int64_t kSplitLargeKeys = 4096;
 // 87.5; 69.7, 77.8).
 constexpr int kSplitSmaller[] = {6, 5};
 
-template <typename T, int D, int WARPS>
-cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
+template <typename T, int D, int WARPS, bool LONG>
+cudaError_t launch_attention_split_k(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
 {
     constexpr int smem = SplitConfig<WARPS>::template smem<D>;
-    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS>, true>(smem);
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS, LONG>, true>(smem);
     if (e != cudaSuccess)
         return e;
     SplitConfig<WARPS> cfg(ctas, ranks, smem, st);
     const int32_t tiles = static_cast<int32_t>((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
     const int32_t ordered = WARPS == 4 && ctas > 3 * device_sms() && a.B > 1 && a.B <= kSplitOrdered;
-    return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS>, a, tiles, ordered);
+    return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS, LONG>, a, tiles, ordered);
+}
+
+template <typename T, int D, int WARPS>
+cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
+{
+    // A warp takes every WARPS-th of its CTA's blocks, of which the keys can make one more than an even share.
+    const bool is_long = split_keys(a) / (ranks * WARPS) + 2 * kSplitKeys > kCarryTerms<T>;
+    return is_long ? launch_attention_split_k<T, D, WARPS, true>(a, ctas, ranks, st)
+                   : launch_attention_split_k<T, D, WARPS, false>(a, ctas, ranks, st);
 }
 
 // The clusters go by the keys that the rows keep, not by the cache: under a sliding

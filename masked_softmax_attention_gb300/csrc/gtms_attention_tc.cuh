@@ -316,6 +316,85 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Long sums. The tensor cores' fp32 accumulators cut off what does not fit instead of
+// rounding it, so that every product of 16 terms can lose a unit in the last place, toward
+// zero: a sum of 2^20 terms of one sign comes out 0.5 to 0.7 % short. So after every
+// kCarryTerms terms the thread that owns a row of results takes the part that 16 bits
+// hold out of the accumulator and carries it in the result's own place in memory, which
+// nobody else reads; the rest, exact in fp32, stays in. The next part is added to it
+// there, and in the end the last one. Sums of up to kCarryTerms terms stay as they are,
+// short by 2e-4 at most in fp16 and 9e-4 in bf16, where half a step is 5e-4 and 4e-3.
+// Kernels come with (LONG) and without the code for it: its mere presence costs the shorter
+// sums of every other call 1 to 4 % (forward 271 -> 275 and 242 -> 249 us, backward 577 ->
+// 581 and 712 -> 741 at [4,32/8,4096,128], [32,16,2048,64], [2,32/8,4096,128] and
+// [32,16,2048,64]).
+template <typename T>
+constexpr int kCarryTerms = std::is_same<T, __half>::value ? 1 << 15 : 1 << 17;
+
+// Keys that a tile of 128 rows keeps at most, and rows that keep one of a tile of 128 keys.
+inline int64_t kept_at_most(const AttentionArgs& a, int32_t extent)
+{
+    const int32_t reach = a.window + kTile;
+    return a.mask_kind == GTMS_MASK_SLIDING_WINDOW && reach < extent ? reach : extent;
+}
+
+// x += unit times what row `at` carries.
+template <typename T, int N>
+__device__ __forceinline__ void add_carried(float (&x)[N], const T* at, float unit)
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at + j);
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[j + k] += unit * static_cast<float>(e[k]);
+    }
+}
+
+// Carries round(x / unit), finite always, and leaves the rest in x (per_unit = 1 / unit).
+template <typename T, int N>
+__device__ __forceinline__ void carry(float (&x)[N], T* at, float unit, float per_unit)
+{
+    constexpr float top = std::is_same<T, __half>::value ? 65504.0f : 3.3895313892515355e38f;
+#pragma unroll
+    for (int j = 0; j < N; j += 8) {
+        uint4 v;
+        uint32_t* r = reinterpret_cast<uint32_t*>(&v);
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            r[k] = pack2<T>(fminf(fmaxf(x[j + 2 * k] * per_unit, -top), top), fminf(fmaxf(x[j + 2 * k + 1] * per_unit, -top), top));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[j + k] -= unit * static_cast<float>(e[k]);
+        *reinterpret_cast<uint4*>(at + j) = v;
+    }
+}
+
+// The same for COLS columns of an accumulator at `acc` (a whole warp calls; a lane
+// without a row passes null): what row `at` carries already counts `before` each.
+template <typename T, int COLS>
+__device__ __forceinline__ void carry_accumulator(uint32_t acc, T* at, float before, float unit, float per_unit)
+{
+#pragma unroll 1
+    for (int k = 0; k < COLS; k += 16) {
+        float x[16];
+        uint32_t r[16];
+        tc::tmem_ld16(acc + k, x);
+        if (at) {
+            if (before != 0.0f)
+                add_carried(x, at + k, before);
+            carry(x, at + k, unit, per_unit);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            r[j] = __float_as_uint(x[j]);
+        tc::tmem_st16(acc + k, r);
+    }
+    tc::tmem_wait_st();
+}
+
 // The lowest n bits, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t bits_below(int32_t n)
 {

@@ -29,25 +29,28 @@ cudaError_t run(gtms::AttentionArgs a, void* workspace, cudaStream_t st, uint64_
 // Contiguous bf16 tensors: q, k, v, o (forward, without a workspace), and dout, dq, dk, dv with one (backward).
 // Waits run out after wait_ns.
 extern "C" __attribute__((visibility("default"))) int gtms_test_attention_late(
-    void* const* tensors, float* lse, const int32_t* seq_lens, int32_t B, int32_t Hq, int32_t Hkv, int32_t S, int32_t D,
-    float scale, int32_t mask_kind, uint32_t late_warps, uint32_t late_ns, int32_t* status, void* workspace, void* stream,
+    void* const* tensors, float* lse, const int32_t* seq_lens, const int32_t* q_offsets, int32_t B, int32_t Hq, int32_t Hkv,
+    int32_t Sq, int32_t Skv, int32_t D, float scale, int32_t mask_kind, uint32_t late_warps, uint32_t late_ns, int32_t* status, void* workspace, void* stream,
     uint64_t wait_ns)
 {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     gtms::AttentionArgs a{};
     gtms::HeadsRef* const ref[8] = {&a.q, &a.k, &a.v, &a.o, &a.dout, &a.dq, &a.dk, &a.dv};
     for (int i = 0; i < 8; ++i) {
-        const int64_t H = i == 1 || i == 2 || i >= 6 ? Hkv : Hq, row = D, head = S * row;
+        const bool of_k = i == 1 || i == 2 || i >= 6;
+        const int64_t H = of_k ? Hkv : Hq, row = D, head = (of_k ? Skv : Sq) * row;
         *ref[i] = {tensors[i], H * head, head, row};
     }
     a.lse = lse;
     a.seq_lens = seq_lens;
+    a.q_offsets = q_offsets;
     a.status = status;
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.group = Hq / Hkv;
-    a.Sq = a.Skv = S;
+    a.Sq = Sq;
+    a.Skv = Skv;
     a.mask_kind = mask_kind;
     a.scale = scale;
     cudaError_t e = cudaMemcpyToSymbolAsync(gtms_late_warps, &late_warps, 4, 0, cudaMemcpyHostToDevice, st);

@@ -31,7 +31,7 @@ def probe():
         os.replace(tmp, path)
     fn = ctypes.CDLL(path).gtms_test_attention_late
     vp, i32, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32
-    fn.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float, i32, u32, u32, vp, vp, vp, ctypes.c_uint64]
+    fn.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float, i32, u32, u32, vp, vp, vp, ctypes.c_uint64]
     fn.restype = ctypes.c_int
     return fn
 
@@ -39,26 +39,30 @@ def probe():
 class Run:
     """One problem, its results from the normal build, and the probe's on the same inputs."""
 
-    def __init__(self, B, Hq, Hkv, S, d, lens, mask):
+    def __init__(self, B, Hq, Hkv, S, d, lens, mask, Sq=None):
         gen = torch.Generator(device="cuda").manual_seed(S + d)
+        Sq = Sq or S
         self.q, self.k, self.v, self.dout = (
-            torch.randn(B, H, S, d, generator=gen, device="cuda").to(torch.bfloat16) for H in (Hq, Hkv, Hkv, Hq))
+            torch.randn(B, H, n, d, generator=gen, device="cuda").to(torch.bfloat16)
+            for H, n in ((Hq, Sq), (Hkv, S), (Hkv, S), (Hq, Sq)))
         self.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.off = self.lens - Sq if Sq != S else torch.zeros_like(self.lens)
         self.mask, self.scale = mask, d ** -0.5
-        self.o, self.lse = gtms.attention_forward(self.q, self.k, self.v, self.lens, self.scale, mask_kind=mask)
+        options = dict(mask_kind=mask, q_offsets=self.off)
+        self.o, self.lse = gtms.attention_forward(self.q, self.k, self.v, self.lens, self.scale, **options)
         self.grads = gtms.attention_backward(self.q, self.k, self.v, self.o, self.lse, self.dout, self.lens, self.scale,
-                                             mask_kind=mask)
+                                             **options)
 
     def check(self, probe, backward, late_warps=0, late_ns=0, wait_ns=1_000_000_000):
-        B, Hq, S, d = self.q.shape
+        (B, Hq, Sq, d), (_, Hkv, S, _) = self.q.shape, self.k.shape
         o, lse = torch.full_like(self.o, 7.0), torch.full_like(self.lse, 7.0)
         grads = [torch.full_like(t, 7.0) for t in self.grads]
         tensors = (ctypes.c_void_p * 8)(*(t.data_ptr() for t in (
             self.q, self.k, self.v, self.o if backward else o, self.dout, *grads)))
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        work = torch.empty(8 * (B * Hq * (S + 127) + 1024), dtype=torch.uint8, device="cuda")
-        rc = probe(tensors, (self.lse if backward else lse).data_ptr(), self.lens.data_ptr(), B, Hq, self.k.shape[1], S, d,
-                   self.scale, self.mask, late_warps, late_ns, status.data_ptr(), work.data_ptr() if backward else None,
+        work = torch.empty(8 * (B * Hq * (Sq + 127) + 1024), dtype=torch.uint8, device="cuda")
+        rc = probe(tensors, (self.lse if backward else lse).data_ptr(), self.lens.data_ptr(), self.off.data_ptr(), B, Hq,
+                   Hkv, Sq, S, d, self.scale, self.mask, late_warps, late_ns, status.data_ptr(), work.data_ptr() if backward else None,
                    torch.cuda.current_stream().cuda_stream, wait_ns)
         torch.cuda.synchronize()
         assert rc == 0 and int(status.item()) == 0
@@ -77,6 +81,10 @@ def test_late_warps_change_nothing(probe, backward, d, late):
     bits = {"mma": 1 << n, "load": 2 << n, "deal": 4 << n, "first element-wise": 1, "last element-wise": 1 << (n - 1),
             "mma and load": 3 << n}[late]
     Run(2, 4, 2, 700, d, (700, 613), TRIL).check(probe, backward, bits, 20_000)
+    # sums of several parts: rows of many heads into dk and dv, many keys into o and dq
+    if backward:
+        Run(1, 130, 1, 1050, d, (1050,), LENGTH).check(probe, backward, bits, 5_000)
+    Run(1, 16, 1, 140000, d, (140000,), LENGTH, 300).check(probe, backward, bits, 5_000)
 
 
 @pytest.mark.parametrize("d", [64, 128])
