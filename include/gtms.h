@@ -325,6 +325,117 @@ int gtms_attention_backward(const gtms_attention_shape* shape, const gtms_heads*
 int gtms_attention_backward_workspace(const gtms_attention_shape* shape, uint64_t* bytes);
 
 /*
+ * Attention for a batch whose sequences share long prefixes (samples of one
+ * prompt, questions on one document, requests behind one instruction). Of the
+ * B = groups * n sequences, sequence b keeps, beside its own keys, the first
+ * P_g = clamp(prefix_lens[g], 0, prefix) keys of prefix g = b / n:
+ *   o_i = softmax(scale q_i . [k_prefix, k])  [v_prefix, v],  lse_i over both,
+ * as gtms_attention_forward over the two put end to end, but each prefix's keys are
+ * read once for all of its sequences.
+ *   q, k, v, o, lse, seq_lens, q_offsets, status   as in gtms_attention_forward:
+ *                     positions and lengths count a sequence's own keys, and rows
+ *                     outside [0, L) keep nothing, of the prefix neither.
+ *   k_prefix, v_prefix [groups, Hkv, prefix, head_dim], read-only; keys behind P_g
+ *                     are never used.
+ *   prefix_lens       device int32[groups], or NULL: every prefix is full.
+ *   workspace         device memory of at least the bytes that
+ *                     gtms_attention_shared_prefix_workspace gives (which may be 0),
+ *                     16-byte aligned; its contents need not be set, and calls that
+ *                     may run at the same time need one each.
+ * The prefix is seen whole, so that masks are GTMS_MASK_GROUPED_TRIL or
+ * GTMS_MASK_LENGTH. Partial sums over the parts of a prefix are joined in fp32;
+ * otherwise types, roundings and a NaN's reach are gtms_attention_forward's, and so
+ * are the errors, and GTMS_ERR_INVALID_ARG: negative groups or prefix, B not a
+ * multiple of groups, a missing or too small workspace, a workspace that overlaps
+ * another argument; GTMS_ERR_UNSUPPORTED: the sliding window, prefix above
+ * GTMS_ATTENTION_MAX_S.
+ */
+int gtms_attention_shared_prefix(const gtms_attention_shape* shape, int64_t groups, int64_t prefix, const gtms_heads* q,
+                                 const gtms_heads* k_prefix, const gtms_heads* v_prefix, const gtms_heads* k,
+                                 const gtms_heads* v, const gtms_heads* o, float* lse, const int32_t* prefix_lens,
+                                 const int32_t* seq_lens, const int32_t* q_offsets, void* workspace,
+                                 uint64_t workspace_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace that gtms_attention_shared_prefix needs for this shape. Host-only, enqueues nothing. */
+int gtms_attention_shared_prefix_workspace(const gtms_attention_shape* shape, int64_t groups, int64_t prefix,
+                                           uint64_t* bytes);
+
+/*
+ * The weight that each key of a cache received: with p_ic = exp(scale q_i . k_c - lse_i)
+ * over the kept entries of gtms_attention_forward,
+ *   w[b][h][c] = sum of p_ic over the rows i that keep c and the query heads that share
+ *                key/value head h,
+ * which is what gtms_cache_evict goes by. With the lse of gtms_attention_shared_prefix
+ * it is the weight of a sequence's own keys in the whole softmax.
+ *   q, k, seq_lens, q_offsets   as in gtms_attention_forward.
+ *   lse         fp32 [B, Hq, Sq], contiguous: what the forward wrote. A row whose lse is
+ *               -infinity adds nothing.
+ *   weights     fp32 [B, Hkv, Skv], contiguous: w, and +0.0 where no row keeps the key; with
+ *               `accumulate` not 0 w is added to what stands there, and keys at c >= L
+ *               are left alone.
+ *   workspace   as in gtms_attention_shared_prefix, of the bytes that
+ *               gtms_attention_key_weights_workspace gives.
+ *   status      as in gtms_attention_forward.
+ * Sums are fp32, in a fixed order: the same inputs give the same bits. k at c >= L, q and
+ * lse of rows that keep nothing are never used; a NaN or infinity in a live key stays in
+ * its own weight, one in a live row or its lse in the weights of the keys that it keeps.
+ * Types, sizes, alignment and errors as in gtms_attention_forward, without v and o.
+ */
+int gtms_attention_key_weights(const gtms_attention_shape* shape, const gtms_heads* q, const gtms_heads* k,
+                               const float* lse, float* weights, int accumulate, const int32_t* seq_lens,
+                               const int32_t* q_offsets, void* workspace, uint64_t workspace_bytes, int32_t* status,
+                               void* stream);
+
+/* Bytes of workspace that gtms_attention_key_weights needs for this shape. Host-only, enqueues nothing. */
+int gtms_attention_key_weights_workspace(const gtms_attention_shape* shape, uint64_t* bytes);
+
+/*
+ * Sizes of an eviction: caches k and v [B, H, S, head_dim] of `dtype` that go to
+ * [B, H, S_out, head_dim]; sequences longer than `keep` are cut to it.
+ */
+typedef struct {
+    int64_t B, H, S, S_out, head_dim;
+    int64_t keep, first, recent;
+    int32_t dtype;
+} gtms_evict_shape;
+
+/*
+ * Evicts the entries of least weight from a key/value cache. Of a sequence of
+ * n = clamp(seq_lens[b], 0, S) entries, n > keep, there stay for each head the first
+ * `first`, the last `recent` and, of those between, the keep - first - recent of highest
+ * weight: equal weights go to the lowest index, NaN counts above every number, -0 as +0.
+ * Shorter sequences stay whole. What stays moves to the front in the order in which it
+ * stood:
+ *   k_out, v_out   row j is row kept[j] of k, v;
+ *   weights_out    fp32 [B, H, S_out]: weights[kept[j]], weights being fp32 [B, H, S];
+ *   positions_out  int32 [B, H, S_out], or NULL: positions[kept[j]], positions being
+ *                  int32 [B, H, S], or NULL: 0, 1, 2, ...;
+ *   lens_out       int32 [B]: min(n, keep).
+ * weights, positions and their outputs are contiguous. Rows at and behind lens_out are
+ * left as they were. An output may be its input itself (same data and strides, S_out == S):
+ * it is then compacted in place. What a row of attention keeps afterwards goes by the
+ * places in the cache: new tokens follow at lens_out.
+ *   workspace      as in gtms_attention_shared_prefix, of the bytes that
+ *                  gtms_cache_evict_workspace gives.
+ * dtype GTMS_F32, GTMS_BF16 or GTMS_F16; rows of whole 16-byte units, head_dim up to 1024; data and
+ * strides as in gtms_attention_forward (16 bytes). With keep == 0 only lens_out is
+ * written and the other pointers may be NULL.
+ * GTMS_ERR_INVALID_ARG: null arguments, negative sizes or strides, first + recent > keep,
+ * S_out below min(keep, S), no heads, outputs that repeat themselves or overlap anything
+ * other than as above (seq_lens and lens_out among them), misaligned pointers, a missing
+ * or too small workspace. GTMS_ERR_UNSUPPORTED: other dtypes and row sizes, S or S_out
+ * above GTMS_ATTENTION_MAX_S, data or strides not aligned as above, more work than a grid
+ * holds. B == 0 is GTMS_OK.
+ */
+int gtms_cache_evict(const gtms_evict_shape* shape, const gtms_heads* k, const gtms_heads* v, const float* weights,
+                     const int32_t* positions, const gtms_heads* k_out, const gtms_heads* v_out, float* weights_out,
+                     int32_t* positions_out, const int32_t* seq_lens, int32_t* lens_out, void* workspace,
+                     uint64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that gtms_cache_evict needs for this shape. Host-only, enqueues nothing. */
+int gtms_cache_evict_workspace(const gtms_evict_shape* shape, uint64_t* bytes);
+
+/*
  * Rotary positions: pair j of the first rot_dim elements of each head is turned
  * by the angle a = positions[b][s] * inv_freq[j],
  *   y1 = amplitude (x1 cos a - x2 sin a),  y2 = amplitude (x2 cos a + x1 sin a),

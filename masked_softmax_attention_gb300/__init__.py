@@ -36,7 +36,10 @@ EXPORTED_SYMBOLS = ("gtms_forward", "gtms_backward", "gtms_status_string", "gtms
                     "gtms_backward_masked", "gtms_forward_explicit", "gtms_backward_explicit",
                     "gtms_attention_softmax_backward", "gtms_forward_staged",
                     "gtms_attention_forward", "gtms_attention_backward", "gtms_attention_backward_workspace",
-                    "gtms_rotary", "gtms_rotary_frequencies")
+                    "gtms_rotary", "gtms_rotary_frequencies",
+                    "gtms_attention_shared_prefix", "gtms_attention_shared_prefix_workspace",
+                    "gtms_attention_key_weights", "gtms_attention_key_weights_workspace",
+                    "gtms_cache_evict", "gtms_cache_evict_workspace")
 
 _lib = None
 _lock = threading.Lock()
@@ -55,6 +58,14 @@ class AttentionShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("Sq", ctypes.c_int64),
                 ("Skv", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("window", ctypes.c_int64),
                 ("mask_kind", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class EvictShape(ctypes.Structure):
+    """``gtms_evict_shape``: sizes of an eviction from a cache."""
+
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("S", ctypes.c_int64), ("S_out", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("keep", ctypes.c_int64), ("first", ctypes.c_int64),
+                ("recent", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class GtmsError(RuntimeError):
@@ -111,6 +122,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.gtms_rotary_frequencies.argtypes = [i64, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
                                                 ctypes.c_double, i64, vp]
         lib.gtms_rotary_frequencies.restype = ctypes.c_int
+        u64p, evict = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(EvictShape)
+        lib.gtms_attention_shared_prefix.argtypes = [shape, i64, i64, heads, heads, heads, heads, heads, heads, vp, vp, vp,
+                                                     vp, vp, ctypes.c_uint64, vp, vp]
+        lib.gtms_attention_shared_prefix.restype = ctypes.c_int
+        lib.gtms_attention_shared_prefix_workspace.argtypes = [shape, i64, i64, u64p]
+        lib.gtms_attention_shared_prefix_workspace.restype = ctypes.c_int
+        lib.gtms_attention_key_weights.argtypes = [shape, heads, heads, vp, vp, ctypes.c_int, vp, vp, vp, ctypes.c_uint64,
+                                                   vp, vp]
+        lib.gtms_attention_key_weights.restype = ctypes.c_int
+        lib.gtms_attention_key_weights_workspace.argtypes = [shape, u64p]
+        lib.gtms_attention_key_weights_workspace.restype = ctypes.c_int
+        lib.gtms_cache_evict.argtypes = [evict, heads, heads, vp, vp, heads, heads, vp, vp, vp, vp, vp, ctypes.c_uint64, vp]
+        lib.gtms_cache_evict.restype = ctypes.c_int
+        lib.gtms_cache_evict_workspace.argtypes = [evict, u64p]
+        lib.gtms_cache_evict_workspace.restype = ctypes.c_int
         lib.gtms_status_string.argtypes = [ctypes.c_int]
         lib.gtms_status_string.restype = ctypes.c_char_p
         lib.gtms_version.argtypes = []
@@ -189,6 +215,37 @@ def gtms_rotary(x, y, x2, y2, B, H, H2, S, head_dim, rot_dim, positions, positio
 def gtms_rotary_frequencies(rot_dim, base, scaling, factor, low_turns, high_turns, original_length, inv_freq) -> int:
     return load_library().gtms_rotary_frequencies(rot_dim, base, scaling, factor, low_turns, high_turns,
                                                   original_length, inv_freq)
+
+
+def gtms_attention_shared_prefix(shape, groups, prefix, q, k_prefix, v_prefix, k, v, o, lse, prefix_lens, seq_lens,
+                                 q_offsets, workspace, workspace_bytes, status, stream) -> int:
+    return load_library().gtms_attention_shared_prefix(shape, groups, prefix, q, k_prefix, v_prefix, k, v, o, lse,
+                                                       prefix_lens, seq_lens, q_offsets, workspace, workspace_bytes,
+                                                       status, stream)
+
+
+def gtms_attention_shared_prefix_workspace(shape, groups, prefix, num_bytes) -> int:
+    return load_library().gtms_attention_shared_prefix_workspace(shape, groups, prefix, num_bytes)
+
+
+def gtms_attention_key_weights(shape, q, k, lse, weights, accumulate, seq_lens, q_offsets, workspace, workspace_bytes,
+                               status, stream) -> int:
+    return load_library().gtms_attention_key_weights(shape, q, k, lse, weights, accumulate, seq_lens, q_offsets,
+                                                     workspace, workspace_bytes, status, stream)
+
+
+def gtms_attention_key_weights_workspace(shape, num_bytes) -> int:
+    return load_library().gtms_attention_key_weights_workspace(shape, num_bytes)
+
+
+def gtms_cache_evict(shape, k, v, weights, positions, k_out, v_out, weights_out, positions_out, seq_lens, lens_out,
+                     workspace, workspace_bytes, stream) -> int:
+    return load_library().gtms_cache_evict(shape, k, v, weights, positions, k_out, v_out, weights_out, positions_out,
+                                           seq_lens, lens_out, workspace, workspace_bytes, stream)
+
+
+def gtms_cache_evict_workspace(shape, num_bytes) -> int:
+    return load_library().gtms_cache_evict_workspace(shape, num_bytes)
 
 
 def status_string(status: int) -> str:
@@ -634,6 +691,132 @@ def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=
             _heads("dout", dout, dtype, dev), _heads("dq", dq, dtype, dev), _heads("dk", dk, dtype, dev),
             _heads("dv", dv, dtype, dev), lens, off, workspace.data_ptr(), need.value, status)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Caches: prefixes that a batch shares, the weight that keys received, eviction.
+# ---------------------------------------------------------------------------
+
+_pack_evict = struct.Struct("@8qi4x").pack          # gtms_evict_shape
+
+
+def _workspace(fn, device, *shape):
+    """(tensor, address, bytes) of the workspace that a call of this shape needs; the tensor is to outlive the call."""
+    import torch
+
+    need = ctypes.c_uint64()
+    rc = (_direct_calls.get(fn) or _direct(fn))(*shape, ctypes.byref(need))
+    if rc != GTMS_OK:
+        raise GtmsError(fn, rc)
+    if need.value == 0:
+        return None, None, 0
+    t = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), need.value
+
+
+def _labels(name, t, dtype, shape, device):
+    """Address of a contiguous tensor with one element to a cache entry."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on the same device")
+    return t.data_ptr()
+
+
+def attention_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens, scale: float = 1.0, out=None,
+                            mask_kind: int = GTMS_MASK_GROUPED_TRIL, q_offsets=None, prefix_lens=None, status=None):
+    """(o, lse) of attention for a batch whose sequences share long prefixes (gtms_attention_shared_prefix): as
+    ``attention_forward`` over the keys of a sequence's prefix and its own put end to end.
+
+    ``k_prefix`` / ``v_prefix`` [G, Hkv, P, d]: of the batch of B = G n sequences, sequence b has prefix b // n, of
+    which the first ``prefix_lens[b // n]`` keys (int32 [G]; all without it) are seen by each of its live rows.
+    ``seq_lens`` and ``q_offsets`` count the sequences' own keys ``k`` / ``v`` [B, Hkv, Skv, d]. Masks: grouped tril or
+    length. Everything else as in ``attention_forward``."""
+    import torch
+
+    dtype, dev = q.dtype, q.get_device()
+    q_, k_, v_ = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
+    kp_, vp_ = _heads("k_prefix", k_prefix, dtype, dev), _heads("v_prefix", v_prefix, dtype, dev)
+    B, Sq, shape = _attention_shape(q, k, v, scale, mask_kind, 0)
+    G, Hkv, P, d = ps = k_prefix.shape
+    if ps != v_prefix.shape or Hkv != k.shape[1] or d != k.shape[3]:
+        raise ValueError(f"k_prefix and v_prefix must be [G, Hkv, P, head_dim] matching k, got {tuple(ps)} and "
+                         f"{tuple(v_prefix.shape)}")
+    lens, off = _int32("seq_lens", seq_lens, (B,), dev), _int32("q_offsets", q_offsets, (B,), dev)
+    plens, status = _int32("prefix_lens", prefix_lens, (G,), dev), _int32("status", status, (1,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must match q in shape")
+    lse = torch.empty((B, q.shape[1], Sq), dtype=torch.float32, device=q.device)
+    _keep, work, size = _workspace("gtms_attention_shared_prefix_workspace", q.device, shape, G, P)
+    _launch("gtms_attention_shared_prefix", dev, shape, G, P, q_, kp_, vp_, k_, v_, _heads("out", out, dtype, dev),
+            lse.data_ptr(), plens, lens, off, work, size, status)
+    return out, lse
+
+
+def attention_key_weights(q, k, lse, seq_lens, scale: float = 1.0, out=None, accumulate: bool = False,
+                          mask_kind: int = GTMS_MASK_GROUPED_TRIL, window: int = 0, q_offsets=None, status=None):
+    """The weight that each key received, fp32 [B, Hkv, Skv] (gtms_attention_key_weights): its probabilities summed over
+    the rows that keep it and the query heads that share it, recomputed from the ``lse`` that ``attention_forward``
+    (or ``attention_shared_prefix``) returned for these rows.
+
+    ``out``, a contiguous fp32 tensor, receives the weights; with ``accumulate`` they are added to what stands there,
+    and entries at and behind ``seq_lens`` stay. The same inputs give the same bits. ``q``, ``k`` and the options as in
+    ``attention_forward``."""
+    import torch
+
+    dtype, dev = q.dtype, q.get_device()
+    q_, k_ = _heads("q", q, dtype, dev), _heads("k", k, dtype, dev)
+    B, Sq, shape = _attention_shape(q, k, k, scale, mask_kind, window)
+    lens, off = _int32("seq_lens", seq_lens, (B,), dev), _int32("q_offsets", q_offsets, (B,), dev)
+    status = _int32("status", status, (1,), dev)
+    lse_ = _labels("lse", lse, torch.float32, (B, q.shape[1], Sq), dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(k.shape[:3], dtype=torch.float32, device=q.device)
+    out_ = _labels("out", out, torch.float32, k.shape[:3], dev)
+    _keep, work, size = _workspace("gtms_attention_key_weights_workspace", q.device, shape)
+    _launch("gtms_attention_key_weights", dev, shape, q_, k_, lse_, out_, bool(accumulate), lens, off, work, size, status)
+    return out
+
+
+def cache_evict(k, v, weights, seq_lens, keep: int, first: int = 0, recent: int = 0, positions=None, out=None):
+    """(k, v, weights, positions, lens) of a cache cut to ``keep`` entries a sequence and head (gtms_cache_evict).
+
+    ``k`` / ``v`` [B, H, S, d], ``weights`` fp32 and ``positions`` int32 [B, H, S] (contiguous; without it an entry's
+    index). Of a sequence of more than ``keep`` entries stay the first ``first``, the last ``recent`` and those of
+    highest weight between them, ties to the lowest index, in their order; shorter ones stay whole. ``out``: four tensors
+    of min(keep, S) or more rows to write to, whose rows behind the new lengths are left as they are; ``(k, v, weights,
+    positions)`` themselves compact the cache in place, and None in the last place leaves positions out. Without it
+    new ones of min(keep, S) rows are made, zero behind the new lengths. New tokens follow at ``lens``, for which
+    ``attention_forward`` takes ``seq_lens`` and ``q_offsets``: rows go by places in the cache."""
+    import torch
+
+    dtype, dev = k.dtype, k.get_device()
+    k_, v_ = _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
+    B, H, S, d = shape4 = k.shape
+    if v.shape != shape4:
+        raise ValueError("k and v must match in shape")
+    weights_ = _labels("weights", weights, torch.float32, (B, H, S), dev)
+    positions_ = None if positions is None else _labels("positions", positions, torch.int32, (B, H, S), dev)
+    lens = _int32("seq_lens", seq_lens, (B,), dev)
+    if out is None:
+        rows = max(0, min(int(keep), S))
+        out = (torch.zeros((B, H, rows, d), dtype=dtype, device=k.device), torch.zeros((B, H, rows, d), dtype=dtype, device=k.device),
+               torch.zeros((B, H, rows), dtype=torch.float32, device=k.device),
+               torch.zeros((B, H, rows), dtype=torch.int32, device=k.device))
+    k_out, v_out, weights_out, positions_out = out
+    rows = k_out.shape[2] if k_out.dim() == 4 else -1
+    if k_out.shape != (B, H, rows, d) or v_out.shape != k_out.shape:
+        raise ValueError("out's k and v must match k and v in every dimension but the rows")
+    wo = _labels("out's weights", weights_out, torch.float32, (B, H, rows), dev)
+    po = None if positions_out is None else _labels("out's positions", positions_out, torch.int32, (B, H, rows), dev)
+    new = torch.empty_like(seq_lens)
+    shape = _pack_evict(B, H, S, rows, d, int(keep), int(first), int(recent), _dtype_code(k))
+    _keep, work, size = _workspace("gtms_cache_evict_workspace", k.device, shape)
+    _launch("gtms_cache_evict", dev, shape, k_, v_, weights_, positions_, _heads("out's k", k_out, dtype, dev),
+            _heads("out's v", v_out, dtype, dev), wo, po, lens, new.data_ptr(), work, size)
+    return k_out, v_out, weights_out, positions_out, new
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = GTMS_ROTARY_PLAIN, factor: float = 1.0,

@@ -122,28 +122,41 @@ struct FwdItem {
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
 };
 
-template <int W>
+// Where the kernel finds its keys and rows: in one cache (this), or as the two forms
+// for a batch that shares prefixes say (gtms_shared_prefix.cuh).
+struct OneCache {
+    static constexpr bool prefixed = false, packed = false;
+    template <int W>
+    using Item = FwdItem<W>;
+    template <int W>
+    __device__ __forceinline__ void set(Item<W>& it, const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks) const
+    {
+        it.set(a, item, heads, blocks);
+    }
+};
+
+template <int W, typename Item>
 struct FwdShared {
     uint64_t qfull[W], qempty[W];
     uint64_t kvfull[4], kvempty[4], vraw;
     uint64_t sfull[W], pready[W][2], ofull[W], oempty[W];
-    ItemSlot<FwdItem<W>> items;
+    ItemSlot<Item> items;
     uint64_t mma_done;
     uint32_t tmem_slot;
     int flag;
 };
 
-template <typename T, int D, bool LONG>
+template <typename T, int D, bool LONG, typename Source = OneCache>
 __global__ void __launch_bounds__(FwdTile<D>::threads, FwdTile<D>::ctas)
 gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_constant__ HeadsMap mk,
                           const __grid_constant__ HeadsMap mv, const __grid_constant__ AttentionArgs a, uint32_t heads,
-                          int32_t blocks, uint64_t wait_ns)
+                          int32_t blocks, uint64_t wait_ns, const __grid_constant__ Source source)
 {
     using TL = FwdTile<D>;
     constexpr int ST = TL::stages, W = TL::W, carry_tiles = kCarryTerms<T> / kTile;
-    using Item = FwdItem<W>;
+    using Item = typename Source::template Item<W>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ FwdShared<W> sh;
+    __shared__ FwdShared<W, Item> sh;
     const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
@@ -151,7 +164,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int w = 0; w < W; ++w) {
-            tc::mbar_init(&sh.qfull[w], 1);
+            tc::mbar_init(&sh.qfull[w], Source::packed ? 4 : 1);
             tc::mbar_init(&sh.qempty[w], 1);
             tc::mbar_init(&sh.sfull[w], 1);
             for (int k = 0; k < 2; ++k)
@@ -182,7 +195,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         if (warp == TL::deal_warp) {
             deal_items(sh.items, up, lane, a, [&](int32_t index) {
                 Item it;
-                it.set(a, index, heads, blocks);
+                source.template set<W>(it, a, index, heads, blocks);
                 return it;
             });
         } else if (warp == TL::load_warp) {
@@ -191,7 +204,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             bool ok = true;
             while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
                 const int32_t hk = it.h / a.group;
-                auto tile = [&](const HeadsMap& m, int32_t t, bool tail) {
+                auto tile = [&](const HeadsMap& m, int32_t t, int32_t b, int32_t L, bool tail) {
                     const uint32_t s = g % ST;
                     ok = up.warp_wait(&sh.kvempty[s], ((g / ST) & 1u) ^ 1u);
                     if (!ok)
@@ -200,7 +213,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     uint64_t* bar = tail ? &sh.vraw : &sh.kvfull[s];
                     if (lane == 0) {
                         tc::mbar_arrive_expect_tx(bar, TL::bytes);
-                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, it.b, bar);
+                        load_tile<D, kTile>(base + dst, m, t * kTile, hk, b, bar);
                     }
                     if (tail) {
                         // Keys behind the length may hold anything, and 0 x NaN is NaN: zero their rows of V.
@@ -208,7 +221,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         ++nraw;
                         if (!ok)
                             return;
-                        zero_tile_rows<D, kTile>(smem + dst, it.L - t * kTile, kTile, lane);
+                        zero_tile_rows<D, kTile>(smem + dst, L - t * kTile, kTile, lane);
                         tc::fence_smem_for_async();
                         __syncwarp();
                         if (lane == 0)
@@ -231,14 +244,25 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 for (int32_t t = it.top() - 1; t >= it.bottom() && ok; --t) {
 #pragma unroll
                     for (int w = 0; w < W; ++w)
-                        if (ok && !(loaded & (1u << w)) && it.has(w, t)) {
+                        if (!Source::packed && ok && !(loaded & (1u << w)) && it.has(w, t)) {
                             loaded |= 1u << w;
                             queries(w);
                         }
-                    if (ok)
-                        tile(mk, t, false);
-                    if (ok)
-                        tile(mv, t, (t + 1) * kTile > it.L && it.L < a.Skv);
+                    if constexpr (Source::prefixed) {
+                        // The prefix's tiles stand before the sequence's own.
+                        const bool shared = t < it.prefix_tiles;
+                        const int32_t own = shared ? t : t - it.prefix_tiles, L = shared ? it.prefix : it.L;
+                        const int32_t b = shared ? it.g : it.b;
+                        if (ok)
+                            tile(shared ? source.mk : mk, own, b, L, false);
+                        if (ok)
+                            tile(shared ? source.mv : mv, own, b, L, (own + 1) * kTile > L && L < (shared ? source.p.P : a.Skv));
+                    } else {
+                        if (ok)
+                            tile(mk, t, it.b, it.L, false);
+                        if (ok)
+                            tile(mv, t, it.b, it.L, (t + 1) * kTile > it.L && it.L < a.Skv);
+                    }
                 }
             }
             if (!ok) {   // let the copies already issued land before the CTA can exit
@@ -348,11 +372,22 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         uint32_t ns = 0, no = 0, taken = 0;
         bool ok = true;
         int32_t b = 0, h = 0, i = 0, c0 = 0, c1 = 0, lo = 0, hi = 0, full0 = 0, full1 = 0;
+        [[maybe_unused]] int32_t part = 0, prefix_tiles = 0, prefix = 0;   // of the forms for shared prefixes
+        [[maybe_unused]] uint32_t nq = 0;
         auto read = [&](const Item& it) {
             b = it.b;
             h = it.h;
             i = it.i0 + w * kTile + (warp & 3) * 32 + lane;
-            a.kept(it.off + i, it.L, c0, c1);
+            if constexpr (Source::packed) {
+                c1 = it.L;
+                part = it.part;
+            } else {
+                a.kept(it.off + i, it.L, c0, c1);
+            }
+            if constexpr (Source::prefixed) {
+                prefix_tiles = it.prefix_tiles;
+                prefix = it.prefix;
+            }
             lo = it.lo[w];
             hi = it.hi[w];
             full0 = it.full0[w];
@@ -360,6 +395,32 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         };
         while (take_item(sh.items, up, lane, taken, ok, read)) {
             const bool live = c0 < c1 && i < a.Sq;
+            if constexpr (Source::packed) {
+                // This warp's 32 rows, which stand at any strides, into the query tile.
+                if (hi > lo) {
+                    ok = up.warp_wait(&sh.qempty[w], (nq & 1u) ^ 1u);
+                    ++nq;
+                    if (!ok)
+                        break;
+                    const uint64_t mine = reinterpret_cast<uint64_t>(i < a.Sq ? source.template row<T>(b, h, i) : nullptr);
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        constexpr int CH = D / 8;   // 16-byte chunks of a row
+                        const int r = (32 * k + lane) / CH, x = (32 * k + lane) % CH, row = (warp & 3) * 32 + r;
+                        const uint64_t from = __shfl_sync(0xffffffffu, mine, r);
+                        tc::cp_async16(base + w * TL::bytes + (x >> 3) * TL::box + row * 128 + (((x & 7) ^ (row & 7)) << 4),
+                                       reinterpret_cast<const uint8_t*>(from ? from : reinterpret_cast<uint64_t>(source.q.data)) +
+                                           (from ? 16 * x : 0),
+                                       from ? 16u : 0u);
+                    }
+                    tc::cp_async_commit();
+                    tc::cp_async_wait_all();
+                    tc::fence_smem_for_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.qfull[w]);
+                }
+            }
             float m = -INFINITY, l = 0.0f;
             float m_carried = -INFINITY, l_carried = 0.0f;   // of the part of O that the row of o carries, in units of l
             auto carried = [&] { return l_carried > 0.0f ? l_carried * exp2_approx((m_carried - m) * c) : 0.0f; };
@@ -383,8 +444,11 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     for (int j = 0; j < kTile; ++j)
                         s[j] *= pre;
                 }
-                if (__builtin_expect((t + 1) * kTile > full1 || t * kTile < full0, 0)) {
-                    const int32_t k0 = c0 - t * kTile, k1 = c1 - t * kTile;
+                // Columns count from a tile's own source; the prefix's are all kept.
+                const bool shared = Source::prefixed && t < prefix_tiles;
+                const int32_t col = (Source::prefixed && !shared ? t - prefix_tiles : t) * kTile;
+                if (__builtin_expect(col + kTile > (shared ? prefix : full1) || col < full0, 0)) {
+                    const int32_t k0 = c0 - col, k1 = (shared && live ? prefix : c1) - col;
 #pragma unroll
                     for (int k = 0; k < kTile; k += 32) {
                         const uint32_t keep = bits_below(k1 - k) & ~bits_below(k0 - k);
@@ -459,8 +523,36 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             }
             if (!ok)
                 break;
-            T* out = i < a.Sq ? a.o.row<T>(b, h, i) : nullptr;
             uint8_t* stage = smem + TL::off_out + warp * TL::stage;
+            if constexpr (Source::packed) {
+                // The part's sums as they are, in fp32, at its maximum in base 2.
+                const int64_t at = source.index(part, b, h, i);
+                if (i < a.Sq)
+                    source.out.ml[at] = hi > lo ? make_float2(m * c, l) : make_float2(-INFINITY, 0.0f);
+                if (hi <= lo)
+                    continue;
+                ok = up.warp_wait(&sh.ofull[w], no & 1u);
+                ++no;
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    uint32_t r[32];
+                    tc::tmem_ld32(to + k, o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = __float_as_uint(o[j]);
+                    store_rows<64>(stage, lane, r, i < a.Sq ? source.out.o + at * D + k : nullptr);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.oempty[w]);
+                continue;
+            }
+            T* out = i < a.Sq ? a.o.row<T>(b, h, i) : nullptr;
             const float inv = live ? 1.0f / l : 0.0f;
             const bool any = hi > lo;
             if (any) {
@@ -530,7 +622,7 @@ cudaError_t launch_attention_fwd_tc(const AttentionArgs& a, cudaStream_t st, uin
         const cudaError_t e = allow_smem<kern>(smem);
         return e != cudaSuccess ? e
                                 : launch_kernel(kern, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv, a,
-                                                static_cast<uint32_t>(heads), blocks, wait_ns);
+                                                static_cast<uint32_t>(heads), blocks, wait_ns, OneCache());
     };
     return kept_at_most(a, a.Skv) > kCarryTerms<T> ? launch(std::true_type()) : launch(std::false_type());
 }

@@ -21,7 +21,7 @@
 #include <atomic>
 #include <cooperative_groups.h>
 
-#include "gtms_attention_tc.cuh"
+#include "gtms_attention_fwd.cuh"
 
 namespace gtms {
 
@@ -37,29 +37,6 @@ constexpr int kSplitLarge[] = {16, 12, 10};          // larger ones, where the c
 // clusters then run at once (one token, 10 key/value heads of 8192 keys, 80 CTAs: head
 // dim 128 23.8 -> 17.5 us, 64 16.5 -> 11.6; 16 heads, whose 128 CTAs do not: 27.9, 32.4).
 
-template <typename T>
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// 16 bytes that are read once, zero where !use (nothing is read then).
-template <typename T>
-__device__ __forceinline__ uint4 load_once(const T* p, bool use)
-{
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (use)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 template <int D, int WARPS>
 struct SplitShared {
     uint4 q[kSplitRows][D / 8 + 1];                  // + 1: rows start in different banks
@@ -69,11 +46,17 @@ struct SplitShared {
     int32_t length[kSplitOrdered], batch;            // of all batches; the one this CTA takes
 };
 
+// What the rows' sums are joined with at the end: nothing, or the parts of a shared
+// prefix (gtms_shared_prefix.cuh).
+struct NoParts {
+    static constexpr bool any = false;
+};
+
 // LONG: where a warp may have more than kCarryTerms keys (code of its own, whose registers
 // the others would spill for).
-template <typename T, int D, int WARPS, bool LONG>
+template <typename T, int D, int WARPS, bool LONG, typename Parts = NoParts>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 3 : 1)
-gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordered)
+gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordered, const Parts parts)
 {
     namespace cg = cooperative_groups;
     constexpr int THREADS = 32 * WARPS;
@@ -339,6 +322,9 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
     else
         __syncthreads();
 
+    if constexpr (Parts::any)
+        await_last_launch();   // which wrote them
+
     // Join the CTAs: each writes its share of the rows' element pairs.
     for (int32_t i = rank * THREADS + threadIdx.x; i < kSplitRows * (D / 2); i += ranks * THREADS) {
         const int32_t r = i / (D / 2), d = 2 * (i % (D / 2));
@@ -347,6 +333,8 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
         float top = -INFINITY;
         for (int32_t k = 0; k < ranks; ++k)
             top = fmaxf(top, *cluster.map_shared_rank(&sh.cta_m[r], k));
+        if constexpr (Parts::any)
+            top = fmaxf(top, parts.top(b, hk, tile * kSplitRows + r));
         int32_t k0, k1;
         a.kept(off + row_of(r), L, k0, k1);
         const bool live = k0 < k1;
@@ -359,6 +347,9 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
             x += f * e.x;
             y += f * e.y;
         }
+        if constexpr (Parts::any)
+            if (live)
+                parts.template add<D>(b, hk, tile * kSplitRows + r, d, base, sum, x, y);
         const float inv = live ? 1.0f / sum : 0.0f;
         *reinterpret_cast<uint32_t*>(a.o.row<T>(b, head_of(r), row_of(r)) + d) = live ? pack2<T>(x * inv, y * inv) : 0u;
         if (a.lse && d == 0)
@@ -430,20 +421,23 @@ template <int WARPS>
 struct SplitConfig {
     template <int D>
     static constexpr int smem = static_cast<int>(sizeof(SplitShared<D, WARPS>));
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
 
-    SplitConfig(int64_t ctas, int ranks, int bytes, cudaStream_t st)
+    // beside_last: may start while the last launch still runs (see await_last_launch).
+    SplitConfig(int64_t ctas, int ranks, int bytes, cudaStream_t st, bool beside_last = false)
     {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         cfg.blockDim = dim3(32 * WARPS);
         cfg.dynamicSmemBytes = bytes;
         cfg.stream = st;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = beside_last ? 2 : 1;
     }
 };
 
@@ -488,26 +482,26 @@ constexpr int64_t kSplitLargeKeys = 4096;
 // 87.5; 69.7, 77.8).
 constexpr int kSplitSmaller[] = {6, 5};
 
-template <typename T, int D, int WARPS, bool LONG>
-cudaError_t launch_attention_split_k(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
+template <typename T, int D, int WARPS, bool LONG, typename Parts>
+cudaError_t launch_attention_split_k(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st, const Parts& parts)
 {
     constexpr int smem = SplitConfig<WARPS>::template smem<D>;
-    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS, LONG>, true>(smem);
+    const cudaError_t e = allow_smem<gtms_attention_split_kernel<T, D, WARPS, LONG, Parts>, true>(smem);
     if (e != cudaSuccess)
         return e;
-    SplitConfig<WARPS> cfg(ctas, ranks, smem, st);
+    SplitConfig<WARPS> cfg(ctas, ranks, smem, st, Parts::any);
     const int32_t tiles = static_cast<int32_t>((static_cast<int64_t>(a.group) * a.Sq + kSplitRows - 1) / kSplitRows);
     const int32_t ordered = WARPS == 4 && ctas > 3 * device_sms() && a.B > 1 && a.B <= kSplitOrdered;
-    return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS, LONG>, a, tiles, ordered);
+    return cudaLaunchKernelEx(&cfg.cfg, gtms_attention_split_kernel<T, D, WARPS, LONG, Parts>, a, tiles, ordered, parts);
 }
 
-template <typename T, int D, int WARPS>
-cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st)
+template <typename T, int D, int WARPS, typename Parts>
+cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int ranks, cudaStream_t st, const Parts& parts)
 {
     // A warp takes every WARPS-th of its CTA's blocks, of which the keys can make one more than an even share.
     const bool is_long = split_keys(a) / (ranks * WARPS) + 2 * kSplitKeys > kCarryTerms<T>;
-    return is_long ? launch_attention_split_k<T, D, WARPS, true>(a, ctas, ranks, st)
-                   : launch_attention_split_k<T, D, WARPS, false>(a, ctas, ranks, st);
+    return is_long ? launch_attention_split_k<T, D, WARPS, true>(a, ctas, ranks, st, parts)
+                   : launch_attention_split_k<T, D, WARPS, false>(a, ctas, ranks, st, parts);
 }
 
 // The clusters go by the keys that the rows keep, not by the cache: under a sliding
@@ -516,8 +510,8 @@ cudaError_t launch_attention_split_w(const AttentionArgs& a, int64_t ctas, int r
 // 18.5, 7.8). Where all clusters run at once a window's warps are left with one block of
 // keys instead of two (8 heads of 128, window 256: 7.8 us with clusters of 2, 6.9 of 4,
 // 7.1 of 8; 32 heads 8.4, 7.5, 7.7).
-template <typename T, int D>
-cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
+template <typename T, int D, typename Parts = NoParts>
+cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st, const Parts& parts = Parts())
 {
     const int nsm = device_sms();
     if (nsm <= 0)
@@ -534,17 +528,17 @@ cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t st)
     const bool large = keys >= kSplitLargeKeys;
     for (int r : kSplitLarge)
         if (large && units <= clusters_at_once<T, D, 8>(r))
-            return launch_attention_split_w<T, D, 8>(a, units * r, r, st);
+            return launch_attention_split_w<T, D, 8>(a, units * r, r, st, parts);
     if (units <= clusters_at_once<T, D, 8>(ranks))
-        return launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st);
+        return launch_attention_split_w<T, D, 8>(a, units * ranks, ranks, st, parts);
     for (int r : kSplitLarge)
         if (large && units <= clusters_at_once<T, D, 4>(r))
-            return launch_attention_split_w<T, D, 4>(a, units * r, r, st);
+            return launch_attention_split_w<T, D, 4>(a, units * r, r, st, parts);
     if (ranks == kSplitMaxCluster && units > clusters_at_once<T, D, 4>(ranks))
         for (int r : kSplitSmaller)
             if (units <= clusters_at_once<T, D, 4>(r))
-                return launch_attention_split_w<T, D, 4>(a, units * r, r, st);
-    return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st);
+                return launch_attention_split_w<T, D, 4>(a, units * r, r, st, parts);
+    return launch_attention_split_w<T, D, 4>(a, units * ranks, ranks, st, parts);
 }
 
 }  // namespace gtms

@@ -1,0 +1,169 @@
+// gtms_shared_prefix.cuh -- attention for a batch whose sequences share long prefixes.
+//
+// Sequence b of n G keeps, beside its own keys, all keys of prefix b / n:
+//   o_i = sum_c exp(s_ic - lse_i) v_c over the prefix's keys and its own kept ones.
+//
+// Two forms, of the two attention kernels:
+//   rows of their own   (prompts, long chunks) a tile of query rows walks over the
+//                       tiles of the prefix and then its own, as over one cache
+//                       (PrefixedCache). One launch; a prefix tile is read once for 128
+//                       or 256 rows of one head, from L2 mostly;
+//   rows packed         (new tokens) the rows of all sequences and heads that share a
+//                       prefix's head stand in one matrix, 128 to a tile, so that its
+//                       keys are read once for all of them and by the tensor cores'
+//                       full width. The keys are dealt out in parts, each part's sums
+//                       (m, l, O) go to the workspace in fp32 (PrefixRows), and the
+//                       split kernel joins them with what it finds in the sequences'
+//                       own caches (PrefixParts).
+#pragma once
+
+#include "gtms_attention_fwd.cuh"
+#include "gtms_attention_split.cuh"
+#include "gtms_caches.h"
+
+namespace gtms {
+
+// Tiles [0, prefix_tiles) of an item are the prefix's, those behind them its own.
+struct PrefixedCache {
+    static constexpr bool prefixed = true, packed = false;
+    HeadsMap mk, mv;
+    PrefixArgs p;
+
+    template <int W>
+    struct Item : FwdItem<W> {
+        int32_t g, prefix, prefix_tiles;
+    };
+    template <int W>
+    __device__ __forceinline__ void set(Item<W>& it, const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t blocks) const
+    {
+        it.set(a, item, heads, blocks);
+        it.g = it.b / p.n;
+        it.prefix = p.length(it.g);
+        it.prefix_tiles = (it.prefix + kTile - 1) / kTile;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            it.hi[w] += it.hi[w] > 0 ? it.prefix_tiles : 0;   // lo is 0: no windows here
+    }
+};
+
+// The partial sums of a prefix's keys: row R of (prefix g, key/value head h) is query
+// row (R / group) % Sq, shared head R % group of its sequence R / (group Sq).
+struct PrefixParts {
+    static constexpr bool any = true;
+    float* o;        // [parts, G Hkv, rows, D], not divided by l
+    float2* ml;      // [parts, G Hkv, rows]: maximum in base 2 and sum; (-inf, 0) without keys, and o is not written
+    int32_t parts, n, G, Hkv, per;   // per: rows of a sequence (group Sq)
+
+    __host__ __device__ __forceinline__ int64_t stride() const { return static_cast<int64_t>(G) * Hkv * n * per; }
+    __device__ __forceinline__ int64_t at(int32_t b, int32_t hk, int32_t r) const
+    {
+        const int32_t g = b / n;
+        return (static_cast<int64_t>(g) * Hkv + hk) * (static_cast<int64_t>(n) * per) + static_cast<int64_t>(b - g * n) * per + r;
+    }
+    __device__ __forceinline__ float top(int32_t b, int32_t hk, int32_t r) const
+    {
+        const float2* x = ml + at(b, hk, r);
+        float t = -INFINITY;
+#pragma unroll 4
+        for (int32_t k = 0; k < parts; ++k)
+            t = fmaxf(t, x[k * stride()].x);
+        return t;
+    }
+    // Adds them to a row's sums at maximum `base`: l, and the elements d and d + 1.
+    template <int D>
+    __device__ __forceinline__ void add(int32_t b, int32_t hk, int32_t r, int32_t d, float base, float& l, float& x, float& y) const
+    {
+        const int64_t i = at(b, hk, r);
+#pragma unroll 4
+        for (int32_t k = 0; k < parts; ++k) {
+            const float2 s = ml[i + k * stride()];
+            if (s.y > 0.0f) {
+                const float f = exp2_approx(s.x - base);
+                const float2 e = *reinterpret_cast<const float2*>(o + (i + k * stride()) * D + d);
+                l += f * s.y;
+                x += f * e.x;
+                y += f * e.y;
+            }
+        }
+    }
+};
+
+// Work items (prefix, head, rows, part of the keys) of the packed rows. The kernel's
+// AttentionArgs are those of one batch of G over the prefixes, Sq its packed rows.
+struct PrefixRows {
+    static constexpr bool prefixed = false, packed = true;
+    HeadsRef q;
+    PrefixArgs p;
+    PrefixParts out;
+    int32_t Sq, group;
+
+    template <int W>
+    struct Item : FwdItem<W> {
+        int32_t part;
+    };
+    template <int W>
+    __device__ __forceinline__ void set(Item<W>& it, const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t) const
+    {
+        const int32_t gh = static_cast<int32_t>(item % heads), rest = static_cast<int32_t>(item / heads);
+        it.part = rest % out.parts;
+        it.b = gh / a.Hkv;
+        it.h = gh - it.b * a.Hkv;
+        it.i0 = rest / out.parts * W * kTile;
+        it.off = 0;
+        it.L = p.length(it.b);
+        const int32_t tiles = (it.L + kTile - 1) / kTile, per = (tiles + out.parts - 1) / out.parts;
+        const int32_t lo = it.part * per, hi = lo + per < tiles ? lo + per : tiles;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const bool any = lo < hi && it.i0 + w * kTile < a.Sq;
+            it.lo[w] = any ? lo : 0;
+            it.hi[w] = any ? hi : 0;
+            it.full0[w] = 0;
+            it.full1[w] = it.L;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ const T* row(int32_t g, int32_t h, int32_t r) const
+    {
+        const int32_t b = r / out.per, i = r - b * out.per, s = i / group;
+        return q.row<T>(g * p.n + b, h * group + (i - s * group), s);
+    }
+    __device__ __forceinline__ int64_t index(int32_t part, int32_t g, int32_t h, int32_t r) const
+    {
+        return part * out.stride() + (static_cast<int64_t>(g) * out.Hkv + h) * (static_cast<int64_t>(p.n) * out.per) + r;
+    }
+};
+
+template <typename T, int D>
+cudaError_t launch_prefixed_whole(const AttentionArgs& a, const PrefixArgs& p, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
+{
+    using TL = FwdTile<D>;
+    if (!bind_context())
+        return cudaErrorUnknown;
+    // Without keys no tile is loaded, and q stands in for k and v in the maps.
+    const bool keys = a.Skv > 0, shared = p.P > 0;
+    HeadsMap mq, mk, mv;
+    PrefixedCache source;
+    source.p = p;
+    if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, kTile) ||
+        !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
+        !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
+        !encode_heads<T>(source.mk, shared ? p.k : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile) ||
+        !encode_heads<T>(source.mv, shared ? p.v : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile))
+        return cudaErrorInvalidValue;
+    const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
+    auto launch = [&](auto is_long) {
+        constexpr auto* kern = gtms_attention_fwd_kernel<T, D, is_long(), PrefixedCache>;
+        constexpr int smem = static_cast<int>(TL::smem);
+        const cudaError_t e = allow_smem<kern>(smem);
+        return e != cudaSuccess ? e
+                                : launch_kernel(kern, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv, a,
+                                                static_cast<uint32_t>(heads), blocks, wait_ns, source);
+    };
+    // A tile counts as whole even where the prefix ends inside it.
+    const int64_t most = static_cast<int64_t>(p.P) + kTile + a.Skv;
+    return most > kCarryTerms<T> ? launch(std::true_type()) : launch(std::false_type());
+}
+
+}  // namespace gtms
