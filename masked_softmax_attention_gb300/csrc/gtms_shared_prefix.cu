@@ -3,12 +3,27 @@
 
 namespace gtms {
 
-uint64_t shared_prefix_workspace_bytes(const AttentionArgs&, const PrefixArgs&, int64_t) { return 0; }
+namespace {
+
+template <int D>
+uint64_t workspace_bytes(const AttentionArgs& a, const PrefixArgs& p)
+{
+    const PackedPlan x = packed_plan<D>(a, p);
+    return prefer_packed<D>(a, p, x) ? packed_bytes(a, p, x, D) : 0;
+}
+
+}  // namespace
+
+uint64_t shared_prefix_workspace_bytes(const AttentionArgs& a, const PrefixArgs& p, int64_t D)
+{
+    return D == 64 ? workspace_bytes<64>(a, p) : workspace_bytes<128>(a, p);
+}
 
 template <typename T, int D>
-cudaError_t launch_shared_prefix(const AttentionArgs& a, const PrefixArgs& p, void*, cudaStream_t st)
+cudaError_t launch_shared_prefix(const AttentionArgs& a, const PrefixArgs& p, void* workspace, cudaStream_t st)
 {
-    return launch_prefixed_whole<T, D>(a, p, st);
+    const PackedPlan x = packed_plan<D>(a, p);
+    return prefer_packed<D>(a, p, x) ? launch_prefix_packed<T, D>(a, p, x, workspace, st) : launch_prefixed_whole<T, D>(a, p, st);
 }
 
 #define GTMS_SHARED_PREFIX(T, D) \

@@ -111,7 +111,7 @@ struct PrefixRows {
         it.i0 = rest / out.parts * W * kTile;
         it.off = 0;
         it.L = p.length(it.b);
-        const int32_t tiles = (it.L + kTile - 1) / kTile, per = (tiles + out.parts - 1) / out.parts;
+        const int32_t tiles = (it.L + kTile - 1) / kTile, per = (tiles + out.parts - 1) / out.parts;   // of this prefix
         const int32_t lo = it.part * per, hi = lo + per < tiles ? lo + per : tiles;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -164,6 +164,112 @@ cudaError_t launch_prefixed_whole(const AttentionArgs& a, const PrefixArgs& p, c
     // A tile counts as whole even where the prefix ends inside it.
     const int64_t most = static_cast<int64_t>(p.P) + kTile + a.Skv;
     return most > kCarryTerms<T> ? launch(std::true_type()) : launch(std::false_type());
+}
+
+// How a call's packed rows are dealt out: tiles of rows, parts of the keys.
+struct PackedPlan {
+    int64_t rows;     // of one prefix and key/value head
+    int64_t blocks;   // items of rows
+    int32_t parts;
+    double us;        // of the first launch
+};
+
+// Microseconds of an item of rows x keys, and of 128 keys of one (with both CTAs of a
+// multiprocessor busy at head dim 64), as measured for the forward kernel.
+template <int D>
+constexpr double kItemUs = D == 64 ? 4.0 : 5.0;
+template <int D>
+constexpr double kTileUs = D == 64 ? 1.0 : 1.15;
+
+// Parts: as many as take the least time. A part's keys are below kCarryTerms of either
+// type, so that no sum in an accumulator is long.
+template <int D>
+PackedPlan packed_plan(const AttentionArgs& a, const PrefixArgs& p)
+{
+    using TL = FwdTile<D>;
+    PackedPlan x;
+    x.rows = static_cast<int64_t>(p.n) * a.Sq * a.group;
+    x.blocks = (x.rows + TL::rows - 1) / TL::rows;
+    const int64_t items = static_cast<int64_t>(p.G) * a.Hkv * x.blocks, slots = int64_t(kChipSms) * TL::ctas;
+    const int64_t tiles = (static_cast<int64_t>(p.P) + kTile - 1) / kTile, least = (tiles + 255) / 256;
+    x.parts = 1;
+    x.us = 0.0;
+    for (int64_t parts = least; parts <= tiles && parts <= least + 63; ++parts) {
+        const int64_t turns = (items * parts + slots - 1) / slots, per = (tiles + parts - 1) / parts;
+        // Each part is written once and read once by the second launch, in fp32, at about 10 TB/s (L2).
+        const double us = static_cast<double>(turns) * (kItemUs<D> + kTileUs<D> * static_cast<double>(per)) +
+                          static_cast<double>(items * parts) * TL::rows * D * 8 * 1e-7;
+        if (parts == least || us < x.us) {
+            x.us = us;
+            x.parts = static_cast<int32_t>(parts);
+        }
+    }
+    return x;
+}
+
+// Whether to pack: always where the rows of a sequence's head fill one tile of the
+// split kernel, otherwise by the time that both forms take (see prefer_split).
+template <int D>
+bool prefer_packed(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x)
+{
+    const int64_t rows = static_cast<int64_t>(a.group) * a.Sq;
+    if (p.P == 0 || rows > kSplitMaxRows || x.rows > (1 << 24) || x.blocks * x.parts * p.G * a.Hkv > INT32_MAX)
+        return false;
+    if (rows <= kSplitRows)
+        return true;
+    const double items = static_cast<double>(a.B) * a.Hq * ((a.Sq + FwdTile<D>::rows - 1) / FwdTile<D>::rows);
+    const double loads = items / (static_cast<double>(kChipSms) * FwdTile<D>::ctas);
+    const int64_t tiles = (static_cast<int64_t>(p.P) + kTile - 1) / kTile + (static_cast<int64_t>(a.Skv) + kTile - 1) / kTile;
+    const double whole = (loads > 1.0 ? loads : 1.0) * (kItemUs<D> + kTileUs<D> * static_cast<double>(tiles));
+    const int64_t units = split_units(a), ranks = split_ranks(units, a.Skv, kChipSms);
+    const double turns = static_cast<double>(units * ranks) / (3 * kChipSms);
+    const double block = turns > 1.0 ? (D == 64 ? 1.3 : 2.3) : (D == 64 ? 1.0 : 1.8);
+    const double split = (turns > 1.0 ? turns : 1.0) * (6.0 + block * static_cast<double>((a.Skv + ranks * 64 - 1) / (ranks * 64)));
+    return x.us + split < whole;
+}
+
+inline uint64_t packed_bytes(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x, int64_t D)
+{
+    return static_cast<uint64_t>(x.parts) * p.G * a.Hkv * x.rows * (D * 4 + 8);
+}
+
+template <typename T, int D>
+cudaError_t launch_prefix_packed(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x, void* workspace,
+                                 cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
+{
+    using TL = FwdTile<D>;
+    if (!bind_context())
+        return cudaErrorUnknown;
+    const int64_t heads = static_cast<int64_t>(p.G) * a.Hkv;
+    HeadsMap mk, mv;
+    if (!encode_heads<T>(mk, p.k, p.G, a.Hkv, p.P, D, kTile) || !encode_heads<T>(mv, p.v, p.G, a.Hkv, p.P, D, kTile))
+        return cudaErrorInvalidValue;
+    PrefixRows source;
+    source.q = a.q;
+    source.p = p;
+    source.Sq = a.Sq;
+    source.group = a.group;
+    source.out.o = static_cast<float*>(workspace);
+    source.out.ml = reinterpret_cast<float2*>(source.out.o + x.parts * heads * x.rows * D);
+    source.out.parts = x.parts;
+    source.out.n = p.n;
+    source.out.G = p.G;
+    source.out.Hkv = a.Hkv;
+    source.out.per = a.group * a.Sq;
+    AttentionArgs rows = a;   // one batch of G, its queries the packed rows
+    rows.B = p.G;
+    rows.Hq = a.Hkv;
+    rows.group = 1;
+    rows.Sq = static_cast<int32_t>(x.rows);
+    rows.Skv = p.P;
+    rows.mask_kind = GTMS_MASK_LENGTH;
+    constexpr auto* kern = gtms_attention_fwd_kernel<T, D, false, PrefixRows>;
+    constexpr int smem = static_cast<int>(TL::smem);
+    cudaError_t e = allow_smem<kern>(smem);
+    if (e == cudaSuccess)
+        e = launch_kernel(kern, static_cast<unsigned>(heads * x.blocks * x.parts), TL::threads, smem, st, mk, mk, mv, rows,
+                          static_cast<uint32_t>(heads), static_cast<int32_t>(x.blocks), wait_ns, source);
+    return e != cudaSuccess ? e : launch_attention_split<T, D>(a, st, source.out);
 }
 
 }  // namespace gtms
