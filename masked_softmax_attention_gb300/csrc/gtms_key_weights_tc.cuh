@@ -1,0 +1,477 @@
+// gtms_key_weights_tc.cuh -- the weight that each key of a cache received, on the tensor
+// cores: many query rows, or some rows over many keys.
+//
+//   w_c = sum over the query heads of a key/value head and rows i with c in K(i) of
+//         exp(scale q_i . k_c - lse_i)
+//
+// The transposed product S = K Q^T has a key to a row, so that the thread that owns a
+// row of S in tensor memory sums its exponentials by itself: no maximum, no exchange,
+// nothing written back. A work item is two tiles of 128 keys, which stay in shared
+// memory, and the column tiles of query rows that keep any of them, which stream past.
+// The rows of the heads that share the keys are packed side by side (a 5-D map: element,
+// head, row, key/value head, batch), so that one new token fills as many columns as it
+// has heads, and a window's or a causal mask's kept columns of a key are one range.
+// Roles:
+//   deal (1 warp)    the work items (see ItemSlot);
+//   load (1 warp)    TMA: the key tiles into one ring, the column tiles into another;
+//   shift (1 warp)   -lse of the columns, in base 2, -infinity for those that do not count;
+//   MMA (1 warp)     S of each key tile, held twice, so that the next column tile's
+//                    products run while this one's exponentials do;
+//   sum (16 warps)   four to a key tile and half of its columns; the halves meet once an item.
+// Where few items make the grid (short caches of few heads), their rows are cut into
+// parts, whose sums a second launch adds in order.
+#pragma once
+
+#include "gtms_attention_tc.cuh"
+#include "gtms_caches.h"
+
+namespace gtms {
+
+template <int D>
+struct KeyTile {
+    static constexpr int W = 2, keys = W * kTile;                          // key tiles and keys of a work item
+    static constexpr int NK = D == 64 ? 6 : 3, ST = D == 64 ? 4 : 3;       // stages of the rings of key and column tiles
+    static constexpr int sum_warps = 16, mma_warp = 16, load_warp = 17, shift_warp = 18, deal_warp = 19, threads = 640;
+    static constexpr uint32_t bytes = kTile * D * 2, box = kTile * 128;    // a 128-row tile, 64 columns of it
+    static constexpr uint32_t off_q = NK * bytes;
+    static constexpr uint32_t smem = off_q + ST * bytes + 1024;            // slack to align the base
+    static constexpr int tmem = 512;                                       // two S of each key tile
+    static_assert(smem <= 226 * 1024, "shared memory of a CTA");
+};
+
+// How query rows become columns: `heads` shared heads (all, or 128 of more) of `rows` rows to a tile.
+struct KeyColumns {
+    int32_t heads, rows, head_tiles;
+    int32_t mb;   // of the map of q: 0 where one batch serves all (see HeadsMap)
+};
+
+inline KeyColumns key_columns(int32_t group)
+{
+    KeyColumns c;
+    c.heads = group < kTile ? group : kTile;
+    c.rows = kTile / c.heads;
+    c.head_tiles = (group + c.heads - 1) / c.heads;
+    c.mb = 1;
+    return c;
+}
+
+struct KeyItem {
+    int32_t b, hk, key0, tiles, off, L, part;
+    int32_t i0, i1;        // rows that keep any of the keys
+    int32_t ct0, ct1;      // this part's column tiles, counted from row i0
+
+    __device__ __forceinline__ void set(const AttentionArgs& a, const KeyColumns& col, uint32_t item, uint32_t heads,
+                                        int32_t parts)
+    {
+        const int32_t bg = static_cast<int32_t>(item % heads), rest = static_cast<int32_t>(item / heads);
+        part = rest % parts;
+        key0 = rest / parts * (2 * kTile);
+        b = bg / a.Hkv;
+        hk = bg - b * a.Hkv;
+        off = a.offset(b);
+        L = a.length(b);
+        tiles = 0;
+        i0 = i1 = ct0 = ct1 = 0;
+        if (key0 >= L)
+            return;
+        tiles = key0 + kTile < L ? 2 : 1;
+        const int32_t last = (key0 + 2 * kTile < L ? key0 + 2 * kTile : L) - 1;
+        i0 = off < 0 ? -off : 0;
+        i1 = L - off < a.Sq ? L - off : a.Sq;
+        if (a.mask_kind != GTMS_MASK_LENGTH && key0 - off > i0)
+            i0 = key0 - off;
+        if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && last + a.window - off < i1)
+            i1 = last + a.window - off;
+        if (i0 >= i1)
+            return;
+        const int32_t all = (i1 - i0 + col.rows - 1) / col.rows * col.head_tiles, per = (all + parts - 1) / parts;
+        ct0 = part * per < all ? part * per : all;
+        ct1 = ct0 + per < all ? ct0 + per : all;
+    }
+    __device__ __forceinline__ uint32_t steps(const AttentionArgs&) const { return ct1 - ct0; }
+};
+
+template <int D>
+struct KeyShared {
+    using TL = KeyTile<D>;
+    uint64_t kfull[TL::NK], kempty[TL::NK], qfull[TL::ST], qempty[TL::ST], hfull[TL::ST], hempty[TL::ST];
+    uint64_t sfull[2][TL::W], sempty[2][TL::W], rfull[TL::W], rempty[TL::W], mma_done;
+    ItemSlot<KeyItem> items;
+    __align__(16) float shift[TL::ST][kTile];
+    float half[TL::W][kTile];
+    uint32_t tmem_slot;
+    int flag;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(KeyTile<D>::threads, 1)
+gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ HeadsMap mk,
+                        const __grid_constant__ KeyWeightsArgs kw, const KeyColumns col, uint32_t heads, int32_t parts,
+                        uint64_t wait_ns)
+{
+    using TL = KeyTile<D>;
+    constexpr int W = TL::W, NK = TL::NK, ST = TL::ST;
+    const AttentionArgs& a = kw.a;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ KeyShared<D> sh;
+    const int warp = warp_value(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const GiveUp up{&sh.flag, a.status, wait_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NK; ++s) {
+            tc::mbar_init(&sh.kfull[s], 1);
+            tc::mbar_init(&sh.kempty[s], 1);
+        }
+        for (int s = 0; s < ST; ++s) {
+            tc::mbar_init(&sh.qfull[s], 1);
+            tc::mbar_init(&sh.qempty[s], 1);
+            tc::mbar_init(&sh.hfull[s], 1);
+            tc::mbar_init(&sh.hempty[s], TL::sum_warps);
+        }
+        for (int w = 0; w < W; ++w) {
+            for (int k = 0; k < 2; ++k) {
+                tc::mbar_init(&sh.sfull[k][w], 1);
+                tc::mbar_init(&sh.sempty[k][w], 8);
+            }
+            tc::mbar_init(&sh.rfull[w], 4);
+            tc::mbar_init(&sh.rempty[w], 4);
+        }
+        tc::mbar_init(&sh.mma_done, 1);
+        init_items(sh.items, TL::sum_warps + 3);   // load, shift, MMA and sum warps
+        sh.flag = 0;
+    }
+    // Columns that no row fills stay zero for good: the copies do not reach them.
+    const int32_t filled = col.heads * col.rows;
+    for (int32_t i = threadIdx.x; i < ST * (D / 64) * (kTile - filled) * 8; i += TL::threads) {
+        const int32_t blk = i / ((kTile - filled) * 8), at = i % ((kTile - filled) * 8);
+        *reinterpret_cast<uint4*>(smem + TL::off_q + blk * TL::box + filled * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+    }
+    tc::fence_smem_for_async();
+    if (warp == TL::mma_warp) {
+        __syncwarp();
+        tc::tmem_alloc<TL::tmem>(&sh.tmem_slot);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = warp_value(sh.tmem_slot);
+
+    if (warp == TL::deal_warp) {
+        deal_items(sh.items, up, lane, a, [&](int32_t index) {
+            KeyItem it;
+            it.set(a, col, index, heads, parts);
+            return it;
+        });
+    } else if (warp == TL::load_warp) {
+        uint32_t nk = 0, nq = 0, taken = 0;
+        KeyItem it;
+        bool ok = true;
+        while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
+            if (it.ct0 >= it.ct1)
+                continue;
+            for (int w = 0; w < it.tiles && ok; ++w) {
+                const uint32_t s = nk % NK;
+                ok = item_wait(sh.items, up, &sh.kempty[s], ((nk / NK) & 1u) ^ 1u);   // held for a whole item
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&sh.kfull[s], TL::bytes);
+                    load_tile<D, kTile>(base + s * TL::bytes, mk, it.key0 + w * kTile, it.hk, it.b, &sh.kfull[s]);
+                }
+                ++nk;
+            }
+            for (int32_t t = it.ct0; t < it.ct1 && ok; ++t) {
+                const uint32_t s = nq % ST;
+                ok = up.warp_wait(&sh.qempty[s], ((nq / ST) & 1u) ^ 1u);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
+                    tc::mbar_arrive_expect_tx(&sh.qfull[s], filled * D * 2);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tc::tma_load_5d(base + TL::off_q + s * TL::bytes + x * TL::box, &mq, x * 64, j, i, it.hk, it.b * col.mb,
+                                        &sh.qfull[s]);
+                }
+                ++nq;
+            }
+        }
+        if (!ok) {   // let the copies already issued land before the CTA can exit
+            for (uint32_t k = 0; k < static_cast<uint32_t>(NK) && k < nk; ++k)
+                tc::mbar_wait(&sh.kfull[(nk - 1 - k) % NK], ((nk - 1 - k) / NK) & 1u, kAttnDrainWaitNs);
+            for (uint32_t k = 0; k < static_cast<uint32_t>(ST) && k < nq; ++k)
+                tc::mbar_wait(&sh.qfull[(nq - 1 - k) % ST], ((nq - 1 - k) / ST) & 1u, kAttnDrainWaitNs);
+        }
+    } else if (warp == TL::shift_warp) {
+        // This lane's four columns of a tile, as row and head in it.
+        int32_t ci[4], cj[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            ci[k] = (32 * k + lane) / col.heads;
+            cj[k] = (32 * k + lane) % col.heads;
+        }
+        uint32_t n = 0, taken = 0;
+        KeyItem it;
+        bool ok = true;
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
+            for (int32_t t = it.ct0; t < it.ct1; ++t, ++n) {
+                const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
+                float x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool counts = ci[k] < col.rows && i + ci[k] < it.i1 && j + cj[k] < a.group;
+                    const int64_t head = static_cast<int64_t>(it.b) * a.Hq + it.hk * a.group + j + cj[k];
+                    x[k] = counts ? __ldg(a.lse + head * a.Sq + i + ci[k]) : -INFINITY;
+                }
+                const uint32_t s = n % ST;
+                ok = up.warp_wait(&sh.hempty[s], ((n / ST) & 1u) ^ 1u);
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // a row that kept nothing gives nothing
+                    sh.shift[s][32 * k + lane] = x[k] == -INFINITY ? -INFINITY : -x[k] * kLog2e;
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.hfull[s]);
+            }
+        }
+    } else if (warp == TL::mma_warp) {
+        uint32_t nk = 0, nq = 0, taken = 0;
+        uint32_t ns[W] = {};   // products into S of key tile w
+        KeyItem it;
+        bool ok = true;
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
+            const int32_t ct0 = warp_value(it.ct0), ct1 = warp_value(it.ct1), tiles = warp_value(it.tiles);
+            for (int32_t t = ct0; t < ct1 && ok; ++t, ++nq) {
+                const uint32_t sq = nq % ST;
+                ok = up.warp_wait(&sh.qfull[sq], (nq / ST) & 1u);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if (w >= tiles || !ok)
+                        break;
+                    const uint32_t sk = (nk + w) % NK, buf = ns[w] & 1u;
+                    if (t == ct0)
+                        ok = up.warp_wait(&sh.kfull[sk], ((nk + w) / NK) & 1u);
+                    ok = ok && up.warp_wait(&sh.sempty[buf][w], ((ns[w] >> 1) & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    mma_abt<T, D, kTile>(tmem + (buf * W + w) * kTile, base + sk * TL::bytes, base + TL::off_q + sq * TL::bytes);
+                    tc::commit_warp(&sh.sfull[buf][w]);
+                    if (t == ct1 - 1)
+                        tc::commit_warp(&sh.kempty[sk]);
+                    ++ns[w];
+                }
+                if (ok)
+                    tc::commit_warp(&sh.qempty[sq]);
+            }
+            if (ct0 < ct1)
+                nk += tiles;
+        }
+        // Nothing may be in flight when the tensor memory is freed.
+        tc::commit_warp(&sh.mma_done);
+        tc::mbar_wait(&sh.mma_done, 0, kAttnDrainWaitNs);
+    } else {
+        const int w = (warp >> 2) & 1, half = warp >> 3, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 tensor-memory lanes per warp, lane in bits 16..
+        const float c = a.scale * kLog2e;
+        uint32_t n = 0, ns = 0, nr = 0, taken = 0;
+        KeyItem it;
+        bool ok = true;
+        while (take_item(sh.items, up, lane, taken, it, ok)) {
+            const int32_t first = it.key0 + w * kTile, key = first + row;
+            const int32_t last = (first + kTile < it.L ? first + kTile : it.L) - 1;   // the tile's last live key
+            // Rows that keep this key.
+            int32_t k0 = it.i0, k1 = it.i1;
+            if (a.mask_kind != GTMS_MASK_LENGTH && key - it.off > k0)
+                k0 = key - it.off;
+            if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && key + a.window - it.off < k1)
+                k1 = key + a.window - it.off;
+            float sum = 0.0f;
+            for (int32_t t = it.ct0; t < it.ct1; ++t, ++n) {
+                const uint32_t s = n % ST;
+                ok = item_wait(sh.items, up, &sh.hfull[s], (n / ST) & 1u);
+                if (!ok)
+                    break;
+                if (w < it.tiles) {
+                    const uint32_t buf = ns & 1u;
+                    ok = item_wait(sh.items, up, &sh.sfull[buf][w], (ns >> 1) & 1u);
+                    ++ns;
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    float x[64];
+                    tc::tmem_ld64(tmem + lanes + (buf * W + w) * kTile + half * 64, x);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.sempty[buf][w]);
+                    const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
+                    const float4* shift = reinterpret_cast<const float4*>(&sh.shift[s][half * 64]);
+                    const float2 c2 = make_float2(c, c);
+                    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    // Every row of the tile keeps every live key of this one.
+                    const bool whole = i + col.rows <= it.i1 && j + col.heads <= a.group &&
+                                       (a.mask_kind == GTMS_MASK_LENGTH || i + it.off >= last) &&
+                                       (a.mask_kind != GTMS_MASK_SLIDING_WINDOW || i + col.rows - 1 + it.off < first + a.window);
+                    if (__builtin_expect(whole, 1)) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float4 h = shift[k];
+                            float2 e = __ffma2_rn(make_float2(x[4 * k], x[4 * k + 1]), c2, make_float2(h.x, h.y));
+                            float2 f = __ffma2_rn(make_float2(x[4 * k + 2], x[4 * k + 3]), c2, make_float2(h.z, h.w));
+                            acc[0] = __fadd2_rn(acc[0], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
+                            acc[1] = __fadd2_rn(acc[1], make_float2(exp2_approx(f.x), exp2_approx(f.y)));
+                        }
+                    } else {
+                        // Columns [n0, n1) of the tile, as rows of it times heads.
+                        const int32_t r0 = min(max(k0 - i, 0), kTile), r1 = min(max(k1 - i, 0), kTile);
+                        const int32_t n0 = r0 * col.heads - half * 64;
+                        int32_t n1 = r1 * col.heads;
+                        n1 = (col.head_tiles > 1 && n1 > a.group - j ? a.group - j : n1) - half * 64;
+#pragma unroll
+                        for (int k = 0; k < 64; k += 32) {
+                            const uint32_t keep = bits_below(n1 - k) & ~bits_below(n0 - k);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const float4 h = shift[k / 4 + y];
+                                const float hh[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const float e = exp2_approx(fmaf(x[k + 4 * y + z], c, hh[z]));
+                                    acc[z & 1].x += keep & (1u << (4 * y + z)) ? e : 0.0f;
+                                }
+                            }
+                        }
+                    }
+                    sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.hempty[s]);
+            }
+            if (!ok)
+                break;
+            // The halves of a tile's columns meet.
+            if (it.ct0 < it.ct1 && w < it.tiles) {
+                if (half == 1) {
+                    ok = up.warp_wait(&sh.rempty[w], (nr & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    sh.half[w][row] = sum;
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.rfull[w]);
+                } else {
+                    ok = up.warp_wait(&sh.rfull[w], nr & 1u);
+                    if (!ok)
+                        break;
+                    sum += sh.half[w][row];
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.rempty[w]);
+                }
+                ++nr;
+            }
+            if (half == 0 && key < a.Skv) {
+                const int64_t at = (static_cast<int64_t>(it.b) * a.Hkv + it.hk) * a.Skv + key;
+                if (parts > 1) {
+                    if (key < it.L)
+                        kw.parts[it.part * (static_cast<int64_t>(a.B) * a.Hkv * a.Skv) + at] = sum;
+                } else if (key < it.L) {
+                    kw.weights[at] = kw.accumulate ? kw.weights[at] + sum : sum;
+                } else if (!kw.accumulate) {
+                    kw.weights[at] = 0.0f;
+                }
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == TL::mma_warp) {
+        __syncwarp();
+        tc::tmem_free<TL::tmem>(tmem);
+    }
+}
+
+// The parts' sums, in order.
+inline constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) gtms_key_weights_join_kernel(const KeyWeightsArgs kw, int32_t parts)
+{
+    const AttentionArgs& a = kw.a;
+    const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * a.Skv, at = blockIdx.x * static_cast<int64_t>(kJoinThreads) + threadIdx.x;
+    if (at >= all)
+        return;
+    const int64_t bg = at / a.Skv;
+    const int32_t key = static_cast<int32_t>(at - bg * a.Skv), L = a.length(static_cast<int32_t>(bg / a.Hkv));
+    await_last_launch();
+    if (key >= L) {
+        if (!kw.accumulate)
+            kw.weights[at] = 0.0f;
+        return;
+    }
+    float sum = 0.0f;
+    for (int32_t p = 0; p < parts; ++p)
+        sum += kw.parts[p * all + at];
+    kw.weights[at] = kw.accumulate ? kw.weights[at] + sum : sum;
+}
+
+// Parts of an item's rows: more than one where the items would leave multiprocessors
+// idle, of four column tiles at least.
+inline int32_t key_weights_parts(const AttentionArgs& a)
+{
+    const KeyColumns col = key_columns(a.group);
+    const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * ((static_cast<int64_t>(a.Skv) + 2 * kTile - 1) / (2 * kTile));
+    const int64_t tiles = (static_cast<int64_t>(a.Sq) + col.rows - 1) / col.rows * col.head_tiles;
+    int64_t parts = (4 * kChipSms + items - 1) / items;
+    parts = parts < tiles / 4 ? parts : tiles / 4;
+    return parts > 1 ? static_cast<int32_t>(parts) : 1;
+}
+
+template <typename T, int D>
+cudaError_t launch_key_weights_tc(const KeyWeightsArgs& kw, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
+{
+    using TL = KeyTile<D>;
+    const AttentionArgs& a = kw.a;
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!bind_context() || !enc)
+        return cudaErrorUnknown;
+    HeadsMap mk;
+    if (!encode_heads<T>(mk, a.k, a.B, a.Hkv, a.Skv, D, kTile))
+        return cudaErrorInvalidValue;
+    KeyColumns col = key_columns(a.group);
+    col.mb = a.B > 1 && a.q.sb != 0;
+    // A stride that is never stepped over still has to be a legal one.
+    const cuuint64_t any = D * 2;
+    CUtensorMap mq;
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.group), static_cast<cuuint64_t>(a.Sq),
+                                static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(col.mb ? a.B : 1)};
+    const cuuint64_t strides[4] = {a.group > 1 ? static_cast<cuuint64_t>(a.q.sh) * 2 : any, a.Sq > 1 ? static_cast<cuuint64_t>(a.q.ss) * 2 : any,
+                                   a.Hkv > 1 ? static_cast<cuuint64_t>(a.q.sh) * a.group * 2 : any,
+                                   col.mb ? static_cast<cuuint64_t>(a.q.sb) * 2 : any};
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(col.heads), static_cast<cuuint32_t>(col.rows), 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+    if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, a.q.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
+    const int32_t parts = key_weights_parts(a);
+    const int64_t items = heads * ((static_cast<int64_t>(a.Skv) + TL::keys - 1) / TL::keys) * parts;
+    if (items > INT32_MAX)
+        return cudaErrorNotSupported;
+    constexpr auto* kern = gtms_key_weights_kernel<T, D>;
+    constexpr int smem = static_cast<int>(TL::smem);
+    cudaError_t e = allow_smem<kern>(smem);
+    if (e == cudaSuccess)
+        e = launch_kernel(kern, static_cast<unsigned>(items), TL::threads, smem, st, mq, mk, kw, col, static_cast<uint32_t>(heads),
+                          parts, wait_ns);
+    if (e != cudaSuccess || parts == 1)
+        return e;
+    const int64_t blocks = (heads * a.Skv + kJoinThreads - 1) / kJoinThreads;
+    return launch_beside_last(true, gtms_key_weights_join_kernel, static_cast<unsigned>(blocks), kJoinThreads, 0, st, kw, parts);
+}
+
+}  // namespace gtms

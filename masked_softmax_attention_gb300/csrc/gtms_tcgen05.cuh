@@ -246,6 +246,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int3
                  : "memory");
 }
 
+// The same of a 5-D tensor map.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            int32_t v, uint64_t* mbar)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(mbar))
+                 : "memory");
+}
+
 // Warpgroup-collective (4 aligned warps): raise or lower this warpgroup's registers
 // per thread. The shares of all warpgroups must add up to no more than the block
 // was launched with.
