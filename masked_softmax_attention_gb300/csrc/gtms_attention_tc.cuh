@@ -195,13 +195,13 @@ __device__ __forceinline__ bool item_wait(const ItemSlot<Item>& s, const GiveUp&
     return up.warp_wait_tiles(bar, parity, &s.longest);
 }
 
-// The dealing warp: make(index) is the item of a CTA index, whose steps(a) are the
-// tiles that a warp walks over; an item with b < 0 ends the deal. The next item is asked
+// The dealing warp: make(index, steps) is the item of a CTA index, of `steps` tiles
+// that a warp walks over; an item with b < 0 ends the deal. The next item is asked
 // for once every reader has taken the last. Where a role has given up, the CTAs that are
 // left are taken over all the same and dropped, so that a grid that cannot make progress
 // ends at once and not CTA by CTA.
 template <typename Item, typename Make>
-__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, const AttentionArgs& a, Make make)
+__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, Make make)
 {
     int32_t index = blockIdx.x;
     bool ok = true;
@@ -227,8 +227,7 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
         it.b = -1;
         uint32_t steps = 0;
         if (index >= 0) {
-            it = make(index);
-            steps = it.steps(a);
+            it = make(index, steps);
         }
         if (lane == 0) {
             s.item = it;
@@ -237,6 +236,17 @@ __device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, 
             tc::mbar_arrive(&s.full);
         }
     }
+}
+
+// The same with make(index), whose steps(a) are the tiles.
+template <typename Item, typename Make>
+__device__ __forceinline__ void deal_items(ItemSlot<Item>& s, const GiveUp& up, int lane, const AttentionArgs& a, Make make)
+{
+    deal_items(s, up, lane, [&](int32_t index, uint32_t& steps) {
+        const Item it = make(index);
+        steps = it.steps(a);
+        return it;
+    });
 }
 
 // The next item, for a reading warp (n counts its items), handed to read() while it

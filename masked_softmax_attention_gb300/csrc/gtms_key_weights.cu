@@ -20,7 +20,7 @@ bool mapped(const AttentionArgs& a)
 
 uint64_t key_weights_workspace_bytes(const AttentionArgs& a)
 {
-    const int32_t parts = few(a) ? 1 : key_weights_parts(a);
+    const int32_t parts = few(a) ? 1 : key_plan(a).parts;
     return parts > 1 ? static_cast<uint64_t>(parts) * a.B * a.Hkv * a.Skv * 4 : 0;
 }
 

@@ -6,8 +6,8 @@
 //
 // The transposed product S = K Q^T has a key to a row, so that the thread that owns a
 // row of S in tensor memory sums its exponentials by itself: no maximum, no exchange,
-// nothing written back. A work item is two tiles of 128 keys, which stay in shared
-// memory, and the column tiles of query rows that keep any of them, which stream past.
+// nothing written back. Two tiles of 128 keys stay in shared memory while the column
+// tiles of the query rows that keep any of them stream past.
 // The rows of the heads that share the keys are packed side by side (a 5-D map: element,
 // head, row, key/value head, batch), so that one new token fills as many columns as it
 // has heads, and a window's or a causal mask's kept columns of a key are one range.
@@ -55,49 +55,72 @@ inline KeyColumns key_columns(int32_t group)
     return c;
 }
 
+// Blocks [block0, block1) of 256 keys of one key/value head, and a part of the rows
+// that keep any of them (parts only of single blocks).
 struct KeyItem {
-    int32_t b, hk, key0, tiles, off, L, part;
-    int32_t i0, i1;        // rows that keep any of the keys
-    int32_t ct0, ct1;      // this part's column tiles, counted from row i0
+    int32_t b, hk, off, L, block0, block1, part;
 
-    __device__ __forceinline__ void set(const AttentionArgs& a, const KeyColumns& col, uint32_t item, uint32_t heads,
-                                        int32_t parts)
+    __device__ __forceinline__ void set(const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t per, int32_t parts)
     {
         const int32_t bg = static_cast<int32_t>(item % heads), rest = static_cast<int32_t>(item / heads);
+        const int32_t blocks = (a.Skv + 2 * kTile - 1) / (2 * kTile);
         part = rest % parts;
-        key0 = rest / parts * (2 * kTile);
+        block0 = rest / parts * per;
+        block1 = block0 + per < blocks ? block0 + per : blocks;
         b = bg / a.Hkv;
         hk = bg - b * a.Hkv;
         off = a.offset(b);
         L = a.length(b);
-        tiles = 0;
-        i0 = i1 = ct0 = ct1 = 0;
-        if (key0 >= L)
-            return;
-        tiles = key0 + kTile < L ? 2 : 1;
-        const int32_t last = (key0 + 2 * kTile < L ? key0 + 2 * kTile : L) - 1;
-        i0 = off < 0 ? -off : 0;
-        i1 = L - off < a.Sq ? L - off : a.Sq;
-        if (a.mask_kind != GTMS_MASK_LENGTH && key0 - off > i0)
-            i0 = key0 - off;
-        if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && last + a.window - off < i1)
-            i1 = last + a.window - off;
-        if (i0 >= i1)
-            return;
-        const int32_t all = (i1 - i0 + col.rows - 1) / col.rows * col.head_tiles, per = (all + parts - 1) / parts;
-        ct0 = part * per < all ? part * per : all;
-        ct1 = ct0 + per < all ? ct0 + per : all;
     }
-    __device__ __forceinline__ uint32_t steps(const AttentionArgs&) const { return ct1 - ct0; }
+};
+
+// What an item has to do for one block: rows [i0, i1) keep any of its keys; this part
+// takes their column tiles from row i, head j on, `tiles` of them.
+struct KeyRange {
+    int32_t i0, i1, i, j, tiles;
+
+    __device__ __forceinline__ KeyRange(const AttentionArgs& a, const KeyColumns& col, const KeyItem& it, int32_t block,
+                                        int32_t parts)
+    {
+        const int32_t key0 = block * (2 * kTile), last = (key0 + 2 * kTile < it.L ? key0 + 2 * kTile : it.L) - 1;
+        i0 = it.off < 0 ? -it.off : 0;
+        i1 = it.L - it.off < a.Sq ? it.L - it.off : a.Sq;
+        if (a.mask_kind != GTMS_MASK_LENGTH && key0 - it.off > i0)
+            i0 = key0 - it.off;
+        if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && last + a.window - it.off < i1)
+            i1 = last + a.window - it.off;
+        i = i0;
+        j = tiles = 0;
+        if (key0 >= it.L || i0 >= i1)
+            return;
+        const int32_t all = (i1 - i0 + col.rows - 1) / col.rows * col.head_tiles;
+        if (parts == 1) {
+            tiles = all;
+            return;
+        }
+        const int32_t per = (all + parts - 1) / parts, t0 = it.part * per < all ? it.part * per : all;
+        tiles = t0 + per < all ? per : all - t0;
+        i = i0 + t0 / col.head_tiles * col.rows;
+        j = t0 % col.head_tiles * col.heads;
+    }
+    __device__ __forceinline__ void next(const KeyColumns& col)
+    {
+        j += col.heads;
+        if (j >= col.heads * col.head_tiles) {
+            j = 0;
+            i += col.rows;
+        }
+    }
 };
 
 template <int D>
 struct KeyShared {
     using TL = KeyTile<D>;
-    uint64_t kfull[TL::NK], kempty[TL::NK], qfull[TL::ST], qempty[TL::ST], hfull[TL::ST], hempty[TL::ST];
-    uint64_t sfull[2][TL::W], sempty[2][TL::W], rfull[TL::W], rempty[TL::W], mma_done;
+    uint64_t kfull[TL::NK], kempty[TL::NK], qfull[TL::ST], qempty[TL::ST];
+    // S and the shifts are held twice, and one barrier a key tile says that both have come.
+    uint64_t sfull[2][TL::W], sempty[2][TL::W], hempty[2], rfull[TL::W], rempty[TL::W], mma_done;
     ItemSlot<KeyItem> items;
-    __align__(16) float shift[TL::ST][kTile];
+    __align__(16) float shift[2][kTile];
     float half[TL::W][kTile];
     uint32_t tmem_slot;
     int flag;
@@ -106,8 +129,8 @@ struct KeyShared {
 template <typename T, int D>
 __global__ void __launch_bounds__(KeyTile<D>::threads, 1)
 gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ HeadsMap mk,
-                        const __grid_constant__ KeyWeightsArgs kw, const KeyColumns col, uint32_t heads, int32_t parts,
-                        uint64_t wait_ns)
+                        const __grid_constant__ KeyWeightsArgs kw, const KeyColumns col, uint32_t heads, int32_t per,
+                        int32_t parts, uint64_t wait_ns)
 {
     using TL = KeyTile<D>;
     constexpr int W = TL::W, NK = TL::NK, ST = TL::ST;
@@ -127,14 +150,13 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
         for (int s = 0; s < ST; ++s) {
             tc::mbar_init(&sh.qfull[s], 1);
             tc::mbar_init(&sh.qempty[s], 1);
-            tc::mbar_init(&sh.hfull[s], 1);
-            tc::mbar_init(&sh.hempty[s], TL::sum_warps);
         }
         for (int w = 0; w < W; ++w) {
             for (int k = 0; k < 2; ++k) {
-                tc::mbar_init(&sh.sfull[k][w], 1);
+                tc::mbar_init(&sh.sfull[k][w], 2);
                 tc::mbar_init(&sh.sempty[k][w], 8);
             }
+            tc::mbar_init(&sh.hempty[w], TL::sum_warps);   // W == 2
             tc::mbar_init(&sh.rfull[w], 4);
             tc::mbar_init(&sh.rempty[w], 4);
         }
@@ -159,9 +181,12 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
     const uint32_t tmem = warp_value(sh.tmem_slot);
 
     if (warp == TL::deal_warp) {
-        deal_items(sh.items, up, lane, a, [&](int32_t index) {
+        deal_items(sh.items, up, lane, [&](int32_t index, uint32_t& steps) {
             KeyItem it;
-            it.set(a, col, index, heads, parts);
+            it.set(a, index, heads, per, parts);
+            steps = 0;
+            for (int32_t k = it.block0; k < it.block1; ++k)
+                steps += KeyRange(a, col, it, k, parts).tiles;
             return it;
         });
     } else if (warp == TL::load_warp) {
@@ -169,33 +194,33 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
         KeyItem it;
         bool ok = true;
         while (!kAttnNoLoads && take_item(sh.items, up, lane, taken, it, ok)) {
-            if (it.ct0 >= it.ct1)
-                continue;
-            for (int w = 0; w < it.tiles && ok; ++w) {
-                const uint32_t s = nk % NK;
-                ok = item_wait(sh.items, up, &sh.kempty[s], ((nk / NK) & 1u) ^ 1u);   // held for a whole item
-                if (!ok)
-                    break;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&sh.kfull[s], TL::bytes);
-                    load_tile<D, kTile>(base + s * TL::bytes, mk, it.key0 + w * kTile, it.hk, it.b, &sh.kfull[s]);
+            for (int32_t k = it.block0; k < it.block1 && ok; ++k) {
+                KeyRange r(a, col, it, k, parts);
+                for (int w = 0; w < W && r.tiles > 0 && ok; ++w) {
+                    const uint32_t s = nk % NK;
+                    ok = item_wait(sh.items, up, &sh.kempty[s], ((nk / NK) & 1u) ^ 1u);   // held for a whole item
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&sh.kfull[s], TL::bytes);
+                        load_tile<D, kTile>(base + s * TL::bytes, mk, (k * W + w) * kTile, it.hk, it.b, &sh.kfull[s]);
+                    }
+                    ++nk;
                 }
-                ++nk;
-            }
-            for (int32_t t = it.ct0; t < it.ct1 && ok; ++t) {
-                const uint32_t s = nq % ST;
-                ok = up.warp_wait(&sh.qempty[s], ((nq / ST) & 1u) ^ 1u);
-                if (!ok)
-                    break;
-                if (lane == 0) {
-                    const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
-                    tc::mbar_arrive_expect_tx(&sh.qfull[s], filled * D * 2);
+                for (int32_t t = 0; t < r.tiles && ok; ++t, r.next(col)) {
+                    const uint32_t s = nq % ST;
+                    ok = up.warp_wait(&sh.qempty[s], ((nq / ST) & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&sh.qfull[s], filled * D * 2);
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tc::tma_load_5d(base + TL::off_q + s * TL::bytes + x * TL::box, &mq, x * 64, j, i, it.hk, it.b * col.mb,
-                                        &sh.qfull[s]);
+                        for (int x = 0; x < D / 64; ++x)
+                            tc::tma_load_5d(base + TL::off_q + s * TL::bytes + x * TL::box, &mq, x * 64, r.j, r.i, it.hk,
+                                            it.b * col.mb, &sh.qfull[s]);
+                    }
+                    ++nq;
                 }
-                ++nq;
             }
         }
         if (!ok) {   // let the copies already issued land before the CTA can exit
@@ -216,59 +241,58 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
         KeyItem it;
         bool ok = true;
         while (take_item(sh.items, up, lane, taken, it, ok)) {
-            for (int32_t t = it.ct0; t < it.ct1; ++t, ++n) {
-                const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
-                float x[4];
+            const float* lse = a.lse + (static_cast<int64_t>(it.b) * a.Hq + it.hk * a.group) * a.Sq;
+            for (int32_t k = it.block0; k < it.block1 && ok; ++k) {
+                KeyRange r(a, col, it, k, parts);
+                for (int32_t t = 0; t < r.tiles; ++t, ++n, r.next(col)) {
+                    float x[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool counts = ci[k] < col.rows && i + ci[k] < it.i1 && j + cj[k] < a.group;
-                    const int64_t head = static_cast<int64_t>(it.b) * a.Hq + it.hk * a.group + j + cj[k];
-                    x[k] = counts ? __ldg(a.lse + head * a.Sq + i + ci[k]) : -INFINITY;
+                    for (int y = 0; y < 4; ++y) {
+                        const bool counts = ci[y] < col.rows && r.i + ci[y] < r.i1 && r.j + cj[y] < a.group;
+                        x[y] = counts ? __ldg(lse + static_cast<int64_t>(r.j + cj[y]) * a.Sq + r.i + ci[y]) : -INFINITY;
+                    }
+                    const uint32_t buf = n & 1u;
+                    ok = up.warp_wait(&sh.hempty[buf], ((n >> 1) & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)   // a row that kept nothing gives nothing
+                        sh.shift[buf][32 * y + lane] = x[y] == -INFINITY ? -INFINITY : -x[y] * kLog2e;
+                    __syncwarp();
+                    if (lane < W)
+                        tc::mbar_arrive(&sh.sfull[buf][lane]);
                 }
-                const uint32_t s = n % ST;
-                ok = up.warp_wait(&sh.hempty[s], ((n / ST) & 1u) ^ 1u);
-                if (!ok)
-                    break;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)   // a row that kept nothing gives nothing
-                    sh.shift[s][32 * k + lane] = x[k] == -INFINITY ? -INFINITY : -x[k] * kLog2e;
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.hfull[s]);
             }
         }
     } else if (warp == TL::mma_warp) {
         uint32_t nk = 0, nq = 0, taken = 0;
-        uint32_t ns[W] = {};   // products into S of key tile w
         KeyItem it;
         bool ok = true;
         while (take_item(sh.items, up, lane, taken, it, ok)) {
-            const int32_t ct0 = warp_value(it.ct0), ct1 = warp_value(it.ct1), tiles = warp_value(it.tiles);
-            for (int32_t t = ct0; t < ct1 && ok; ++t, ++nq) {
-                const uint32_t sq = nq % ST;
-                ok = up.warp_wait(&sh.qfull[sq], (nq / ST) & 1u);
+            for (int32_t k = it.block0; k < it.block1 && ok; ++k) {
+                const int32_t tiles = warp_value(KeyRange(a, col, it, k, parts).tiles);
+                for (int32_t t = 0; t < tiles && ok; ++t, ++nq) {
+                    const uint32_t sq = nq % ST, buf = nq & 1u;
+                    ok = up.warp_wait(&sh.qfull[sq], (nq / ST) & 1u);
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    if (w >= tiles || !ok)
-                        break;
-                    const uint32_t sk = (nk + w) % NK, buf = ns[w] & 1u;
-                    if (t == ct0)
-                        ok = up.warp_wait(&sh.kfull[sk], ((nk + w) / NK) & 1u);
-                    ok = ok && up.warp_wait(&sh.sempty[buf][w], ((ns[w] >> 1) & 1u) ^ 1u);
-                    if (!ok)
-                        break;
-                    tc::fence_after_sync();
-                    mma_abt<T, D, kTile>(tmem + (buf * W + w) * kTile, base + sk * TL::bytes, base + TL::off_q + sq * TL::bytes);
-                    tc::commit_warp(&sh.sfull[buf][w]);
-                    if (t == ct1 - 1)
-                        tc::commit_warp(&sh.kempty[sk]);
-                    ++ns[w];
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t sk = (nk + w) % NK;
+                        if (t == 0)
+                            ok = ok && up.warp_wait(&sh.kfull[sk], ((nk + w) / NK) & 1u);
+                        ok = ok && up.warp_wait(&sh.sempty[buf][w], ((nq >> 1) & 1u) ^ 1u);
+                        if (!ok)
+                            break;
+                        tc::fence_after_sync();
+                        mma_abt<T, D, kTile>(tmem + (buf * W + w) * kTile, base + sk * TL::bytes, base + TL::off_q + sq * TL::bytes);
+                        tc::commit_warp(&sh.sfull[buf][w]);
+                        if (t == tiles - 1)
+                            tc::commit_warp(&sh.kempty[sk]);
+                    }
+                    if (ok)
+                        tc::commit_warp(&sh.qempty[sq]);
                 }
-                if (ok)
-                    tc::commit_warp(&sh.qempty[sq]);
+                nk += tiles > 0 ? W : 0;
             }
-            if (ct0 < ct1)
-                nk += tiles;
         }
         // Nothing may be in flight when the tensor memory is freed.
         tc::commit_warp(&sh.mma_done);
@@ -277,60 +301,57 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
         const int w = (warp >> 2) & 1, half = warp >> 3, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 tensor-memory lanes per warp, lane in bits 16..
         const float c = a.scale * kLog2e;
-        uint32_t n = 0, ns = 0, nr = 0, taken = 0;
+        const uint32_t ts = tmem + lanes + w * kTile + half * 64;
+        uint32_t n = 0, nr = 0, taken = 0;
         KeyItem it;
         bool ok = true;
         while (take_item(sh.items, up, lane, taken, it, ok)) {
-            const int32_t first = it.key0 + w * kTile, key = first + row;
-            const int32_t last = (first + kTile < it.L ? first + kTile : it.L) - 1;   // the tile's last live key
-            // Rows that keep this key.
-            int32_t k0 = it.i0, k1 = it.i1;
-            if (a.mask_kind != GTMS_MASK_LENGTH && key - it.off > k0)
-                k0 = key - it.off;
-            if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW && key + a.window - it.off < k1)
-                k1 = key + a.window - it.off;
-            float sum = 0.0f;
-            for (int32_t t = it.ct0; t < it.ct1; ++t, ++n) {
-                const uint32_t s = n % ST;
-                ok = item_wait(sh.items, up, &sh.hfull[s], (n / ST) & 1u);
-                if (!ok)
-                    break;
-                if (w < it.tiles) {
-                    const uint32_t buf = ns & 1u;
-                    ok = item_wait(sh.items, up, &sh.sfull[buf][w], (ns >> 1) & 1u);
-                    ++ns;
+            for (int32_t block = it.block0; block < it.block1 && ok; ++block) {
+                KeyRange r(a, col, it, block, parts);
+                const int32_t first = (block * W + w) * kTile, key = first + row;
+                const int32_t last = (first + kTile < it.L ? first + kTile : it.L) - 1;   // the tile's last live key
+                // Rows [k0, k1) keep this key; tiles from row [whole0, whole1] keep every live key of this tile with every row.
+                int32_t k0 = r.i0, k1 = r.i1, whole0 = r.i0, whole1 = r.i1 - col.rows;
+                if (a.mask_kind != GTMS_MASK_LENGTH) {
+                    k0 = key - it.off > k0 ? key - it.off : k0;
+                    whole0 = last - it.off;
+                }
+                if (a.mask_kind == GTMS_MASK_SLIDING_WINDOW) {
+                    k1 = key + a.window - it.off < k1 ? key + a.window - it.off : k1;
+                    whole1 = first + a.window - it.off - col.rows < whole1 ? first + a.window - it.off - col.rows : whole1;
+                }
+                const bool any = r.tiles > 0;
+                float sum = 0.0f;
+                for (int32_t t = 0; t < r.tiles; ++t, ++n, r.next(col)) {
+                    const uint32_t buf = n & 1u;
+                    ok = item_wait(sh.items, up, &sh.sfull[buf][w], (n >> 1) & 1u);
                     if (!ok)
                         break;
                     tc::fence_after_sync();
                     float x[64];
-                    tc::tmem_ld64(tmem + lanes + (buf * W + w) * kTile + half * 64, x);
+                    tc::tmem_ld64(ts + buf * (W * kTile), x);
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
                         tc::mbar_arrive(&sh.sempty[buf][w]);
-                    const int32_t i = it.i0 + t / col.head_tiles * col.rows, j = t % col.head_tiles * col.heads;
-                    const float4* shift = reinterpret_cast<const float4*>(&sh.shift[s][half * 64]);
-                    const float2 c2 = make_float2(c, c);
+                    const float4* shift = reinterpret_cast<const float4*>(&sh.shift[buf][half * 64]);
                     float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    // Every row of the tile keeps every live key of this one.
-                    const bool whole = i + col.rows <= it.i1 && j + col.heads <= a.group &&
-                                       (a.mask_kind == GTMS_MASK_LENGTH || i + it.off >= last) &&
-                                       (a.mask_kind != GTMS_MASK_SLIDING_WINDOW || i + col.rows - 1 + it.off < first + a.window);
-                    if (__builtin_expect(whole, 1)) {
+                    if (__builtin_expect(r.i >= whole0 && r.i <= whole1 && r.j + col.heads <= a.group, 1)) {
+                        const float2 c2 = make_float2(c, c);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float4 h = shift[k];
-                            float2 e = __ffma2_rn(make_float2(x[4 * k], x[4 * k + 1]), c2, make_float2(h.x, h.y));
-                            float2 f = __ffma2_rn(make_float2(x[4 * k + 2], x[4 * k + 3]), c2, make_float2(h.z, h.w));
+                            const float2 e = __ffma2_rn(make_float2(x[4 * k], x[4 * k + 1]), c2, make_float2(h.x, h.y));
+                            const float2 f = __ffma2_rn(make_float2(x[4 * k + 2], x[4 * k + 3]), c2, make_float2(h.z, h.w));
                             acc[0] = __fadd2_rn(acc[0], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
                             acc[1] = __fadd2_rn(acc[1], make_float2(exp2_approx(f.x), exp2_approx(f.y)));
                         }
                     } else {
-                        // Columns [n0, n1) of the tile, as rows of it times heads.
-                        const int32_t r0 = min(max(k0 - i, 0), kTile), r1 = min(max(k1 - i, 0), kTile);
+                        // Columns [n0, n1) of this half: rows of the tile times heads.
+                        const int32_t r0 = min(max(k0 - r.i, 0), kTile), r1 = min(max(k1 - r.i, 0), kTile);
                         const int32_t n0 = r0 * col.heads - half * 64;
                         int32_t n1 = r1 * col.heads;
-                        n1 = (col.head_tiles > 1 && n1 > a.group - j ? a.group - j : n1) - half * 64;
+                        n1 = (col.head_tiles > 1 && n1 > a.group - r.j ? a.group - r.j : n1) - half * 64;
 #pragma unroll
                         for (int k = 0; k < 64; k += 32) {
                             const uint32_t keep = bits_below(n1 - k) & ~bits_below(n0 - k);
@@ -346,44 +367,44 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
                             }
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.hempty[buf]);
                     sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 }
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.hempty[s]);
-            }
-            if (!ok)
-                break;
-            // The halves of a tile's columns meet.
-            if (it.ct0 < it.ct1 && w < it.tiles) {
-                if (half == 1) {
-                    ok = up.warp_wait(&sh.rempty[w], (nr & 1u) ^ 1u);
-                    if (!ok)
-                        break;
-                    sh.half[w][row] = sum;
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(&sh.rfull[w]);
-                } else {
-                    ok = up.warp_wait(&sh.rfull[w], nr & 1u);
-                    if (!ok)
-                        break;
-                    sum += sh.half[w][row];
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(&sh.rempty[w]);
+                if (!ok)
+                    break;
+                // The halves of a tile's columns meet.
+                if (any) {
+                    if (half == 1) {
+                        ok = up.warp_wait(&sh.rempty[w], (nr & 1u) ^ 1u);
+                        if (!ok)
+                            break;
+                        sh.half[w][row] = sum;
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(&sh.rfull[w]);
+                    } else {
+                        ok = up.warp_wait(&sh.rfull[w], nr & 1u);
+                        if (!ok)
+                            break;
+                        sum += sh.half[w][row];
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(&sh.rempty[w]);
+                    }
+                    ++nr;
                 }
-                ++nr;
-            }
-            if (half == 0 && key < a.Skv) {
-                const int64_t at = (static_cast<int64_t>(it.b) * a.Hkv + it.hk) * a.Skv + key;
-                if (parts > 1) {
-                    if (key < it.L)
-                        kw.parts[it.part * (static_cast<int64_t>(a.B) * a.Hkv * a.Skv) + at] = sum;
-                } else if (key < it.L) {
-                    kw.weights[at] = kw.accumulate ? kw.weights[at] + sum : sum;
-                } else if (!kw.accumulate) {
-                    kw.weights[at] = 0.0f;
+                if (half == 0 && key < a.Skv) {
+                    const int64_t at = (static_cast<int64_t>(it.b) * a.Hkv + it.hk) * a.Skv + key;
+                    if (parts > 1) {
+                        if (key < it.L)
+                            kw.parts[it.part * (static_cast<int64_t>(a.B) * a.Hkv * a.Skv) + at] = sum;
+                    } else if (key < it.L) {
+                        kw.weights[at] = kw.accumulate ? kw.weights[at] + sum : sum;
+                    } else if (!kw.accumulate) {
+                        kw.weights[at] = 0.0f;
+                    }
                 }
             }
         }
@@ -420,16 +441,31 @@ __global__ void __launch_bounds__(kJoinThreads) gtms_key_weights_join_kernel(con
     kw.weights[at] = kw.accumulate ? kw.weights[at] + sum : sum;
 }
 
-// Parts of an item's rows: more than one where the items would leave multiprocessors
-// idle, of four column tiles at least.
-inline int32_t key_weights_parts(const AttentionArgs& a)
+// How the work is cut: an item of many column tiles into parts of its rows, so that
+// whoever is done first finds something left; blocks of few column tiles put together,
+// so that keys stream in without a pause between items.
+struct KeyPlan {
+    int32_t per;     // blocks of 256 keys of an item
+    int32_t parts;   // of its rows
+};
+
+inline KeyPlan key_plan(const AttentionArgs& a)
 {
     const KeyColumns col = key_columns(a.group);
-    const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * ((static_cast<int64_t>(a.Skv) + 2 * kTile - 1) / (2 * kTile));
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv, blocks = (static_cast<int64_t>(a.Skv) + 2 * kTile - 1) / (2 * kTile);
     const int64_t tiles = (static_cast<int64_t>(a.Sq) + col.rows - 1) / col.rows * col.head_tiles;
-    int64_t parts = (4 * kChipSms + items - 1) / items;
-    parts = parts < tiles / 4 ? parts : tiles / 4;
-    return parts > 1 ? static_cast<int32_t>(parts) : 1;
+    KeyPlan p{1, 1};
+    const int64_t want = 8 * kChipSms;   // items
+    if (heads * blocks < want) {
+        const int64_t parts = (want + heads * blocks - 1) / (heads * blocks);
+        p.parts = static_cast<int32_t>(parts < tiles / 4 ? parts : tiles / 4);
+        p.parts = p.parts > 1 ? p.parts : 1;
+    } else if (tiles < 16) {
+        int64_t per = 16 / tiles;
+        per = per < heads * blocks / want ? per : heads * blocks / want;
+        p.per = per > 1 ? static_cast<int32_t>(per) : 1;
+    }
+    return p;
 }
 
 template <typename T, int D>
@@ -458,8 +494,9 @@ cudaError_t launch_key_weights_tc(const KeyWeightsArgs& kw, cudaStream_t st, uin
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
-    const int32_t parts = key_weights_parts(a);
-    const int64_t items = heads * ((static_cast<int64_t>(a.Skv) + TL::keys - 1) / TL::keys) * parts;
+    const KeyPlan plan = key_plan(a);
+    const int64_t blocks = (static_cast<int64_t>(a.Skv) + TL::keys - 1) / TL::keys;
+    const int64_t items = heads * ((blocks + plan.per - 1) / plan.per) * plan.parts;
     if (items > INT32_MAX)
         return cudaErrorNotSupported;
     constexpr auto* kern = gtms_key_weights_kernel<T, D>;
@@ -467,11 +504,11 @@ cudaError_t launch_key_weights_tc(const KeyWeightsArgs& kw, cudaStream_t st, uin
     cudaError_t e = allow_smem<kern>(smem);
     if (e == cudaSuccess)
         e = launch_kernel(kern, static_cast<unsigned>(items), TL::threads, smem, st, mq, mk, kw, col, static_cast<uint32_t>(heads),
-                          parts, wait_ns);
-    if (e != cudaSuccess || parts == 1)
+                          plan.per, plan.parts, wait_ns);
+    if (e != cudaSuccess || plan.parts == 1)
         return e;
-    const int64_t blocks = (heads * a.Skv + kJoinThreads - 1) / kJoinThreads;
-    return launch_beside_last(true, gtms_key_weights_join_kernel, static_cast<unsigned>(blocks), kJoinThreads, 0, st, kw, parts);
+    const int64_t ctas = (heads * a.Skv + kJoinThreads - 1) / kJoinThreads;
+    return launch_beside_last(true, gtms_key_weights_join_kernel, static_cast<unsigned>(ctas), kJoinThreads, 0, st, kw, plan.parts);
 }
 
 }  // namespace gtms
