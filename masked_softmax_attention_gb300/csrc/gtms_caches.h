@@ -25,7 +25,7 @@ struct EvictArgs {
     int32_t* kept;                // workspace [B, H, keep]: indices, written where a sequence is longer than keep
     int32_t B, H, S, S_out, keep, first, recent;
     int32_t units;                // 16-byte units of a row
-    int32_t moved;                // bits 0, 1: k, v go elsewhere (otherwise they are compacted in place)
+    int32_t moved;                // bits 0 to 2: k, v, weights and positions go elsewhere (otherwise they are compacted in place)
 
 #ifdef __CUDACC__
     __device__ __forceinline__ int32_t length(int32_t b) const

@@ -2,38 +2,40 @@
 //
 // Of a sequence's n > keep entries stay the first `first`, the last `recent` and, of
 // those between, the keep - first - recent of highest weight (ties to the lowest
-// index), in the order in which they stood. Two launches:
-//   select  finds them: the weight of the last one that stays by four histograms of 8
-//           bits of the weights' order-preserving bits, then each entry's place by
-//           counting those before it. No atomics on results, so the same inputs give
-//           the same cache; a cluster of CTAs shares a long row.
-//   gather  moves rows of k and v, weights and positions. What bounds the call: the
-//           kept rows are read once and written once (a weight is 4 of its 4 + 4 D bytes).
+// index), in the order in which they stood. Two launches, the second's start under the
+// first's end:
+//   select  finds them: the weight of the last one that stays by three histograms of the
+//           weights' order-preserving bits, then each entry's place by counting those
+//           before it. No atomics on results, so the same inputs give the same cache; a
+//           cluster of CTAs shares a long row.
+//   gather  (or move, in place) takes rows of k and v, weights and positions. What bounds
+//           the call: the kept rows are read once and written once (a weight is 4 of its
+//           4 + 4 D bytes).
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "gtms_attention_tc.cuh"
 #include "gtms_caches.h"
-#include "gtms_device.h"
-#include "gtms_tcgen05.cuh"
 
 namespace gtms {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32, kSelectCluster = 8;
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32, kSelectCluster = 8;
 // Weights that a CTA holds in shared memory; of longer shares every pass reads memory anew.
 constexpr int kSelectStaged = 40960;
-// Copies of a histogram, one a lane: neighbouring weights share their exponents, and 32
-// lanes that count into one place would wait for each other.
-constexpr int kCopies = 32;
+// Bins of a histogram (11, 11 and 10 bits), and its copies, by lane: neighbouring weights
+// share their exponents, and lanes that count into one place wait for each other.
+constexpr int kBins = 2048, kCopies = 4;
+static_assert(kBins == 2 * kSelectThreads, "two bins to a thread");
 
 struct SelectShared {
-    uint32_t hist[256][kCopies];
-    uint32_t total[2][256];        // of this CTA, by the pass's parity, so that the others may still read the last one
-    uint32_t sum[256];             // over the cluster
-    uint32_t digit, above;         // found: the digit, entries above it
+    __align__(16) uint32_t hist[kBins][kCopies];
+    __align__(16) uint32_t total[2][kBins];   // of this CTA, by the pass's parity, so that the others may still read the last one
+    uint32_t warp_sum[kSelectWarps];
+    uint32_t digit, above;                    // found: the digit, entries above it
     uint32_t gt[kSelectWarps], eq[kSelectWarps];
     uint32_t cta_gt, cta_eq;
 };
@@ -53,8 +55,10 @@ template <bool STAGED>
 __global__ void __launch_bounds__(kSelectThreads)
 gtms_evict_select_kernel(const EvictArgs a)
 {
-    extern __shared__ __align__(16) uint32_t keys[];   // this CTA's share, ordered
-    __shared__ SelectShared sh;
+    extern __shared__ __align__(16) uint4 raw[];
+    SelectShared& sh = *reinterpret_cast<SelectShared*>(raw);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(&sh + 1);   // this CTA's share, ordered
+    let_next_launch_start();   // it waits for what this one writes
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -85,66 +89,60 @@ gtms_evict_select_kernel(const EvictArgs a)
     const float* mine = w + from;
     auto key_at = [&](int32_t i) { return STAGED ? keys[i] : ordered(__ldg(mine + i)); };
     if (STAGED)
+#pragma unroll 8
         for (int32_t i = threadIdx.x; i < count; i += kSelectThreads)
             keys[i] = ordered(__ldg(mine + i));
 
     uint32_t prefix = 0, mask = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int32_t i = threadIdx.x; i < 256 * kCopies; i += kSelectThreads)
-            (&sh.hist[0][0])[i] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const uint32_t digits = pass < 2 ? kBins - 1u : kBins / 2 - 1u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            reinterpret_cast<uint4*>(&sh.hist[0][0])[threadIdx.x + k * kSelectThreads] = make_uint4(0, 0, 0, 0);
         __syncthreads();
+#pragma unroll 4
         for (int32_t i = threadIdx.x; i < count; i += kSelectThreads) {
             const uint32_t k = key_at(i);
             if ((k & mask) == prefix)
-                atomicAdd(&sh.hist[(k >> shift) & 255u][lane % kCopies], 1u);   // counts: their order does not matter
+                atomicAdd(&sh.hist[(k >> shift) & digits][lane % kCopies], 1u);   // counts: their order does not matter
         }
         __syncthreads();
-        // A warp adds up 256 / kSelectWarps bins, a lane a copy.
-        for (int d = warp; d < 256; d += kSelectWarps) {
-            const uint32_t t = __reduce_add_sync(0xffffffffu, sh.hist[d][lane]);
-            if (lane == 0)
-                sh.total[pass & 1][d] = t;
+        // Thread t has bins 2047 - 2 t and 2046 - 2 t: the highest first.
+        const int bin = kBins - 2 - 2 * static_cast<int>(threadIdx.x);
+        {
+            const uint4 x = *reinterpret_cast<const uint4*>(sh.hist[bin]), y = *reinterpret_cast<const uint4*>(sh.hist[bin + 1]);
+            *reinterpret_cast<uint2*>(&sh.total[pass & 1][bin]) = make_uint2(x.x + x.y + x.z + x.w, y.x + y.y + y.z + y.w);
         }
         if (ranks > 1)
             cluster.sync();
-        else
-            __syncthreads();
-        if (threadIdx.x < 256) {
-            uint32_t t = 0;
-            for (uint32_t r = 0; r < ranks; ++r)
-                t += *cluster.map_shared_rank(&sh.total[pass & 1][threadIdx.x], r);
-            sh.sum[threadIdx.x] = t;
+        uint32_t low = 0, high = 0;
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const uint2 t = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.total[pass & 1][bin], r));
+            low += t.x;
+            high += t.y;
         }
+        // Entries in the bins above this thread's.
+        uint32_t up = low + high;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
+            up += lane >= o ? x : 0;
+        }
+        if (lane == 31)
+            sh.warp_sum[warp] = up;
         __syncthreads();
-        if (warp == 0) {   // the bin in which the need-th largest stands; lane 0 has the highest eight
-            uint32_t t[8], mass = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                mass += t[j] = sh.sum[255 - 8 * lane - j];
-            uint32_t up = mass;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
-                up += lane >= o ? x : 0;
-            }
-            uint32_t above = up - mass;
-            if (above < need && need <= up) {
-                int j = 0;
-#pragma unroll
-                for (int x = 0; x < 7; ++x)
-                    if (j == x && above + t[x] < need) {
-                        above += t[x];
-                        ++j;
-                    }
-                sh.digit = 255 - 8 * lane - j;
-                sh.above = above;
-            }
+        const uint32_t below_me = lane < warp ? sh.warp_sum[lane] : 0;
+        const uint32_t above = up - low - high + __reduce_add_sync(0xffffffffu, below_me);
+        if (above < need && need <= above + low + high) {   // one thread's bins hold the need-th largest
+            const bool first = need <= above + high;
+            sh.digit = first ? bin + 1 : bin;
+            sh.above = first ? above : above + high;
         }
         __syncthreads();
         prefix |= sh.digit << shift;
-        mask |= 255u << shift;
+        mask |= digits << shift;
         need -= sh.above;
     }
     // Those above `prefix` stay, and the first `need` that equal it.
@@ -205,46 +203,57 @@ gtms_evict_select_kernel(const EvictArgs a)
 
 constexpr int kGatherThreads = 256, kGatherUnroll = 4;
 
-// Rows go elsewhere: a CTA moves its part of one (batch, head)'s rows of k (blockIdx.y
-// 0) or v. Neighbouring threads take the 16-byte units of a row.
+// Rows go elsewhere: a CTA moves its part of one (batch, head)'s rows of k and v, and of
+// weights and positions. Neighbouring threads take the 16-byte units of a row; a thread
+// has its unit of several rows of both in flight.
 __global__ void __launch_bounds__(kGatherThreads)
 gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 {
-    const int which = blockIdx.y;
     const int64_t bh = blockIdx.x / parts;
     const int32_t part = static_cast<int32_t>(blockIdx.x % parts);
     const int32_t b = static_cast<int32_t>(bh / a.H), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.H);
     const int32_t n = a.length(b), stay = n < a.keep ? n : a.keep;
     const int32_t j0 = part * rows, j1 = stay - j0 < rows ? stay : j0 + rows;
-    if (j0 >= j1 || !(a.moved >> which & 1))
+    await_last_launch();   // which wrote `kept`; every CTA waits, so that this launch ends after that one
+    if (j0 >= j1)
         return;
     const int32_t* kept = n > a.keep ? a.kept + bh * a.keep : nullptr;
-    const uint8_t* in = a.in[which].row<uint8_t>(0, 0, 0);
-    uint8_t* out = a.out[which].row<uint8_t>(0, 0, 0);
-    const int64_t in0 = (b * a.in[which].sb + h * a.in[which].sh) * 16, out0 = (b * a.out[which].sb + h * a.out[which].sh) * 16;
-    const int32_t total = (j1 - j0) * a.units;   // rows * units stays below 2^31 (see the launch)
-    for (int32_t i0 = threadIdx.x; i0 < total; i0 += kGatherThreads * kGatherUnroll) {
+    const int32_t unit = threadIdx.x % a.units, mine = threadIdx.x / a.units, turn = kGatherThreads / a.units;
+    const uint4 *ki = a.in[0].row<uint4>(b, h, 0) + unit, *vi = a.in[1].row<uint4>(b, h, 0) + unit;
+    uint4 *ko = a.out[0].row<uint4>(b, h, 0) + unit, *vo = a.out[1].row<uint4>(b, h, 0) + unit;
+    const bool take_k = (a.moved & 1) && mine < turn, take_v = (a.moved & 2) && mine < turn;
+    for (int32_t j = j0 + mine; j < j1; j += turn * kGatherUnroll) {
         int32_t from[kGatherUnroll];
-        uint4 v[kGatherUnroll];
+        uint4 kr[kGatherUnroll], vr[kGatherUnroll];
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int32_t i = i0 + u * kGatherThreads;
-            if (i < total)
-                from[u] = kept ? kept[j0 + i / a.units] : j0 + i / a.units;
+            const int32_t x = j + u * turn;
+            from[u] = x < j1 && kept ? kept[x] : x;
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int32_t i = i0 + u * kGatherThreads;
-            if (i < total)
-                v[u] = __ldcs(reinterpret_cast<const uint4*>(in + in0 + (from[u] * a.in[which].ss + i % a.units) * 16));
+            const bool any = j + u * turn < j1;
+            if (any && take_k)
+                kr[u] = __ldcs(ki + from[u] * a.in[0].ss);
+            if (any && take_v)
+                vr[u] = __ldcs(vi + from[u] * a.in[1].ss);
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int32_t i = i0 + u * kGatherThreads;
-            if (i < total)
-                *reinterpret_cast<uint4*>(out + out0 + ((j0 + i / a.units) * a.out[which].ss + i % a.units) * 16) = v[u];
+            const int32_t x = j + u * turn;
+            if (x < j1 && take_k)
+                __stcs(ko + x * a.out[0].ss, kr[u]);
+            if (x < j1 && take_v)
+                __stcs(vo + x * a.out[1].ss, vr[u]);
         }
     }
+    if (a.moved & 4)
+        for (int32_t j = j0 + threadIdx.x; j < j1; j += kGatherThreads) {
+            const int32_t from = kept ? kept[j] : j;
+            a.weights_out[bh * a.S_out + j] = a.weights[bh * a.S + from];
+            if (a.positions_out)
+                a.positions_out[bh * a.S_out + j] = a.positions ? a.positions[bh * a.S + from] : from;
+        }
 }
 
 // Rows stay in their cache: entry j goes to row j, at or before where it stood, so a
@@ -253,19 +262,59 @@ gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 // writes. What runs side by side is columns: a CTA moves `width` 16-byte units of every
 // row, several steps of copies in flight in shared memory.
 constexpr int kMoveStages = 4, kMoveUnroll = 4;
+constexpr int kMoveBytes = kMoveStages * kMoveUnroll * kGatherThreads * 16;
 
+// Weights and positions in place, or one of them: all of a step have been read before
+// any is written, as above.
+__device__ __forceinline__ void move_labels(const EvictArgs& a, int64_t bh, const int32_t* kept, int32_t stay, uint8_t* smem)
+{
+    constexpr int N = 16, STEP = N * kGatherThreads;
+    static_assert(STEP * 8 <= kMoveBytes, "a step of both");
+    float* w = reinterpret_cast<float*>(smem);
+    int32_t* p = reinterpret_cast<int32_t*>(smem) + STEP;
+    for (int32_t j0 = 0; j0 < stay; j0 += STEP) {
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int32_t i = u * kGatherThreads + threadIdx.x;
+            if (i < stay - j0) {
+                const int32_t from = kept ? kept[j0 + i] : j0 + i;
+                w[i] = a.weights[bh * a.S + from];
+                p[i] = a.positions ? a.positions[bh * a.S + from] : from;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int32_t i = u * kGatherThreads + threadIdx.x;
+            if (i < stay - j0) {
+                a.weights_out[bh * a.S_out + j0 + i] = w[i];
+                if (a.positions_out)
+                    a.positions_out[bh * a.S_out + j0 + i] = p[i];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// blockIdx.y: k, v, and the weights and positions (of one CTA's a head).
 __global__ void __launch_bounds__(kGatherThreads)
 gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
 {
-    extern __shared__ __align__(16) uint4 ring[];   // kMoveStages x kMoveUnroll x threads
+    extern __shared__ __align__(16) uint4 raw[];   // kMoveStages x kMoveUnroll x threads
+    uint4* ring = raw;
     const int which = blockIdx.y;
     const int64_t bh = blockIdx.x / slices;
     const int32_t unit0 = static_cast<int32_t>(blockIdx.x % slices) * width;
     const int32_t b = static_cast<int32_t>(bh / a.H), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.H);
     const int32_t n = a.length(b);
-    if (n <= a.keep || (a.moved >> which & 1))
+    await_last_launch();   // as above
+    if ((a.moved >> which & 1) || (which == 2 && unit0 > 0))
+        return;
+    const int32_t* kept = n > a.keep ? a.kept + bh * a.keep : nullptr;
+    if (which == 2)
+        return move_labels(a, bh, kept, n < a.keep ? n : a.keep, reinterpret_cast<uint8_t*>(ring));
+    if (!kept)
         return;   // everything stands where it is to stand
-    const int32_t* kept = a.kept + bh * a.keep;
     // The first entries that stay are where they belong: kept[j] - j never falls.
     int32_t lo = 0, hi = a.keep;
     while (lo < hi) {
@@ -278,7 +327,7 @@ gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
     const int32_t w = a.units - unit0 < width ? a.units - unit0 : width;
     const int32_t rows = kGatherThreads * kMoveUnroll / w;   // of a step
     const int32_t steps = (a.keep - lo + rows - 1) / rows;
-    uint8_t* base = a.in[which].row<uint8_t>(0, 0, 0) + (b * a.in[which].sb + h * a.in[which].sh + unit0) * 16;
+    uint4* base = a.in[which].row<uint4>(b, h, 0) + unit0;
     const int64_t ss = a.in[which].ss;
     auto load = [&](int32_t s) {
 #pragma unroll
@@ -286,7 +335,7 @@ gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
             const int32_t i = u * kGatherThreads + threadIdx.x, r = i / w, j = lo + s * rows + r;
             if (s < steps && r < rows && j < a.keep)
                 tc::cp_async16(tc::smem_u32(ring + (s % kMoveStages) * (kMoveUnroll * kGatherThreads) + i),
-                               base + (kept[j] * ss + i % w) * 16, 16);
+                               base + kept[j] * ss + i % w, 16);
         }
         tc::cp_async_commit();
     };
@@ -300,92 +349,51 @@ gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
         for (int u = 0; u < kMoveUnroll; ++u) {
             const int32_t i = u * kGatherThreads + threadIdx.x, r = i / w, j = lo + s * rows + r;
             if (r < rows && j < a.keep)
-                *reinterpret_cast<uint4*>(base + (j * ss + i % w) * 16) =
-                    ring[(s % kMoveStages) * (kMoveUnroll * kGatherThreads) + i];
+                base[j * ss + i % w] = ring[(s % kMoveStages) * (kMoveUnroll * kGatherThreads) + i];
         }
     }
 }
 
-// Weights and positions. In place one CTA takes a (batch, head)'s in steps, a step held
-// in shared memory until all of it has been read; otherwise a CTA takes one step.
-template <int THREADS, int N>
-__global__ void __launch_bounds__(THREADS)
-gtms_evict_labels_kernel(const EvictArgs a, int32_t parts)
-{
-    constexpr int STEP = THREADS * N;
-    extern __shared__ __align__(16) uint4 ring[];
-    float* w = reinterpret_cast<float*>(ring);
-    int32_t* p = reinterpret_cast<int32_t*>(ring) + STEP;
-    const int64_t bh = blockIdx.x / parts;
-    const int32_t b = static_cast<int32_t>(bh / a.H);
-    const int32_t n = a.length(b), stay = n < a.keep ? n : a.keep;
-    const int32_t* kept = n > a.keep ? a.kept + bh * a.keep : nullptr;
-    for (int64_t j0 = static_cast<int64_t>(blockIdx.x % parts) * STEP; j0 < stay; j0 += static_cast<int64_t>(parts) * STEP) {
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int32_t i = u * THREADS + threadIdx.x;
-            if (j0 + i < stay) {
-                const int32_t from = kept ? kept[j0 + i] : static_cast<int32_t>(j0 + i);
-                w[i] = a.weights[bh * a.S + from];
-                p[i] = a.positions ? a.positions[bh * a.S + from] : from;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int32_t i = u * THREADS + threadIdx.x;
-            if (j0 + i < stay) {
-                a.weights_out[bh * a.S_out + j0 + i] = w[i];
-                if (a.positions_out)
-                    a.positions_out[bh * a.S_out + j0 + i] = p[i];
-            }
-        }
-        __syncthreads();
-    }
-}
-
+// ranks: CTAs of a cluster; beside: may start while the last launch still runs (see await_last_launch).
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, unsigned ranks, cudaStream_t st, Args... args)
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, unsigned ranks, bool beside, cudaStream_t st,
+                   Args... args)
 {
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    if (beside) {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+    } else {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = ranks;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = ranks > 1;
+    cfg.numAttrs = beside || ranks > 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <bool STAGED>
 cudaError_t launch_select(const EvictArgs& a, unsigned ranks, int32_t share, cudaStream_t st)
 {
-    const cudaError_t e = allow_smem<gtms_evict_select_kernel<STAGED>>(kSelectStaged * 4);
+    constexpr int most = static_cast<int>(sizeof(SelectShared)) + kSelectStaged * 4;
+    static_assert(most <= 226 * 1024, "shared memory of a CTA");
+    const cudaError_t e = allow_smem<gtms_evict_select_kernel<STAGED>>(most);
     return e != cudaSuccess ? e
                             : launch(gtms_evict_select_kernel<STAGED>, dim3(static_cast<unsigned>(a.B) * a.H * ranks),
-                                     kSelectThreads, STAGED ? share * 4 : 0, ranks, st, a);
-}
-
-template <int THREADS, int N>
-cudaError_t launch_labels(const EvictArgs& a, int64_t heads, int64_t parts, cudaStream_t st)
-{
-    constexpr int smem = THREADS * N * 8;
-    if (heads * parts > INT32_MAX)
-        return cudaErrorNotSupported;
-    const cudaError_t e = allow_smem<gtms_evict_labels_kernel<THREADS, N>>(smem);
-    return e != cudaSuccess ? e
-                            : launch(gtms_evict_labels_kernel<THREADS, N>, dim3(static_cast<unsigned>(heads * parts)), THREADS,
-                                     smem, 1, st, a, static_cast<int32_t>(parts));
+                                     kSelectThreads, sizeof(SelectShared) + (STAGED ? share * 4 : 0), ranks, false, st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st)
+cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t st)
 {
+    EvictArgs a = args;
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
     // Select: CTAs to a row until the chip is busy, 4096 weights to each at least.
     unsigned ranks = 1;
@@ -396,33 +404,33 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st)
     cudaError_t e = share <= kSelectStaged ? launch_select<true>(a, ranks, share, st) : launch_select<false>(a, ranks, share, st);
     if (e != cudaSuccess || a.keep == 0)
         return e;
-    const int32_t stay = a.keep;
+    // Weights and positions go with whoever moves, in order where either is compacted in place.
+    if (!(a.weights == a.weights_out || (a.positions && a.positions == a.positions_out)))
+        a.moved |= 4;
     if (a.moved) {
-        // Rows of a CTA: 16 turns of its threads, fewer until there are eight CTAs to a multiprocessor.
-        int32_t rows = (16 * kGatherThreads * kGatherUnroll + a.units - 1) / a.units;
-        while (rows > 16 && heads * 2 * ((stay + rows - 1) / rows) < 8 * kChipSms)
+        // Rows of a CTA: 8 turns of its threads, fewer until there are six CTAs to a multiprocessor.
+        const int32_t turn = kGatherThreads / a.units * kGatherUnroll;
+        int32_t rows = 8 * turn;
+        while (rows > turn && heads * ((a.keep + rows - 1) / rows) < 6 * kChipSms)
             rows /= 2;
-        const int64_t parts = (stay + rows - 1) / rows;
+        const int64_t parts = (a.keep + rows - 1) / rows;
         if (heads * parts > INT32_MAX)
             return cudaErrorNotSupported;
-        if ((e = launch(gtms_evict_gather_kernel, dim3(static_cast<unsigned>(heads * parts), 2), kGatherThreads, 0, 1, st, a,
+        if ((e = launch(gtms_evict_gather_kernel, dim3(static_cast<unsigned>(heads * parts)), kGatherThreads, 0, 1, true, st, a,
                         static_cast<int32_t>(parts), rows)) != cudaSuccess)
             return e;
     }
-    if (a.moved != 3) {
+    if (a.moved != 7) {
         // Columns of a CTA: whole rows, or slices of 32 bytes at least until there are two CTAs to a multiprocessor.
         int32_t width = a.units;
         while (width > 2 && heads * 2 * ((a.units + width - 1) / width) < 2 * kChipSms)
             width = (width + 1) / 2;
         const int32_t slices = (a.units + width - 1) / width;
-        constexpr int smem = kMoveStages * kMoveUnroll * kGatherThreads * 16;
-        if ((e = allow_smem<gtms_evict_move_kernel>(smem)) != cudaSuccess ||
-            (e = launch(gtms_evict_move_kernel, dim3(static_cast<unsigned>(heads * slices), 2), kGatherThreads, smem, 1, st, a,
-                        slices, width)) != cudaSuccess)
-            return e;
+        if ((e = allow_smem<gtms_evict_move_kernel>(kMoveBytes)) == cudaSuccess)
+            e = launch(gtms_evict_move_kernel, dim3(static_cast<unsigned>(heads * slices), 3), kGatherThreads, kMoveBytes, 1, true,
+                       st, a, slices, width);
     }
-    const bool in_place = a.weights == a.weights_out || (a.positions && a.positions == a.positions_out);
-    return in_place ? launch_labels<1024, 8>(a, heads, 1, st) : launch_labels<256, 4>(a, heads, (stay + 1023) / 1024, st);
+    return e;
 }
 
 }  // namespace gtms

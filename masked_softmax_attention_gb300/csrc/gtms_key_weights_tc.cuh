@@ -425,11 +425,11 @@ __global__ void __launch_bounds__(kJoinThreads) gtms_key_weights_join_kernel(con
 {
     const AttentionArgs& a = kw.a;
     const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * a.Skv, at = blockIdx.x * static_cast<int64_t>(kJoinThreads) + threadIdx.x;
+    await_last_launch();
     if (at >= all)
         return;
     const int64_t bg = at / a.Skv;
     const int32_t key = static_cast<int32_t>(at - bg * a.Skv), L = a.length(static_cast<int32_t>(bg / a.Hkv));
-    await_last_launch();
     if (key >= L) {
         if (!kw.accumulate)
             kw.weights[at] = 0.0f;
