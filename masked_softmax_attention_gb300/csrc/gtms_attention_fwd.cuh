@@ -190,6 +190,9 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
     tc::fence_after_sync();
     const uint32_t tmem = warp_value(sh.tmem_slot);
 
+    if constexpr (Source::packed)
+        let_next_launch_start();   // it waits for what this one writes
+
     if (warp >= TL::mma_warp) {
         tc::regs_lower<TL::other_regs>();
         if (warp == TL::deal_warp) {
@@ -529,27 +532,30 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 const int64_t at = source.index(part, b, h, i);
                 if (i < a.Sq)
                     source.out.ml[at] = hi > lo ? make_float2(m * c, l) : make_float2(-INFINITY, 0.0f);
-                if (hi <= lo)
-                    continue;
-                ok = up.warp_wait(&sh.ofull[w], no & 1u);
-                ++no;
-                if (!ok)
-                    break;
-                tc::fence_after_sync();
+                if (hi > lo) {
+                    ok = up.warp_wait(&sh.ofull[w], no & 1u);
+                    ++no;
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                }
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
                     uint32_t r[32];
-                    tc::tmem_ld32(to + k, o);
+                    if (hi > lo)
+                        tc::tmem_ld32(to + k, o);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        r[j] = __float_as_uint(o[j]);
+                        r[j] = hi > lo ? __float_as_uint(o[j]) : 0u;
                     store_rows<64>(stage, lane, r, i < a.Sq ? source.out.o + at * D + k : nullptr);
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.oempty[w]);
+                if (hi > lo) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.oempty[w]);
+                }
                 continue;
             }
             T* out = i < a.Sq ? a.o.row<T>(b, h, i) : nullptr;

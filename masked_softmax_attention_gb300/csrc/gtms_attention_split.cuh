@@ -333,8 +333,6 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
         float top = -INFINITY;
         for (int32_t k = 0; k < ranks; ++k)
             top = fmaxf(top, *cluster.map_shared_rank(&sh.cta_m[r], k));
-        if constexpr (Parts::any)
-            top = fmaxf(top, parts.top(b, hk, tile * kSplitRows + r));
         int32_t k0, k1;
         a.kept(off + row_of(r), L, k0, k1);
         const bool live = k0 < k1;
@@ -349,7 +347,7 @@ gtms_attention_split_kernel(const AttentionArgs a, int32_t tiles, int32_t ordere
         }
         if constexpr (Parts::any)
             if (live)
-                parts.template add<D>(b, hk, tile * kSplitRows + r, d, base, sum, x, y);
+                parts.template add<D>(b, hk, tile * kSplitRows + r, d, top, sum, x, y);
         const float inv = live ? 1.0f / sum : 0.0f;
         *reinterpret_cast<uint32_t*>(a.o.row<T>(b, head_of(r), row_of(r)) + d) = live ? pack2<T>(x * inv, y * inv) : 0u;
         if (a.lse && d == 0)

@@ -3,6 +3,11 @@
 
 namespace gtms {
 
+extern template cudaError_t launch_attention_forward<__nv_bfloat16, 64>(const AttentionArgs&, cudaStream_t);
+extern template cudaError_t launch_attention_forward<__nv_bfloat16, 128>(const AttentionArgs&, cudaStream_t);
+extern template cudaError_t launch_attention_forward<__half, 64>(const AttentionArgs&, cudaStream_t);
+extern template cudaError_t launch_attention_forward<__half, 128>(const AttentionArgs&, cudaStream_t);
+
 namespace {
 
 template <int D>
@@ -22,6 +27,8 @@ uint64_t shared_prefix_workspace_bytes(const AttentionArgs& a, const PrefixArgs&
 template <typename T, int D>
 cudaError_t launch_shared_prefix(const AttentionArgs& a, const PrefixArgs& p, void* workspace, cudaStream_t st)
 {
+    if (p.P == 0)
+        return launch_attention_forward<T, D>(a, st);
     const PackedPlan x = packed_plan<D>(a, p);
     return prefer_packed<D>(a, p, x) ? launch_prefix_packed<T, D>(a, p, x, workspace, st) : launch_prefixed_whole<T, D>(a, p, st);
 }

@@ -51,7 +51,7 @@ struct PrefixedCache {
 struct PrefixParts {
     static constexpr bool any = true;
     float* o;        // [parts, G Hkv, rows, D], not divided by l
-    float2* ml;      // [parts, G Hkv, rows]: maximum in base 2 and sum; (-inf, 0) without keys, and o is not written
+    float2* ml;      // [parts, G Hkv, rows]: maximum in base 2 and sum; (-inf, 0) without keys, and o is zero
     int32_t parts, n, G, Hkv, per;   // per: rows of a sequence (group Sq)
 
     __host__ __device__ __forceinline__ int64_t stride() const { return static_cast<int64_t>(G) * Hkv * n * per; }
@@ -60,30 +60,40 @@ struct PrefixParts {
         const int32_t g = b / n;
         return (static_cast<int64_t>(g) * Hkv + hk) * (static_cast<int64_t>(n) * per) + static_cast<int64_t>(b - g * n) * per + r;
     }
-    __device__ __forceinline__ float top(int32_t b, int32_t hk, int32_t r) const
-    {
-        const float2* x = ml + at(b, hk, r);
-        float t = -INFINITY;
-#pragma unroll 4
-        for (int32_t k = 0; k < parts; ++k)
-            t = fmaxf(t, x[k * stride()].x);
-        return t;
-    }
-    // Adds them to a row's sums at maximum `base`: l, and the elements d and d + 1.
+    // Adds them to a row's sums at maximum `top`: l, and the elements d and d + 1. Eight parts at a time, their loads
+    // in flight together (one after the other the parts took most of the call).
     template <int D>
-    __device__ __forceinline__ void add(int32_t b, int32_t hk, int32_t r, int32_t d, float base, float& l, float& x, float& y) const
+    __device__ __forceinline__ void add(int32_t b, int32_t hk, int32_t r, int32_t d, float& top, float& l, float& x, float& y) const
     {
-        const int64_t i = at(b, hk, r);
-#pragma unroll 4
-        for (int32_t k = 0; k < parts; ++k) {
-            const float2 s = ml[i + k * stride()];
-            if (s.y > 0.0f) {
-                const float f = exp2_approx(s.x - base);
-                const float2 e = *reinterpret_cast<const float2*>(o + (i + k * stride()) * D + d);
-                l += f * s.y;
-                x += f * e.x;
-                y += f * e.y;
+        constexpr int N = 8;
+        const int64_t i = at(b, hk, r), step = stride();
+        for (int32_t k = 0; k < parts; k += N) {
+            float2 s[N], e[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                s[u] = make_float2(-INFINITY, 0.0f);
+                e[u] = make_float2(0.0f, 0.0f);
+                if (k + u < parts) {
+                    s[u] = ml[i + (k + u) * step];
+                    e[u] = *reinterpret_cast<const float2*>(o + (i + (k + u) * step) * D + d);
+                }
             }
+            float t = top;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                t = fmaxf(t, s[u].x);
+            const float base = t == -INFINITY ? 0.0f : t, f = exp2_approx(top - base);
+            l *= f;
+            x *= f;
+            y *= f;
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const float g = exp2_approx(s[u].x - base);
+                l += g * s[u].y;
+                x += g * e[u].x;
+                y += g * e[u].y;
+            }
+            top = t;
         }
     }
 };
