@@ -594,7 +594,16 @@ def _heads(name, t, dtype, device):
     return _pack_heads(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
-_int32_dtype = None
+_int32_dtype = _uint8_dtype = None
+
+
+def _uint8():
+    global _uint8_dtype
+    if _uint8_dtype is None:
+        import torch
+
+        _uint8_dtype = torch.uint8
+    return _uint8_dtype
 
 
 def _int32(name, t, shape, device):
@@ -700,18 +709,26 @@ def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=
 _pack_evict = struct.Struct("@8qi4x").pack          # gtms_evict_shape
 
 
-def _workspace(fn, device, *shape):
-    """(tensor, address, bytes) of the workspace that a call of this shape needs; the tensor is to outlive the call."""
-    import torch
+_workspace_sizes: dict = {}
 
-    need = ctypes.c_uint64()
-    rc = (_direct_calls.get(fn) or _direct(fn))(*shape, ctypes.byref(need))
-    if rc != GTMS_OK:
-        raise GtmsError(fn, rc)
-    if need.value == 0:
+
+def _workspace(fn, like, *shape):
+    """(tensor, address, bytes) of the workspace that a call of this shape needs, on the device of ``like``; the tensor
+    is to outlive the call. The bytes follow from the shape alone, and asking costs as much as a launch's checks."""
+    key = fn, *shape
+    size = _workspace_sizes.get(key)
+    if size is None:
+        need = ctypes.c_uint64()
+        rc = (_direct_calls.get(fn) or _direct(fn))(*shape, ctypes.byref(need))
+        if rc != GTMS_OK:
+            raise GtmsError(fn, rc)
+        if len(_workspace_sizes) >= 1024:
+            _workspace_sizes.clear()
+        size = _workspace_sizes[key] = need.value
+    if size == 0:
         return None, None, 0
-    t = torch.empty(need.value, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), need.value
+    t = like.new_empty(size, dtype=_uint8())
+    return t, t.data_ptr(), size
 
 
 def _labels(name, t, dtype, shape, device):
@@ -746,8 +763,8 @@ def attention_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens, scale: float 
         out = torch.empty_like(q)
     elif out.shape != q.shape:
         raise ValueError("out must match q in shape")
-    lse = torch.empty((B, q.shape[1], Sq), dtype=torch.float32, device=q.device)
-    _keep, work, size = _workspace("gtms_attention_shared_prefix_workspace", q.device, shape, G, P)
+    lse = q.new_empty((B, q.shape[1], Sq), dtype=torch.float32)
+    _keep, work, size = _workspace("gtms_attention_shared_prefix_workspace", q, shape, G, P)
     _launch("gtms_attention_shared_prefix", dev, shape, G, P, q_, kp_, vp_, k_, v_, _heads("out", out, dtype, dev),
             lse.data_ptr(), plens, lens, off, work, size, status)
     return out, lse
@@ -775,7 +792,7 @@ def attention_key_weights(q, k, lse, seq_lens, scale: float = 1.0, out=None, acc
             raise ValueError("accumulate needs out")
         out = torch.empty(k.shape[:3], dtype=torch.float32, device=q.device)
     out_ = _labels("out", out, torch.float32, k.shape[:3], dev)
-    _keep, work, size = _workspace("gtms_attention_key_weights_workspace", q.device, shape)
+    _keep, work, size = _workspace("gtms_attention_key_weights_workspace", q, shape)
     _launch("gtms_attention_key_weights", dev, shape, q_, k_, lse_, out_, bool(accumulate), lens, off, work, size, status)
     return out
 
@@ -813,7 +830,7 @@ def cache_evict(k, v, weights, seq_lens, keep: int, first: int = 0, recent: int 
     po = None if positions_out is None else _labels("out's positions", positions_out, torch.int32, (B, H, rows), dev)
     new = torch.empty_like(seq_lens)
     shape = _pack_evict(B, H, S, rows, d, int(keep), int(first), int(recent), _dtype_code(k))
-    _keep, work, size = _workspace("gtms_cache_evict_workspace", k.device, shape)
+    _keep, work, size = _workspace("gtms_cache_evict_workspace", k, shape)
     _launch("gtms_cache_evict", dev, shape, k_, v_, weights_, positions_, _heads("out's k", k_out, dtype, dev),
             _heads("out's v", v_out, dtype, dev), wo, po, lens, new.data_ptr(), work, size)
     return k_out, v_out, weights_out, positions_out, new

@@ -29,7 +29,7 @@ constexpr int kSelectStaged = 40960;
 // Bins of a histogram (11, 11 and 10 bits), and its copies, by lane: neighbouring weights
 // share their exponents, and lanes that count into one place wait for each other.
 constexpr int kBins = 2048, kCopies = 4;
-static_assert(kBins == 2 * kSelectThreads, "two bins to a thread");
+static_assert(kBins == 2 * kSelectThreads && kSelectWarps == 32, "two bins to a thread, a warp's count to a lane");
 
 struct SelectShared {
     __align__(16) uint32_t hist[kBins][kCopies];
@@ -118,8 +118,10 @@ gtms_evict_select_kernel(const EvictArgs a)
         if (ranks > 1)
             cluster.sync();
         uint32_t low = 0, high = 0;
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const uint2 t = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.total[pass & 1][bin], r));
+#pragma unroll
+        for (uint32_t r = 0; r < kSelectCluster; ++r) {   // their loads in flight together
+            const uint2 t = r < ranks ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.total[pass & 1][bin], r))
+                                      : make_uint2(0u, 0u);
             low += t.x;
             high += t.y;
         }
@@ -163,27 +165,23 @@ gtms_evict_select_kernel(const EvictArgs a)
         sh.eq[warp] = eq;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        uint32_t g = 0, e = 0;
-        for (int i = 0; i < kSelectWarps; ++i) {
-            g += sh.gt[i];
-            e += sh.eq[i];
+    if (warp == 0) {
+        const uint32_t g = __reduce_add_sync(0xffffffffu, sh.gt[lane]), e = __reduce_add_sync(0xffffffffu, sh.eq[lane]);
+        if (lane == 0) {
+            sh.cta_gt = g;
+            sh.cta_eq = e;
         }
-        sh.cta_gt = g;
-        sh.cta_eq = e;
     }
     if (ranks > 1)
         cluster.sync();
     else
         __syncthreads();
     gt = eq = 0;
-    for (uint32_t r = 0; r < rank; ++r) {
-        gt += *cluster.map_shared_rank(&sh.cta_gt, r);
-        eq += *cluster.map_shared_rank(&sh.cta_eq, r);
-    }
-    for (int i = 0; i < warp; ++i) {
-        gt += sh.gt[i];
-        eq += sh.eq[i];
+    {   // those of the CTAs before, and of this one's warps before
+        const bool before = lane < static_cast<int>(rank);
+        const uint32_t g = before ? *cluster.map_shared_rank(&sh.cta_gt, lane) : 0, e = before ? *cluster.map_shared_rank(&sh.cta_eq, lane) : 0;
+        gt = __reduce_add_sync(0xffffffffu, g + (lane < warp ? sh.gt[lane] : 0));
+        eq = __reduce_add_sync(0xffffffffu, e + (lane < warp ? sh.eq[lane] : 0));
     }
     int32_t* to = kept + a.first;
     const uint32_t below = (1u << lane) - 1u;

@@ -532,21 +532,22 @@ PackedPlan packed_plan(const AttentionArgs& a, const PrefixArgs& p)
     return x;
 }
 
-// Whether to pack: always where the rows of a sequence's head fill one tile of the
-// split kernel, otherwise by the time that both forms take (see prefer_split).
+// Whether to pack, by the time that both forms take (see prefer_split). Its two launches
+// more cost the host as much as some tiles cost the chip: 4 sequences, 16 / 4 heads of 64, a
+// prefix of 500 keys, 8 us on the device either way, through the call 34 us packed, 25 whole.
+constexpr double kLaunchesUs = 4.0;
+
 template <int D>
 bool prefer_packed(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x)
 {
-    const int64_t rows = static_cast<int64_t>(a.group) * a.Sq;
-    if (p.P == 0 || rows > kSplitMaxRows || x.rows > (1 << 24) || x.blocks * x.parts * p.G * a.Hkv > INT32_MAX)
+    if (p.P == 0 || static_cast<int64_t>(a.group) * a.Sq > kSplitMaxRows || x.rows > (1 << 24) ||
+        x.blocks * x.parts * p.G * a.Hkv > INT32_MAX)
         return false;
-    if (rows <= kSplitRows)
-        return true;
     const double items = static_cast<double>(a.B) * a.Hq * ((a.Sq + FwdTile<D>::rows - 1) / FwdTile<D>::rows);
     const double loads = items / (static_cast<double>(kChipSms) * FwdTile<D>::ctas);
     const int64_t tiles = (static_cast<int64_t>(p.P) + kTile - 1) / kTile + (static_cast<int64_t>(a.Skv) + kTile - 1) / kTile;
     const double whole = (loads > 1.0 ? loads : 1.0) * (kItemUs<D> + kTileUs<D> * static_cast<double>(tiles));
-    return x.us < whole;
+    return x.us + kLaunchesUs < whole;
 }
 
 inline uint64_t packed_bytes(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x, int64_t D)
