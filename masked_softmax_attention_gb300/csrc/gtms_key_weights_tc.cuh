@@ -420,11 +420,11 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
 }
 
 // The parts' sums, in order.
-inline constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) gtms_key_weights_join_kernel(const KeyWeightsArgs kw, int32_t parts)
+inline constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) gtms_key_weights_join_kernel(const KeyWeightsArgs kw, int32_t parts)
 {
     const AttentionArgs& a = kw.a;
-    const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * a.Skv, at = blockIdx.x * static_cast<int64_t>(kJoinThreads) + threadIdx.x;
+    const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * a.Skv, at = blockIdx.x * static_cast<int64_t>(kSumThreads) + threadIdx.x;
     await_last_launch();
     if (at >= all)
         return;
@@ -507,8 +507,8 @@ cudaError_t launch_key_weights_tc(const KeyWeightsArgs& kw, cudaStream_t st, uin
                           plan.per, plan.parts, wait_ns);
     if (e != cudaSuccess || plan.parts == 1)
         return e;
-    const int64_t ctas = (heads * a.Skv + kJoinThreads - 1) / kJoinThreads;
-    return launch_beside_last(true, gtms_key_weights_join_kernel, static_cast<unsigned>(ctas), kJoinThreads, 0, st, kw, plan.parts);
+    const int64_t ctas = (heads * a.Skv + kSumThreads - 1) / kSumThreads;
+    return launch_beside_last(true, gtms_key_weights_join_kernel, static_cast<unsigned>(ctas), kSumThreads, 0, st, kw, plan.parts);
 }
 
 }  // namespace gtms
