@@ -120,6 +120,7 @@ struct FwdItem {
     }
     __device__ __forceinline__ uint32_t steps(const AttentionArgs&) const { return top() > 0 ? top() - bottom() : 0; }
     __device__ __forceinline__ bool has(int w, int32_t t) const { return t >= lo[w] && t < hi[w]; }
+    __device__ __forceinline__ bool alternating() const { return false; }
 };
 
 // Where the kernel finds its keys and rows: in one cache (this), or as the two forms
@@ -346,11 +347,18 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                     arrived(2 * n + 1);
                     if (ok && t > bottom)
                         arrived(2 * n + 2);
+                    if constexpr (Source::packed) {
+                        // Tiles of keys that alternate: the next one's scores do not wait for this one's softmax.
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+                            if (ok && it.alternate && it.has(w, t - 1))
+                                scores(w, t - 1, n + 1);
+                    }
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         if (ok && it.has(w, t))
                             output(w, t);
-                        if (ok && it.has(w, t - 1))
+                        if (ok && !(Source::packed && it.alternating()) && it.has(w, t - 1))
                             scores(w, t - 1, n + 1);
                     }
                     if (ok) {
@@ -375,7 +383,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
         uint32_t ns = 0, no = 0, taken = 0;
         bool ok = true;
         int32_t b = 0, h = 0, i = 0, c0 = 0, c1 = 0, lo = 0, hi = 0, full0 = 0, full1 = 0;
-        [[maybe_unused]] int32_t part = 0, prefix_tiles = 0, prefix = 0;   // of the forms for shared prefixes
+        [[maybe_unused]] int32_t part = 0, step = 1, prefix_tiles = 0, prefix = 0;   // of the forms for shared prefixes
         [[maybe_unused]] uint32_t nq = 0;
         auto read = [&](const Item& it) {
             b = it.b;
@@ -384,6 +392,11 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             if constexpr (Source::packed) {
                 c1 = it.L;
                 part = it.part;
+                if (it.alternate) {
+                    i -= w * kTile;
+                    part = 2 * part + w;
+                }
+                step = it.alternate ? 2 : 1;
             } else {
                 a.kept(it.off + i, it.L, c0, c1);
             }
@@ -427,7 +440,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
             float m = -INFINITY, l = 0.0f;
             float m_carried = -INFINITY, l_carried = 0.0f;   // of the part of O that the row of o carries, in units of l
             auto carried = [&] { return l_carried > 0.0f ? l_carried * exp2_approx((m_carried - m) * c) : 0.0f; };
-            for (int32_t t = hi - 1; t >= lo; --t) {
+            for (int32_t t = hi - 1; t >= lo; t -= Source::packed ? step : 1) {
                 // The first scores may have to wait while the other tile has a whole item to itself.
                 ok = item_wait(sh.items, up, &sh.sfull[w], ns & 1u);
                 ++ns;

@@ -394,28 +394,43 @@ struct PrefixRows {
     PrefixArgs p;
     PrefixParts out;
     int32_t Sq, group;
+    // Where one tile holds all rows, a CTA's two work on alternate tiles of keys, a part each, instead of one on all of
+    // them, waiting for itself (4 x 8 sequences of 8 heads to a key over prefixes of 32768 keys in 8 items each: 51 us,
+    // 46 so; in 12: 41, 40).
+    bool alternate;
 
     template <int W>
     struct Item : FwdItem<W> {
         int32_t part;
+        bool alternate;
+
+        __device__ __forceinline__ bool has(int w, int32_t t) const
+        {
+            return FwdItem<W>::has(w, t) && (!alternate || (t & 1) == w);
+        }
+        __device__ __forceinline__ bool alternating() const { return alternate; }
     };
     template <int W>
     __device__ __forceinline__ void set(Item<W>& it, const AttentionArgs& a, uint32_t item, uint32_t heads, int32_t) const
     {
         const int32_t gh = static_cast<int32_t>(item % heads), rest = static_cast<int32_t>(item / heads);
-        it.part = rest % out.parts;
+        const int32_t parts = alternate ? out.parts / 2 : out.parts;   // items
+        it.alternate = alternate;
+        it.part = rest % parts;
         it.b = gh / a.Hkv;
         it.h = gh - it.b * a.Hkv;
-        it.i0 = rest / out.parts * W * kTile;
+        it.i0 = rest / parts * W * kTile;
         it.off = 0;
         it.L = p.length(it.b);
-        const int32_t tiles = (it.L + kTile - 1) / kTile, per = (tiles + out.parts - 1) / out.parts;   // of this prefix
+        const int32_t tiles = (it.L + kTile - 1) / kTile, per = (tiles + parts - 1) / parts;   // of this prefix
         const int32_t lo = it.part * per, hi = lo + per < tiles ? lo + per : tiles;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const bool any = lo < hi && it.i0 + w * kTile < a.Sq;
-            it.lo[w] = any ? lo : 0;
-            it.hi[w] = any ? hi : 0;
+            // Its first and its last tile, where they alternate those whose number is w modulo 2.
+            const int32_t lo_w = alternate ? lo + ((w - lo) & 1) : lo, hi_w = alternate ? hi - ((hi - 1 - w) & 1) : hi;
+            const bool any = lo_w < hi_w && (alternate || it.i0 + w * kTile < a.Sq);
+            it.lo[w] = any ? lo_w : 0;
+            it.hi[w] = any ? hi_w : 0;
             it.full0[w] = 0;
             it.full1[w] = it.L;
         }
@@ -469,7 +484,8 @@ cudaError_t launch_prefixed_whole(const AttentionArgs& a, const PrefixArgs& p, c
 struct PackedPlan {
     int64_t rows;            // of one prefix and key/value head
     int64_t blocks;          // items of rows
-    int32_t parts;
+    bool alternate;          // see PrefixRows
+    int32_t parts;           // of the keys: items, two parts each where they alternate
     int32_t tile;            // rows of a warp's chunk
     int32_t chunk, chunks;   // keys of a chunk, chunks of a sequence's own cache; 0: the split kernel takes them
     double us;               // of the call, about
@@ -489,8 +505,9 @@ constexpr int32_t kChunk = 128;
 
 // Parts of the prefix: as many as make the call shortest, since the prefix's items and the
 // chunks share the chip. Microseconds, measured (parts: time):
-//   64 sequences of 100 to 1024 keys, 8 heads of 128, prefix 8192:    4: 47, 8: 48, 12: 53, 16: 57
-//   4 x 8 of 300 to 2048, 2 heads of 128 (8 to a key), prefixes 32768: 8: 51, 12: 40, 16: 41, 19: 42
+//   64 sequences of 100 to 1024 keys, 8 heads of 128, prefix 8192:    4: 47, 8: 49, 12: 53, 16: 57
+//   64 sequences of 128 keys, the same:                               4: 38, 8: 27, 12: 27, 16: 36
+//   4 x 8 of 300 to 2048, 2 heads of 128 (8 to a key), prefixes 32768: 8: 46, 12: 40, 14: 38, 16: 42
 //   24 x 5 rows of 50 to 333, 4 heads of 64, prefix 5003:              4: 18, 8: 14, 12: 15, 16: 15
 // A part's keys are below kCarryTerms of either type, so that no sum in an accumulator is long.
 template <int D>
@@ -500,6 +517,7 @@ PackedPlan packed_plan(const AttentionArgs& a, const PrefixArgs& p)
     PackedPlan x;
     x.rows = static_cast<int64_t>(p.n) * a.Sq * a.group;
     x.blocks = (x.rows + TL::rows - 1) / TL::rows;
+    x.alternate = TL::W == 2 && x.rows <= kTile;
 
     const int64_t rows = a.group * int64_t(a.Sq);
     x.tile = rows <= 8 ? 8 : 16;
@@ -521,10 +539,13 @@ PackedPlan packed_plan(const AttentionArgs& a, const PrefixArgs& p)
     x.us = 0.0;
     for (int64_t parts = least; parts <= tiles && parts <= least + 31; ++parts) {
         const int64_t turns = (items * parts + slots - 1) / slots, per = (tiles + parts - 1) / parts;
-        const double item = kItemUs<D> + kTileUs<D> * static_cast<double>(per), first = static_cast<double>(turns) * item;
+        const double item = kItemUs<D> + (x.alternate ? 0.7 : 1.0) * kTileUs<D> * static_cast<double>(per);
+        const double first = static_cast<double>(turns) * item;
         const double both = own + static_cast<double>(items * parts) * item / static_cast<double>(slots);
-        const double us = (first > both ? first : both) + 3.0 + 0.25 * static_cast<double>(parts);
-        if (parts == least || us < x.us) {
+        const double us = (first > both ? first : both) + 0.1 * first + 3.0 + 0.25 * static_cast<double>(x.alternate ? 2 * parts : parts);
+        // A third of the chip is left to the chunks from the start (64 x 128 keys, prefix 8192: 12 parts, 96 of 152
+        // multiprocessors, 27 us; 13, 104 of them: 36).
+        if (parts == least || (us < x.us && (x.chunks == 0 || 3 * items * parts <= 2 * slots))) {
             x.us = us;
             x.parts = static_cast<int32_t>(parts);
         }
@@ -552,7 +573,7 @@ bool prefer_packed(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan
 
 inline uint64_t packed_bytes(const AttentionArgs& a, const PrefixArgs& p, const PackedPlan& x, int64_t D)
 {
-    return static_cast<uint64_t>(x.parts + x.chunks) * p.G * a.Hkv * x.rows * (D * 4 + 8);
+    return static_cast<uint64_t>((x.alternate ? 2 : 1) * x.parts + x.chunks) * p.G * a.Hkv * x.rows * (D * 4 + 8);
 }
 
 template <typename T, int D>
@@ -572,8 +593,9 @@ cudaError_t launch_prefix_packed(const AttentionArgs& a, const PrefixArgs& p, co
     source.Sq = a.Sq;
     source.group = a.group;
     source.out.o = static_cast<float*>(workspace);
-    source.out.ml = reinterpret_cast<float2*>(source.out.o + (x.parts + x.chunks) * heads * x.rows * D);
-    source.out.parts = x.parts;
+    source.alternate = x.alternate;
+    source.out.parts = x.alternate ? 2 * x.parts : x.parts;
+    source.out.ml = reinterpret_cast<float2*>(source.out.o + (source.out.parts + x.chunks) * heads * x.rows * D);
     source.out.n = p.n;
     source.out.G = p.G;
     source.out.Hkv = a.Hkv;
