@@ -449,6 +449,8 @@ struct KeyPlan {
     int32_t parts;   // of its rows
 };
 
+constexpr int64_t kLongTiles = 8192;
+
 inline KeyPlan key_plan(const AttentionArgs& a)
 {
     const KeyColumns col = key_columns(a.group);
@@ -465,6 +467,9 @@ inline KeyPlan key_plan(const AttentionArgs& a)
         per = per < heads * blocks / want ? per : heads * blocks / want;
         p.per = per > 1 ? static_cast<int32_t>(per) : 1;
     }
+    // Long sums in parts too: one of 8192 tiles' sums, a million rows, drops 2^-11 of itself at most.
+    const int64_t least = (tiles + kLongTiles - 1) / kLongTiles;
+    p.parts = p.parts > least ? p.parts : static_cast<int32_t>(least);
     return p;
 }
 

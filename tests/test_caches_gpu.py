@@ -108,6 +108,12 @@ TOKENS = [
     (1, 2, 128, 1, 2, 200, 12, 64, BF16, None, (12, 2), "last", TRIL, "bhsd"),           # 128 heads to a key
     (1, 2, 4, 2, 1, 0, 9, 128, BF16, None, (9, 4), "last", TRIL, "bhsd"),                # no prefix at all
     (1, 3, 4, 2, 2, 300, 40, 128, F16, None, (40, 40, 40), (38, -1, 41), TRIL, "bhsd"),  # rows before and behind the length
+    (64, 2, 8, 8, 1, 300, 20, 128, F16, None, (20, 7), "last", TRIL, "bhsd"),            # more items than multiprocessors
+    (48, 3, 16, 16, 1, 700, 20, 64, BF16, None, (20, 7, 0), "last", TRIL, "bshd"),
+    (1, 2, 4, 1, 1, 3000, 5000, 128, BF16, None, (5000, 2100), "last", TRIL, "bhsd"),    # few long caches of their own
+    (1, 2, 5, 1, 3, 3000, 4500, 64, F16, (2900,), (4500, 3), "last", TRIL, "bshd"),
+    (2, 4, 4, 2, 1, 900, 20000, 64, BF16, None, (20000, 7000, 9, 0), "last", TRIL, "bhsd"),
+    (1, 33, 2, 1, 1, 3000, 70, 128, BF16, None, (70, 1), "last", LENGTH, "bhsd"),
 ]
 PROMPTS = [
     (1, 2, 2, 1, 77, 130, 77, 64, BF16, None, (77, 41), None, TRIL, "bhsd"),
