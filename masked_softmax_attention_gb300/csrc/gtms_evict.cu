@@ -393,9 +393,10 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t st)
 {
     EvictArgs a = args;
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
-    // Select: CTAs to a row until the chip is busy, 4096 weights to each at least.
+    // Select: CTAs to a row as long as all run at once, 4096 weights to each at least (32 heads of 60129 weights: clusters
+    // of 8, which take two turns, 63 us the call, of 4 35).
     unsigned ranks = 1;
-    while (ranks < kSelectCluster && heads * ranks < kChipSms && static_cast<int64_t>(ranks) * 8192 <= a.S)
+    while (ranks < kSelectCluster && 2 * heads * ranks <= kChipSms && static_cast<int64_t>(ranks) * 8192 <= a.S)
         ranks *= 2;
     const int32_t step = 32 * kSelectWarps;
     const int32_t share = static_cast<int32_t>((static_cast<int64_t>(a.S) + ranks - 1) / ranks + step - 1) / step * step;

@@ -455,9 +455,13 @@ inline KeyPlan key_plan(const AttentionArgs& a)
 {
     const KeyColumns col = key_columns(a.group);
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv, blocks = (static_cast<int64_t>(a.Skv) + 2 * kTile - 1) / (2 * kTile);
-    const int64_t tiles = (static_cast<int64_t>(a.Sq) + col.rows - 1) / col.rows * col.head_tiles;
+    // Column tiles of a block at most: a window leaves a key few rows.
+    const int64_t reach = a.mask_kind == GTMS_MASK_SLIDING_WINDOW && a.window + 2 * kTile < a.Sq ? a.window + 2 * kTile : a.Sq;
+    const int64_t tiles = (reach + col.rows - 1) / col.rows * col.head_tiles;
     KeyPlan p{1, 1};
-    const int64_t want = 8 * kChipSms;   // items
+    // Items. Five to a multiprocessor (2, 3, 5, 8: [4,32/8,4096,128] 200, 200, 179, 176 us, the last 32 rows over 16384
+    // keys 57, 49, 46, 48, [4,16/2,1816,64] 38, 31, 28, 31, [1,16/4,4266,64] 46, 43, 41, 46).
+    const int64_t want = 5 * kChipSms;
     if (heads * blocks < want) {
         const int64_t parts = (want + heads * blocks - 1) / (heads * blocks);
         p.parts = static_cast<int32_t>(parts < tiles / 4 ? parts : tiles / 4);

@@ -323,20 +323,23 @@ gtms_attention_chunks_kernel(const AttentionArgs a, const PrefixParts out, int32
         await_last_launch();
 }
 
-// The parts of a row, the prefix's and those of its own keys, which follow them: a CTA to
-// each 128 / D rows, whose warps take every fourth part and meet in shared memory (one
-// thread that walks over all parts waits for memory as often as it has eights of them: 4 x
-// 8 sequences over prefixes of 32768 keys, 12 us instead of 6).
+// The parts of a row, the prefix's and those of its own keys, which follow them: four
+// elements a thread, four parts in flight. Where parts are many, a CTA's four warps take
+// every fourth one of the same rows and meet in shared memory (one thread that walks over
+// all parts waits for memory as often as it has fours of them: 4 x 8 sequences over prefixes
+// of 32768 keys, 12 us instead of 6); where they are few or rows many, each has rows of its own
+// (88 x 16 rows of 32 heads over prefixes of 1700 keys: the call 133 -> 80 us).
 constexpr int kJoinThreads = 128;
-template <typename T, int D>
+template <typename T, int D, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads)
 gtms_attention_parts_kernel(const AttentionArgs a, const PrefixParts in, int32_t chunk)
 {
-    constexpr int LANES = D / 4, ROWS = 32 / LANES, WARPS = kJoinThreads / 32, N = 4;   // 4 elements a thread
+    constexpr int LANES = D / 4, ROWS = 32 / LANES, WARPS = SHARED ? kJoinThreads / 32 : 1, N = 4;
     __shared__ float2 ml[WARPS][ROWS];
     __shared__ float4 sums[WARPS][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = lane % LANES * 4;
-    const int64_t x = blockIdx.x * static_cast<int64_t>(ROWS) + lane / LANES;   // (batch, key/value head, row of it)
+    const int warp = SHARED ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31, d = lane % LANES * 4;
+    const int64_t group = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int64_t x = group * ROWS + lane / LANES;   // (batch, key/value head, row of it)
     const int64_t bg = x / in.per;
     const int32_t r = static_cast<int32_t>(x - bg * in.per), b = static_cast<int32_t>(bg / a.Hkv);
     const int32_t hk = static_cast<int32_t>(bg - static_cast<int64_t>(b) * a.Hkv);
@@ -369,15 +372,19 @@ gtms_attention_parts_kernel(const AttentionArgs a, const PrefixParts in, int32_t
             if (k + u * WARPS < parts)
                 add(s[u].x, s[u].y, e[u]);
     }
-    sums[warp][lane] = y;
-    if (d == 0)
-        ml[warp][lane / LANES] = make_float2(top, l);
-    __syncthreads();
-    if (warp != 0 || b >= a.B)
-        return;
+    if (SHARED) {
+        sums[warp][lane] = y;
+        if (d == 0)
+            ml[warp][lane / LANES] = make_float2(top, l);
+        __syncthreads();
+        if (warp != 0)
+            return;
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w)
-        add(ml[w][lane / LANES].x, ml[w][lane / LANES].y, sums[w][lane]);
+        for (int w = 1; w < WARPS; ++w)
+            add(ml[w][lane / LANES].x, ml[w][lane / LANES].y, sums[w][lane]);
+    }
+    if (b >= a.B)
+        return;
     const float inv = parts > 0 ? 1.0f / l : 0.0f;
     const int32_t h = hk * a.group + r % a.group, row = r / a.group;
     *reinterpret_cast<uint2*>(a.o.row<T>(b, h, row) + d) =
@@ -497,6 +504,9 @@ template <int D>
 constexpr double kItemUs = D == 64 ? 4.0 : 5.0;
 template <int D>
 constexpr double kTileUs = D == 64 ? 1.0 : 1.15;
+
+// Rows of a call up to which a CTA each joins its parts.
+constexpr int64_t kJoinRows = 8192;
 
 // Own keys go in chunks of 128 (64 to 256 of them differ by 1 to 5 %), longer ones where a
 // cache would make more than 64; long caches of a few sequences, whose chunks would not
@@ -627,10 +637,14 @@ cudaError_t launch_prefix_packed(const AttentionArgs& a, const PrefixArgs& p, co
     e = x.tile == 8 ? chunks(std::integral_constant<int, 1>()) : chunks(std::integral_constant<int, 2>());
     if (e != cudaSuccess)
         return e;
-    constexpr int rows_of_cta = 128 / D;
     const int64_t all = static_cast<int64_t>(a.B) * a.Hkv * source.out.per;
-    return launch_beside_last(true, gtms_attention_parts_kernel<T, D>, static_cast<unsigned>((all + rows_of_cta - 1) / rows_of_cta),
-                              kJoinThreads, 0, st, a, source.out, x.chunk);
+    auto join = [&](auto shared) {
+        constexpr int rows_of_cta = 128 / D * (shared() ? 1 : kJoinThreads / 32);
+        return launch_beside_last(true, gtms_attention_parts_kernel<T, D, shared()>,
+                                  static_cast<unsigned>((all + rows_of_cta - 1) / rows_of_cta), kJoinThreads, 0, st, a, source.out,
+                                  x.chunk);
+    };
+    return source.out.parts + x.chunks > 8 && all <= kJoinRows ? join(std::true_type()) : join(std::false_type());
 }
 
 }  // namespace gtms
