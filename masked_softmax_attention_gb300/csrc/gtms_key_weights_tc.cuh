@@ -334,42 +334,46 @@ gtms_key_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_con
                     __syncwarp();
                     if (lane == 0)
                         tc::mbar_arrive(&sh.sempty[buf][w]);
+                    // The exponents, all of them before the first exponential.
                     const float4* shift = reinterpret_cast<const float4*>(&sh.shift[buf][half * 64]);
-                    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    if (__builtin_expect(r.i >= whole0 && r.i <= whole1 && r.j + col.heads <= a.group, 1)) {
-                        const float2 c2 = make_float2(c, c);
+                    const float2 c2 = make_float2(c, c);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float4 h = shift[k];
-                            const float2 e = __ffma2_rn(make_float2(x[4 * k], x[4 * k + 1]), c2, make_float2(h.x, h.y));
-                            const float2 f = __ffma2_rn(make_float2(x[4 * k + 2], x[4 * k + 3]), c2, make_float2(h.z, h.w));
-                            acc[0] = __fadd2_rn(acc[0], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
-                            acc[1] = __fadd2_rn(acc[1], make_float2(exp2_approx(f.x), exp2_approx(f.y)));
-                        }
-                    } else {
-                        // Columns [n0, n1) of this half: rows of the tile times heads.
-                        const int32_t r0 = min(max(k0 - r.i, 0), kTile), r1 = min(max(k1 - r.i, 0), kTile);
-                        const int32_t n0 = r0 * col.heads - half * 64;
-                        int32_t n1 = r1 * col.heads;
-                        n1 = (col.head_tiles > 1 && n1 > a.group - r.j ? a.group - r.j : n1) - half * 64;
-#pragma unroll
-                        for (int k = 0; k < 64; k += 32) {
-                            const uint32_t keep = bits_below(n1 - k) & ~bits_below(n0 - k);
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const float4 h = shift[k / 4 + y];
-                                const float hh[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const float e = exp2_approx(fmaf(x[k + 4 * y + z], c, hh[z]));
-                                    acc[z & 1].x += keep & (1u << (4 * y + z)) ? e : 0.0f;
-                                }
-                            }
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 h = shift[k];
+                        const float2 e = __ffma2_rn(make_float2(x[4 * k], x[4 * k + 1]), c2, make_float2(h.x, h.y));
+                        const float2 f = __ffma2_rn(make_float2(x[4 * k + 2], x[4 * k + 3]), c2, make_float2(h.z, h.w));
+                        x[4 * k] = e.x;
+                        x[4 * k + 1] = e.y;
+                        x[4 * k + 2] = f.x;
+                        x[4 * k + 3] = f.y;
                     }
                     __syncwarp();
                     if (lane == 0)
                         tc::mbar_arrive(&sh.hempty[buf]);
+                    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    if (__builtin_expect(r.i >= whole0 && r.i <= whole1 && r.j + col.heads <= a.group, 1)) {
+#pragma unroll
+                        for (int k = 0; k < 64; k += 4) {
+                            acc[0] = __fadd2_rn(acc[0], make_float2(exp2_approx(x[k]), exp2_approx(x[k + 1])));
+                            acc[1] = __fadd2_rn(acc[1], make_float2(exp2_approx(x[k + 2]), exp2_approx(x[k + 3])));
+                        }
+                    } else {
+                        // Rows [k0, k1) keep this key: columns [n0, n1) of this half, rows of the tile times heads.
+                        const int32_t n0 = min(max(k0 - r.i, 0), kTile) * col.heads - half * 64;
+                        int32_t n1 = min(max(k1 - r.i, 0), kTile) * col.heads;
+                        n1 = (col.head_tiles > 1 && n1 > a.group - r.j ? a.group - r.j : n1) - half * 64;
+#pragma unroll
+                        for (int k = 0; k < 64; k += 32) {
+                            const uint32_t keep = bits_below(n1 - k) & ~bits_below(n0 - k);
+                            if (__any_sync(0xffffffffu, keep != 0)) {   // a narrow window's keys see few of the rows
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) {
+                                    const float e = exp2_approx(x[k + y]);
+                                    acc[y & 1].x += keep & (1u << y) ? e : 0.0f;
+                                }
+                            }
+                        }
+                    }
                     sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 }
                 if (!ok)
