@@ -542,7 +542,7 @@ PackedPlan packed_plan(const AttentionArgs& a, const PrefixArgs& p)
     }
 
     const int64_t items = static_cast<int64_t>(p.G) * a.Hkv * x.blocks, slots = int64_t(kChipSms) * TL::ctas;
-    const int64_t tiles = (static_cast<int64_t>(p.P) + kTile - 1) / kTile, least = (tiles + 255) / 256;
+    const int64_t tiles = p.P > 0 ? (static_cast<int64_t>(p.P) + kTile - 1) / kTile : 1, least = (tiles + 255) / 256;
     // The own keys take the whole chip this long, caches half filled: 5 TB/s, once for each tile of rows.
     const double own = 0.5 * static_cast<double>(units) * a.Skv * D * 4 / 5e6;
     x.parts = 1;

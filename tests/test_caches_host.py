@@ -107,6 +107,26 @@ def test_prefix_workspace(kw):
     assert gtms.gtms_attention_shared_prefix_workspace(shape(mask=2, window=1), 2, 5000, ctypes.byref(need)) == UNSUPPORTED
 
 
+def test_workspaces_of_any_shape():
+    """Also without a prefix, own keys or rows; never negative or beyond what its parts can hold."""
+    need = ctypes.c_uint64()
+    for G, n in ((1, 1), (1, 64), (7, 3)):
+        for Hq, Hkv in ((1, 1), (8, 2), (130, 1)):
+            for Sq, Skv in ((0, 5), (1, 0), (1, 1), (1, 70000), (5, 300), (700, 700), (MAX, MAX)):
+                for P in (0, 1, 500, 70000, MAX):
+                    for d in (64, 128):
+                        s = shape(B=G * n, Hq=Hq, Hkv=Hkv, Sq=Sq, Skv=Skv, d=d)
+                        rc = gtms.gtms_attention_shared_prefix_workspace(s, G, P, ctypes.byref(need))
+                        if G * n * Hq * ((max(Sq, Skv) + 63) // 64) >= 1 << 31:
+                            assert rc == UNSUPPORTED
+                            continue
+                        # At most 2 parts of each of 512 + 31 splits of the prefix and 64 of the own keys.
+                        assert rc == OK and need.value <= (2 * 543 + 64) * G * n * Hq * Sq * (d * 4 + 8)
+                        assert need.value == 0 or P * Sq > 0
+                        assert gtms.gtms_attention_key_weights_workspace(s, ctypes.byref(need)) == OK
+                        assert need.value % 4 == 0 and (need.value == 0 or Sq * Skv > 0)
+
+
 # ---------------------------------------------------------------------------
 # Key weights
 # ---------------------------------------------------------------------------
