@@ -114,6 +114,15 @@ TOKENS = [
     (1, 2, 5, 1, 3, 3000, 4500, 64, F16, (2900,), (4500, 3), "last", TRIL, "bshd"),
     (2, 4, 4, 2, 1, 900, 20000, 64, BF16, None, (20000, 7000, 9, 0), "last", TRIL, "bhsd"),
     (1, 33, 2, 1, 1, 3000, 70, 128, BF16, None, (70, 1), "last", LENGTH, "bhsd"),
+    # shapes as above at sizes that pack the rows
+    (2, 30, 6, 2, 1, 3000, 40, 128, F16, (0, 1299), (40, 7), "last", TRIL, "bshd"),
+    (3, 40, 5, 1, 1, 5000, 130, 64, BF16, (5000, 1, 640), (130, 129), "last", LENGTH, "sliced"),
+    (4, 16, 16, 2, 1, 3850, 50, 128, BF16, (3850, 2560, 2559, 3841), (50, 0), "last", TRIL, "bshd"),
+    (2, 60, 4, 4, 1, 5000, 64, 64, F16, (-7, 5000), (64, 60), "last", TRIL, "bhsd"),
+    (1, 64, 12, 4, 5, 5003, 33, 64, F16, None, (33, 5, 17), "last", TRIL, "bshd"),
+    (1, 40, 14, 2, 3, 6400, 200, 128, BF16, (5130,), (200, 3), "last", LENGTH, "bhsd"),
+    (1, 20, 128, 1, 2, 4000, 12, 64, BF16, None, (12, 2), "last", TRIL, "bhsd"),
+    (1, 60, 4, 2, 2, 6000, 40, 128, F16, None, (40,), (38, -1, 41) * 20, TRIL, "bhsd"),
 ]
 PROMPTS = [
     (1, 2, 2, 1, 77, 130, 77, 64, BF16, None, (77, 41), None, TRIL, "bhsd"),
@@ -141,13 +150,13 @@ def test_shared_prefix_masked_places_may_hold_anything(dev, case):
 
 
 @pytest.mark.parametrize("scale,std", [(-0.2, 1.0), (0.0, 1.0), (1.0, 3.0), (0.125, 20.0)])
-@pytest.mark.parametrize("case", [TOKENS[2], PROMPTS[1]], ids=str)
+@pytest.mark.parametrize("case", [TOKENS[2], TOKENS[-6], TOKENS[-3], PROMPTS[1]], ids=str)
 def test_shared_prefix_scales_and_steep_rows(dev, case, scale, std):
     c = Shared(*case, scale=scale, std=std)
     c.check(*c.run())
 
 
-@pytest.mark.parametrize("case", [TOKENS[3], PROMPTS[1]], ids=str)
+@pytest.mark.parametrize("case", [TOKENS[3], TOKENS[-5], TOKENS[-4], PROMPTS[1]], ids=str)
 def test_shared_prefix_is_attention_over_the_keys_end_to_end(dev, case):
     """Beside the framework's own attention, for sequences whose prefix is full: within both calls' roundings."""
     c = Shared(*case[:9], None, *case[10:])
@@ -160,6 +169,18 @@ def test_shared_prefix_is_attention_over_the_keys_end_to_end(dev, case):
     live = live.expand_as(lse)
     _close("o", o, o2.double(), 2 * tol)
     _close("lse", lse[live], lse2[live].double(), 2 * tol_lse[live])
+
+
+@pytest.mark.parametrize("P,Skv,Sq", [(0, 0, 1), (300, 0, 1), (5000, 0, 3), (0, 40, 1), (0, 200, 200), (300, 20, 0)])
+def test_shared_prefix_without_keys_or_rows(dev, P, Skv, Sq):
+    """Without own keys no row is live, whatever the prefix; without a prefix it is attention over the own keys."""
+    c = Shared(2, 40, 8, 2, Sq, P, Skv, 64, BF16, None, (Skv,), "last" if Skv != Sq else None)
+    o, lse = c.run()
+    if Skv == 0 or Sq == 0:
+        assert o.shape == c.q.shape and bool((o == 0).all()) and bool((lse == -math.inf).all())
+    else:
+        o2, lse2 = gtms.attention_forward(c.q, c.k, c.v, c.lens, c.scale, q_offsets=c.off)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_shared_prefix_layouts_of_inputs_and_out(dev):
@@ -175,7 +196,7 @@ def test_shared_prefix_layouts_of_inputs_and_out(dev):
     c.check(o, lse)
 
 
-@pytest.mark.parametrize("case", [TOKENS[2], TOKENS[8], PROMPTS[0]], ids=str)
+@pytest.mark.parametrize("case", [TOKENS[2], TOKENS[8], TOKENS[-7], PROMPTS[0]], ids=str)
 def test_shared_prefix_streams_and_graphs(dev, case):
     """On a side stream, two calls at once, and captured: always the bits of a call by itself."""
     c, e = Shared(*case), Shared(*case, seed=2)
