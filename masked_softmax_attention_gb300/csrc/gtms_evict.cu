@@ -343,60 +343,62 @@ gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 // Rows stay in their cache: entry j goes to row j, at or before where it stood, so a
 // (batch, head)'s rows go in order, in steps: all of a step have been read (the barrier)
 // before any is written, and later steps read only rows behind those that this one
-// writes. What runs side by side is columns: a CTA moves `width` 16-byte units of every
-// row, several steps of copies in flight in shared memory.
-constexpr int kMoveStages = 4, kMoveUnroll = 4;
+// writes. A cluster's CTAs share the rows of a step; several steps of copies are in flight
+// in shared memory, and the rows' numbers are read a step before them.
+constexpr int kMoveStages = 4, kMoveUnroll = 2, kMoveCluster = 8;
 constexpr int kMoveBytes = kMoveStages * kMoveUnroll * kGatherThreads * 16;
 
 // Weights and positions in place, or one of them: all of a step have been read before
 // any is written, as above.
-__device__ __forceinline__ void move_labels(const EvictArgs& a, int64_t bh, const int32_t* kept, int32_t stay, uint8_t* smem)
+__device__ __forceinline__ void move_labels(const EvictArgs& a, int64_t bh, const int32_t* kept, int32_t stay, int32_t rank, int32_t ranks)
 {
-    constexpr int N = 16, STEP = N * kGatherThreads;
-    static_assert(STEP * 8 <= kMoveBytes, "a step of both");
-    float* w = reinterpret_cast<float*>(smem);
-    int32_t* p = reinterpret_cast<int32_t*>(smem) + STEP;
-    for (int32_t j0 = 0; j0 < stay; j0 += STEP) {
+    constexpr int N = 8, STEP = N * kGatherThreads;
+    const cg::cluster_group cluster = cg::this_cluster();
+    for (int32_t s = 0; s < stay; s += STEP * ranks) {
+        const int32_t j0 = s + rank * STEP;
+        float w[N];
+        int32_t p[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int32_t i = u * kGatherThreads + threadIdx.x;
-            if (i < stay - j0) {
-                const int32_t from = kept ? kept[j0 + i] : j0 + i;
-                w[i] = a.weights[bh * a.S + from];
-                p[i] = a.positions ? a.positions[bh * a.S + from] : from;
-            }
+            p[u] = i < stay - j0 ? (kept ? kept[j0 + i] : j0 + i) : 0;
         }
-        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const bool any = u * kGatherThreads + static_cast<int32_t>(threadIdx.x) < stay - j0;
+            w[u] = any ? a.weights[bh * a.S + p[u]] : 0.f;
+            p[u] = any && a.positions ? a.positions[bh * a.S + p[u]] : p[u];
+        }
+        cluster.sync();
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int32_t i = u * kGatherThreads + threadIdx.x;
             if (i < stay - j0) {
-                a.weights_out[bh * a.S_out + j0 + i] = w[i];
+                a.weights_out[bh * a.S_out + j0 + i] = w[u];
                 if (a.positions_out)
-                    a.positions_out[bh * a.S_out + j0 + i] = p[i];
+                    a.positions_out[bh * a.S_out + j0 + i] = p[u];
             }
         }
-        __syncthreads();
     }
 }
 
-// blockIdx.y: k, v, and the weights and positions (of one CTA's a head).
+// blockIdx.y: k, v, and the weights and positions; blockIdx.x: CTAs of a cluster, heads.
 __global__ void __launch_bounds__(kGatherThreads)
-gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
+gtms_evict_move_kernel(const EvictArgs a)
 {
     extern __shared__ __align__(16) uint4 raw[];   // kMoveStages x kMoveUnroll x threads
-    uint4* ring = raw;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int which = blockIdx.y;
-    const int64_t bh = blockIdx.x / slices;
-    const int32_t unit0 = static_cast<int32_t>(blockIdx.x % slices) * width;
+    const int64_t bh = blockIdx.x / ranks;
     const int32_t b = static_cast<int32_t>(bh / a.H), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * a.H);
     const int32_t n = a.length(b);
     await_last_launch();   // as above
-    if ((a.moved >> which & 1) || (which == 2 && unit0 > 0))
+    if (a.moved >> which & 1)
         return;
     const int32_t* kept = n > a.keep ? a.kept + bh * a.keep : nullptr;
     if (which == 2)
-        return move_labels(a, bh, kept, n < a.keep ? n : a.keep, reinterpret_cast<uint8_t*>(ring));
+        return move_labels(a, bh, kept, n < a.keep ? n : a.keep, rank, ranks);
     if (!kept)
         return;   // everything stands where it is to stand
     // The first entries that stay are where they belong: kept[j] - j never falls.
@@ -408,33 +410,38 @@ gtms_evict_move_kernel(const EvictArgs a, int32_t slices, int32_t width)
         else
             lo = mid + 1;
     }
-    const int32_t w = a.units - unit0 < width ? a.units - unit0 : width;
-    const int32_t rows = kGatherThreads * kMoveUnroll / w;   // of a step
-    const int32_t steps = (a.keep - lo + rows - 1) / rows;
-    uint4* base = a.in[which].row<uint4>(b, h, 0) + unit0;
+    const int32_t turn = kGatherThreads / a.units, row = threadIdx.x / a.units, rows = turn * kMoveUnroll;
+    const int32_t end = row < turn ? a.keep : 0;   // of this thread
+    const int32_t steps = (a.keep - lo + rows * ranks - 1) / (rows * ranks), first = lo + rank * rows + row;
+    uint4* base = a.in[which].row<uint4>(b, h, 0) + threadIdx.x % a.units;
     const int64_t ss = a.in[which].ss;
+    auto place = [&](int32_t s, int u) { return first + s * rows * ranks + u * turn; };
+    auto stage = [&](int32_t s, int u) { return raw + (s % kMoveStages * kMoveUnroll + u) * kGatherThreads + threadIdx.x; };
+    int32_t from[kMoveUnroll];   // of the step that `load` copies next
+    auto ask = [&](int32_t s) {
+#pragma unroll
+        for (int u = 0; u < kMoveUnroll; ++u)
+            from[u] = s < steps && place(s, u) < end ? kept[place(s, u)] : -1;
+    };
     auto load = [&](int32_t s) {
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int32_t i = u * kGatherThreads + threadIdx.x, r = i / w, j = lo + s * rows + r;
-            if (s < steps && r < rows && j < a.keep)
-                tc::cp_async16(tc::smem_u32(ring + (s % kMoveStages) * (kMoveUnroll * kGatherThreads) + i),
-                               base + kept[j] * ss + i % w, 16);
-        }
+        for (int u = 0; u < kMoveUnroll; ++u)
+            if (from[u] >= 0)
+                tc::cp_async16(tc::smem_u32(stage(s, u)), base + from[u] * ss, 16);
         tc::cp_async_commit();
+        ask(s + 1);
     };
+    ask(0);
     for (int32_t s = 0; s < kMoveStages - 1; ++s)
         load(s);
     for (int32_t s = 0; s < steps; ++s) {
-        load(s + kMoveStages - 1);   // the stage of step s - 1, whose thread this is for all of its units
+        load(s + kMoveStages - 1);   // the stage of step s - 1, which this thread alone reads and writes
         asm volatile("cp.async.wait_group %0;" :: "n"(kMoveStages - 1) : "memory");
-        __syncthreads();   // everyone's copies of step s have landed
+        cluster.sync();   // everyone's copies of step s have landed
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int32_t i = u * kGatherThreads + threadIdx.x, r = i / w, j = lo + s * rows + r;
-            if (r < rows && j < a.keep)
-                base[j * ss + i % w] = ring[(s % kMoveStages) * (kMoveUnroll * kGatherThreads) + i];
-        }
+        for (int u = 0; u < kMoveUnroll; ++u)
+            if (place(s, u) < end)
+                base[place(s, u) * ss] = *stage(s, u);
     }
 }
 
@@ -443,22 +450,23 @@ template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, unsigned ranks, bool beside, cudaStream_t st,
                    Args... args)
 {
-    cudaLaunchAttribute attr;
-    if (beside) {
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-    } else {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = ranks;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    }
+    cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = {};
+    if (beside) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (ranks > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = ranks;
+        attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = beside || ranks > 1;
+    cfg.attrs = attrs;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -510,14 +518,14 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t st)
             return e;
     }
     if (a.moved != 7) {
-        // Columns of a CTA: whole rows, or slices of 32 bytes at least until there are two CTAs to a multiprocessor.
-        int32_t width = a.units;
-        while (width > 2 && heads * 2 * ((a.units + width - 1) / width) < 2 * kChipSms)
-            width = (width + 1) / 2;
-        const int32_t slices = (a.units + width - 1) / width;
+        // CTAs of a cluster to a head's rows until there are two to a multiprocessor, each with rows for two steps at least.
+        const int64_t rows = kGatherThreads / a.units * kMoveUnroll;
+        unsigned ranks = 1;
+        while (ranks < kMoveCluster && heads * 2 * ranks < 2 * kChipSms && 4 * ranks * rows <= a.keep)
+            ranks *= 2;
         if ((e = allow_smem<gtms_evict_move_kernel>(kMoveBytes)) == cudaSuccess)
-            e = launch(gtms_evict_move_kernel, dim3(static_cast<unsigned>(heads * slices), 3), kGatherThreads, kMoveBytes, 1, true,
-                       st, a, slices, width);
+            e = launch(gtms_evict_move_kernel, dim3(static_cast<unsigned>(heads * ranks), 3), kGatherThreads, kMoveBytes, ranks, true,
+                       st, a);
     }
     return e;
 }

@@ -490,6 +490,11 @@ CUTS = [
     (2, 2, 64, 64, F16, (64, 10), 100, 20, 80, "bhsd", "spread", 14, 0),              # room for all
     (40, 8, 300, 128, BF16, tuple(range(20, 300, 7)), 150, 4, 32, "bhsd", "spread", 15, 0),
     (1, 8, 3000, 128, BF16, (3000,), 2999, 0, 0, "bhsd", "spread", 16, 0),            # one goes
+    (5, 10, 20000, 64, F16, (20000, 16400, 9000, 15000, 19999), 7000, 4, 64, "bhsd", "ties", 17, 0),   # two CTAs to a row
+    (2, 8, 33000, 64, BF16, (33000, 20001), 4096, 0, 0, "bshd", "spread", 18, 0),     # eight
+    (20, 4, 17000, 8, F32, tuple(range(7000, 17000, 500)), 5000, 1, 1, "bhsd", "ties", 19, 0),         # one, in shared memory
+    (1, 1, 140000, 16, F16, (140000,), 131000, 100, 7, "bhsd", "ties", 20, 0),        # a cluster, in shared memory
+    (40, 2, 41500, 8, F16, tuple(range(1500, 41500, 1000)), 30000, 5, 99, "bhsd", "spread", 21, 0),    # one, in memory
 ]
 
 
