@@ -343,9 +343,12 @@ gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 // Rows stay in their cache: entry j goes to row j, at or before where it stood, so a
 // (batch, head)'s rows go in order, in steps: all of a step have been read (the barrier)
 // before any is written, and later steps read only rows behind those that this one
-// writes. A cluster's CTAs share the rows of a step; several steps of copies are in flight
-// in shared memory, and the rows' numbers are read a step before them.
-constexpr int kMoveStages = 4, kMoveUnroll = 2, kMoveCluster = 8;
+// writes. A cluster's CTAs share the rows of a step; the copies of the steps that follow
+// are in flight in shared memory meanwhile, and their rows' numbers are read a step before.
+// The two calls above in place: 358 and 89 us (a CTA to a slice of every row's columns
+// instead: 698 and 224). A step of 32 KB a CTA, since the cluster's barrier takes a
+// microsecond of each: of 16 KB 369 and 113, of 8 KB 371 and 160; two stages 413 and 98.
+constexpr int kMoveStages = 3, kMoveUnroll = 8, kMoveCluster = 8;
 constexpr int kMoveBytes = kMoveStages * kMoveUnroll * kGatherThreads * 16;
 
 // Weights and positions in place, or one of them: all of a step have been read before
@@ -434,15 +437,19 @@ gtms_evict_move_kernel(const EvictArgs a)
     ask(0);
     for (int32_t s = 0; s < kMoveStages - 1; ++s)
         load(s);
+    asm volatile("cp.async.wait_group %0;" :: "n"(kMoveStages - 2) : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // copies of step 0 have landed
     for (int32_t s = 0; s < steps; ++s) {
         load(s + kMoveStages - 1);   // the stage of step s - 1, which this thread alone reads and writes
-        asm volatile("cp.async.wait_group %0;" :: "n"(kMoveStages - 1) : "memory");
-        cluster.sync();   // everyone's copies of step s have landed
+        asm volatile("cp.async.wait_group %0;" :: "n"(kMoveStages - 2) : "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // everyone's of step s
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this thread's of step s + 1
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
             if (place(s, u) < end)
                 base[place(s, u) * ss] = *stage(s, u);
     }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ranks: CTAs of a cluster; beside: may start while the last launch still runs (see await_last_launch).
