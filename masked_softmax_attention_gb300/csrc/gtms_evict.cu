@@ -11,8 +11,8 @@
 //   gather  (or move, in place) takes rows of k and v, weights and positions. What bounds
 //           the call: the kept rows are read once and written once (a weight is 4 of its
 //           4 + 4 D bytes).
-// 32 x 8 heads, half of 16384 rows of 256 bytes: 347 us, 6.2 TB/s, of which the selection
-// takes some 20. One sequence, 8 heads, a quarter of 131072: 64 us, of them 19 (64 CTAs; a
+// 32 x 8 heads, half of 16384 rows of 256 bytes: 344 us, 6.3 TB/s, of which the selection
+// takes some 20. One sequence, 8 heads, a quarter of 131072: 63 us, of them 18 (64 CTAs; a
 // cluster's sums of 2048 bins, two barriers each, come to 2.7 us of each histogram).
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -44,7 +44,7 @@ struct SelectShared {
     __align__(16) uint32_t theirs[kBins];           // the ranks' counts of the bins that this one sums
     uint32_t sums[kBins / 2], groups[kBins / 64];   // their sums, and those of 32 bins
     uint32_t warp_sum[kSelectWarps];
-    uint32_t digit, above;                    // found: the digit, entries above it
+    uint32_t digit, above, in;                // found: the digit, entries above it, entries of it
     uint32_t gt[kSelectWarps], eq[kSelectWarps];
     uint32_t cta_gt, cta_eq;
 };
@@ -103,7 +103,7 @@ gtms_evict_select_kernel(const EvictArgs a)
     const int32_t w0 = warp * part < count ? warp * part : count, w1 = w0 + part < count ? w0 + part : count;
     uint32_t held[WHERE == Keys::held ? kSelectKeys : 1];
     // f(first entry of 32, this lane's key) in the order of the warp's entries; the key behind the last is 0, which is no
-    // weight's.
+    // weight's and counts in a bin that none of them has.
     auto in_order = [&](auto&& f) {
         if constexpr (WHERE == Keys::held) {
 #pragma unroll
@@ -149,12 +149,13 @@ gtms_evict_select_kernel(const EvictArgs a)
     }
 
     uint32_t prefix = 0, mask = 0;
+    bool tied = false;   // some of those that equal the last that stays go
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t digits = pass < 2 ? kBins - 1u : kBins / 2 - 1u;
         any_order([&](uint32_t k) {
-            if ((k & mask) == prefix && k != 0)
+            if ((k & mask) == prefix)
                 atomicAdd(&sh.hist[(k >> shift) & digits][lane % kCopies], 1u);   // counts: their order does not matter
         });
         __syncthreads();
@@ -181,6 +182,7 @@ gtms_evict_select_kernel(const EvictArgs a)
                 const bool first = need <= above + high;
                 sh.digit = first ? bin + 1 : bin;
                 sh.above = first ? above : above + high;
+                sh.in = first ? high : low;
             }
         } else {
             // A rank sums kBins / ranks bins over the cluster: every rank hands it its counts (all ranks reading all bins of
@@ -228,6 +230,7 @@ gtms_evict_select_kernel(const EvictArgs a)
                 if (lane == __ffs(__ballot_sync(0xffffffffu, need <= above + up)) - 1) {
                     sh.digit = mine_bin;
                     sh.above = above + up - c;
+                    sh.in = c;
                 }
             }
         }
@@ -235,6 +238,7 @@ gtms_evict_select_kernel(const EvictArgs a)
         prefix |= sh.digit << shift;
         mask |= digits << shift;
         need -= sh.above;
+        tied = sh.in > need;
     }
     // Those above `prefix` stay, and the first `need` that equal it.
 
@@ -271,6 +275,16 @@ gtms_evict_select_kernel(const EvictArgs a)
     }
     int32_t* to = kept + a.first;
     const uint32_t below = (1u << lane) - 1u;
+    if (!tied) {   // no count of those that equal it (2 % of both times above)
+        const uint32_t at_least = prefix - 1;
+        uint32_t before = gt + (eq < need ? eq : need);
+        in_order([&](int32_t i, uint32_t k) {   // the whole warp
+            const uint32_t g = __ballot_sync(0xffffffffu, k > at_least);
+            if (k > at_least)
+                to[before + __popc(g & below)] = from + i + lane;
+            before += __popc(g);
+        });
+    } else {
     in_order([&](int32_t i, uint32_t k) {   // the whole warp
         const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix);
         const uint32_t eq_before = eq + __popc(e & below);
@@ -279,6 +293,7 @@ gtms_evict_select_kernel(const EvictArgs a)
         gt += __popc(g);
         eq += __popc(e);
     });
+    }
     if (ranks > 1)
         cluster.sync();   // the others may still be reading this CTA's counts
 }
