@@ -126,7 +126,7 @@ struct FwdItem {
 // Where the kernel finds its keys and rows: in one cache (this), or as the two forms
 // for a batch that shares prefixes say (gtms_shared_prefix.cuh).
 struct OneCache {
-    static constexpr bool prefixed = false, packed = false;
+    static constexpr bool prefixed = false, packed = false, fine = false;
     template <int W>
     using Item = FwdItem<W>;
     template <int W>
@@ -324,6 +324,12 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                             tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * kTile + ks * 8,
                                                 tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, !first || ks > 0);
                     }
+                    if constexpr (Source::fine) {   // what the rounding of P has left
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc::mma_f16_ts_warp(tmem + TL::t_o + w * D, tmem + w * kTile + kTile / 2 + ks * 8,
+                                                tc::smem_desc_sw128_mn(v0 + ks * 2048, TL::box), idesc_o, true);
+                    }
                     np ^= 1u << w;
                     if (t == it.lo[w]) {
                         tc::commit_warp(&sh.ofull[w]);
@@ -483,7 +489,7 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 // 32 probabilities from column k on: exp2(c s - c m), summed in fp32, and rounded to 16 bits, the type of
                 // V, with which alone the tensor cores multiply them at full rate (o is off by 1.3 to 1.5 roundings of its
-                // own type instead of 1).
+                // own type instead of 1; a `fine` source's P is two numbers, the second what the first's rounding left).
                 auto exponentiate = [&](int k, float shift, uint32_t(&r)[16]) {
                     const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
 #pragma unroll
@@ -492,6 +498,11 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                         e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                         sum[j & 1] = __fadd2_rn(sum[j & 1], e);
                         r[j] = pack2<T>(e.x, e.y);
+                        if constexpr (Source::fine) {
+                            const float2 h = unpack2<T>(r[j]);
+                            s[k + 2 * j] = e.x - h.x;   // these scores have been used
+                            s[k + 2 * j + 1] = e.y - h.y;
+                        }
                     }
                 };
                 const bool opening = t == hi - 1;   // nothing to rescale yet
@@ -534,6 +545,15 @@ gtms_attention_fwd_kernel(const __grid_constant__ HeadsMap mq, const __grid_cons
                 tc::tmem_st16(ts + 32, r0);
                 exponentiate(96, shift, r1);
                 tc::tmem_st16(ts + 48, r1);
+                if constexpr (Source::fine) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 2; k += 16) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            r0[j] = pack2<T>(s[2 * (k + j)], s[2 * (k + j) + 1]);
+                        tc::tmem_st16(ts + kTile / 2 + k, r0);
+                    }
+                }
                 hand_over(&sh.pready[w][TL::parts - 1]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }

@@ -325,6 +325,14 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v)
+{
+    if constexpr (std::is_same_v<T, __half>)
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    else
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
 
 // Long sums. The tensor cores' fp32 accumulators cut off what does not fit instead of
 // rounding it, so that every product of 16 terms can lose a unit in the last place, toward

@@ -29,8 +29,9 @@
 namespace gtms {
 
 // Tiles [0, prefix_tiles) of an item are the prefix's, those behind them its own.
+template <bool FINE>
 struct PrefixedCache {
-    static constexpr bool prefixed = true, packed = false;
+    static constexpr bool prefixed = true, packed = false, fine = FINE;
     HeadsMap mk, mv;
     PrefixArgs p;
 
@@ -396,7 +397,7 @@ gtms_attention_parts_kernel(const AttentionArgs a, const PrefixParts in, int32_t
 // Work items (prefix, head, rows, part of the keys) of the packed rows. The kernel's
 // AttentionArgs are those of one batch of G over the prefixes, Sq its packed rows.
 struct PrefixRows {
-    static constexpr bool prefixed = false, packed = true;
+    static constexpr bool prefixed = false, packed = true, fine = false;
     HeadsRef q;
     PrefixArgs p;
     PrefixParts out;
@@ -454,6 +455,14 @@ struct PrefixRows {
     }
 };
 
+// Calls of few items and keys, which take less of the chip's time than of the host's (22 us):
+// with P as two numbers o is as near as its own rounding. One rounding of P makes the
+// error of many rows 1.4 times that, but of one or two rows, whose outputs share it, 1.1 to
+// 1.8 times (2 sequences, 2 heads of 64, 36 keys). It costs 3 of 11 us on the device (4
+// sequences, 16 / 4 heads of 64, 500 keys in the prefix), so where rows are more they have
+// the one.
+constexpr int64_t kFineItems = 32, kFineKeys = 1024;
+
 template <typename T, int D>
 cudaError_t launch_prefixed_whole(const AttentionArgs& a, const PrefixArgs& p, cudaStream_t st, uint64_t wait_ns = kAttnWaitNs)
 {
@@ -462,28 +471,31 @@ cudaError_t launch_prefixed_whole(const AttentionArgs& a, const PrefixArgs& p, c
         return cudaErrorUnknown;
     // Without keys no tile is loaded, and q stands in for k and v in the maps.
     const bool keys = a.Skv > 0, shared = p.P > 0;
-    HeadsMap mq, mk, mv;
-    PrefixedCache source;
-    source.p = p;
+    HeadsMap mq, mk, mv, mkp, mvp;
     if (!encode_heads<T>(mq, a.q, a.B, a.Hq, a.Sq, D, kTile) ||
         !encode_heads<T>(mk, keys ? a.k : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
         !encode_heads<T>(mv, keys ? a.v : a.q, a.B, a.Hkv, keys ? a.Skv : 1, D, kTile) ||
-        !encode_heads<T>(source.mk, shared ? p.k : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile) ||
-        !encode_heads<T>(source.mv, shared ? p.v : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile))
+        !encode_heads<T>(mkp, shared ? p.k : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile) ||
+        !encode_heads<T>(mvp, shared ? p.v : a.q, p.G, a.Hkv, shared ? p.P : 1, D, kTile))
         return cudaErrorInvalidValue;
     const int32_t blocks = (a.Sq + TL::rows - 1) / TL::rows;
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hq;
-    auto launch = [&](auto is_long) {
-        constexpr auto* kern = gtms_attention_fwd_kernel<T, D, is_long(), PrefixedCache>;
+    auto launch = [&](auto is_long, auto fine) {
+        constexpr auto* kern = gtms_attention_fwd_kernel<T, D, is_long(), PrefixedCache<fine()>>;
         constexpr int smem = static_cast<int>(TL::smem);
         const cudaError_t e = allow_smem<kern>(smem);
         return e != cudaSuccess ? e
                                 : launch_kernel(kern, static_cast<unsigned>(heads * blocks), TL::threads, smem, st, mq, mk, mv, a,
-                                                static_cast<uint32_t>(heads), blocks, wait_ns, source);
+                                                static_cast<uint32_t>(heads), blocks, wait_ns,
+                                                PrefixedCache<fine()>{mkp, mvp, p});
     };
     // A tile counts as whole even where the prefix ends inside it.
     const int64_t most = static_cast<int64_t>(p.P) + kTile + a.Skv;
-    return most > kCarryTerms<T> ? launch(std::true_type()) : launch(std::false_type());
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if (heads * blocks <= kFineItems && most <= kFineKeys)
+        return launch(no, yes);
+    return most > kCarryTerms<T> ? launch(yes, no) : launch(no, no);
 }
 
 // How a call's packed rows are dealt out: tiles of rows, parts of the keys; and the

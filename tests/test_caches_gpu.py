@@ -171,6 +171,22 @@ def test_shared_prefix_is_attention_over_the_keys_end_to_end(dev, case):
     _close("lse", lse[live], lse2[live].double(), 2 * tol_lse[live])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P,Skv", [(1, 1), (2, 3), (129, 1), (100, 140)])
+def test_shared_prefix_rounds_few_rows_once(dev, d, dtype, P, Skv):
+    """Of few rows and keys o is its own rounding: beside half a step of o, (eps / 2)^2 of P's second rounding, below
+    2^-16, scores off by at most 2^-16 (d terms of below 8 each, summed to 2^-23 of them, times d^-1/2), exponentials by
+    2^-21 and sums of up to 256 terms by 2^-18, together below 2^-14 of sum p |v|. One rounding of P: eps / 2."""
+    c = Shared(4, 2, 4, 2, 1, P, Skv, d, dtype, None, (Skv,), "last")
+    o, _ = c.run()
+    want, size = (joined(c.q, c.kp, vp, c.k, v, c.lens, c.scale, c.plens, c.mask, c.off)[0].double()
+                  for vp, v in ((c.vp, c.v), (c.vp.abs(), c.v.abs())))
+    half = torch.finfo(dtype).eps / 2
+    bound = half * (want.abs() + 2.0 ** -14 * size) + 2.0 ** -14 * size + (2.0 ** -25 if dtype is F16 else 0.0)
+    assert bool(((o.double() - want).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("P,Skv,Sq", [(0, 0, 1), (300, 0, 1), (5000, 0, 3), (0, 40, 1), (0, 200, 200), (300, 20, 0)])
 def test_shared_prefix_without_keys_or_rows(dev, P, Skv, Sq):
     """Without own keys no row is live, whatever the prefix; without a prefix it is attention over the own keys."""
