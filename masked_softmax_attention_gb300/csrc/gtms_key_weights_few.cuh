@@ -163,12 +163,12 @@ gtms_key_weights_few_kernel(const KeyWeightsArgs kw, int32_t chunks, int32_t chu
         }
     }
     __syncthreads();
-    for (int32_t c = k0 + threadIdx.x; c < end; c += kFewThreads) {
-        const float w = c < k1 ? sh.sum[c - k0] : 0.0f;
-        if (kw.accumulate)
-            out[c] += w;
-        else
-            out[c] = w;
+    if (kw.accumulate) {   // what stands behind the length is not this call's: another stream may be writing there
+        for (int32_t c = k0 + threadIdx.x; c < k1; c += kFewThreads)
+            out[c] += sh.sum[c - k0];
+    } else {
+        for (int32_t c = k0 + threadIdx.x; c < end; c += kFewThreads)
+            out[c] = c < k1 ? sh.sum[c - k0] : 0.0f;
     }
 }
 

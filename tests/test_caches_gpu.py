@@ -329,6 +329,18 @@ def test_key_weights_accumulate(dev, case):
 
 
 @pytest.mark.parametrize("case", KEYS, ids=str)
+def test_key_weights_accumulate_leaves_places_behind_the_length(dev, case):
+    """Bit for bit: a zero keeps its sign and a NaN its payload."""
+    c = Weights(*case)
+    bits = torch.tensor([-(1 << 31), 0x7fc01234, 0x7f801234, 1], dtype=torch.int32, device="cuda")   # -0, NaNs, the least number
+    at = torch.arange(c.before.shape[2], device="cuda")
+    behind = at >= c.lens.clamp(min=0)[:, None, None]
+    before = torch.where(behind, bits[at % 4], c.before.view(torch.int32))
+    w = c.run(out=before.clone().view(torch.float32), accumulate=True)
+    assert torch.equal(w.view(torch.int32)[behind.expand_as(w)], before[behind.expand_as(w)])
+
+
+@pytest.mark.parametrize("case", KEYS, ids=str)
 def test_key_weights_masked_places_may_hold_anything(dev, case):
     c = Weights(*case)
     want = c.run()
