@@ -18,6 +18,7 @@ bool mapped(const AttentionArgs& a)
 
 }  // namespace
 
+// By the shape alone, which does not say how q's heads stand: where they are broadcast the workspace is not used.
 uint64_t key_weights_workspace_bytes(const AttentionArgs& a)
 {
     const int32_t parts = few(a) ? 1 : key_plan(a).parts;

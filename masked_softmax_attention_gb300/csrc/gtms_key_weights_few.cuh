@@ -26,13 +26,17 @@ namespace gtms {
 
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kFewChunk = 1024;   // keys of a CTA at most
+// Where q's heads are broadcast rows are many, and sums long: of a power of two of row tiles at a time, and of those, so
+// that a key's sum is off by half a step for each of 128 and of 1 / 128 of its tiles at most (2^21 rows: 2^-14 of it).
+// One after the other those were 2^-11.6.
+constexpr int64_t kFewTiles = 128;
 
 template <int D, int NT>
 struct FewShared {
     uint4 q[8 * NT][D / 8 + 1];                 // + 1: rows start in different banks
     float shift[8 * NT];                        // -lse in base 2; -infinity for rows that do not count
     int32_t lo[8 * NT], hi[8 * NT];             // keys that a row keeps
-    float sum[kFewChunk];
+    float sum[kFewChunk], total[kFewChunk];     // of the last tiles; of those before
 };
 
 template <typename T, int D, int NT>
@@ -68,7 +72,7 @@ gtms_key_weights_few_kernel(const KeyWeightsArgs kw, int32_t chunks, int32_t chu
         return;
     }
     for (int32_t c = threadIdx.x; c < chunk; c += kFewThreads)
-        sh.sum[c] = 0.0f;
+        sh.sum[c] = sh.total[c] = 0.0f;
 
     const float c2 = a.scale * kLog2e;
     const T* kbase = a.k.row<T>(b, hk, 0) + 8 * t;
@@ -107,6 +111,7 @@ gtms_key_weights_few_kernel(const KeyWeightsArgs kw, int32_t chunks, int32_t chu
         f0 = __reduce_max_sync(0xffffffffu, f0);
         f1 = __reduce_min_sync(0xffffffffu, f1);
 
+        const bool carry = r0 / R % kFewTiles == kFewTiles - 1;
         uint4 kr[2][D / 32];
         auto load = [&](int32_t key0) {
 #pragma unroll
@@ -157,18 +162,22 @@ gtms_key_weights_few_kernel(const KeyWeightsArgs kw, int32_t chunks, int32_t chu
                 sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
                 sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
                 const int32_t key = key0 + g + 8 * k;
-                if (t == 0 && key < k1)
-                    sh.sum[key - k0] += sum[k];   // this warp's keys alone
+                if (t == 0 && key < k1) {   // this warp's keys alone
+                    const float so_far = sh.sum[key - k0] + sum[k];
+                    sh.sum[key - k0] = carry ? 0.0f : so_far;
+                    if (carry)
+                        sh.total[key - k0] += so_far;
+                }
             }
         }
     }
     __syncthreads();
     if (kw.accumulate) {   // what stands behind the length is not this call's: another stream may be writing there
         for (int32_t c = k0 + threadIdx.x; c < k1; c += kFewThreads)
-            out[c] += sh.sum[c - k0];
+            out[c] += sh.total[c - k0] + sh.sum[c - k0];
     } else {
         for (int32_t c = k0 + threadIdx.x; c < end; c += kFewThreads)
-            out[c] = c < k1 ? sh.sum[c - k0] : 0.0f;
+            out[c] = c < k1 ? sh.total[c - k0] + sh.sum[c - k0] : 0.0f;
     }
 }
 

@@ -428,6 +428,50 @@ def test_key_weights_streams_and_graphs(dev, case):
     assert torch.equal(w, want[1])
 
 
+class Broadcast(Weights):
+    """q with a batch or head stride of 0."""
+
+    def __init__(self, case, batch, heads):
+        super().__init__(*case)
+        q = self.q[:1] if batch else self.q
+        self.q = (q[:, :1] if heads else q).expand(self.q.shape)
+        self.lse = gtms.attention_forward(self.q, self.k, self.k, self.lens, self.scale, mask_kind=self.mask,
+                                          window=self.window, q_offsets=self.off)[1]
+
+
+@pytest.mark.parametrize("batch,heads", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("case", [KEYS[i] for i in (3, 4, 7, 8, 10, 13, 18, 19, 20, 21, 23)], ids=str)
+def test_key_weights_of_broadcast_rows(dev, case, batch, heads):
+    """One q for all batches or heads, of few rows and of many, and added to what stands there."""
+    c = Broadcast(case, batch, heads)
+    assert (c.q.stride(0) == 0 or c.q.shape[0] == 1 or not batch) and (c.q.stride(1) == 0 or c.q.shape[1] == 1 or not heads)
+    w = c.run()
+    c.check(w)
+    assert torch.equal(c.run(), w)
+    c.check(c.run(out=c.before.clone(), accumulate=True), c.before)
+    if not heads:
+        c.q = c.q.contiguous()
+        assert torch.equal(c.run(), w), "the bits of rows of their own"
+
+
+def test_key_weights_of_broadcast_heads_sum_two_million_rows(dev):
+    """128 heads that share one q of zeros, 16384 rows: each of a key's 2^21 terms is p = exp(-lse), the same number, which
+    a call of one row gives. Added up one after the other, 32 rows at a time, 32 p = 22.05 is rounded to a multiple of 1/8
+    from 2^20 on, by 0.2 % of what it adds. In two steps a sum passes through 7 additions of a tile, those of 128 tiles and
+    those of 512 such sums, each off by half a step at most: 647 2^-24 < 2^-14 of it."""
+    rows, heads = 1 << 14, 128
+    q = torch.zeros(1, 1, rows, 64, dtype=BF16, device="cuda").expand(1, heads, rows, 64)
+    k = torch.randn(1, 1, rows, 64, dtype=F32, device="cuda").to(BF16)
+    lse = torch.full((1, heads, rows), -math.log(22.05 / 32), device="cuda")
+    lens = _int32((rows,))
+    w = gtms.attention_key_weights(q, k, lse, lens, 1.0, mask_kind=LENGTH)
+    one = gtms.attention_key_weights(q[:, :1, :1].contiguous(), k, lse[:, :1, :1].contiguous(), lens, 1.0, mask_kind=LENGTH)
+    p = one[0, 0, 0].double()
+    assert abs(float(p) - 22.05 / 32) < 2.0 ** -20 and bool((one == one[0, 0, 0]).all())
+    off = (w.double() / (p * rows * heads) - 1).abs().max()
+    assert float(off) <= 2.0 ** -14, float(off)
+
+
 def test_key_weights_beyond_32_bit_offsets(dev):
     """Keys whose elements stand more than 2^32 elements into the cache."""
     B, H, S, d = 1, 2, 1 << 14, 128
