@@ -372,7 +372,8 @@ int gtms_attention_shared_prefix_workspace(const gtms_attention_shape* shape, in
  *               -infinity adds nothing.
  *   weights     fp32 [B, Hkv, Skv], contiguous: w, and +0.0 where no row keeps the key; with
  *               `accumulate` not 0 w is added to what stands there, and keys at c >= L
- *               are left alone.
+ *               are left alone: the caller sets the weights of keys that are new since
+ *               the last call (to 0), where after an eviction older ones' may stand.
  *   workspace   as in gtms_attention_shared_prefix, of the bytes that
  *               gtms_attention_key_weights_workspace gives.
  *   status      as in gtms_attention_forward.
@@ -413,8 +414,10 @@ typedef struct {
  *   lens_out       int32 [B]: min(n, keep).
  * weights, positions and their outputs are contiguous. Rows at and behind lens_out are
  * left as they were. An output may be its input itself (same data and strides, S_out == S):
- * it is then compacted in place. What a row of attention keeps afterwards goes by the
- * places in the cache: new tokens follow at lens_out.
+ * it is then compacted in place, and weights and positions of entries that have gone or
+ * moved still stand behind lens_out. What a row of attention keeps afterwards goes by the
+ * places in the cache: new tokens follow at lens_out, and whoever puts them there sets
+ * their weights (to 0, before gtms_attention_key_weights adds to them) and positions.
  *   workspace      as in gtms_attention_shared_prefix, of the bytes that
  *                  gtms_cache_evict_workspace gives.
  * dtype GTMS_F32, GTMS_BF16 or GTMS_F16; rows of whole 16-byte units, head_dim up to 1024; data and

@@ -777,7 +777,8 @@ def attention_key_weights(q, k, lse, seq_lens, scale: float = 1.0, out=None, acc
     (or ``attention_shared_prefix``) returned for these rows.
 
     ``out``, a contiguous fp32 tensor, receives the weights; with ``accumulate`` they are added to what stands there,
-    and entries at and behind ``seq_lens`` stay. The same inputs give the same bits. ``q``, ``k`` and the options as in
+    and entries at and behind ``seq_lens`` stay: set those of new keys to 0 first, since after an eviction an older key's
+    may stand in their place. The same inputs give the same bits. ``q``, ``k`` and the options as in
     ``attention_forward``."""
     import torch
 
@@ -806,7 +807,9 @@ def cache_evict(k, v, weights, seq_lens, keep: int, first: int = 0, recent: int 
     of min(keep, S) or more rows to write to, whose rows behind the new lengths are left as they are; ``(k, v, weights,
     positions)`` themselves compact the cache in place, and None in the last place leaves positions out. Without it
     new ones of min(keep, S) rows are made, zero behind the new lengths. New tokens follow at ``lens``, for which
-    ``attention_forward`` takes ``seq_lens`` and ``q_offsets``: rows go by places in the cache."""
+    ``attention_forward`` takes ``seq_lens`` and ``q_offsets``: rows go by places in the cache. Their weights (0, for
+    ``attention_key_weights`` to add to) and positions are the caller's to set: compacted in place, the cache still has
+    older entries' there."""
     import torch
 
     dtype, dev = k.dtype, k.get_device()

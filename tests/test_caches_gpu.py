@@ -1,5 +1,7 @@
 """Attention over shared prefixes, key weights and cache eviction against their definitions (caches_reference.py)."""
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -696,3 +698,52 @@ def test_samples_of_a_prompt_with_caches_that_are_cut(dev, d, dtype):
         w, tol = key_weights(q, k, lse, kept(lens, new, room, TRIL, 0, off), scale)
         _close("weights", weights, before.double() + w, tol + 2.0 ** -24 * (before.double() + w))
     assert cuts >= 1
+
+
+def test_readme_serving_loop(dev):
+    """The loop that README.md shows, run as it stands for two cuts."""
+    text = open(os.path.join(os.path.dirname(gtms.__file__), "..", "README.md")).read()
+    step = next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "cache_evict" in b)
+    prompts, n, Hq, Hkv, P, d, limit, keep, dtype = 2, 3, 4, 2, 50, 64, 96, 80, BF16
+    B, gen, scale = prompts * n, torch.Generator(device="cuda").manual_seed(9), d ** -0.5
+    start = torch.tensor((80, 3, 41, 79, 80, 1), device="cuda", dtype=torch.int32)
+    k_prompt, v_prompt = (_heads(gen, prompts, Hkv, P, d, dtype, "bhsd") for _ in range(2))
+    k, v = (_heads(gen, B, Hkv, limit, d, dtype, "bhsd") for _ in range(2))
+    weights = torch.zeros(B, Hkv, limit, device="cuda")
+    positions = torch.arange(limit, device="cuda", dtype=torch.int32).expand(B, Hkv, limit).contiguous()
+    names = dict(k_prompt=k_prompt, v_prompt=v_prompt, k=k, v=v, weights=weights, positions=positions, scale=scale, limit=limit,
+                 keep=keep, lens=start.clone(), steps_since_last_cut=0, rows=torch.arange(B, device="cuda"))
+    total = torch.zeros(B, Hkv, 256, dtype=torch.float64, device="cuda")   # by position
+    bound = torch.zeros_like(total)
+    stood = positions.clone()
+    rows, cuts = torch.arange(B, device="cuda"), 0
+    for t in range(40):
+        names["lens"] = names["lens"] + 1
+        names["steps_since_last_cut"] += 1
+        names["token"] = start + t               # the new token's position
+        slot = (names["lens"] - 1).long()
+        k[rows, :, slot], v[rows, :, slot] = (_heads(gen, B, Hkv, 1, d, dtype, "bhsd")[:, :, 0] for _ in range(2))
+        stood[rows, :, slot] = names["token"][:, None]
+        names["q"] = q = _heads(gen, B, Hq, 1, d, dtype, "bhsd")
+        lens, keys = names["lens"], k.clone()
+        exec(step, names)
+        w, tol = key_weights(q, keys, names["lse"], kept(lens, 1, limit, TRIL, 0, lens - 1), scale)
+        at = stood.long()
+        live = torch.arange(limit, device="cuda") < lens[:, None, None]
+        total.scatter_add_(2, torch.where(live, at, 255), torch.where(live, w, 0.0))
+        bound.scatter_add_(2, torch.where(live, at, 255), torch.where(live, tol, 0.0))
+        bound += 2.0 ** -24 * total
+        if names["lens"] is not lens:
+            assert names["lens"].tolist() == [min(x, keep) for x in lens.tolist()]
+            names["steps_since_last_cut"] = 0
+            cuts += 1
+            live = torch.arange(limit, device="cuda") < names["lens"][:, None, None]
+            at = positions.long()
+            stood = torch.where(live, positions, stood)
+        live = live.expand_as(weights)
+        at = torch.where(live, at, 255)
+        _close("weights", weights[live], total.gather(2, at)[live], bound.gather(2, at)[live])
+        assert torch.equal(positions[live], stood[live])
+        assert bool((positions[rows, :, (names["lens"] - 1).long()] == names["token"][:, None]).all())
+        assert bool(((positions[:, :, 1:] > positions[:, :, :-1]) | ~live[:, :, 1:]).all())
+    assert cuts == 2
