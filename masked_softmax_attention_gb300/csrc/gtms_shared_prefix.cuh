@@ -455,12 +455,15 @@ struct PrefixRows {
     }
 };
 
-// Calls of few items and keys, which take less of the chip's time than of the host's (22 us):
-// with P as two numbers o is as near as its own rounding. One rounding of P makes the
-// error of many rows 1.4 times that, but of one or two rows, whose outputs share it, 1.1 to
-// 1.8 times (2 sequences, 2 heads of 64, 36 keys). It costs 3 of 11 us on the device (4
-// sequences, 16 / 4 heads of 64, 500 keys in the prefix), so where rows are more they have
-// the one.
+// Calls of few items and keys have P as two numbers, so that o is its own rounding. One
+// rounding of P, the forward kernel's, adds an error of that size, 1.4 times it together;
+// but a row's outputs share P's errors, so that over few rows of few keys the figure
+// scatters (12 draws each): one row of 36 keys 1.1 to 1.9, 4 rows 1.2 to 1.5, 32 rows 1.24 to
+// 1.41. More than 32 items are more rows, more keys even it out within a row (36 rows of 564
+// keys 1.34 to 1.45, 4 rows of 2064, packed, 1.25 to 1.46), and those have the one rounding.
+// The price of the other (32 rows on the device; through the call 22 to 24 us either way): 36
+// keys of head dim 64 7.1 -> 8.3 us, 564 10.3 -> 13.1, of 128 11.8 -> 15.7, 864 15.3 -> 21.5; 2 sequences
+// of 16 heads and 128 rows, 32 items too, 11.7 -> 15.2. fp16 spills 184 and 160 bytes there.
 constexpr int64_t kFineItems = 32, kFineKeys = 1024;
 
 template <typename T, int D>

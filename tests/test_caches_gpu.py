@@ -189,6 +189,38 @@ def test_shared_prefix_rounds_few_rows_once(dev, d, dtype, P, Skv):
     assert bool(((o.double() - want).abs() <= bound).all())
 
 
+# G, n, Hq, Hkv, Sq, P, Skv ("tile": the rows of an item); whether P is two numbers
+SMALL = [
+    (4, 2, 4, 2, 1, 100, 140, True),            # 32 items
+    (1, 11, 3, 1, 1, 100, 140, False),          # 33
+    (1, 4, 8, 2, 1, 800, 96, True),             # 896 keys
+    (1, 4, 8, 2, 1, 801, 96, False),            # 897
+    (1, 2, 16, 4, "tile", 300, 300, True),      # 32 items of all their rows
+    (1, 2, 16, 4, "tile + 1", 300, 300, False),
+    (1, 1, 8, 2, 1, 57, 829, False),            # 886 keys, but packed at head dim 128
+    (1, 4, 2, 1, 1, 3000, 64, False),           # packed
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", SMALL, ids=str)
+def test_shared_prefix_roundings_on_both_sides_of_their_rule(dev, case, d, dtype):
+    """All within the bounds of P's one rounding; where P is two numbers within that of the last test: up to 160 products of
+    16 terms cut 2^-23 each, 2^-15.7 in all, sums pass through 43 additions, and scores count twice, in a row's sum too: 2^-14."""
+    G, n, Hq, Hkv, Sq, P, Skv, two = case
+    Sq = {"tile": 2 * d, "tile + 1": 2 * d + 1}.get(Sq, Sq)
+    c = Shared(G, n, Hq, Hkv, Sq, P, Skv, d, dtype, None, (Skv,), "last")
+    o, lse = c.run()
+    c.check(o, lse)
+    if two:
+        want, size = (joined(c.q, c.kp, vp, c.k, v, c.lens, c.scale, c.plens, c.mask, c.off)[0].double()
+                      for vp, v in ((c.vp, c.v), (c.vp.abs(), c.v.abs())))
+        half = torch.finfo(dtype).eps / 2
+        bound = half * (want.abs() + 2.0 ** -14 * size) + 2.0 ** -14 * size + (2.0 ** -25 if dtype is F16 else 0.0)
+        assert bool(((o.double() - want).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("P,Skv,Sq", [(0, 0, 1), (300, 0, 1), (5000, 0, 3), (0, 40, 1), (0, 200, 200), (300, 20, 0)])
 def test_shared_prefix_without_keys_or_rows(dev, P, Skv, Sq):
     """Without own keys no row is live, whatever the prefix; without a prefix it is attention over the own keys."""
