@@ -109,6 +109,20 @@ def test_late_warps_change_no_rows_over_prefixes(probe, d, late):
     Run(PACKED, 80, 16, 2, 1, 40, d, tuple(range(40)) * 2, G=2, P=5000).check(probe, late_warps=bits, late_ns=20_000)
 
 
+# As above; a CTA's two tiles, where one holds all rows, on alternate tiles of keys, of which an item has 5 (one tile three
+# of them, the other two) or 9; and P as two numbers, over 5 tiles of a prefix and 2 of a sequence's own keys.
+@pytest.mark.parametrize("late", ["mma", "load", "deal", "first softmax", "last softmax", "mma and load", "one tile", "the other"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_late_warps_change_no_small_calls_over_prefixes(probe, d, late):
+    n = 8 if d == 128 else 4
+    bits = {"mma": 1 << n, "load": 2 << n, "deal": 4 << n, "first softmax": 1, "last softmax": 1 << (n - 1),
+            "mma and load": 3 << n, "one tile": 0x0f, "the other": 0xf0 if d == 128 else 0x01}[late]
+    Run(PACKED, 16, 8, 2, 1, 40, d, tuple(range(25, 41)), G=2, P=5000).check(probe, late_warps=bits, late_ns=20_000)
+    Run(PACKED, 32, 16, 8, 1, 40, d, tuple(range(9, 41)), G=4, P=3300).check(probe, late_warps=bits, late_ns=20_000)
+    Run(WHOLE, 4, 4, 2, 1, 200, d, (200, 0, 129, 7), G=2, P=600).check(probe, late_warps=bits, late_ns=20_000)
+    Run(WHOLE, 4, 4, 2, 100, 200, d, (200, 0, 129, 7), G=2, P=600).check(probe, late_warps=bits, late_ns=20_000)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_items_may_outlast_the_limit_of_a_wait(probe, d):
     """The limit is that of a hand-off inside a tile (1 to 2 us of work), however many tiles an item has: here it is 120 us,
