@@ -703,7 +703,8 @@ def attention_backward(q, k, v, o, lse, dout, seq_lens, scale: float = 1.0, out=
 
 
 # ---------------------------------------------------------------------------
-# Caches: prefixes that a batch shares, the weight that keys received, eviction.
+# Caches: prefixes that a batch shares, the weight that keys received, eviction. Calls of serving: none of them is
+# differentiable.
 # ---------------------------------------------------------------------------
 
 _pack_evict = struct.Struct("@8qi4x").pack          # gtms_evict_shape
@@ -746,7 +747,8 @@ def attention_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens, scale: float 
     ``k_prefix`` / ``v_prefix`` [G, Hkv, P, d]: of the batch of B = G n sequences, sequence b has prefix b // n, of
     which the first ``prefix_lens[b // n]`` keys (int32 [G]; all without it) are seen by each of its live rows.
     ``seq_lens`` and ``q_offsets`` count the sequences' own keys ``k`` / ``v`` [B, Hkv, Skv, d]. Masks: grouped tril or
-    length. Everything else as in ``attention_forward``."""
+    length. Everything else as in ``attention_forward``; like its, the results carry no gradient, whatever the inputs
+    ask for (``attention`` over the keys put end to end has one)."""
     import torch
 
     dtype, dev = q.dtype, q.get_device()

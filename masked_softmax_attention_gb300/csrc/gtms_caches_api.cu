@@ -239,9 +239,10 @@ int check_evict_shape(const gtms_evict_shape* p, int64_t* keep)
     if ((p->dtype != GTMS_F32 && p->dtype != GTMS_BF16 && p->dtype != GTMS_F16) || p->head_dim > 1024 ||
         (p->head_dim * elem) % 16 != 0 || p->S > GTMS_ATTENTION_MAX_S || p->S_out > GTMS_ATTENTION_MAX_S)
         return GTMS_ERR_UNSUPPORTED;
-    // A grid of up to 128 CTAs to a (batch, head), or one to 16 rows.
+    // Clusters of up to 8 CTAs to a (batch, head), and a CTA to 8 rows of 4 KB, more shorter ones, of those that stay (to
+    // fewer only while CTAs are few beside the multiprocessors).
     int64_t heads = 0, ctas = 0;
-    if (__builtin_mul_overflow(p->B, p->H, &heads) || __builtin_mul_overflow(heads, *keep / 16 + 129, &ctas) ||
+    if (__builtin_mul_overflow(p->B, p->H, &heads) || __builtin_mul_overflow(heads, *keep / 8 + 129, &ctas) ||
         ctas > INT32_MAX)
         return GTMS_ERR_UNSUPPORTED;
     return GTMS_OK;

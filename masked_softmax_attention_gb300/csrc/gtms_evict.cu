@@ -11,9 +11,11 @@
 //   gather  (or move, in place) takes rows of k and v, weights and positions. What bounds
 //           the call: the kept rows are read once and written once (a weight is 4 of its
 //           4 + 4 D bytes).
-// 32 x 8 heads, half of 16384 rows of 256 bytes: 344 us, 6.3 TB/s, of which the selection
-// takes some 20. One sequence, 8 heads, a quarter of 131072: 63 us, of them 18 (64 CTAs; a
-// cluster's sums of 2048 bins, two barriers each, come to 2.7 us of each histogram).
+// Timed here, on the device, rows of 256 bytes: HALF, 32 sequences of 7000 to 16384 entries, 8
+// heads, of which 8192 stay: 345 us, 6.3 TB/s, the selection's share some 20; and QUARTER, one
+// sequence of 131072, 8 heads, of which 32768 stay: 63 us, of them 18 (64 CTAs; a cluster's
+// sums of 2048 bins, two barriers each, come to 2.7 us of each histogram). The figures
+// below are those of this code with the one thing changed.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -28,10 +30,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32, kSelectCluster = 8;
 // Where a CTA of select has its weights: in registers, in shared memory, or, longer
-// shares, in memory, which every pass reads anew. Registers, not shared memory: the two
-// times above 365 beside 371 and 68 beside 72 us; shared memory, not memory (8 heads of
-// 262144, 16384 stay): 56 beside 69. One CTA to a multiprocessor: with two, whose shared
-// memory leaves little first-level cache for gather's loads, the first took 430.
+// shares, in memory, which every pass reads anew. In shared memory instead of registers
+// HALF takes 352 us and QUARTER 66, two such CTAs to a multiprocessor 412 and 71 (they leave
+// little first-level cache for gather's loads); in memory instead of shared memory 8 heads of
+// 262144, 16384 stay, 66 instead of 52.
 constexpr int kSelectKeys = 16, kSelectHeld = kSelectKeys * kSelectThreads, kSelectStaged = 40960;
 enum class Keys { held, staged, memory };
 // Bins of a histogram (11, 11 and 10 bits), and its copies, by lane: neighbouring weights
@@ -275,7 +277,7 @@ gtms_evict_select_kernel(const EvictArgs a)
     }
     int32_t* to = kept + a.first;
     const uint32_t below = (1u << lane) - 1u;
-    if (!tied) {   // no count of those that equal it (2 % of both times above)
+    if (!tied) {   // no count of those that equal it (with it HALF 347 us, QUARTER 64)
         const uint32_t at_least = prefix - 1;
         uint32_t before = gt + (eq < need ? eq : need);
         in_order([&](int32_t i, uint32_t k) {   // the whole warp
@@ -285,14 +287,14 @@ gtms_evict_select_kernel(const EvictArgs a)
             before += __popc(g);
         });
     } else {
-    in_order([&](int32_t i, uint32_t k) {   // the whole warp
-        const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix);
-        const uint32_t eq_before = eq + __popc(e & below);
-        if (k > prefix || (k == prefix && eq_before < need))
-            to[gt + __popc(g & below) + (eq_before < need ? eq_before : need)] = from + i + lane;
-        gt += __popc(g);
-        eq += __popc(e);
-    });
+        in_order([&](int32_t i, uint32_t k) {   // the whole warp
+            const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix);
+            const uint32_t eq_before = eq + __popc(e & below);
+            if (k > prefix || (k == prefix && eq_before < need))
+                to[gt + __popc(g & below) + (eq_before < need ? eq_before : need)] = from + i + lane;
+            gt += __popc(g);
+            eq += __popc(e);
+        });
     }
     if (ranks > 1)
         cluster.sync();   // the others may still be reading this CTA's counts
@@ -303,8 +305,8 @@ constexpr int kGatherThreads = 256, kGatherUnroll = 2;
 // Rows go elsewhere: a CTA moves its part of one (batch, head)'s rows of k and v, and of
 // weights and positions. Neighbouring threads take the 16-byte units of a row; a thread
 // has its unit of two rows of both in flight (of four, with fewer CTAs for their
-// registers: 365 beside 350 us at the first of the times above, 68 beside 64; of one: 355;
-// more CTAs by a limit on registers: 360 and more).
+// registers: HALF 363 us, QUARTER 67; of one: 351 and 63; six or eight CTAs by a limit on
+// registers: 354 and 65, 385 and 71).
 __global__ void __launch_bounds__(kGatherThreads)
 gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 {
@@ -360,9 +362,10 @@ gtms_evict_gather_kernel(const EvictArgs a, int32_t parts, int32_t rows)
 // before any is written, and later steps read only rows behind those that this one
 // writes. A cluster's CTAs share the rows of a step; the copies of the steps that follow
 // are in flight in shared memory meanwhile, and their rows' numbers are read a step before.
-// The two calls above in place: 358 and 89 us (a CTA to a slice of every row's columns
-// instead: 698 and 224). A step of 32 KB a CTA, since the cluster's barrier takes a
-// microsecond of each: of 16 KB 369 and 113, of 8 KB 371 and 160; two stages 413 and 98.
+// In place HALF takes 318 us (the sequences of up to 8192 entries stay as they are; all of
+// 16384: 357) and QUARTER 87; a CTA to a slice of every row's columns instead took about
+// twice as long. A step of 32 KB a CTA, since the cluster's barrier takes a microsecond of each: of
+// 16 KB, all of 16384, 378, and QUARTER 111; of 8 KB 367 and 156; two stages 411 and 97.
 constexpr int kMoveStages = 3, kMoveUnroll = 8, kMoveCluster = 8;
 constexpr int kMoveBytes = kMoveStages * kMoveUnroll * kGatherThreads * 16;
 
@@ -511,7 +514,7 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t st)
     EvictArgs a = args;
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
     // Select: CTAs to a row as long as all run at once, 4096 weights to each at least (32 heads of 60129 weights: clusters
-    // of 8, which take two turns, 63 us the call, of 4 35).
+    // of 8, which take two turns, 63 us the call, of 4 38).
     unsigned ranks = 1;
     while (ranks < kSelectCluster && 2 * heads * ranks <= kChipSms && static_cast<int64_t>(ranks) * 8192 <= a.S)
         ranks *= 2;
@@ -526,8 +529,8 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t st)
     if (!(a.weights == a.weights_out || (a.positions && a.positions == a.positions_out)))
         a.moved |= 4;
     if (a.moved) {
-        // Rows of a CTA: 4 turns of its threads (347 us at 32 x 8 heads of 8192 rows; 8 turns 350, 2 turns 358, 32 turns
-        // 368), fewer until there are six CTAs to a multiprocessor.
+        // Rows of a CTA: 4 turns of its threads (HALF 345 us; 8 turns 348, 2 turns 356, 32 turns 365), fewer until there
+        // are six CTAs to a multiprocessor.
         const int32_t turn = kGatherThreads / a.units * kGatherUnroll;
         int32_t rows = 4 * turn;
         while (rows > turn && heads * ((a.keep + rows - 1) / rows) < 6 * kChipSms)

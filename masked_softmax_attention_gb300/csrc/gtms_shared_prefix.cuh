@@ -118,13 +118,12 @@ struct ChunkWarp {
     static constexpr int KC = 2 * (D / 32), VC = 4 * (D / 64);   // 16-byte chunks a lane takes of 16 keys, of their values
     uint4 kv[ST][KC + VC][32];        // [chunk][lane]: every lane reads back what it asked for itself
     uint4 q[R][D / 8];                // chunk x of row r at x ^ r % 8
-    static constexpr int per_sm = 227 * 1024 / (ST * (KC + VC) * 512 + R * D * 2 + 1024);   // warps of a multiprocessor
 };
 
 // A chunk of a sequence's own keys to a warp (a CTA), which shares nothing with any other:
-// a part more of its rows' sums. Copies run three blocks of 16 keys ahead through shared
-// memory: with the next block in registers, as in the split kernel, 16 warps have 64 to
-// 128 KB of a multiprocessor in flight, and the 2 to 3 us of a busy memory want 150.
+// a part more of its rows' sums. Copies run through three stages of 16 keys in shared
+// memory, two of them ahead of the products: 8 warps of 26.6 KB to a multiprocessor at head
+// dim 128, 16 at 64, have 128 KB in flight, where the 2 to 3 us of a busy memory want 150.
 // The keys are the M side of both products (S^T = K Q^T, O^T = V^T P^T), so that a tile is
 // 8 rows per NT, which one token's heads fill. P^T comes out of the first product with a
 // key to a row and goes into the second with a row to a column: an 8 x 8 transposition.
