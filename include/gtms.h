@@ -373,7 +373,7 @@ int gtms_attention_shared_prefix_workspace(const gtms_attention_shape* shape, in
  * it is the weight of a sequence's own keys in the whole softmax.
  *   q, k, seq_lens, q_offsets   as in gtms_attention_forward.
  *   lse         fp32 [B, Hq, Sq], contiguous: what the forward wrote. A row whose lse is
- *               -infinity adds nothing.
+ *               -infinity adds nothing to a key unless their score is NaN or +infinity.
  *   weights     fp32 [B, Hkv, Skv], contiguous: w, and +0.0 where no row keeps the key; with
  *               `accumulate` not 0 w is added to what stands there, and keys at c >= L
  *               are left alone: the caller sets the weights of keys that are new since
