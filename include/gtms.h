@@ -345,9 +345,9 @@ int gtms_attention_backward_workspace(const gtms_attention_shape* shape, uint64_
  * The prefix is seen whole, so that masks are GTMS_MASK_GROUPED_TRIL or
  * GTMS_MASK_LENGTH. Partial sums over the parts of a prefix are joined in fp32.
  * Probabilities are rounded to 16 bits before their product with v, as in
- * gtms_attention_forward, save in small calls (at most 32 tiles of query rows, 128 of one
- * head at head_dim 64 and 256 at 128, and prefix + Skv <= 896, unless Skv is so long that the
- * rows are packed), which carry them as two 16-bit numbers: o is then off by its own
+ * gtms_attention_forward, save in small calls (prefix > 0, at most 32 tiles of query rows,
+ * 128 of one head at head_dim 64 and 256 at 128, and prefix + Skv <= 896, unless Skv is so
+ * long that the rows are packed), which carry them as two 16-bit numbers: o is then off by its own
  * rounding alone. Otherwise types and a NaN's reach are gtms_attention_forward's, and
  * so are the errors, and GTMS_ERR_INVALID_ARG: negative groups or prefix, B not a
  * multiple of groups, a missing or too small workspace, a workspace that overlaps
